@@ -8,8 +8,7 @@
 #include <atomic>
 #include <mutex>
 
-#include "../../include/moe.h"
-#include "internal.h"
+#include "abi.h"
 
 namespace moe {
 
@@ -28,10 +27,6 @@ void *tensor_map_encoder() {
 }
 
 namespace {
-
-constexpr size_t kHeader = 256;  // status word at offset 0
-
-inline size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 struct Layout {
   // route scratch (r_zero: bytes from the start that each call zeroes: header and tickets)
@@ -214,12 +209,13 @@ Layout layout_of(const moe_config *c) {
   return L;
 }
 
-inline bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// ---- optional per-kernel timing
+std::atomic<void *const *> g_events{nullptr};
+std::atomic<int> g_cap{0};
+std::atomic<int> g_count{0};
+const char *g_labels[4096];
 
-struct DevInfo {
-  int sms = 0;
-  bool ok = false;
-};
+}  // namespace
 
 moe_status device_info(DevInfo *out) {
   static DevInfo cache[kMaxDevices];
@@ -239,41 +235,23 @@ moe_status device_info(DevInfo *out) {
   return MOE_OK;
 }
 
-// ---- optional per-kernel timing
-std::atomic<void *const *> g_events{nullptr};
-std::atomic<int> g_cap{0};
-std::atomic<int> g_count{0};
-const char *g_labels[4096];
-
-template <class F>
-moe_status timed(const char *label, cudaStream_t s, F &&launch) {
-  void *const *ev = g_events.load();
-  int slot = -1;
-  if (ev) {
-    slot = g_count.fetch_add(1);
-    if (slot >= g_cap.load() || slot >= 4096) slot = -1;
-  }
-  if (slot >= 0) {
-    g_labels[slot] = label;
-    if (cudaEventRecord(static_cast<cudaEvent_t>(ev[2 * slot]), s) != cudaSuccess) {
-      cudaGetLastError();  // the failed record, not a launch error
-      return MOE_ERR_CUDA;
-    }
-  }
-  cudaError_t e = launch();
-  if (slot >= 0 && e == cudaSuccess &&
-      cudaEventRecord(static_cast<cudaEvent_t>(ev[2 * slot + 1]), s) != cudaSuccess) {
-    cudaGetLastError();
-    return MOE_ERR_CUDA;
-  }
-  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+int timing_slot(const char *label) {
+  if (!g_events.load()) return -1;
+  const int slot = g_count.fetch_add(1);
+  if (slot >= g_cap.load() || slot >= 4096) return -1;
+  g_labels[slot] = label;
+  return slot;
 }
 
-#define MOE_TRY(x)                      \
-  do {                                  \
-    moe_status _st = (x);               \
-    if (_st != MOE_OK) return _st;      \
-  } while (0)
+bool timing_record(int slot, bool after, cudaStream_t s) {
+  void *const *ev = g_events.load();
+  if (!ev) return true;  // detached in between
+  if (cudaEventRecord(static_cast<cudaEvent_t>(ev[2 * slot + (after ? 1 : 0)]), s) == cudaSuccess) return true;
+  cudaGetLastError();  // the failed record, not a launch error
+  return false;
+}
+
+namespace {
 
 // Token-sized arrays may be null when there are no tokens.
 moe_status check_routing(const moe_routing *r, int T) {
