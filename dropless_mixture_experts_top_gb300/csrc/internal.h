@@ -65,6 +65,8 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 // Status flags written by kernels into the scratch status word.
 constexpr int32_t kDevNonfiniteLogit = 0x1;
 constexpr int32_t kDevWaitTimeout = 0x2;
+constexpr int32_t kDevNonfiniteUpdate = 0x4;
+constexpr int32_t kDevBadIndex = 0x8;
 
 // ---- routing (route.cu)
 constexpr int kRouteTokensPerBlock = 64;  // tokens per route block (one histogram row)

@@ -21,6 +21,8 @@ MOE_OK = 0
 PRECISIONS = {"bf16": 0, "fp8_bwd": 1, "mxfp8": 2}
 DEV_NONFINITE_LOGIT = 0x1
 DEV_WAIT_TIMEOUT = 0x2
+DEV_NONFINITE_UPDATE = 0x4
+DEV_BAD_INDEX = 0x8
 
 _lib = None
 
@@ -31,6 +33,8 @@ EXPORTED = [
     "moe_get_device_status",
     "moe_status_string", "moe_timing_attach", "moe_timing_count", "moe_timing_label",
     "moe_selftest_wait_timeout", "moe_router_workspace", "moe_router_forward", "moe_router_backward",
+    "moe_norm_workspace", "moe_norm_forward", "moe_norm_backward",
+    "moe_balance_workspace", "moe_balance_forward", "moe_balance_backward",
 ]
 
 
@@ -42,6 +46,15 @@ class Config(ctypes.Structure):
 class Routing(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("topk_idx", "topk_w", "counts", "offsets", "row_of_slot", "slot_of_row", "w_row")]
+
+
+class NormConfig(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("kind", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
+class BalanceConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "E", "k", "sequences")]
 
 
 class SavedLayout(ctypes.Structure):
@@ -96,6 +109,15 @@ def lib():
         L.moe_router_forward.argtypes = [P, P, P, P, P, sz, P]
         L.moe_router_backward.argtypes = [P, P, P, P, P, P, P, sz, P]
         for f in ("moe_router_workspace", "moe_router_forward", "moe_router_backward"):
+            getattr(L, f).restype = ctypes.c_int
+        L.moe_norm_workspace.argtypes = [P, P]
+        L.moe_norm_forward.argtypes = [P] * 9
+        L.moe_norm_backward.argtypes = [P] * 10 + [sz, P]
+        L.moe_balance_workspace.argtypes = [P, P]
+        L.moe_balance_forward.argtypes = [P] * 10 + [sz, P]
+        L.moe_balance_backward.argtypes = [P] * 5 + [ctypes.c_float, ctypes.c_float, P, ctypes.c_int32, P]
+        for f in ("moe_norm_workspace", "moe_norm_forward", "moe_norm_backward", "moe_balance_workspace",
+                  "moe_balance_forward", "moe_balance_backward"):
             getattr(L, f).restype = ctypes.c_int
         L.moe_status_string.argtypes = [ctypes.c_int]
         L.moe_status_string.restype = ctypes.c_char_p
@@ -272,6 +294,138 @@ class Router:
     def status(self, stream=None) -> dict:
         return {n: get_device_status(b, stream) for n, b in (("forward", self.fwd_scratch),
                                                              ("backward", self.bwd_scratch))}
+
+
+# ---- around the layer: the norm, the balance loss and the orthogonalised update
+
+DTYPES = {"bf16": 0, "fp32": 1}
+NORM_KINDS = {"layer": 0, "rms": 1}
+# what a tensor of each type may be: bf16 also as the int16 view of its bits
+_BF16 = (torch.bfloat16, torch.int16)
+_TORCH_DTYPES = {"bf16": _BF16, "fp32": (torch.float32,)}
+
+
+def _addr(t, name, shape, dtypes, device):
+    """The address of a tensor argument (None: no address), which has to be a dense
+    tensor of this shape and one of these types on this device."""
+    if t is None:
+        return None
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected one of {dtypes}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+    return t.data_ptr()
+
+
+def _device(device):
+    d = torch.device(device)
+    return torch.device("cuda", torch.cuda.current_device()) if d.type == "cuda" and d.index is None else d
+
+
+def _raw_stream(stream):
+    return torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
+
+
+class Norm:
+    """Layer norm (kind "layer") or RMS norm ("rms") over [T, H] of one type
+    ("bf16" or "fp32"), with the residual sum in front of it, and its backward.
+
+    Dictionaries that a call returned may be handed to the next one, which then
+    writes into the same tensors.  Outputs have the type of x (or dy); the
+    statistics and the weight's gradients are fp32."""
+
+    def __init__(self, T, H, kind="layer", dtype="bf16", bias=True, eps=1e-5, device="cuda"):
+        self.cfg = NormConfig(int(T), int(H), NORM_KINDS[kind], DTYPES[dtype], float(eps))
+        n = ctypes.c_size_t()
+        _check(lib().moe_norm_workspace(ctypes.byref(self.cfg), ctypes.byref(n)), "moe_norm_workspace")
+        self.device, self.bias = _device(device), bool(bias)
+        self._cfg, self._types = ctypes.byref(self.cfg), _TORCH_DTYPES[dtype]
+        self._rows, self._cols, self._stats = (torch.Size(s) for s in ((T, H), (H,), (T, 2)))
+        self.bwd_scratch = torch.empty(n.value, dtype=torch.uint8, device=self.device)
+
+    def forward(self, x, weight, bias=None, residual=None, out=None, stream=None) -> dict:
+        """{"y", "sum" (x + residual, or None), "stats" [T, 2]: mean and 1 / deviation}"""
+        d, ty, rows, cols, L = self.device, self._types, self._rows, self._cols, lib()
+        if (bias is not None) != self.bias:
+            raise ValueError("bias: given to a norm without one" if bias is not None else "bias: missing")
+        if out is None:
+            out = {"y": torch.empty_like(x), "sum": torch.empty_like(x) if residual is not None else None,
+                   "stats": torch.empty(self._stats, dtype=torch.float32, device=d)}
+        _check(L.moe_norm_forward(
+            self._cfg, _addr(x, "x", rows, ty, d), _addr(residual, "residual", rows, ty, d),
+            _addr(weight, "weight", cols, ty, d), _addr(bias, "bias", cols, ty, d), _addr(out["y"], "y", rows, ty, d),
+            _addr(out["sum"], "sum", rows, ty, d), _addr(out["stats"], "stats", self._stats, _F32, d),
+            _raw_stream(stream)), "moe_norm_forward")
+        return out
+
+    def backward(self, dy, h, weight, stats, d_sum=None, grads=None, stream=None) -> dict:
+        """{"dx", "dweight", "dbias" (None without a bias)} from the forward's
+        stats and h, its sum (x where there was no residual)."""
+        d, ty, rows, cols, L = self.device, self._types, self._rows, self._cols, lib()
+        if grads is None:
+            grads = {"dx": torch.empty_like(dy), "dweight": torch.empty(cols, dtype=torch.float32, device=d),
+                     "dbias": torch.empty(cols, dtype=torch.float32, device=d) if self.bias else None}
+        _check(L.moe_norm_backward(
+            self._cfg, _addr(dy, "dy", rows, ty, d), _addr(h, "h", rows, ty, d),
+            _addr(weight, "weight", cols, ty, d), _addr(stats, "stats", self._stats, _F32, d),
+            _addr(d_sum, "d_sum", rows, ty, d), _addr(grads["dx"], "dx", rows, ty, d),
+            _addr(grads["dweight"], "dweight", cols, _F32, d), _addr(grads["dbias"], "dbias", cols, _F32, d),
+            self.bwd_scratch.data_ptr(), self.bwd_scratch.numel(), _raw_stream(stream)), "moe_norm_backward")
+        return grads
+
+
+_F32, _I32, _U8 = (torch.float32,), (torch.int32,), (torch.uint8, torch.bool)
+
+
+class BalanceLoss:
+    """The router's balance loss and z loss over `sequences` equal parts of T
+    tokens, with per-expert counts, and their gradient for the logits."""
+
+    def __init__(self, T, E, k, sequences=1, device="cuda"):
+        self.cfg = BalanceConfig(int(T), int(E), int(k), int(sequences))
+        n = ctypes.c_size_t()
+        _check(lib().moe_balance_workspace(ctypes.byref(self.cfg), ctypes.byref(n)), "moe_balance_workspace")
+        self.device, self._cfg = _device(device), ctypes.byref(self.cfg)
+        self._te, self._tk, self._t, self._se, self._s, self._two = (
+            torch.Size(s) for s in ((T, E), (T, k), (T,), (sequences, E), (sequences,), (2,)))
+        self.fwd_scratch = torch.empty(n.value, dtype=torch.uint8, device=self.device)
+
+    def forward(self, logits, topk_idx, mask=None, out=None, stream=None) -> dict:
+        """{"loss" [2]: balance, z; "counts" and "probs" [sequences, E]; "tokens"
+        [sequences]; "lse" [T]}.  mask [T]: zero for padding."""
+        d, L = self.device, lib()
+        if out is None:
+            f32, i32 = dict(dtype=torch.float32, device=d), dict(dtype=torch.int32, device=d)
+            out = {"loss": torch.empty(self._two, **f32), "counts": torch.empty(self._se, **i32),
+                   "probs": torch.empty(self._se, **f32), "tokens": torch.empty(self._s, **i32),
+                   "lse": torch.empty(self._t, **f32)}
+        _check(L.moe_balance_forward(
+            self._cfg, _addr(logits, "logits", self._te, _F32, d), _addr(topk_idx, "topk_idx", self._tk, _I32, d),
+            _addr(mask, "mask", self._t, _U8, d), _addr(out["loss"], "loss", self._two, _F32, d),
+            _addr(out["counts"], "counts", self._se, _I32, d), _addr(out["probs"], "probs", self._se, _F32, d),
+            _addr(out["tokens"], "tokens", self._s, _I32, d), _addr(out["lse"], "lse", self._t, _F32, d),
+            self.fwd_scratch.data_ptr(), self.fwd_scratch.numel(), _raw_stream(stream)), "moe_balance_forward")
+        return out
+
+    def backward(self, logits, counts, tokens, lse, g_balance, g_z, d_logits=None, stream=None):
+        """The gradient of g_balance * loss[0] + g_z * loss[1], added to d_logits in
+        place where that is given (as the layer's backward left it)."""
+        d, L = self.device, lib()
+        add = d_logits is not None
+        if not add:
+            d_logits = torch.empty(self._te, dtype=torch.float32, device=d)
+        _check(L.moe_balance_backward(
+            self._cfg, _addr(logits, "logits", self._te, _F32, d), _addr(counts, "counts", self._se, _I32, d),
+            _addr(tokens, "tokens", self._s, _I32, d), _addr(lse, "lse", self._t, _F32, d), g_balance, g_z,
+            _addr(d_logits, "d_logits", self._te, _F32, d), add, _raw_stream(stream)), "moe_balance_backward")
+        return d_logits
+
+    def status(self, stream=None) -> dict:
+        return {"forward": get_device_status(self.fwd_scratch, stream)}
 
 
 def selftest_wait_timeout(status, stream=None):

@@ -78,6 +78,8 @@ typedef enum {
 /* Device status flags (moe_get_device_status *host_code). */
 #define MOE_DEV_NONFINITE_LOGIT 0x1 /* a logit was NaN or +-Inf; routing outputs unspecified */
 #define MOE_DEV_WAIT_TIMEOUT 0x2    /* a pipeline wait exceeded its bound; outputs unspecified */
+#define MOE_DEV_NONFINITE_UPDATE 0x4 /* moe_ortho_update: a matrix's sum of squares is not finite; it becomes NaN */
+#define MOE_DEV_BAD_INDEX 0x8       /* moe_balance_forward: an expert index outside [0, E); that slot is not counted */
 
 typedef struct {
   int32_t T;         /* tokens */
@@ -256,6 +258,87 @@ moe_status moe_router_forward(const moe_config *cfg, const void *x, const void *
 moe_status moe_router_backward(const moe_config *cfg, const void *x, const void *W_r,
                                const float *d_logits, void *dx, float *dW_r, void *scratch,
                                size_t scratch_bytes, void *stream);
+
+/* ---- what surrounds the layer in a training step: the norm in front of it,
+ * the router's balance loss, and the update of the expert weights.  These
+ * three take configurations of their own; everything else is as above (the
+ * caller's buffers, dense row-major layouts, 16-byte aligned device pointers,
+ * one stream, capturable, nothing allocated). */
+
+typedef enum {
+  MOE_DTYPE_BF16 = 0,
+  MOE_DTYPE_FP32 = 1
+} moe_dtype;
+
+/* Layer norm (or RMS norm) over rows of H elements, with the residual sum in
+ * front of it.  Any 1 <= H <= 8192, 0 <= T <= 2^30; H a multiple of 8 (bf16) or
+ * 4 (fp32) is fastest.  x, residual, weight, bias, y, sum, dy, d_sum and dx are
+ * of the configuration's type, statistics and weight gradients fp32.
+ * Forward: h = x + residual (rounded to the type and written to sum; residual
+ * and sum are both NULL when there is none, and then h = x),
+ *   mu = mean h (MOE_NORM_RMS: 0), r = 1 / sqrt(mean (h - mu)^2 + eps),
+ *   y = (h - mu) r weight + bias   (bias may be NULL),
+ * stats [T,2] = mu, r, which the backward reads.  sum may be x or residual
+ * itself; y overlaps no input.
+ * Backward, from dy, h (the forward's sum, or x), weight and stats, with
+ * xh = (h - mu) r and g = dy weight:
+ *   dx = r (g - mean g - xh mean(g xh)) + d_sum   (MOE_NORM_RMS: no mean g)
+ *   dweight [H] = sum_t dy xh,  dbias [H] = sum_t dy   (overwritten)
+ * d_sum (may be NULL) is the gradient that reaches h past the norm; dx may be
+ * d_sum itself.  dbias may be NULL.  Sums run in a fixed order: the same bits
+ * every time.  With T == 0 the weight gradients are zeroed. */
+typedef enum {
+  MOE_NORM_LAYER = 0,
+  MOE_NORM_RMS = 1
+} moe_norm_kind;
+typedef struct {
+  int32_t T;     /* rows */
+  int32_t H;     /* elements per row */
+  int32_t kind;  /* moe_norm_kind */
+  int32_t dtype; /* moe_dtype */
+  float eps;     /* >= 0 */
+} moe_norm_config;
+moe_status moe_norm_workspace(const moe_norm_config *cfg, size_t *bwd_scratch);
+moe_status moe_norm_forward(const moe_norm_config *cfg, const void *x, const void *residual, const void *weight,
+                            const void *bias, void *y, void *sum, float *stats, void *stream);
+moe_status moe_norm_backward(const moe_norm_config *cfg, const void *dy, const void *h, const void *weight,
+                             const float *stats, const void *d_sum, void *dx, float *dweight, float *dbias,
+                             void *scratch, size_t scratch_bytes, void *stream);
+
+/* The router's auxiliary losses, from the logits and the experts chosen
+ * (moe_routing's topk_idx).  The T tokens are `sequences` sequences of T /
+ * sequences tokens each (1 <= sequences, a divisor of T; 1 for the whole batch);
+ * 1 <= E <= 256, 1 <= k <= min(E, 16), T <= 2^30.  mask [T] (may be NULL): tokens
+ * with a zero byte are padding.  Padding, and tokens whose logits are all -inf,
+ * have no part in any sum or count, whatever they hold.  With c_se = the slots of
+ * sequence s's tokens that chose e, N_s its tokens, N their sum, S' the sequences
+ * that have any, f_se = c_se / (k N_s), P_se = the mean softmax probability:
+ *   loss[0] = (1/S') sum_s E sum_e f_se P_se     (1 when the load is even)
+ *   loss[1] = (1/N) sum_t lse_t^2                (the z loss; lse: log sum exp)
+ *   counts [sequences,E] = c, probs [sequences,E] = P (0 where N_s = 0),
+ *   tokens [sequences] = N_s, lse [T] (+inf for tokens without a part).
+ * Single logits of -inf are experts that a token may not choose.  A NaN or
+ * +inf logit makes the losses NaN and sets MOE_DEV_NONFINITE_LOGIT; the status
+ * word is at the start of the scratch.
+ * Backward, from what the forward left, for the training loss g_balance *
+ * loss[0] + g_z * loss[1] (counts are constants):
+ *   d_logits_te (+)= g_balance E / (S' N_s) p_te (f_se - sum_e' f_se' p_te')
+ *                    + g_z (2/N) lse_t p_te,     0 for tokens without a part,
+ * added to d_logits (as moe_backward leaves it) when accumulate is nonzero,
+ * else written. */
+typedef struct {
+  int32_t T;         /* tokens */
+  int32_t E;         /* experts */
+  int32_t k;         /* experts per token */
+  int32_t sequences; /* equal parts of the tokens, each balanced by itself */
+} moe_balance_config;
+moe_status moe_balance_workspace(const moe_balance_config *cfg, size_t *fwd_scratch);
+moe_status moe_balance_forward(const moe_balance_config *cfg, const float *logits, const int32_t *topk_idx,
+                               const uint8_t *mask, float *loss, int32_t *counts, float *probs, int32_t *tokens,
+                               float *lse, void *scratch, size_t scratch_bytes, void *stream);
+moe_status moe_balance_backward(const moe_balance_config *cfg, const float *logits, const int32_t *counts,
+                                const int32_t *tokens, const float *lse, float g_balance, float g_z,
+                                float *d_logits, int32_t accumulate, void *stream);
 
 /* Routing without a caller-provided scratch buffer.  The paper has no
  * counterpart: it exists for callers that cannot allocate device memory --
