@@ -124,6 +124,17 @@ __device__ __forceinline__ void tma_load_2d_pair(void *smem_dst, const void *tma
       : "memory");
 }
 
+// The same from a 3-D map (a batch of matrices): c2 is the matrix.  Coordinates
+// past a matrix's own rows or columns read as zero.
+__device__ __forceinline__ void tma_load_3d_pair(void *smem_dst, const void *tmap, uint32_t bar_cluster_addr,
+                                                 int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_addr(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar_cluster_addr), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
 // Tensor maps kept in global memory: set one global dimension of a map, publish
 // the change to the tensor-map proxy, and (in the consumer) acquire it.
 __device__ __forceinline__ void tmap_set_global_dim(void *gmap, int ord, uint32_t value) {
@@ -293,6 +304,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_
          | (static_cast<uint32_t>(b_mn) << 16)       // B major
          | (static_cast<uint32_t>(N >> 3) << 17)     // N / 8
          | (static_cast<uint32_t>(M >> 4) << 24);    // M / 16
+}
+
+// The same with fp16 A/B.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn) {
+  return idesc_bf16(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
 }
 
 }  // namespace moe

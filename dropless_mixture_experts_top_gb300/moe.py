@@ -35,6 +35,7 @@ EXPORTED = [
     "moe_selftest_wait_timeout", "moe_router_workspace", "moe_router_forward", "moe_router_backward",
     "moe_norm_workspace", "moe_norm_forward", "moe_norm_backward",
     "moe_balance_workspace", "moe_balance_forward", "moe_balance_backward",
+    "moe_ortho_workspace", "moe_ortho_update",
 ]
 
 
@@ -55,6 +56,10 @@ class NormConfig(ctypes.Structure):
 
 class BalanceConfig(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "E", "k", "sequences")]
+
+
+class OrthoConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "R", "C", "steps", "dtype")] + [("eps", ctypes.c_float)]
 
 
 class SavedLayout(ctypes.Structure):
@@ -116,7 +121,9 @@ def lib():
         L.moe_balance_workspace.argtypes = [P, P]
         L.moe_balance_forward.argtypes = [P] * 10 + [sz, P]
         L.moe_balance_backward.argtypes = [P] * 5 + [ctypes.c_float, ctypes.c_float, P, ctypes.c_int32, P]
-        for f in ("moe_norm_workspace", "moe_norm_forward", "moe_norm_backward", "moe_balance_workspace",
+        L.moe_ortho_workspace.argtypes = [P, P]
+        L.moe_ortho_update.argtypes = [P, P, P, P, ctypes.c_float, ctypes.c_int32, ctypes.c_float, P, P, sz, P]
+        for f in ("moe_ortho_workspace", "moe_ortho_update", "moe_norm_workspace", "moe_norm_forward", "moe_norm_backward", "moe_balance_workspace",
                   "moe_balance_forward", "moe_balance_backward"):
             getattr(L, f).restype = ctypes.c_int
         L.moe_status_string.argtypes = [ctypes.c_int]
@@ -426,6 +433,43 @@ class BalanceLoss:
 
     def status(self, stream=None) -> dict:
         return {"forward": get_device_status(self.fwd_scratch, stream)}
+
+
+# the quintic Newton-Schulz step whose five-fold use is the Muon optimiser's
+MUON_COEFS = ((3.4445, -4.7750, 2.0315),) * 5
+
+
+class Orthogonaliser:
+    """The orthogonalised update of `batch` matrices [R, C] by Newton-Schulz
+    products, optionally through a momentum, over a scratch buffer of its own.
+    coefs: one (a, b, c) per step."""
+
+    def __init__(self, batch, R, C, dtype="bf16", coefs=MUON_COEFS, eps=1e-7, device="cuda"):
+        coefs = [float(v) for step in coefs for v in step]
+        if not coefs or len(coefs) % 3:
+            raise ValueError("coefs: three numbers for each of one or more steps")
+        self.cfg = OrthoConfig(int(batch), int(R), int(C), len(coefs) // 3, DTYPES[dtype], float(eps))
+        n = ctypes.c_size_t()
+        _check(lib().moe_ortho_workspace(ctypes.byref(self.cfg), ctypes.byref(n)), "moe_ortho_workspace")
+        self.device, self._cfg, self._types = _device(device), ctypes.byref(self.cfg), _TORCH_DTYPES[dtype]
+        self._shape = torch.Size((batch, R, C))
+        self._coefs = (ctypes.c_float * len(coefs))(*coefs)
+        self.scratch = torch.empty(n.value, dtype=torch.uint8, device=self.device)
+
+    def update(self, g, momentum=None, beta=0.95, nesterov=True, scale=1.0, out=None, stream=None):
+        """scale times the orthogonalised update, bf16 [batch, R, C]; momentum (fp32)
+        is advanced in place."""
+        d, s, L = self.device, self._shape, lib()
+        if out is None:
+            out = torch.empty(s, dtype=g.dtype if g.dtype in _BF16 else torch.bfloat16, device=d)
+        _check(L.moe_ortho_update(
+            self._cfg, self._coefs, _addr(g, "g", s, self._types, d), _addr(momentum, "momentum", s, _F32, d), beta,
+            nesterov, scale, _addr(out, "out", s, _BF16, d), self.scratch.data_ptr(), self.scratch.numel(),
+            _raw_stream(stream)), "moe_ortho_update")
+        return out
+
+    def status(self, stream=None) -> dict:
+        return {"update": get_device_status(self.scratch, stream)}
 
 
 def selftest_wait_timeout(status, stream=None):

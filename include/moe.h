@@ -340,6 +340,37 @@ moe_status moe_balance_backward(const moe_balance_config *cfg, const float *logi
                                 const int32_t *tokens, const float *lse, float g_balance, float g_z,
                                 float *d_logits, int32_t accumulate, void *stream);
 
+/* The orthogonalised update of a batch of matrices by Newton-Schulz products
+ * (the Muon optimiser's, for example of dW_gate, dW_up [E,H,I] or dW_down
+ * [E,I,H]).  g: device [batch,R,C] of the configuration's type; momentum: device
+ * fp32 [batch,R,C], updated in place, or NULL.  Per matrix, in fp32,
+ *   u = g, or with momentum:  m <- beta m + g,  u = g + beta m (nesterov) or m;
+ *   X = u / max(|u|_F, eps);
+ *   steps times, with step i's (a, b, c) = coefs[3i .. 3i+2] (host memory, read
+ *   during the call):  S = X X^T (R <= C) or X^T X,  P = a I + b S + c S^2,
+ *   X <- P X or X P;
+ *   out = scale X, bf16 [batch,R,C].
+ * X, S and P are rounded to fp16 between products, whose sums are fp32; the
+ * coefficients are to keep X's singular values below about 100 (the usual quintic,
+ * 3.4445 -4.7750 2.0315 five times, keeps them below 1.3).  Singular values far below
+ * |u|_F / 1000 grow out of the roundings as they do out of a bf16 gradient's own.
+ * 1 <= R, C <= 16384, 0 <= batch <= 65535, 1 <= steps <= 64, any alignment of rows
+ * (multiples of 8 columns are fastest).  out may not overlap g or momentum.  A
+ * matrix of zeros gives zeros; one whose sum of squares is not finite gives NaN
+ * and sets MOE_DEV_NONFINITE_UPDATE (status word at the start of the scratch), and
+ * no other matrix is touched by it. */
+typedef struct {
+  int32_t batch; /* matrices */
+  int32_t R, C;  /* rows and columns of each */
+  int32_t steps; /* Newton-Schulz steps */
+  int32_t dtype; /* moe_dtype of g */
+  float eps;     /* >= 0: the least norm divided by */
+} moe_ortho_config;
+moe_status moe_ortho_workspace(const moe_ortho_config *cfg, size_t *scratch);
+moe_status moe_ortho_update(const moe_ortho_config *cfg, const float *coefs, const void *g, float *momentum,
+                            float beta, int32_t nesterov, float scale, void *out, void *scratch,
+                            size_t scratch_bytes, void *stream);
+
 /* Routing without a caller-provided scratch buffer.  The paper has no
  * counterpart: it exists for callers that cannot allocate device memory --
  * code running while a CUDA graph is captured (cudaMalloc is not allowed

@@ -38,6 +38,17 @@ def test_balance_configurations(L, bad):
     assert L.moe_balance_workspace(ctypes.byref(moe.BalanceConfig(**{**good, **bad})), ctypes.byref(n)) == -1
 
 
+@pytest.mark.parametrize("bad", [dict(batch=-1), dict(batch=65536), dict(R=0), dict(C=0), dict(R=16385),
+                                 dict(C=16385), dict(steps=0), dict(steps=65), dict(dtype=2), dict(eps=-1.0),
+                                 dict(eps=float("nan"))])
+def test_ortho_configurations(L, bad):
+    good = dict(batch=4, R=64, C=48, steps=5, dtype=0, eps=1e-7)
+    n = ctypes.c_size_t()
+    assert L.moe_ortho_workspace(ctypes.byref(moe.OrthoConfig(**good)), ctypes.byref(n)) == 0
+    assert n.value >= 256 + 4 * (2 * 64 * 48 + 2 * 48 * 48) * 2
+    assert L.moe_ortho_workspace(ctypes.byref(moe.OrthoConfig(**{**good, **bad})), ctypes.byref(n)) == -1
+
+
 # Made-up device addresses, in a child process that sees no GPU: no kernel could ever get them.
 _SCRIPT = r"""
 import ctypes, sys
@@ -64,13 +75,21 @@ res["bal_misaligned_mask"] = L.moe_balance_forward(B(c), a[0], a[7], odd, a[1], 
 res["bal_small"] = L.moe_balance_forward(B(c), a[0], a[7], None, a[1], a[2], a[3], a[4], a[5], a[6], n.value - 1, None)
 res["bal_bwd_null"] = L.moe_balance_backward(B(c), a[0], None, a[1], a[2], 1.0, 1.0, a[3], 0, None)
 res["bal_bwd_misaligned"] = L.moe_balance_backward(B(c), a[0], a[4], a[1], a[2], 1.0, 1.0, odd, 1, None)
+c = moe.OrthoConfig(4, 64, 48, 1, 0, 1e-7)
+L.moe_ortho_workspace(B(c), B(n))
+f = (ctypes.c_float * 3)(1.5, -0.5, 0.0)
+res["ortho_null_coefs"] = L.moe_ortho_update(B(c), None, a[0], None, 0.9, 1, 1.0, a[1], a[2], n.value, None)
+res["ortho_null_out"] = L.moe_ortho_update(B(c), f, a[0], None, 0.9, 1, 1.0, None, a[2], n.value, None)
+res["ortho_misaligned"] = L.moe_ortho_update(B(c), f, a[0], odd, 0.9, 1, 1.0, a[1], a[2], n.value, None)
+res["ortho_small"] = L.moe_ortho_update(B(c), f, a[0], None, 0.9, 1, 1.0, a[1], a[2], n.value - 1, None)
 print(repr(res))
 """
 
 EXPECTED = {"norm_null_x": -1, "norm_sum_without_residual": -1, "norm_residual_without_sum": -1,
             "norm_misaligned": -2, "norm_bwd_small": -3, "norm_bwd_null_dweight": -1, "norm_bwd_misaligned": -2,
             "bal_null_idx": -1, "bal_misaligned_mask": -2, "bal_small": -3, "bal_bwd_null": -1,
-            "bal_bwd_misaligned": -2}
+            "bal_bwd_misaligned": -2, "ortho_null_coefs": -1, "ortho_null_out": -1, "ortho_misaligned": -2,
+            "ortho_small": -3}
 
 
 def test_refusals_before_launch(L):
