@@ -14,10 +14,12 @@
 // holding kElems elements in V vectors that lie TPR vectors apart, so a warp's
 // accesses are contiguous.  Blocks are persistent over rows: a thread's columns
 // stay the same, so the weight (and in the backward the column sums of dy xh
-// and dy) stay in its registers, and the next row's loads are issued before
-// this row's sums.  The backward's blocks leave one partial row of column sums
-// each, which a second kernel adds in a fixed order: no atomics, the same bits
-// every time.
+// and dy) stay in its registers, while asynchronous copies bring the coming rows
+// into a ring in shared memory.  The backward's blocks leave one partial row of
+// column sums each, which a second kernel adds in a fixed order: no atomics, the
+// same bits every time.
+#include <type_traits>
+
 #include "abi.h"
 #include "common.cuh"
 
@@ -26,7 +28,6 @@ namespace {
 
 constexpr int kMaxH = 8192;
 constexpr int kElems = 16;         // elements of a row per thread
-constexpr int kMaxTpr = kMaxH / kElems;
 constexpr int kThreads = 256;      // threads per block (a wider row takes one block of its own)
 constexpr int kBwdBlocks = 304;    // the backward's partial rows at most: two blocks on each of 152 SMs
 
@@ -113,18 +114,64 @@ __device__ __forceinline__ float2 row_sum(float2 v, int tpr, float2 (*buf)[32], 
   return v;
 }
 
-template <class El, int VB>
-__global__ void __launch_bounds__(512) norm_fwd_kernel(const NormArgs a) {
+// A thread's own vectors of the coming rows: a ring of D rows in shared memory
+// (Q inputs, V vectors per thread), filled by asynchronous copies of VB bytes and
+// read back by the same thread, so no barrier is needed.  Rows of an odd number of
+// bf16 elements have no copies that small; they are stored by the thread itself.
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <int VB, class Raw>
+__device__ __forceinline__ void copy_vec(Raw *dst, const Raw *src) {
+  if constexpr (VB == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+  else if constexpr (VB == 4)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+  else
+    *dst = *src;
+}
+
+// Rows in flight: what fits 64 to 96 KB of a block.
+template <class El, int Q>
+__host__ __device__ constexpr int ring_depth() {
+  return sizeof(El) == 2 ? (Q == 1 ? 4 : 3) : (Q == 1 ? 4 : 2);
+}
+template <class El, int Q>
+__host__ __device__ constexpr int ring_bytes(int threads) {
+  return ring_depth<El, Q>() * Q * kElems * static_cast<int>(sizeof(El)) * threads;
+}
+
+template <class El, int VB, bool RES, int TH>
+__global__ void __launch_bounds__(TH, 1024 / TH) norm_fwd_kernel(const NormArgs a) {
   griddep_wait();  // the previous kernel in the stream has completed
   using Vc = Vec<El, VB>;
   using Raw = typename Vc::Raw;
-  constexpr int N = Vc::N, V = kElems / N;
+  constexpr int N = Vc::N, V = kElems / N, Q = RES ? 2 : 1, D = ring_depth<El, Q>();
+  extern __shared__ __align__(16) uint8_t s_dyn[];
   __shared__ float2 s_red[2][32];
+  Raw *ring = reinterpret_cast<Raw *>(s_dyn) + threadIdx.x;  // vector (d, q, u) is ((d Q + q) V + u) TH further
   int turn = 0;
-  const int tpr = a.tpr, rows = blockDim.x / tpr, lane = threadIdx.x % tpr, g = threadIdx.x / tpr;
+  const int tpr = a.tpr, rows = TH / tpr, lane = threadIdx.x % tpr, g = threadIdx.x / tpr;
   const int nv = a.H / N;
   const float inv = 1.f / static_cast<float>(a.H);
   const Raw *x = static_cast<const Raw *>(a.x), *res = static_cast<const Raw *>(a.res);
+  const int step = gridDim.x * rows, t0 = blockIdx.x * rows + g;
+  auto fetch = [&](int t, int d) {
+    if (t < a.T) {
+      const size_t at = static_cast<size_t>(t) * nv + lane;
+#pragma unroll
+      for (int u = 0; u < V; ++u)
+        if (lane + tpr * u < nv) {
+          copy_vec<VB>(ring + ((d * Q) * V + u) * TH, x + at + tpr * u);
+          if (RES) copy_vec<VB>(ring + ((d * Q + 1) * V + u) * TH, res + at + tpr * u);
+        }
+    }
+    copies_commit();
+  };
+#pragma unroll
+  for (int d = 0; d < D - 1; ++d) fetch(t0 + d * step, d);
   Raw wr[V], br[V];
 #pragma unroll
   for (int u = 0; u < V; ++u) {
@@ -132,41 +179,32 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormArgs a) {
     wr[u] = v < nv ? static_cast<const Raw *>(a.w)[v] : Vc::zero();
     br[u] = v < nv && a.b ? static_cast<const Raw *>(a.b)[v] : Vc::zero();
   }
-  Raw cx[V], cr[V];
-  auto load = [&](int t) {
-    const size_t at = static_cast<size_t>(t) * nv;
-#pragma unroll
-    for (int u = 0; u < V; ++u) {
-      const int v = lane + tpr * u;
-      const bool in = t < a.T && v < nv;
-      cx[u] = in ? x[at + v] : Vc::zero();
-      cr[u] = in && res ? res[at + v] : Vc::zero();
-    }
-  };
-  const int step = gridDim.x * rows;
-  load(blockIdx.x * rows + g);
+  int d = 0;
   for (int r0 = blockIdx.x * rows; r0 < a.T; r0 += step) {
     const int t = r0 + g;
+    fetch(t + (D - 1) * step, d == 0 ? D - 1 : d - 1);
+    copies_wait<D - 1>();
     const size_t at = static_cast<size_t>(t) * nv;
     float f[kElems];
     float2 s = make_float2(0.f, 0.f);
 #pragma unroll
     for (int u = 0; u < V; ++u) {
-      Vc::unpack(cx[u], f + N * u);
-      if (res) {
+      const int v = lane + tpr * u;
+      const bool in = t < a.T && v < nv;
+      Vc::unpack(in ? ring[((d * Q) * V + u) * TH] : Vc::zero(), f + N * u);
+      if (RES) {
         float q[N];
-        Vc::unpack(cr[u], q);
+        Vc::unpack(in ? ring[((d * Q + 1) * V + u) * TH] : Vc::zero(), q);
 #pragma unroll
         for (int i = 0; i < N; ++i) f[N * u + i] += q[i];
         const Raw h = Vc::pack(f + N * u);
         Vc::unpack(h, f + N * u);  // the norm is that of the stored sum
-        const int v = lane + tpr * u;
-        if (t < a.T && v < nv) static_cast<Raw *>(a.sum)[at + v] = h;
+        if (in) static_cast<Raw *>(a.sum)[at + v] = h;
       }
 #pragma unroll
       for (int i = 0; i < N; ++i) s.x += f[N * u + i];
     }
-    load(t + step);  // the next row, while this one is summed
+    if (++d == D) d = 0;
     float mu = 0.f;
     if (a.layer) mu = row_sum(s, tpr, s_red, turn).x * inv;
     s = make_float2(0.f, 0.f);
@@ -184,33 +222,51 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormArgs a) {
 #pragma unroll
       for (int u = 0; u < V; ++u) {
         const int v = lane + tpr * u;
-        if (v >= nv) break;
-        float w[N], b[N], o[N];
-        Vc::unpack(wr[u], w);
-        Vc::unpack(br[u], b);
+        if (v < nv) {
+          float w[N], b[N], o[N];
+          Vc::unpack(wr[u], w);
+          Vc::unpack(br[u], b);
 #pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = fmaf(f[N * u + i] * r, w[i], b[i]);
-        static_cast<Raw *>(a.y)[at + v] = Vc::pack(o);
+          for (int i = 0; i < N; ++i) o[i] = fmaf(f[N * u + i] * r, w[i], b[i]);
+          static_cast<Raw *>(a.y)[at + v] = Vc::pack(o);
+        }
       }
       if (lane == 0) a.stats[t] = make_float2(mu, r);
     }
   }
 }
 
-template <class El, int VB>
-__global__ void __launch_bounds__(512) norm_bwd_kernel(const NormArgs a) {
+template <class El, int VB, bool RES, int TH>
+__global__ void __launch_bounds__(TH, 512 / TH) norm_bwd_kernel(const NormArgs a) {
   griddep_wait();  // the previous kernel in the stream has completed
   using Vc = Vec<El, VB>;
   using Raw = typename Vc::Raw;
-  constexpr int N = Vc::N, V = kElems / N;
-  extern __shared__ float s_col[];  // [2][H] when several rows share the block
+  constexpr int N = Vc::N, V = kElems / N, Q = RES ? 3 : 2, D = ring_depth<El, Q>();
+  extern __shared__ __align__(16) uint8_t s_dyn[];
   __shared__ float2 s_red[2][32];
+  Raw *ring = reinterpret_cast<Raw *>(s_dyn) + threadIdx.x;
   int turn = 0;
-  const int tpr = a.tpr, rows = blockDim.x / tpr, lane = threadIdx.x % tpr, g = threadIdx.x / tpr;
+  const int tpr = a.tpr, rows = TH / tpr, lane = threadIdx.x % tpr, g = threadIdx.x / tpr;
   const int nv = a.H / N;
   const float inv = 1.f / static_cast<float>(a.H);
   const Raw *x = static_cast<const Raw *>(a.x), *dy = static_cast<const Raw *>(a.dy);
   const Raw *ds = static_cast<const Raw *>(a.res);
+  const int step = gridDim.x * rows, t0 = blockIdx.x * rows + g;
+  auto fetch = [&](int t, int d) {
+    if (t < a.T) {
+      const size_t at = static_cast<size_t>(t) * nv + lane;
+#pragma unroll
+      for (int u = 0; u < V; ++u)
+        if (lane + tpr * u < nv) {
+          copy_vec<VB>(ring + ((d * Q) * V + u) * TH, x + at + tpr * u);
+          copy_vec<VB>(ring + ((d * Q + 1) * V + u) * TH, dy + at + tpr * u);
+          if (RES) copy_vec<VB>(ring + ((d * Q + 2) * V + u) * TH, ds + at + tpr * u);
+        }
+    }
+    copies_commit();
+  };
+#pragma unroll
+  for (int d = 0; d < D - 1; ++d) fetch(t0 + d * step, d);
   Raw wr[V];
 #pragma unroll
   for (int u = 0; u < V; ++u) {
@@ -220,122 +276,111 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormArgs a) {
   float aw[kElems], ab[kElems];
 #pragma unroll
   for (int i = 0; i < kElems; ++i) aw[i] = ab[i] = 0.f;
-  Raw cx[V], cd[V], cs[V];
-  float2 st = make_float2(0.f, 0.f);
-  auto load = [&](int t) {
-    const size_t at = static_cast<size_t>(t) * nv;
-    st = t < a.T ? a.stats[t] : make_float2(0.f, 0.f);
-#pragma unroll
-    for (int u = 0; u < V; ++u) {
-      const int v = lane + tpr * u;
-      const bool in = t < a.T && v < nv;
-      cx[u] = in ? x[at + v] : Vc::zero();
-      cd[u] = in ? dy[at + v] : Vc::zero();
-      cs[u] = in && ds ? ds[at + v] : Vc::zero();
-    }
-  };
-  const int step = gridDim.x * rows;
-  load(blockIdx.x * rows + g);
+  float2 next = t0 < a.T ? a.stats[t0] : make_float2(0.f, 0.f);
+  int d = 0;
   for (int r0 = blockIdx.x * rows; r0 < a.T; r0 += step) {
     const int t = r0 + g;
+    fetch(t + (D - 1) * step, d == 0 ? D - 1 : d - 1);
+    const float mu = next.x, r = next.y;
+    if (t + step < a.T) next = a.stats[t + step];
+    copies_wait<D - 1>();
     const size_t at = static_cast<size_t>(t) * nv;
-    const float mu = st.x, r = st.y;
     float xh[kElems], gw[kElems];
-    Raw sv[V];
     float2 s = make_float2(0.f, 0.f);
 #pragma unroll
     for (int u = 0; u < V; ++u) {
-      float w[N], d[N];
-      Vc::unpack(cx[u], xh + N * u);
-      Vc::unpack(cd[u], d);
-      Vc::unpack(wr[u], w);
-      sv[u] = cs[u];
+      float w[N], e[N];
       const bool in = t < a.T && lane + tpr * u < nv;
+      Vc::unpack(in ? ring[((d * Q) * V + u) * TH] : Vc::zero(), xh + N * u);
+      Vc::unpack(in ? ring[((d * Q + 1) * V + u) * TH] : Vc::zero(), e);
+      Vc::unpack(wr[u], w);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int j = N * u + i;
         xh[j] = in ? (xh[j] - mu) * r : 0.f;
-        gw[j] = d[i] * w[i];
+        gw[j] = e[i] * w[i];
         s.x += gw[j];
         s.y = fmaf(gw[j], xh[j], s.y);
-        aw[j] = fmaf(d[i], xh[j], aw[j]);
-        ab[j] += d[i];
+        aw[j] = fmaf(e[i], xh[j], aw[j]);
+        ab[j] += e[i];
       }
     }
-    load(t + step);  // the next row, while this one is summed
     s = row_sum(s, tpr, s_red, turn);
     const float c1 = s.y * inv, c2 = a.layer ? s.x * inv : 0.f;
     if (t < a.T) {
 #pragma unroll
       for (int u = 0; u < V; ++u) {
         const int v = lane + tpr * u;
-        if (v >= nv) break;
-        float o[N];
-        Vc::unpack(sv[u], o);
+        if (v < nv) {
+          float o[N];
+          Vc::unpack(RES ? ring[((d * Q + 2) * V + u) * TH] : Vc::zero(), o);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int j = N * u + i;
-          o[i] = fmaf(r, gw[j] - c2 - xh[j] * c1, o[i]);
+          for (int i = 0; i < N; ++i) {
+            const int j = N * u + i;
+            o[i] = fmaf(r, gw[j] - c2 - xh[j] * c1, o[i]);
+          }
+          static_cast<Raw *>(a.y)[at + v] = Vc::pack(o);
         }
-        static_cast<Raw *>(a.y)[at + v] = Vc::pack(o);
       }
     }
+    if (++d == D) d = 0;
   }
   // the block's column sums: its row groups added in order, one after another
+  copies_wait<0>();
+  __syncthreads();  // the ring is no longer read: it holds the sums
+  float *s_col = reinterpret_cast<float *>(s_dyn);  // [2][H] when several rows share the block (H <= TH kElems / 2)
   float *part = a.part + static_cast<size_t>(blockIdx.x) * 2 * a.H;
-  float *dst = rows > 1 ? s_col : part;
   for (int q = 0; q < rows; ++q) {
     if (q > 0) __syncthreads();
     if (g == q) {
-      float *out = q == rows - 1 ? part : dst;
+      float *out = q == rows - 1 ? part : s_col;
 #pragma unroll
       for (int u = 0; u < V; ++u) {
         const int v = lane + tpr * u;
-        if (v >= nv) break;
+        if (v < nv) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int c = v * N + i;
-          out[c] = q > 0 ? s_col[c] + aw[N * u + i] : aw[N * u + i];
-          out[a.H + c] = q > 0 ? s_col[a.H + c] + ab[N * u + i] : ab[N * u + i];
+          for (int i = 0; i < N; ++i) {
+            const int c = v * N + i;
+            out[c] = q > 0 ? s_col[c] + aw[N * u + i] : aw[N * u + i];
+            out[a.H + c] = q > 0 ? s_col[a.H + c] + ab[N * u + i] : ab[N * u + i];
+          }
         }
       }
     }
   }
 }
 
-// dw[c] and db[c] = the sum over the blocks' partial rows in a fixed order: 32
-// columns x 8 interleaved runs of rows per block, the runs added in order.
+// dw[c] and db[c] = the sum over the blocks' partial rows in a fixed order: 8
+// columns x 32 interleaved runs of rows per block, the runs added in a tree.
 __global__ void __launch_bounds__(256) norm_colsum_kernel(const float *__restrict__ part, int nb, int H,
                                                           float *__restrict__ dw, float *__restrict__ db) {
   griddep_wait();  // the previous kernel in the stream has completed
-  __shared__ float s[8][33];
-  const int cl = threadIdx.x & 31, run = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + cl;
+  __shared__ float s[32][9];
+  const int cl = threadIdx.x & 7, run = threadIdx.x >> 3;
+  const int c = blockIdx.x * 8 + cl;
   const float *src = part + static_cast<size_t>(blockIdx.y) * H + c;
   float acc = 0.f;
   if (c < H) {
-#pragma unroll 8
-    for (int b = run; b < nb; b += 8) acc += src[static_cast<size_t>(b) * 2 * H];
+#pragma unroll 10
+    for (int b = run; b < nb; b += 32) acc += src[static_cast<size_t>(b) * 2 * H];
   }
   s[run][cl] = acc;
   __syncthreads();
-  if (run == 0 && c < H) {
+  if (threadIdx.x < 32) {  // lane = run here: a tree over the 32 runs of each column
 #pragma unroll
-    for (int i = 1; i < 8; ++i) acc += s[i][cl];
-    (blockIdx.y == 0 ? dw : db)[c] = acc;
+    for (int i = 0; i < 8; ++i) {
+      const float v = warp_sum(s[threadIdx.x][i]);
+      if (static_cast<int>(threadIdx.x) == i) acc = v;
+    }
+    const int o = blockIdx.x * 8 + threadIdx.x;
+    if (threadIdx.x < 8 && o < H) (blockIdx.y == 0 ? dw : db)[o] = acc;
   }
 }
 
-struct Shape {
-  int tpr, threads, rows;
-};
-Shape shape_of(int H) {
-  Shape s;
-  s.tpr = 8;
-  while (s.tpr * kElems < H) s.tpr *= 2;
-  s.threads = s.tpr > kThreads ? s.tpr : kThreads;
-  s.rows = s.threads / s.tpr;
-  return s;
+int tpr_of(int H) {
+  int tpr = 8;
+  while (tpr * kElems < H) tpr *= 2;
+  return tpr;
 }
 
 // The widest vectors that divide a row (all base pointers are 16-byte aligned,
@@ -345,22 +390,64 @@ int vector_bytes(int H, int el) {
   return row % 16 == 0 ? 16 : (row % 4 == 0 ? 4 : 2);
 }
 
-template <class El, int VB>
-cudaError_t launch_fwd(const NormArgs &a, int sms, cudaStream_t s) {
-  const Shape sh = shape_of(a.H);
-  const int need = (a.T + sh.rows - 1) / sh.rows, most = sms * (2048 / sh.threads);
-  return launch_pdl(norm_fwd_kernel<El, VB>, dim3(need < most ? need : most), dim3(sh.threads), 0, s, 1, a);
+// Blocks of a kernel that fit the part at once, after its shared-memory opt-in.
+template <class K>
+cudaError_t resident(DeviceOnce &once, K kernel, int threads, int smem, int sms, int *blocks) {
+  return once.get(
+      [&](int *out) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(out, kernel, threads, smem);
+        *out *= sms;
+        return e != cudaSuccess || *out > 0 ? e : cudaErrorInvalidConfiguration;
+      },
+      blocks);
 }
 
-template <class El, int VB>
-cudaError_t launch_bwd(const NormArgs &a, float *dw, float *db, cudaStream_t s) {
-  const Shape sh = shape_of(a.H);
-  const int need = (a.T + sh.rows - 1) / sh.rows, nb = need < kBwdBlocks ? need : kBwdBlocks;
-  const size_t smem = sh.rows > 1 ? static_cast<size_t>(2) * a.H * sizeof(float) : 0;  // H <= 2048 there
-  cudaError_t e = launch_pdl(norm_bwd_kernel<El, VB>, dim3(nb), dim3(sh.threads), smem, s, 1, a);
+template <class El, int VB, bool RES, int TH>
+cudaError_t launch_fwd(const NormArgs &a, int sms, cudaStream_t s) {
+  static DeviceOnce once;
+  constexpr int smem = ring_bytes<El, RES ? 2 : 1>(TH);
+  int most = 0;
+  const cudaError_t e = resident(once, norm_fwd_kernel<El, VB, RES, TH>, TH, smem, sms, &most);
   if (e != cudaSuccess) return e;
-  return launch_pdl(norm_colsum_kernel, dim3((a.H + 31) / 32, db ? 2 : 1), dim3(256), 0, s, 1, a.part, nb, a.H, dw,
-                    db);
+  const int rows = TH / a.tpr, need = (a.T + rows - 1) / rows;
+  return launch_pdl(norm_fwd_kernel<El, VB, RES, TH>, dim3(need < most ? need : most), dim3(TH), smem, s, 1, a);
+}
+
+template <class El, int VB, bool RES, int TH>
+cudaError_t launch_bwd(const NormArgs &a, int sms, float *dw, float *db, cudaStream_t s) {
+  static DeviceOnce once;
+  constexpr int smem = ring_bytes<El, RES ? 3 : 2>(TH);
+  int most = 0;
+  cudaError_t e = resident(once, norm_bwd_kernel<El, VB, RES, TH>, TH, smem, sms, &most);
+  if (e != cudaSuccess) return e;
+  if (most > kBwdBlocks) most = kBwdBlocks;
+  const int rows = TH / a.tpr, need = (a.T + rows - 1) / rows, nb = need < most ? need : most;
+  e = launch_pdl(norm_bwd_kernel<El, VB, RES, TH>, dim3(nb), dim3(TH), smem, s, 1, a);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(norm_colsum_kernel, dim3((a.H + 7) / 8, db ? 2 : 1), dim3(256), 0, s, 1, a.part, nb, a.H, dw, db);
+}
+
+// The variant for a configuration: vectors as wide as the rows allow, 512 threads
+// only where a row takes them.
+template <class F>
+cudaError_t by_form(bool bf, int H, bool res, F &&f) {
+  const bool wide = tpr_of(H) > kThreads;
+  auto pick = [&](auto el, auto vb) {
+    if (res)
+      return wide ? f(el, vb, std::true_type{}, std::integral_constant<int, 512>{})
+                  : f(el, vb, std::true_type{}, std::integral_constant<int, 256>{});
+    return wide ? f(el, vb, std::false_type{}, std::integral_constant<int, 512>{})
+                : f(el, vb, std::false_type{}, std::integral_constant<int, 256>{});
+  };
+  const int vb = vector_bytes(H, bf ? 2 : 4);
+  if (bf) {
+    if (vb == 16) return pick(uint16_t{}, std::integral_constant<int, 16>{});
+    return vb == 4 ? pick(uint16_t{}, std::integral_constant<int, 4>{})
+                   : pick(uint16_t{}, std::integral_constant<int, 2>{});
+  }
+  return vb == 16 ? pick(float{}, std::integral_constant<int, 16>{}) : pick(float{}, std::integral_constant<int, 4>{});
 }
 
 bool norm_ok(const moe_norm_config *c) {
@@ -374,7 +461,7 @@ NormArgs norm_args(const moe_norm_config *c) {
   a.H = c->H;
   a.eps = c->eps;
   a.layer = c->kind == MOE_NORM_LAYER;
-  a.tpr = shape_of(c->H).tpr;
+  a.tpr = tpr_of(c->H);
   return a;
 }
 
@@ -408,15 +495,11 @@ moe_status moe_norm_forward(const moe_norm_config *cfg, const void *x, const voi
   a.y = y;
   a.sum = sum;
   a.stats = reinterpret_cast<float2 *>(stats);
-  const bool bf = cfg->dtype == MOE_DTYPE_BF16;
-  const int vb = vector_bytes(cfg->H, bf ? 2 : 4);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return timed("norm_forward", s, [&] {
-    if (bf) {
-      if (vb == 16) return launch_fwd<uint16_t, 16>(a, di.sms, s);
-      return vb == 4 ? launch_fwd<uint16_t, 4>(a, di.sms, s) : launch_fwd<uint16_t, 2>(a, di.sms, s);
-    }
-    return vb == 16 ? launch_fwd<float, 16>(a, di.sms, s) : launch_fwd<float, 4>(a, di.sms, s);
+    return by_form(cfg->dtype == MOE_DTYPE_BF16, cfg->H, residual != nullptr, [&](auto el, auto vb, auto res, auto th) {
+      return launch_fwd<decltype(el), decltype(vb)::value, decltype(res)::value, decltype(th)::value>(a, di.sms, s);
+    });
   });
 }
 
@@ -448,14 +531,11 @@ moe_status moe_norm_backward(const moe_norm_config *cfg, const void *dy, const v
   a.y = dx;
   a.stats = const_cast<float2 *>(reinterpret_cast<const float2 *>(stats));
   a.part = static_cast<float *>(scratch);
-  const bool bf = cfg->dtype == MOE_DTYPE_BF16;
-  const int vb = vector_bytes(cfg->H, bf ? 2 : 4);
   return timed("norm_backward", s, [&] {
-    if (bf) {
-      if (vb == 16) return launch_bwd<uint16_t, 16>(a, dweight, dbias, s);
-      return vb == 4 ? launch_bwd<uint16_t, 4>(a, dweight, dbias, s) : launch_bwd<uint16_t, 2>(a, dweight, dbias, s);
-    }
-    return vb == 16 ? launch_bwd<float, 16>(a, dweight, dbias, s) : launch_bwd<float, 4>(a, dweight, dbias, s);
+    return by_form(cfg->dtype == MOE_DTYPE_BF16, cfg->H, d_sum != nullptr, [&](auto el, auto vb, auto res, auto th) {
+      return launch_bwd<decltype(el), decltype(vb)::value, decltype(res)::value, decltype(th)::value>(
+          a, di.sms, dweight, dbias, s);
+    });
   });
 }
 

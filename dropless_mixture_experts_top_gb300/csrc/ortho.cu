@@ -281,34 +281,46 @@ __device__ __forceinline__ void tile_to_rows(const uint8_t *tile, uint16_t *g0, 
   }
 }
 
-// One warp's 32 rows of half a tile's columns.
-template <int KIND>
-__device__ __forceinline__ void epilogue(const TileAt &t, uint32_t tb, int row0, int part, const ProductArgs &p,
-                                         uint8_t *tile) {
-  const int lane = threadIdx.x & 31;
-  const int nrows = min(32, p.M - row0);
-  uint16_t *out = p.out + t.b * p.stride;
-  const uint16_t *s = KIND == kSquare ? p.s + t.b * p.stride : nullptr;
-#pragma unroll 1
-  for (int j = 0; j < BN / 64; ++j) {
-    const int cc = part * (BN / 2) + 32 * j, c0 = t.n0 + cc;
-    if (c0 >= p.N || nrows <= 0) break;
-    uint4 sv[4];
-    if constexpr (KIND == kSquare) {  // S's rows, coalesced, while the accumulator is read
+constexpr int kChunks = BN / 64;  // 32-column chunks of a warp's half of the columns
+
+// kSquare: S under the warp's 32 rows and half of the tile's columns, in the
+// order its coalesced loads bring it.
+struct SChunks {
+  uint4 v[kChunks][4];
+  __device__ __forceinline__ void load(const TileAt &t, int row0, int part, const ProductArgs &p) {
+    const int lane = threadIdx.x & 31, nrows = min(32, p.M - row0);
+    const uint16_t *s = p.s + t.b * p.stride;
+#pragma unroll
+    for (int j = 0; j < kChunks; ++j) {
+      const int c0 = t.n0 + part * (BN / 2) + 32 * j;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = 8 * i + (lane >> 2);
-        sv[i] = r < nrows ? *reinterpret_cast<const uint4 *>(s + (row0 + r) * static_cast<int64_t>(p.ld) + c0 +
-                                                             (lane & 3) * 8)
-                          : make_uint4(0, 0, 0, 0);
+        v[j][i] = r < nrows && c0 < p.N ? *reinterpret_cast<const uint4 *>(
+                                              s + (row0 + r) * static_cast<int64_t>(p.ld) + c0 + (lane & 3) * 8)
+                                        : make_uint4(0, 0, 0, 0);
       }
     }
+  }
+};
+
+// One warp's 32 rows of half a tile's columns.
+template <int KIND>
+__device__ __forceinline__ void epilogue(const TileAt &t, uint32_t tb, int row0, int part, const ProductArgs &p,
+                                         uint8_t *tile, const SChunks &sc) {
+  const int lane = threadIdx.x & 31;
+  const int nrows = min(32, p.M - row0);
+  uint16_t *out = p.out + t.b * p.stride;
+#pragma unroll KIND == kSquare ? kChunks : 1
+  for (int j = 0; j < kChunks; ++j) {
+    const int cc = part * (BN / 2) + 32 * j, c0 = t.n0 + cc;
+    if (c0 >= p.N || nrows <= 0) break;
     uint32_t acc[32];
     tmem_ld32(tb + cc, acc);
     float v[32];
     if constexpr (KIND == kSquare) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(tile + swz(8 * i + (lane >> 2), lane & 3)) = sv[i];
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(tile + swz(8 * i + (lane >> 2), lane & 3)) = sc.v[j][i];
       __syncwarp();
       tmem_ld_wait();
 #pragma unroll
@@ -530,12 +542,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     int it = 0;
     for (int tile = pair; tile < total; tile += npairs, ++it) {
       const TileAt t = tile_of<KIND>(tile, p);
-      const int buf = it & 1;
+      const int buf = it & 1, row0 = t.m0 + BM * rank + q * 32;
+      SChunks sc;
+      if constexpr (KIND == kSquare) sc.load(t, row0, part, p);  // while the product runs
       if (!wait_lane0(&tfull[buf], (it >> 1) & 1, abort_flag)) break;
       __syncwarp();
       tc_fence_after();
-      epilogue<KIND>(t, tmem_base + buf * BN + (static_cast<uint32_t>(q * 32) << 16), t.m0 + BM * rank + q * 32, part, p,
-                     stile);
+      epilogue<KIND>(t, tmem_base + buf * BN + (static_cast<uint32_t>(q * 32) << 16), row0, part, p, stile, sc);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(buf ? tempty1 : tempty0);

@@ -312,29 +312,26 @@ _BF16 = (torch.bfloat16, torch.int16)
 _TORCH_DTYPES = {"bf16": _BF16, "fp32": (torch.float32,)}
 
 
-def _addr(t, name, shape, dtypes, device):
+def _addr(t, name, shape, dtypes, dev):
     """The address of a tensor argument (None: no address), which has to be a dense
-    tensor of this shape and one of these types on this device."""
+    tensor of this shape and one of these types on GPU dev."""
     if t is None:
         return None
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected one of {dtypes}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: not contiguous")
-    return t.data_ptr()
+    if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, {'' if t.is_contiguous() else 'not '}"
+                     f"contiguous; expected one of {dtypes}, {tuple(shape)}, on GPU {dev}, contiguous")
 
 
 def _device(device):
     d = torch.device(device)
-    return torch.device("cuda", torch.cuda.current_device()) if d.type == "cuda" and d.index is None else d
+    if d.type != "cuda":
+        raise ValueError(f"device: {d}, expected a GPU")
+    return torch.device("cuda", torch.cuda.current_device()) if d.index is None else d
 
 
-def _raw_stream(stream):
-    return torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
+def _raw_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 class Norm:
@@ -350,38 +347,45 @@ class Norm:
         n = ctypes.c_size_t()
         _check(lib().moe_norm_workspace(ctypes.byref(self.cfg), ctypes.byref(n)), "moe_norm_workspace")
         self.device, self.bias = _device(device), bool(bias)
+        self._dev, self._fwd, self._bwd = self.device.index, lib().moe_norm_forward, lib().moe_norm_backward
         self._cfg, self._types = ctypes.byref(self.cfg), _TORCH_DTYPES[dtype]
         self._rows, self._cols, self._stats = (torch.Size(s) for s in ((T, H), (H,), (T, 2)))
         self.bwd_scratch = torch.empty(n.value, dtype=torch.uint8, device=self.device)
+        self._scratch = self.bwd_scratch.data_ptr()
 
     def forward(self, x, weight, bias=None, residual=None, out=None, stream=None) -> dict:
         """{"y", "sum" (x + residual, or None), "stats" [T, 2]: mean and 1 / deviation}"""
-        d, ty, rows, cols, L = self.device, self._types, self._rows, self._cols, lib()
+        d, ty, rows, cols = self._dev, self._types, self._rows, self._cols
         if (bias is not None) != self.bias:
             raise ValueError("bias: given to a norm without one" if bias is not None else "bias: missing")
         if out is None:
             out = {"y": torch.empty_like(x), "sum": torch.empty_like(x) if residual is not None else None,
-                   "stats": torch.empty(self._stats, dtype=torch.float32, device=d)}
-        _check(L.moe_norm_forward(
+                   "stats": torch.empty(self._stats, dtype=torch.float32, device=self.device)}
+        rc = self._fwd(
             self._cfg, _addr(x, "x", rows, ty, d), _addr(residual, "residual", rows, ty, d),
             _addr(weight, "weight", cols, ty, d), _addr(bias, "bias", cols, ty, d), _addr(out["y"], "y", rows, ty, d),
             _addr(out["sum"], "sum", rows, ty, d), _addr(out["stats"], "stats", self._stats, _F32, d),
-            _raw_stream(stream)), "moe_norm_forward")
+            _raw_stream(stream, d))
+        if rc:
+            raise MoEError("moe_norm_forward", rc)
         return out
 
     def backward(self, dy, h, weight, stats, d_sum=None, grads=None, stream=None) -> dict:
         """{"dx", "dweight", "dbias" (None without a bias)} from the forward's
         stats and h, its sum (x where there was no residual)."""
-        d, ty, rows, cols, L = self.device, self._types, self._rows, self._cols, lib()
+        d, ty, rows, cols = self._dev, self._types, self._rows, self._cols
         if grads is None:
-            grads = {"dx": torch.empty_like(dy), "dweight": torch.empty(cols, dtype=torch.float32, device=d),
-                     "dbias": torch.empty(cols, dtype=torch.float32, device=d) if self.bias else None}
-        _check(L.moe_norm_backward(
+            f32 = dict(dtype=torch.float32, device=self.device)
+            grads = {"dx": torch.empty_like(dy), "dweight": torch.empty(cols, **f32),
+                     "dbias": torch.empty(cols, **f32) if self.bias else None}
+        rc = self._bwd(
             self._cfg, _addr(dy, "dy", rows, ty, d), _addr(h, "h", rows, ty, d),
             _addr(weight, "weight", cols, ty, d), _addr(stats, "stats", self._stats, _F32, d),
             _addr(d_sum, "d_sum", rows, ty, d), _addr(grads["dx"], "dx", rows, ty, d),
             _addr(grads["dweight"], "dweight", cols, _F32, d), _addr(grads["dbias"], "dbias", cols, _F32, d),
-            self.bwd_scratch.data_ptr(), self.bwd_scratch.numel(), _raw_stream(stream)), "moe_norm_backward")
+            self._scratch, self.bwd_scratch.numel(), _raw_stream(stream, d))
+        if rc:
+            raise MoEError("moe_norm_backward", rc)
         return grads
 
 
@@ -397,38 +401,43 @@ class BalanceLoss:
         n = ctypes.c_size_t()
         _check(lib().moe_balance_workspace(ctypes.byref(self.cfg), ctypes.byref(n)), "moe_balance_workspace")
         self.device, self._cfg = _device(device), ctypes.byref(self.cfg)
+        self._dev, self._fwd, self._bwd = self.device.index, lib().moe_balance_forward, lib().moe_balance_backward
         self._te, self._tk, self._t, self._se, self._s, self._two = (
             torch.Size(s) for s in ((T, E), (T, k), (T,), (sequences, E), (sequences,), (2,)))
         self.fwd_scratch = torch.empty(n.value, dtype=torch.uint8, device=self.device)
+        self._scratch = self.fwd_scratch.data_ptr()
 
     def forward(self, logits, topk_idx, mask=None, out=None, stream=None) -> dict:
         """{"loss" [2]: balance, z; "counts" and "probs" [sequences, E]; "tokens"
         [sequences]; "lse" [T]}.  mask [T]: zero for padding."""
-        d, L = self.device, lib()
+        d = self._dev
         if out is None:
-            f32, i32 = dict(dtype=torch.float32, device=d), dict(dtype=torch.int32, device=d)
+            f32, i32 = (dict(dtype=t, device=self.device) for t in (torch.float32, torch.int32))
             out = {"loss": torch.empty(self._two, **f32), "counts": torch.empty(self._se, **i32),
                    "probs": torch.empty(self._se, **f32), "tokens": torch.empty(self._s, **i32),
                    "lse": torch.empty(self._t, **f32)}
-        _check(L.moe_balance_forward(
+        rc = self._fwd(
             self._cfg, _addr(logits, "logits", self._te, _F32, d), _addr(topk_idx, "topk_idx", self._tk, _I32, d),
             _addr(mask, "mask", self._t, _U8, d), _addr(out["loss"], "loss", self._two, _F32, d),
             _addr(out["counts"], "counts", self._se, _I32, d), _addr(out["probs"], "probs", self._se, _F32, d),
             _addr(out["tokens"], "tokens", self._s, _I32, d), _addr(out["lse"], "lse", self._t, _F32, d),
-            self.fwd_scratch.data_ptr(), self.fwd_scratch.numel(), _raw_stream(stream)), "moe_balance_forward")
+            self._scratch, self.fwd_scratch.numel(), _raw_stream(stream, d))
+        if rc:
+            raise MoEError("moe_balance_forward", rc)
         return out
 
     def backward(self, logits, counts, tokens, lse, g_balance, g_z, d_logits=None, stream=None):
         """The gradient of g_balance * loss[0] + g_z * loss[1], added to d_logits in
         place where that is given (as the layer's backward left it)."""
-        d, L = self.device, lib()
-        add = d_logits is not None
+        d, add = self._dev, d_logits is not None
         if not add:
-            d_logits = torch.empty(self._te, dtype=torch.float32, device=d)
-        _check(L.moe_balance_backward(
+            d_logits = torch.empty(self._te, dtype=torch.float32, device=self.device)
+        rc = self._bwd(
             self._cfg, _addr(logits, "logits", self._te, _F32, d), _addr(counts, "counts", self._se, _I32, d),
             _addr(tokens, "tokens", self._s, _I32, d), _addr(lse, "lse", self._t, _F32, d), g_balance, g_z,
-            _addr(d_logits, "d_logits", self._te, _F32, d), add, _raw_stream(stream)), "moe_balance_backward")
+            _addr(d_logits, "d_logits", self._te, _F32, d), add, _raw_stream(stream, d))
+        if rc:
+            raise MoEError("moe_balance_backward", rc)
         return d_logits
 
     def status(self, stream=None) -> dict:
@@ -453,19 +462,23 @@ class Orthogonaliser:
         _check(lib().moe_ortho_workspace(ctypes.byref(self.cfg), ctypes.byref(n)), "moe_ortho_workspace")
         self.device, self._cfg, self._types = _device(device), ctypes.byref(self.cfg), _TORCH_DTYPES[dtype]
         self._shape = torch.Size((batch, R, C))
+        self._dev, self._update = self.device.index, lib().moe_ortho_update
         self._coefs = (ctypes.c_float * len(coefs))(*coefs)
         self.scratch = torch.empty(n.value, dtype=torch.uint8, device=self.device)
+        self._scratch = self.scratch.data_ptr()
 
     def update(self, g, momentum=None, beta=0.95, nesterov=True, scale=1.0, out=None, stream=None):
         """scale times the orthogonalised update, bf16 [batch, R, C]; momentum (fp32)
         is advanced in place."""
-        d, s, L = self.device, self._shape, lib()
+        d, s = self._dev, self._shape
         if out is None:
-            out = torch.empty(s, dtype=g.dtype if g.dtype in _BF16 else torch.bfloat16, device=d)
-        _check(L.moe_ortho_update(
+            out = torch.empty(s, dtype=g.dtype if g.dtype in _BF16 else torch.bfloat16, device=self.device)
+        rc = self._update(
             self._cfg, self._coefs, _addr(g, "g", s, self._types, d), _addr(momentum, "momentum", s, _F32, d), beta,
-            nesterov, scale, _addr(out, "out", s, _BF16, d), self.scratch.data_ptr(), self.scratch.numel(),
-            _raw_stream(stream)), "moe_ortho_update")
+            nesterov, scale, _addr(out, "out", s, _BF16, d), self._scratch, self.scratch.numel(),
+            _raw_stream(stream, d))
+        if rc:
+            raise MoEError("moe_ortho_update", rc)
         return out
 
     def status(self, stream=None) -> dict:
