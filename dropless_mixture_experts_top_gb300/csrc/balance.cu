@@ -219,11 +219,21 @@ __global__ void __launch_bounds__(kFinThreads) balance_finish_kernel(const BalAr
   const size_t row0 = static_cast<size_t>(s) * a.nbs;
   float sum = 0.f;
   int cnt = 0;
-  if (e < E) {
-#pragma unroll 4
-    for (int b = run; b < a.nbs; b += runs) {
-      sum += a.psum[(row0 + b) * E + e];
-      cnt += a.pcnt[(row0 + b) * E + e];
+  constexpr int U = 16;  // loads of each kind in flight
+  for (int b0 = run; b0 < a.nbs; b0 += runs * U) {
+    float v[U];
+    int c[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int b = b0 + runs * u;
+      const bool in = b < a.nbs && e < E;
+      v[u] = in ? a.psum[(row0 + b) * E + e] : 0.f;
+      c[u] = in ? a.pcnt[(row0 + b) * E + e] : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      sum += v[u];
+      cnt += c[u];
     }
   }
   s_sum[threadIdx.x] = sum;

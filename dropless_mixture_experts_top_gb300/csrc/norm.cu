@@ -11,13 +11,13 @@
 // Both are bound by memory: every input is read and every output written once.
 //
 // Layout: a row is shared by TPR threads (a power of two, 8 to 512), each
-// holding kElems elements in V vectors that lie TPR vectors apart, so a warp's
-// accesses are contiguous.  Blocks are persistent over rows: a thread's columns
-// stay the same, so the weight (and in the backward the column sums of dy xh
-// and dy) stay in its registers, while asynchronous copies bring the coming rows
-// into a ring in shared memory.  The backward's blocks leave one partial row of
-// column sums each, which a second kernel adds in a fixed order: no atomics, the
-// same bits every time.
+// holding kElems elements, in vectors of 16 bytes that lie TPR vectors apart, so
+// a warp's accesses are contiguous.  Blocks are persistent over rows: a thread's
+// columns stay the same, so the weight (and in the backward the column sums of
+// dy xh and dy) stay in its registers, while asynchronous copies bring the coming
+// rows into a ring in shared memory.  The backward's blocks leave one partial row
+// of column sums each, which a second kernel adds in a fixed order: no atomics,
+// the same bits every time.
 #include <type_traits>
 
 #include "abi.h"
@@ -42,312 +42,443 @@ struct NormArgs {
   bool layer;
 };
 
-// Vectors of VB bytes holding elements of type El (uint16_t: bf16 bits).
-template <int VB> struct RawOf;
-template <> struct RawOf<16> { using type = uint4; };
-template <> struct RawOf<4> { using type = uint32_t; };
-template <> struct RawOf<2> { using type = uint16_t; };
-
-template <class El, int VB>
+// Sixteen-byte vectors of El (uint16_t: bf16 bits) and single elements.
+template <class El>
 struct Vec {
-  using Raw = typename RawOf<VB>::type;
-  static constexpr int N = VB / static_cast<int>(sizeof(El));
-  static __device__ __forceinline__ Raw zero() {
-    Raw r;
-    memset(&r, 0, sizeof(r));
-    return r;
-  }
-  static __device__ __forceinline__ void unpack(const Raw &r, float *f) {
-    if constexpr (sizeof(El) == 4) {
-      memcpy(f, &r, VB);
-    } else if constexpr (VB == 2) {
-      f[0] = __uint_as_float(static_cast<uint32_t>(r) << 16);
-    } else {
-      uint32_t w[VB / 4];
-      memcpy(w, &r, VB);
+  static constexpr int N = 16 / static_cast<int>(sizeof(El));
+  static __device__ __forceinline__ void unpack(const uint4 &r, float *f) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-      for (int i = 0; i < VB / 4; ++i) {
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(El) == 4) {
+        f[i] = __uint_as_float(w[i]);
+      } else {
         f[2 * i] = bf16_lo(w[i]);
         f[2 * i + 1] = bf16_hi(w[i]);
       }
     }
   }
-  static __device__ __forceinline__ Raw pack(const float *f) {
-    Raw r;
-    if constexpr (sizeof(El) == 4) {
-      memcpy(&r, f, VB);
-    } else if constexpr (VB == 2) {
-      r = __bfloat16_as_ushort(__float2bfloat16_rn(f[0]));
-    } else {
-      uint32_t w[VB / 4];
+  static __device__ __forceinline__ uint4 pack(const float *f) {
+    if constexpr (sizeof(El) == 4)
+      return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    else
+      return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                        pack_bf16x2(f[6], f[7]));
+  }
+};
+__device__ __forceinline__ float el_get(float v) { return v; }
+__device__ __forceinline__ float el_get(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+__device__ __forceinline__ void el_set(float *p, float v) { *p = v; }
+__device__ __forceinline__ void el_set(uint16_t *p, float v) { *p = __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+// The value as El stores it.
+__device__ __forceinline__ float el_round(float v, float) { return v; }
+__device__ __forceinline__ float el_round(float v, uint16_t) {
+  return el_get(__bfloat16_as_ushort(__float2bfloat16_rn(v)));
+}
+constexpr uint32_t kAllValid = (1u << kElems) - 1;
+
+// A thread's elements as pairs for the paired fp32 instructions: with single ones
+// the arithmetic alone keeps the schedulers busy three quarters of the time.
+constexpr int kPairs = kElems / 2;
+__device__ __forceinline__ void pairs_of(const float (&f)[kElems], F2 (&p)[kPairs]) {
 #pragma unroll
-      for (int i = 0; i < VB / 4; ++i) w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
-      memcpy(&r, w, VB);
-    }
-    return r;
+  for (int i = 0; i < kPairs; ++i) p[i] = f2(f[2 * i], f[2 * i + 1]);
+}
+__device__ __forceinline__ void unpair(const F2 (&p)[kPairs], float (&f)[kElems]) {
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) {
+    const float2 v = f2_get(p[i]);
+    f[2 * i] = v.x;
+    f[2 * i + 1] = v.y;
+  }
+}
+
+// A thread's place: which of the block's rows (g) and where in it (lane).
+struct Place {
+  int tpr, rows, lane, g;
+  int w0, per;  // the row's first warp, and its warps
+  __device__ __forceinline__ Place(int tpr_, int threads) : tpr(tpr_) {
+    rows = threads / tpr;
+    lane = threadIdx.x & (tpr - 1);
+    g = threadIdx.x / tpr;
+    per = tpr > 32 ? tpr >> 5 : 1;
+    w0 = (threadIdx.x >> 5) & ~(per - 1);
   }
 };
 
-// Sums of a and b over the tpr threads of a row; every thread gets them.  buf:
-// two floats per warp of the block; `turn` alternates so that one barrier per
-// sum is enough (a thread writes the other half while slower ones still read).
-__device__ __forceinline__ float2 row_sum(float2 v, int tpr, float2 (*buf)[32], int &turn) {
+// The sum of v (one float or two) over the threads of a row; every thread gets
+// it.  buf: one value per warp of the block; `turn` alternates so that one barrier
+// per sum is enough (a thread writes one half while slower ones read the other).
+__device__ __forceinline__ float plus(float a, float b) { return a + b; }
+__device__ __forceinline__ float2 plus(float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); }
+__device__ __forceinline__ float shfl(float v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
+__device__ __forceinline__ float2 shfl(float2 v, int o) { return make_float2(shfl(v.x, o), shfl(v.y, o)); }
+template <class S>
+__device__ __forceinline__ S row_sum(S v, const Place &pl, S (*buf)[32], int &turn) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    if (o < tpr) {
-      v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-      v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-    }
-  }
-  if (tpr > 32) {
-    const int warp = threadIdx.x >> 5, per = tpr >> 5;
-    if ((threadIdx.x & 31) == 0) buf[turn][warp] = v;
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < pl.tpr) v = plus(v, shfl(v, o));
+  if (pl.per > 1) {
+    if ((threadIdx.x & 31) == 0) buf[turn][threadIdx.x >> 5] = v;
     __syncthreads();
-    const int w0 = warp / per * per;
-    v = buf[turn][w0];
-    for (int i = 1; i < per; ++i) {
-      v.x += buf[turn][w0 + i].x;
-      v.y += buf[turn][w0 + i].y;
-    }
+    v = buf[turn][pl.w0];
+    for (int i = 1; i < pl.per; ++i) v = plus(v, buf[turn][pl.w0 + i]);
     turn ^= 1;
   }
   return v;
 }
 
-// A thread's own vectors of the coming rows: a ring of D rows in shared memory
-// (Q inputs, V vectors per thread), filled by asynchronous copies of VB bytes and
-// read back by the same thread, so no barrier is needed.  Rows of an odd number of
-// bf16 elements have no copies that small; they are stored by the thread itself.
+// 1 / sqrt(v): the approximation and one Newton step (v = 0 gives infinity).
+__device__ __forceinline__ float inv_sqrt(float v) {
+  const float r = rsqrtf(v);
+  return v > 0.f && v < INFINITY ? r * fmaf(-0.5f * v * r, r, 1.5f) : r;
+}
+
+// Statistics of one row; x2: h in, h - mu out.  valid: which of this thread's
+// elements are the row's (the others hold zeros).
+struct Stats {
+  float mu, r;
+};
+__device__ __forceinline__ Stats normalise(F2 (&x2)[kPairs], uint32_t valid, const NormArgs &a, float inv,
+                                           const Place &pl, float (*buf)[32], int &turn) {
+  Stats st{0.f, 0.f};
+  if (a.layer) {
+    F2 s2 = x2[0];
+#pragma unroll
+    for (int i = 1; i < kPairs; ++i) s2 = f2_add(s2, x2[i]);
+    const float2 s = f2_get(s2);
+    st.mu = row_sum(s.x + s.y, pl, buf, turn) * inv;
+    const F2 m2 = f2(st.mu, st.mu);
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) x2[i] = f2_sub(x2[i], m2);
+    if (valid != kAllValid) {  // what is not the row's does not deviate from its mean
+      float f[kElems];
+      unpair(x2, f);
+#pragma unroll
+      for (int i = 0; i < kElems; ++i) f[i] = (valid >> i) & 1u ? f[i] : 0.f;
+      pairs_of(f, x2);
+    }
+  }
+  F2 q2 = f2_mul(x2[0], x2[0]);
+#pragma unroll
+  for (int i = 1; i < kPairs; ++i) q2 = f2_fma(x2[i], x2[i], q2);
+  const float2 q = f2_get(q2);
+  st.r = inv_sqrt(fmaf(row_sum(q.x + q.y, pl, buf, turn), inv, a.eps));
+  return st;
+}
+__device__ __forceinline__ void scale_shift(F2 (&x2)[kPairs], float r, const float (&w)[kElems],
+                                            const float (&b)[kElems]) {
+  F2 w2[kPairs], b2[kPairs];
+  pairs_of(w, w2);
+  pairs_of(b, b2);
+  const F2 r2 = f2(r, r);
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) x2[i] = f2_fma(f2_mul(x2[i], r2), w2[i], b2[i]);
+}
+
+// Backward of one row: x and dy in (zeros past the row's end, and for rows past
+// the last with r = 0); leaves g = dy w in gw and xh in x2, adds to the column
+// sums, and returns mean(g) and mean(g xh).
+__device__ __forceinline__ float2 row_grad(F2 (&x2)[kPairs], const F2 (&e2)[kPairs], const float (&w)[kElems],
+                                           F2 (&gw)[kPairs], F2 (&aw)[kPairs], F2 (&ab)[kPairs], float2 st, float inv,
+                                           const Place &pl, float2 (*buf)[32], int &turn) {
+  F2 w2[kPairs];
+  pairs_of(w, w2);
+  const F2 m2 = f2(st.x, st.x), r2 = f2(st.y, st.y);
+  F2 sg = f2(0.f, 0.f), sx = sg;
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) {
+    x2[i] = f2_mul(f2_sub(x2[i], m2), r2);
+    gw[i] = f2_mul(e2[i], w2[i]);
+    sg = f2_add(sg, gw[i]);
+    sx = f2_fma(gw[i], x2[i], sx);
+    aw[i] = f2_fma(e2[i], x2[i], aw[i]);
+    ab[i] = f2_add(ab[i], e2[i]);
+  }
+  const float2 pg = f2_get(sg), px = f2_get(sx);
+  const float2 s = row_sum(make_float2(pg.x + pg.y, px.x + px.y), pl, buf, turn);
+  return make_float2(s.x * inv, s.y * inv);
+}
+// o2 (d_sum or zeros) += r (g - c.x - xh c.y)
+__device__ __forceinline__ void row_dx(F2 (&o2)[kPairs], const F2 (&gw)[kPairs], const F2 (&xh)[kPairs], float2 c,
+                                       float r) {
+  const F2 c1 = f2(-c.y, -c.y), c2 = f2(c.x, c.x), r2 = f2(r, r);
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) o2[i] = f2_fma(r2, f2_fma(xh[i], c1, f2_sub(gw[i], c2)), o2[i]);
+}
+
+// The block's column sums: its rows' threads add theirs in order, one row group
+// after another, the last into the block's partial row.  col(j): the column of
+// a thread's element j (one below 0 or past H: none).  s_col: [2][H] in shared memory, used when
+// several rows share the block (H <= 2048 then).
+template <class Col>
+__device__ __forceinline__ void block_colsum(const NormArgs &a, const Place &pl, const F2 (&aw)[kPairs],
+                                             const F2 (&ab)[kPairs], float *s_col, Col &&col) {
+  float cw[kElems], cb[kElems];
+  unpair(aw, cw);
+  unpair(ab, cb);
+  float *part = a.part + static_cast<size_t>(blockIdx.x) * 2 * a.H;
+  for (int q = 0; q < pl.rows; ++q) {
+    if (q > 0) __syncthreads();
+    if (pl.g != q) continue;
+    float *out = q == pl.rows - 1 ? part : s_col;
+#pragma unroll
+    for (int j = 0; j < kElems; ++j) {
+      const int c = col(j);
+      if (c < 0 || c >= a.H) continue;
+      out[c] = q > 0 ? s_col[c] + cw[j] : cw[j];
+      out[a.H + c] = q > 0 ? s_col[a.H + c] + cb[j] : cb[j];
+    }
+  }
+}
+
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-template <int VB, class Raw>
-__device__ __forceinline__ void copy_vec(Raw *dst, const Raw *src) {
-  if constexpr (VB == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
-  else if constexpr (VB == 4)
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
-  else
-    *dst = *src;
+// Sixteen bytes into shared memory; of which only `bytes` are read, the rest zero.
+__device__ __forceinline__ void copy16(void *dst, const void *src, int bytes = 16) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
 }
 
-// Rows in flight: what fits 64 to 96 KB of a block.
-template <class El, int Q>
+// Rows of a group in flight.  Three of bf16, two of fp32 (twice the bytes), and two
+// for a single input, whose blocks are many: more was never faster.  (One where 1024
+// threads share the block's shared memory.)
+template <class El, int Q, int TH>
 __host__ __device__ constexpr int ring_depth() {
-  return sizeof(El) == 2 ? (Q == 1 ? 4 : 3) : (Q == 1 ? 4 : 2);
-}
-template <class El, int Q>
-__host__ __device__ constexpr int ring_bytes(int threads) {
-  return ring_depth<El, Q>() * Q * kElems * static_cast<int>(sizeof(El)) * threads;
+  return TH == 1024 ? 1 : (sizeof(El) == 2 && Q > 1 ? 3 : 2);
 }
 
-template <class El, int VB, bool RES, int TH>
-__global__ void __launch_bounds__(TH, 1024 / TH) norm_fwd_kernel(const NormArgs a) {
-  griddep_wait();  // the previous kernel in the stream has completed
-  using Vc = Vec<El, VB>;
-  using Raw = typename Vc::Raw;
-  constexpr int N = Vc::N, V = kElems / N, Q = RES ? 2 : 1, D = ring_depth<El, Q>();
-  extern __shared__ __align__(16) uint8_t s_dyn[];
-  __shared__ float2 s_red[2][32];
-  Raw *ring = reinterpret_cast<Raw *>(s_dyn) + threadIdx.x;  // vector (d, q, u) is ((d Q + q) V + u) TH further
-  int turn = 0;
-  const int tpr = a.tpr, rows = TH / tpr, lane = threadIdx.x % tpr, g = threadIdx.x / tpr;
-  const int nv = a.H / N;
-  const float inv = 1.f / static_cast<float>(a.H);
-  const Raw *x = static_cast<const Raw *>(a.x), *res = static_cast<const Raw *>(a.res);
-  const int step = gridDim.x * rows, t0 = blockIdx.x * rows + g;
-  auto fetch = [&](int t, int d) {
-    if (t < a.T) {
-      const size_t at = static_cast<size_t>(t) * nv + lane;
+// ---- the rows of one thread.  Memory is read in aligned vectors, and the ring is
+// filled and read back by the same thread, so no barrier is needed.  Rows that are
+// not whole vectors (SPAN) start `phase` elements into one; a group's rows are a
+// multiple of N apart, so its phase, and every thread's columns, stay the same.
+// Elements of a thread's first and last vectors that belong to the neighbouring
+// rows are masked, and such vectors are stored element by element.
+template <class El, bool SPAN>
+struct Lane {
+  static constexpr int N = Vec<El>::N, V = kElems / N;
+  int H, T, tpr, lane, phase;
+  int left;        // vectors of the row from this thread's first one on
+  uint32_t valid;  // which of its elements are the row's
+  __device__ __forceinline__ Lane(const NormArgs &a, const Place &pl, int t0)
+      : H(a.H), T(a.T), tpr(pl.tpr), lane(pl.lane), phase(0), valid(0) {
+    if constexpr (SPAN) phase = static_cast<int>(static_cast<int64_t>(t0) * H & (N - 1));
+    left = (phase + H + N - 1) / N - lane;
 #pragma unroll
-      for (int u = 0; u < V; ++u)
-        if (lane + tpr * u < nv) {
-          copy_vec<VB>(ring + ((d * Q) * V + u) * TH, x + at + tpr * u);
-          if (RES) copy_vec<VB>(ring + ((d * Q + 1) * V + u) * TH, res + at + tpr * u);
-        }
-    }
-    copies_commit();
-  };
-#pragma unroll
-  for (int d = 0; d < D - 1; ++d) fetch(t0 + d * step, d);
-  Raw wr[V], br[V];
-#pragma unroll
-  for (int u = 0; u < V; ++u) {
-    const int v = lane + tpr * u;
-    wr[u] = v < nv ? static_cast<const Raw *>(a.w)[v] : Vc::zero();
-    br[u] = v < nv && a.b ? static_cast<const Raw *>(a.b)[v] : Vc::zero();
+    for (int j = 0; j < kElems; ++j) valid |= (col(j) >= 0 && col(j) < H ? 1u : 0u) << j;
   }
-  int d = 0;
-  for (int r0 = blockIdx.x * rows; r0 < a.T; r0 += step) {
-    const int t = r0 + g;
-    fetch(t + (D - 1) * step, d == 0 ? D - 1 : d - 1);
-    copies_wait<D - 1>();
-    const size_t at = static_cast<size_t>(t) * nv;
-    float f[kElems];
-    float2 s = make_float2(0.f, 0.f);
+  __device__ __forceinline__ int col(int j) const { return (lane + tpr * (j / N)) * N + j % N - phase; }
+  // vector of row t's first one, this thread's first
+  __device__ __forceinline__ size_t first(int t) const { return static_cast<size_t>(t) * H / N + lane; }
+  __device__ __forceinline__ void mask(float (&f)[kElems]) const {
+    if (SPAN && valid != kAllValid) {
+#pragma unroll
+      for (int j = 0; j < kElems; ++j) f[j] = (valid >> j) & 1u ? f[j] : 0.f;
+    }
+  }
+  // a vector of length H (weight, bias), as vectors over this thread's columns
+  __device__ __forceinline__ void load_cols(const void *base, uint4 (&r)[V]) const {
 #pragma unroll
     for (int u = 0; u < V; ++u) {
-      const int v = lane + tpr * u;
-      const bool in = t < a.T && v < nv;
-      Vc::unpack(in ? ring[((d * Q) * V + u) * TH] : Vc::zero(), f + N * u);
-      if (RES) {
-        float q[N];
-        Vc::unpack(in ? ring[((d * Q + 1) * V + u) * TH] : Vc::zero(), q);
+      if constexpr (SPAN) {
+        float f[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) f[N * u + i] += q[i];
-        const Raw h = Vc::pack(f + N * u);
-        Vc::unpack(h, f + N * u);  // the norm is that of the stored sum
-        if (in) static_cast<Raw *>(a.sum)[at + v] = h;
+        for (int i = 0; i < N; ++i)
+          f[i] = base && ((valid >> (N * u + i)) & 1u) ? el_get(static_cast<const El *>(base)[col(N * u + i)]) : 0.f;
+        r[u] = Vec<El>::pack(f);
+      } else {
+        r[u] = base && tpr * u < left ? static_cast<const uint4 *>(base)[lane + tpr * u] : make_uint4(0, 0, 0, 0);
       }
-#pragma unroll
-      for (int i = 0; i < N; ++i) s.x += f[N * u + i];
     }
-    if (++d == D) d = 0;
-    float mu = 0.f;
-    if (a.layer) mu = row_sum(s, tpr, s_red, turn).x * inv;
-    s = make_float2(0.f, 0.f);
+  }
+  __device__ __forceinline__ void store(void *base, int t, const float (&f)[kElems]) const {
+    uint4 *dst = static_cast<uint4 *>(base) + first(t);
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      const uint32_t ok = (valid >> (N * u)) & ((1u << N) - 1);
+      if (!SPAN ? tpr * u < left : ok == (1u << N) - 1) {
+        dst[tpr * u] = Vec<El>::pack(f + N * u);
+      } else if (SPAN && ok) {
+        El *e = reinterpret_cast<El *>(dst + tpr * u);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if ((ok >> i) & 1u) el_set(e + i, f[N * u + i]);
+      }
+    }
+  }
+};
+
+template <class El, int Q, int TH>
+__host__ __device__ constexpr int ring_bytes() {
+  return ring_depth<El, Q, TH>() * Q * kElems * static_cast<int>(sizeof(El)) * TH;
+}
+
+template <class El, bool SPAN, int Q, int TH>
+struct Ring {
+  static constexpr int N = Vec<El>::N, V = kElems / N, D = ring_depth<El, Q, TH>();
+  uint4 *slot;  // this thread's; vector (d, q, u) is ((d Q + q) V + u) TH further
+  const uint4 *src[Q];
+  __device__ __forceinline__ Ring(uint8_t *mem, const Lane<El, SPAN> &ln, const void *const (&in)[Q])
+      : slot(reinterpret_cast<uint4 *>(mem) + threadIdx.x) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) src[q] = static_cast<const uint4 *>(in[q]);
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int u = 0; u < V; ++u)
+          if (ln.tpr * u >= ln.left) at(d, q, u) = make_uint4(0, 0, 0, 0);  // past the row: zeros for good
+  }
+  __device__ __forceinline__ uint4 &at(int d, int q, int u) const { return slot[((d * Q + q) * V + u) * TH]; }
+  __device__ __forceinline__ void fetch(int t, int d, const Lane<El, SPAN> &ln) const {
+    const size_t v0 = ln.first(t);
 #pragma unroll
     for (int u = 0; u < V; ++u)
-      if (lane + tpr * u < nv) {
+      if (ln.tpr * u < ln.left) {
+        int bytes = 16;
+        if (SPAN && t == ln.T - 1) {  // nothing past the end of the last row is read
+          const int over = ln.col(N * u) + N - ln.H;
+          bytes = over > 0 ? 16 - over * static_cast<int>(sizeof(El)) : 16;
+        }
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          f[N * u + i] -= mu;
-          s.x = fmaf(f[N * u + i], f[N * u + i], s.x);
+        for (int q = 0; q < Q; ++q) {
+          if (t < ln.T)
+            copy16(&at(d, q, u), src[q] + v0 + ln.tpr * u, bytes);
+          else
+            at(d, q, u) = make_uint4(0, 0, 0, 0);
         }
       }
-    const float r = 1.f / sqrtf(fmaf(row_sum(s, tpr, s_red, turn).x, inv, a.eps));
+    copies_commit();
+  }
+  __device__ __forceinline__ void get(int d, int q, float (&f)[kElems], const Lane<El, SPAN> &ln) const {
+#pragma unroll
+    for (int u = 0; u < V; ++u) Vec<El>::unpack(at(d, q, u), f + N * u);
+    ln.mask(f);
+  }
+};
+
+template <class El>
+__device__ __forceinline__ void unpack_all(const uint4 *r, float (&f)[kElems]) {
+#pragma unroll
+  for (int u = 0; u < kElems / Vec<El>::N; ++u) Vec<El>::unpack(r[u], f + Vec<El>::N * u);
+}
+
+// Threads per SM that the kernels are built for.  Forward: 1024, or 512 with a
+// residual, whose two reads and two writes run faster from fewer rows at once
+// (16384 x 4096 bf16: 84 against 102 us; without one, 16384 x 2048: 28 against
+// 34 us the other way).  Backward: 512 (its column sums take the registers).
+constexpr int fwd_threads(bool res) { return res ? 512 : 1024; }
+constexpr int at_least_1(int x) { return x > 0 ? x : 1; }
+
+template <class El, bool SPAN, bool RES, int TH>
+__global__ void __launch_bounds__(TH, at_least_1(fwd_threads(RES) / TH)) norm_fwd_kernel(const NormArgs a) {
+  griddep_wait();  // the previous kernel in the stream has completed
+  constexpr int Q = RES ? 2 : 1, D = ring_depth<El, Q, TH>();
+  extern __shared__ __align__(16) uint8_t s_dyn[];
+  __shared__ float s_red[2][32];
+  int turn = 0;
+  const Place pl(a.tpr, TH);
+  const float inv = 1.f / static_cast<float>(a.H);
+  const int step = gridDim.x * pl.rows, t0 = blockIdx.x * pl.rows + pl.g;
+  const Lane<El, SPAN> ln(a, pl, t0);
+  const void *in[Q];
+  in[0] = a.x;
+  if constexpr (RES) in[1] = a.res;
+  const Ring<El, SPAN, Q, TH> ring(s_dyn, ln, in);
+#pragma unroll
+  for (int d = 0; d < D - 1; ++d) ring.fetch(t0 + d * step, d, ln);
+  uint4 wr[ln.V], br[ln.V];
+  ln.load_cols(a.w, wr);
+  ln.load_cols(a.b, br);
+  int d = 0;
+  for (int r0 = blockIdx.x * pl.rows; r0 < a.T; r0 += step) {
+    const int t = r0 + pl.g;
+    ring.fetch(t + (D - 1) * step, d == 0 ? D - 1 : d - 1, ln);
+    copies_wait<D - 1>();
+    float f[kElems];
+    F2 x2[kPairs];
+    ring.get(d, 0, f, ln);
+    if constexpr (RES) {
+      float q[kElems];
+      ring.get(d, 1, q, ln);
+#pragma unroll
+      for (int i = 0; i < kElems; ++i) f[i] = el_round(f[i] + q[i], El{});  // the norm is that of the stored sum
+      if (t < a.T) ln.store(a.sum, t, f);
+    }
+    if (++d == D) d = 0;
+    pairs_of(f, x2);
+    const Stats st = normalise(x2, ln.valid, a, inv, pl, s_red, turn);
     if (t < a.T) {
-#pragma unroll
-      for (int u = 0; u < V; ++u) {
-        const int v = lane + tpr * u;
-        if (v < nv) {
-          float w[N], b[N], o[N];
-          Vc::unpack(wr[u], w);
-          Vc::unpack(br[u], b);
-#pragma unroll
-          for (int i = 0; i < N; ++i) o[i] = fmaf(f[N * u + i] * r, w[i], b[i]);
-          static_cast<Raw *>(a.y)[at + v] = Vc::pack(o);
-        }
-      }
-      if (lane == 0) a.stats[t] = make_float2(mu, r);
+      float w[kElems], b[kElems];
+      unpack_all<El>(wr, w);
+      unpack_all<El>(br, b);
+      scale_shift(x2, st.r, w, b);
+      unpair(x2, f);
+      ln.store(a.y, t, f);
+      if (pl.lane == 0) a.stats[t] = make_float2(st.mu, st.r);
     }
   }
 }
 
-template <class El, int VB, bool RES, int TH>
-__global__ void __launch_bounds__(TH, 512 / TH) norm_bwd_kernel(const NormArgs a) {
+template <class El, bool SPAN, bool RES, int TH>
+__global__ void __launch_bounds__(TH, at_least_1(512 / TH)) norm_bwd_kernel(const NormArgs a) {
   griddep_wait();  // the previous kernel in the stream has completed
-  using Vc = Vec<El, VB>;
-  using Raw = typename Vc::Raw;
-  constexpr int N = Vc::N, V = kElems / N, Q = RES ? 3 : 2, D = ring_depth<El, Q>();
+  constexpr int Q = RES ? 3 : 2, D = ring_depth<El, Q, TH>();
   extern __shared__ __align__(16) uint8_t s_dyn[];
   __shared__ float2 s_red[2][32];
-  Raw *ring = reinterpret_cast<Raw *>(s_dyn) + threadIdx.x;
   int turn = 0;
-  const int tpr = a.tpr, rows = TH / tpr, lane = threadIdx.x % tpr, g = threadIdx.x / tpr;
-  const int nv = a.H / N;
+  const Place pl(a.tpr, TH);
   const float inv = 1.f / static_cast<float>(a.H);
-  const Raw *x = static_cast<const Raw *>(a.x), *dy = static_cast<const Raw *>(a.dy);
-  const Raw *ds = static_cast<const Raw *>(a.res);
-  const int step = gridDim.x * rows, t0 = blockIdx.x * rows + g;
-  auto fetch = [&](int t, int d) {
-    if (t < a.T) {
-      const size_t at = static_cast<size_t>(t) * nv + lane;
+  const int step = gridDim.x * pl.rows, t0 = blockIdx.x * pl.rows + pl.g;
+  const Lane<El, SPAN> ln(a, pl, t0);
+  const void *in[Q];
+  in[0] = a.x;
+  in[1] = a.dy;
+  if constexpr (RES) in[2] = a.res;
+  const Ring<El, SPAN, Q, TH> ring(s_dyn, ln, in);
 #pragma unroll
-      for (int u = 0; u < V; ++u)
-        if (lane + tpr * u < nv) {
-          copy_vec<VB>(ring + ((d * Q) * V + u) * TH, x + at + tpr * u);
-          copy_vec<VB>(ring + ((d * Q + 1) * V + u) * TH, dy + at + tpr * u);
-          if (RES) copy_vec<VB>(ring + ((d * Q + 2) * V + u) * TH, ds + at + tpr * u);
-        }
-    }
-    copies_commit();
-  };
+  for (int d = 0; d < D - 1; ++d) ring.fetch(t0 + d * step, d, ln);
+  uint4 wr[ln.V];
+  ln.load_cols(a.w, wr);
+  F2 aw[kPairs], ab[kPairs];
 #pragma unroll
-  for (int d = 0; d < D - 1; ++d) fetch(t0 + d * step, d);
-  Raw wr[V];
-#pragma unroll
-  for (int u = 0; u < V; ++u) {
-    const int v = lane + tpr * u;
-    wr[u] = v < nv ? static_cast<const Raw *>(a.w)[v] : Vc::zero();
-  }
-  float aw[kElems], ab[kElems];
-#pragma unroll
-  for (int i = 0; i < kElems; ++i) aw[i] = ab[i] = 0.f;
-  float2 next = t0 < a.T ? a.stats[t0] : make_float2(0.f, 0.f);
+  for (int i = 0; i < kPairs; ++i) aw[i] = ab[i] = f2(0.f, 0.f);
+  const float2 none = make_float2(0.f, 0.f);  // rows past the last: xh = 0, dy = 0
+  float2 next = t0 < a.T ? a.stats[t0] : none;
   int d = 0;
-  for (int r0 = blockIdx.x * rows; r0 < a.T; r0 += step) {
-    const int t = r0 + g;
-    fetch(t + (D - 1) * step, d == 0 ? D - 1 : d - 1);
-    const float mu = next.x, r = next.y;
-    if (t + step < a.T) next = a.stats[t + step];
+  for (int r0 = blockIdx.x * pl.rows; r0 < a.T; r0 += step) {
+    const int t = r0 + pl.g;
+    ring.fetch(t + (D - 1) * step, d == 0 ? D - 1 : d - 1, ln);
+    const float2 st = next;
+    next = t + step < a.T ? a.stats[t + step] : none;
     copies_wait<D - 1>();
-    const size_t at = static_cast<size_t>(t) * nv;
-    float xh[kElems], gw[kElems];
-    float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int u = 0; u < V; ++u) {
-      float w[N], e[N];
-      const bool in = t < a.T && lane + tpr * u < nv;
-      Vc::unpack(in ? ring[((d * Q) * V + u) * TH] : Vc::zero(), xh + N * u);
-      Vc::unpack(in ? ring[((d * Q + 1) * V + u) * TH] : Vc::zero(), e);
-      Vc::unpack(wr[u], w);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int j = N * u + i;
-        xh[j] = in ? (xh[j] - mu) * r : 0.f;
-        gw[j] = e[i] * w[i];
-        s.x += gw[j];
-        s.y = fmaf(gw[j], xh[j], s.y);
-        aw[j] = fmaf(e[i], xh[j], aw[j]);
-        ab[j] += e[i];
-      }
-    }
-    s = row_sum(s, tpr, s_red, turn);
-    const float c1 = s.y * inv, c2 = a.layer ? s.x * inv : 0.f;
+    float f[kElems];
+    F2 x2[kPairs], e2[kPairs], gw[kPairs];
+    ring.get(d, 0, f, ln);
+    pairs_of(f, x2);
+    ring.get(d, 1, f, ln);
+    pairs_of(f, e2);
+    unpack_all<El>(wr, f);
+    float2 c = row_grad(x2, e2, f, gw, aw, ab, st, inv, pl, s_red, turn);
+    if (!a.layer) c.x = 0.f;
     if (t < a.T) {
+      F2 o2[kPairs];
 #pragma unroll
-      for (int u = 0; u < V; ++u) {
-        const int v = lane + tpr * u;
-        if (v < nv) {
-          float o[N];
-          Vc::unpack(RES ? ring[((d * Q + 2) * V + u) * TH] : Vc::zero(), o);
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const int j = N * u + i;
-            o[i] = fmaf(r, gw[j] - c2 - xh[j] * c1, o[i]);
-          }
-          static_cast<Raw *>(a.y)[at + v] = Vc::pack(o);
-        }
-      }
+      for (int i = 0; i < kElems; ++i) f[i] = 0.f;
+      if constexpr (RES) ring.get(d, 2, f, ln);
+      pairs_of(f, o2);
+      row_dx(o2, gw, x2, c, st.y);
+      unpair(o2, f);
+      ln.store(a.y, t, f);
     }
     if (++d == D) d = 0;
   }
-  // the block's column sums: its row groups added in order, one after another
   copies_wait<0>();
   __syncthreads();  // the ring is no longer read: it holds the sums
-  float *s_col = reinterpret_cast<float *>(s_dyn);  // [2][H] when several rows share the block (H <= TH kElems / 2)
-  float *part = a.part + static_cast<size_t>(blockIdx.x) * 2 * a.H;
-  for (int q = 0; q < rows; ++q) {
-    if (q > 0) __syncthreads();
-    if (g == q) {
-      float *out = q == rows - 1 ? part : s_col;
-#pragma unroll
-      for (int u = 0; u < V; ++u) {
-        const int v = lane + tpr * u;
-        if (v < nv) {
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const int c = v * N + i;
-            out[c] = q > 0 ? s_col[c] + aw[N * u + i] : aw[N * u + i];
-            out[a.H + c] = q > 0 ? s_col[a.H + c] + ab[N * u + i] : ab[N * u + i];
-          }
-        }
-      }
-    }
-  }
+  block_colsum(a, pl, aw, ab, reinterpret_cast<float *>(s_dyn), [&](int j) { return ln.col(j); });
 }
 
 // dw[c] and db[c] = the sum over the blocks' partial rows in a fixed order: 8
@@ -360,10 +491,12 @@ __global__ void __launch_bounds__(256) norm_colsum_kernel(const float *__restric
   const int c = blockIdx.x * 8 + cl;
   const float *src = part + static_cast<size_t>(blockIdx.y) * H + c;
   float acc = 0.f;
-  if (c < H) {
-#pragma unroll 10
-    for (int b = run; b < nb; b += 32) acc += src[static_cast<size_t>(b) * 2 * H];
-  }
+  constexpr int U = (kBwdBlocks + 31) / 32;  // every load of a run at once
+  float v[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) v[u] = c < H && run + 32 * u < nb ? src[static_cast<size_t>(run + 32 * u) * 2 * H] : 0.f;
+#pragma unroll
+  for (int u = 0; u < U; ++u) acc += v[u];
   s[run][cl] = acc;
   __syncthreads();
   if (threadIdx.x < 32) {  // lane = run here: a tree over the 32 runs of each column
@@ -377,17 +510,22 @@ __global__ void __launch_bounds__(256) norm_colsum_kernel(const float *__restric
   }
 }
 
-int tpr_of(int H) {
+// Rows of whole vectors, and threads per row: enough for the vectors that a row
+// touches wherever it starts.
+bool spans(int H, int el) { return H * el % 16 != 0; }
+int tpr_of(int H, int el) {
+  const int n = 16 / el, need = spans(H, el) ? (H + n - 1 + n - 1) / n * n : H;
   int tpr = 8;
-  while (tpr * kElems < H) tpr *= 2;
+  while (tpr * kElems < need) tpr *= 2;
   return tpr;
 }
-
-// The widest vectors that divide a row (all base pointers are 16-byte aligned,
-// so every row then starts on a vector).
-int vector_bytes(int H, int el) {
-  const int row = H * el;
-  return row % 16 == 0 ? 16 : (row % 4 == 0 ? 4 : 2);
+// Blocks: those that fit at once, and where rows have a phase, a number that keeps
+// a group's rows a multiple of the vector apart.
+int blocks_for(const NormArgs &a, int threads, int most, int el) {
+  const int rows = threads / a.tpr, need = (a.T + rows - 1) / rows;
+  if (need <= most) return need;
+  const int n = 16 / el, unit = spans(a.H, el) && rows < n ? n / rows : 1;
+  return most / unit * unit;
 }
 
 // Blocks of a kernel that fit the part at once, after its shared-memory opt-in.
@@ -404,50 +542,48 @@ cudaError_t resident(DeviceOnce &once, K kernel, int threads, int smem, int sms,
       blocks);
 }
 
-template <class El, int VB, bool RES, int TH>
+template <class El, bool SPAN, bool RES, int TH>
 cudaError_t launch_fwd(const NormArgs &a, int sms, cudaStream_t s) {
   static DeviceOnce once;
-  constexpr int smem = ring_bytes<El, RES ? 2 : 1>(TH);
+  constexpr int smem = ring_bytes<El, RES ? 2 : 1, TH>();
+  auto kernel = norm_fwd_kernel<El, SPAN, RES, TH>;
   int most = 0;
-  const cudaError_t e = resident(once, norm_fwd_kernel<El, VB, RES, TH>, TH, smem, sms, &most);
+  const cudaError_t e = resident(once, kernel, TH, smem, sms, &most);
   if (e != cudaSuccess) return e;
-  const int rows = TH / a.tpr, need = (a.T + rows - 1) / rows;
-  return launch_pdl(norm_fwd_kernel<El, VB, RES, TH>, dim3(need < most ? need : most), dim3(TH), smem, s, 1, a);
+  return launch_pdl(kernel, dim3(blocks_for(a, TH, most, sizeof(El))), dim3(TH), smem, s, 1, a);
 }
 
-template <class El, int VB, bool RES, int TH>
+template <class El, bool SPAN, bool RES, int TH>
 cudaError_t launch_bwd(const NormArgs &a, int sms, float *dw, float *db, cudaStream_t s) {
   static DeviceOnce once;
-  constexpr int smem = ring_bytes<El, RES ? 3 : 2>(TH);
+  constexpr int smem = ring_bytes<El, RES ? 3 : 2, TH>();
+  auto kernel = norm_bwd_kernel<El, SPAN, RES, TH>;
   int most = 0;
-  cudaError_t e = resident(once, norm_bwd_kernel<El, VB, RES, TH>, TH, smem, sms, &most);
+  cudaError_t e = resident(once, kernel, TH, smem, sms, &most);
   if (e != cudaSuccess) return e;
-  if (most > kBwdBlocks) most = kBwdBlocks;
-  const int rows = TH / a.tpr, need = (a.T + rows - 1) / rows, nb = need < most ? need : most;
-  e = launch_pdl(norm_bwd_kernel<El, VB, RES, TH>, dim3(nb), dim3(TH), smem, s, 1, a);
+  const int nb = blocks_for(a, TH, most < kBwdBlocks ? most : kBwdBlocks, sizeof(El));
+  e = launch_pdl(kernel, dim3(nb), dim3(TH), smem, s, 1, a);
   if (e != cudaSuccess) return e;
   return launch_pdl(norm_colsum_kernel, dim3((a.H + 7) / 8, db ? 2 : 1), dim3(256), 0, s, 1, a.part, nb, a.H, dw, db);
 }
 
-// The variant for a configuration: vectors as wide as the rows allow, 512 threads
-// only where a row takes them.
+// The variant for a configuration: 256 threads, or as many as one row takes
+// (1024 only where a row of nearly 8192 elements has a phase).
 template <class F>
-cudaError_t by_form(bool bf, int H, bool res, F &&f) {
-  const bool wide = tpr_of(H) > kThreads;
-  auto pick = [&](auto el, auto vb) {
-    if (res)
-      return wide ? f(el, vb, std::true_type{}, std::integral_constant<int, 512>{})
-                  : f(el, vb, std::true_type{}, std::integral_constant<int, 256>{});
-    return wide ? f(el, vb, std::false_type{}, std::integral_constant<int, 512>{})
-                : f(el, vb, std::false_type{}, std::integral_constant<int, 256>{});
+cudaError_t by_form(const NormArgs &a, bool bf, bool res, F &&f) {
+  auto threads = [&](auto el, auto sp, auto re) {
+    if (a.tpr <= kThreads) return f(el, sp, re, std::integral_constant<int, kThreads>{});
+    if constexpr (decltype(sp)::value)
+      if (a.tpr > 512) return f(el, sp, re, std::integral_constant<int, 1024>{});
+    return f(el, sp, re, std::integral_constant<int, 512>{});
   };
-  const int vb = vector_bytes(H, bf ? 2 : 4);
-  if (bf) {
-    if (vb == 16) return pick(uint16_t{}, std::integral_constant<int, 16>{});
-    return vb == 4 ? pick(uint16_t{}, std::integral_constant<int, 4>{})
-                   : pick(uint16_t{}, std::integral_constant<int, 2>{});
-  }
-  return vb == 16 ? pick(float{}, std::integral_constant<int, 16>{}) : pick(float{}, std::integral_constant<int, 4>{});
+  auto rows = [&](auto el, auto sp) {
+    return res ? threads(el, sp, std::true_type{}) : threads(el, sp, std::false_type{});
+  };
+  auto type = [&](auto el) {
+    return spans(a.H, sizeof(el)) ? rows(el, std::true_type{}) : rows(el, std::false_type{});
+  };
+  return bf ? type(uint16_t{}) : type(float{});
 }
 
 bool norm_ok(const moe_norm_config *c) {
@@ -461,7 +597,7 @@ NormArgs norm_args(const moe_norm_config *c) {
   a.H = c->H;
   a.eps = c->eps;
   a.layer = c->kind == MOE_NORM_LAYER;
-  a.tpr = tpr_of(c->H);
+  a.tpr = tpr_of(c->H, c->dtype == MOE_DTYPE_BF16 ? 2 : 4);
   return a;
 }
 
@@ -497,8 +633,8 @@ moe_status moe_norm_forward(const moe_norm_config *cfg, const void *x, const voi
   a.stats = reinterpret_cast<float2 *>(stats);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return timed("norm_forward", s, [&] {
-    return by_form(cfg->dtype == MOE_DTYPE_BF16, cfg->H, residual != nullptr, [&](auto el, auto vb, auto res, auto th) {
-      return launch_fwd<decltype(el), decltype(vb)::value, decltype(res)::value, decltype(th)::value>(a, di.sms, s);
+    return by_form(a, cfg->dtype == MOE_DTYPE_BF16, residual != nullptr, [&](auto el, auto span, auto res, auto th) {
+      return launch_fwd<decltype(el), decltype(span)::value, decltype(res)::value, decltype(th)::value>(a, di.sms, s);
     });
   });
 }
@@ -532,8 +668,8 @@ moe_status moe_norm_backward(const moe_norm_config *cfg, const void *dy, const v
   a.stats = const_cast<float2 *>(reinterpret_cast<const float2 *>(stats));
   a.part = static_cast<float *>(scratch);
   return timed("norm_backward", s, [&] {
-    return by_form(cfg->dtype == MOE_DTYPE_BF16, cfg->H, d_sum != nullptr, [&](auto el, auto vb, auto res, auto th) {
-      return launch_bwd<decltype(el), decltype(vb)::value, decltype(res)::value, decltype(th)::value>(
+    return by_form(a, cfg->dtype == MOE_DTYPE_BF16, d_sum != nullptr, [&](auto el, auto span, auto res, auto th) {
+      return launch_bwd<decltype(el), decltype(span)::value, decltype(res)::value, decltype(th)::value>(
           a, di.sms, dweight, dbias, s);
     });
   });
