@@ -21,6 +21,8 @@
 // time.  Counts are integers, added in any order.
 #include <math.h>
 
+#include <type_traits>
+
 #include "abi.h"
 #include "common.cuh"
 
@@ -29,8 +31,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kBwdBlocksPerSm = 8;  // backward blocks at most
 constexpr int kMaxBlocks = 304;  // forward blocks over all sequences at most, unless there are more sequences
-constexpr int kUnroll = 4;       // tokens whose loads a lane group has in flight
 
 struct SeqSum {  // one sequence, or one block's share of it
   float bal, z;
@@ -59,30 +61,43 @@ struct BalArgs {
   float *d_logits;
 };
 
-// A lane's columns: four consecutive ones (VEC, E % 4 == 0) or one, G apart.
-template <bool VEC>
+// A lane's columns: W consecutive ones (the widest of 4, 2, 1 that divides E, so
+// that a row's vectors are aligned), then the next W, G lanes further.
+template <int W>
 __device__ __forceinline__ int col_of(int j, int lane, int G) {
-  return VEC ? ((j >> 2) * G + lane) * 4 + (j & 3) : j * G + lane;
+  return ((j / W) * G + lane) * W + j % W;
 }
+template <int W> struct VecOf;
+template <> struct VecOf<4> { using type = float4; };
+template <> struct VecOf<2> { using type = float2; };
+template <> struct VecOf<1> { using type = float; };
 
-template <bool VEC, int NV>
+template <int W, int NV>
 __device__ __forceinline__ void load_row(const float *row, int E, int G, int lane, bool in, float fill,
                                          float (&v)[NV]) {
-  if constexpr (VEC) {
+  using Vt = typename VecOf<W>::type;
 #pragma unroll
-    for (int j = 0; j < NV / 4; ++j) {
-      const int c = (j * G + lane) * 4;
-      const float4 q = in && c < E ? *reinterpret_cast<const float4 *>(row + c) : make_float4(fill, fill, fill, fill);
-      v[4 * j] = q.x;
-      v[4 * j + 1] = q.y;
-      v[4 * j + 2] = q.z;
-      v[4 * j + 3] = q.w;
+  for (int j = 0; j < NV; j += W) {
+    const int c = col_of<W>(j, lane, G);
+    if (in && c < E) {
+      const Vt q = *reinterpret_cast<const Vt *>(row + c);
+      memcpy(&v[j], &q, sizeof(q));
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) v[j + i] = fill;
     }
-  } else {
+  }
+}
+template <int W, int NV>
+__device__ __forceinline__ void store_row(float *row, int E, int G, int lane, const float (&v)[NV]) {
+  using Vt = typename VecOf<W>::type;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = j * G + lane;
-      v[j] = in && c < E ? row[c] : fill;
+  for (int j = 0; j < NV; j += W) {
+    const int c = col_of<W>(j, lane, G);
+    if (c < E) {
+      Vt q;
+      memcpy(&q, &v[j], sizeof(q));
+      *reinterpret_cast<Vt *>(row + c) = q;
     }
   }
 }
@@ -100,18 +115,53 @@ __device__ __forceinline__ float group_max(float v, int G) {
   return v;
 }
 
-template <bool VEC, int NV>
+// One sequence's outputs, by a block's first 256 threads: thread e holds expert e's
+// probability sum and count (0 past E).  r: its z sum, tokens and flags; thread 0
+// gets the sequence's balance term in r.bal.  Every thread of the block calls it.
+__device__ __forceinline__ void finish_seq(const BalArgs &a, int s, float sum, int cnt, SeqSum &r, float *s_w) {
+  const float inv_n = r.n > 0 ? 1.f / static_cast<float>(r.n) : 0.f;
+  const int e = threadIdx.x;
+  if (e < 256) {
+    const float P = sum * inv_n;
+    if (e < a.E) {
+      a.counts[static_cast<size_t>(s) * a.E + e] = cnt;
+      a.probs[static_cast<size_t>(s) * a.E + e] = P;
+    }
+    const float fp = warp_sum(e < a.E ? static_cast<float>(cnt) * P : 0.f);
+    if ((e & 31) == 0) s_w[e >> 5] = fp;
+  }
+  __syncthreads();
+  if (e == 0) {
+    float b = 0.f;
+    for (int w = 0; w < 8; ++w) b += s_w[w];
+    r.bal = b * static_cast<float>(a.E) / static_cast<float>(a.k) * inv_n;
+    a.tokens[s] = r.n;
+  }
+}
+__device__ __forceinline__ void finish_all(const BalArgs &a, float bal, float z, int n, int used, int flags) {
+  a.loss[0] = used > 0 ? bal / static_cast<float>(used) : 0.f;
+  a.loss[1] = n > 0 ? z / static_cast<float>(n) : 0.f;
+  *a.status = flags;
+}
+
+template <int W, int NV, bool SOLO>
 __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(const BalArgs a) {
   griddep_wait();  // the previous kernel in the stream has completed
+  if (!SOLO) griddep_launch_dependents();  // the finishing kernel may be set up meanwhile
   __shared__ int s_cnt[kMaxExperts];
   __shared__ float s_col[kWarps][kMaxExperts];
   __shared__ SeqSum s_blk[kWarps];
+  __shared__ float s_w[kWarps];
   const int warp = threadIdx.x >> 5, l32 = threadIdx.x & 31;
   const int E = a.E, G = a.G, lane = l32 & (G - 1), sub = l32 / G, tpw = 32 / G;
   const int seq = blockIdx.x / a.nbs, blk = blockIdx.x - seq * a.nbs;
   const int i0 = blk * a.per, i1 = min(i0 + a.per, a.L);  // tokens of the sequence
   const size_t tbase = static_cast<size_t>(seq) * a.L;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
+  const int step = kWarps * tpw;  // tokens of one pass of the block
+  float v[NV], next[NV];
+  int ib = i0 + warp * tpw;
+  load_row<W>(a.logits + (tbase + ib + sub) * E, E, G, lane, ib + sub < i1, -INFINITY, next);
+  if (!SOLO && blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
   for (int e = threadIdx.x; e < E; e += kThreads) s_cnt[e] = 0;
   __syncthreads();
   float col[NV];
@@ -119,56 +169,49 @@ __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(const BalArgs a) 
   for (int j = 0; j < NV; ++j) col[j] = 0.f;
   float z = 0.f;
   int n = 0, flags = 0;
-  const int step = kWarps * tpw;  // tokens of one pass of the block
-  for (int ib = i0 + warp * tpw; ib < i1; ib += step * kUnroll) {
-    float v[kUnroll][NV];
-    bool ok[kUnroll];
+  for (; ib < i1; ib += step) {
+    const int i = ib + sub;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = ib + u * step + sub;
-      const bool in = i < i1;
-      load_row<VEC>(a.logits + (tbase + i) * E, E, G, lane, in, -INFINITY, v[u]);
-      ok[u] = in && (!a.mask || a.mask[tbase + i] != 0);
+    for (int j = 0; j < NV; ++j) v[j] = next[j];
+    load_row<W>(a.logits + (tbase + i + step) * E, E, G, lane, i + step < i1, -INFINITY, next);
+    bool ok = i < i1 && (!a.mask || a.mask[tbase + i] != 0);
+    float mx = v[0];
+#pragma unroll
+    for (int j = 1; j < NV; ++j) mx = fmaxf(mx, v[j]);
+    mx = group_max(mx, G);  // NaNs are passed over here, and show in the sum
+    if (__any_sync(0xffffffffu, ok && mx == -INFINITY)) {  // -inf throughout: no part in the losses
+      float nan = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) nan = v[j] != v[j] ? 1.f : nan;
+      nan = group_max(nan, G);  // by every lane of the warp: its shuffles name them all
+      if (mx == -INFINITY && nan == 0.f) ok = false;
     }
+    float sum = 0.f;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = ib + u * step + sub;
-      float mx = -INFINITY, bad = 0.f;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        mx = fmaxf(mx, v[u][j]);
-        if (v[u][j] != v[u][j] || v[u][j] == INFINITY) bad = 1.f;
-      }
-      mx = group_max(mx, G);
-      bad = group_max(bad, G);
-      if (bad == 0.f && mx == -INFINITY) ok[u] = false;  // no finite logit
-      float sum = 0.f, ex[NV];
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        ex[j] = ok[u] ? expf(v[u][j] - mx) : 0.f;
-        sum += ex[j];
-      }
-      sum = group_sum(sum, G);
-      const float lse = bad != 0.f ? NAN : mx + logf(sum);
-      if (ok[u]) {
-        const float inv = bad != 0.f ? NAN : 1.f / sum;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) col[j] = fmaf(ex[j], inv, col[j]);
-        if (lane == 0) {
-          z = fmaf(lse, lse, z);
-          n += 1;
-          if (bad != 0.f) flags |= kDevNonfiniteLogit;
-        }
-        for (int q = lane; q < a.k; q += G) {
-          const int e = a.topk_idx[(tbase + i) * a.k + q];
-          if (static_cast<unsigned>(e) < static_cast<unsigned>(E))
-            atomicAdd(&s_cnt[e], 1);
-          else
-            flags |= kDevBadIndex;
-        }
-      }
-      if (lane == 0 && i < i1) a.lse[tbase + i] = ok[u] ? lse : INFINITY;
+    for (int j = 0; j < NV; ++j) {
+      v[j] = expf(v[j] - mx);
+      sum += v[j];
     }
+    sum = group_sum(sum, G);
+    const float lse = mx + logf(sum);  // NaN with a NaN or +inf logit
+    if (ok) {
+      const float inv = 1.f / sum;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) col[j] = fmaf(v[j], inv, col[j]);
+      if (lane == 0) {
+        z = fmaf(lse, lse, z);
+        n += 1;
+        if (lse != lse) flags |= kDevNonfiniteLogit;
+      }
+      for (int q = lane; q < a.k; q += G) {
+        const int e = a.topk_idx[(tbase + i) * a.k + q];
+        if (static_cast<unsigned>(e) < static_cast<unsigned>(E))
+          atomicAdd(&s_cnt[e], 1);
+        else
+          flags |= kDevBadIndex;
+      }
+    }
+    if (lane == 0 && i < i1) a.lse[tbase + i] = ok ? lse : INFINITY;
   }
   // the warp's token groups, then the block's warps, in a fixed order
 #pragma unroll
@@ -177,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(const BalArgs a) 
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
       if (o >= G) c += __shfl_xor_sync(0xffffffffu, c, o);
-    const int e = col_of<VEC>(j, lane, G);
+    const int e = col_of<W>(j, lane, G);
     if (sub == 0 && e < E) s_col[warp][e] = c;
   }
   z = warp_sum(z);
@@ -185,21 +228,28 @@ __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(const BalArgs a) 
   flags = __reduce_or_sync(0xffffffffu, flags);
   if (l32 == 0) s_blk[warp] = SeqSum{0.f, z, n, flags};
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += kThreads) {
-    float c = 0.f;
+  SeqSum r = s_blk[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) {
+    r.z += s_blk[w].z;
+    r.n += s_blk[w].n;
+    r.flags |= s_blk[w].flags;
+  }
+  float c = 0.f;
+  const int e = threadIdx.x;  // kThreads >= E
+  if (e < E) {
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) c += s_col[w][e];
-    a.psum[static_cast<size_t>(blockIdx.x) * E + e] = c;
-    a.pcnt[static_cast<size_t>(blockIdx.x) * E + e] = s_cnt[e];
   }
-  if (threadIdx.x == 0) {
-    SeqSum r = s_blk[0];
-    for (int w = 1; w < kWarps; ++w) {
-      r.z += s_blk[w].z;
-      r.n += s_blk[w].n;
-      r.flags |= s_blk[w].flags;
+  if constexpr (SOLO) {  // the only block: the results themselves
+    finish_seq(a, 0, e < E ? c : 0.f, e < E ? s_cnt[e] : 0, r, s_w);
+    if (threadIdx.x == 0) finish_all(a, r.n > 0 ? r.bal : 0.f, r.z, r.n, r.n > 0 ? 1 : 0, r.flags);
+  } else {
+    if (e < E) {
+      a.psum[static_cast<size_t>(blockIdx.x) * E + e] = c;
+      a.pcnt[static_cast<size_t>(blockIdx.x) * E + e] = s_cnt[e];
     }
-    a.pblk[blockIdx.x] = r;
+    if (threadIdx.x == 0) a.pblk[blockIdx.x] = r;
   }
 }
 
@@ -252,29 +302,19 @@ __global__ void __launch_bounds__(kFinThreads) balance_finish_kernel(const BalAr
     if (threadIdx.x == 0) s_seq = r;
   }
   __syncthreads();
-  const float inv_n = s_seq.n > 0 ? 1.f / static_cast<float>(s_seq.n) : 0.f;
-  if (threadIdx.x < 256) {  // E <= 256
-    float fp = 0.f;
-    if (threadIdx.x < E) {
-      for (int r = 1; r < runs; ++r) {
-        sum += s_sum[r * ep + threadIdx.x];
-        cnt += s_cnt[r * ep + threadIdx.x];
-      }
-      const float P = sum * inv_n;
-      a.counts[static_cast<size_t>(s) * E + e] = cnt;
-      a.probs[static_cast<size_t>(s) * E + e] = P;
-      fp = static_cast<float>(cnt) * P;
+  SeqSum r = s_seq;
+  if (threadIdx.x < E) {
+    for (int q = 1; q < runs; ++q) {
+      sum += s_sum[q * ep + threadIdx.x];
+      cnt += s_cnt[q * ep + threadIdx.x];
     }
-    fp = warp_sum(fp);
-    if ((threadIdx.x & 31) == 0) s_w[threadIdx.x >> 5] = fp;
   }
-  __syncthreads();
+  finish_seq(a, s, sum, cnt, r, s_w);
+  if (a.S == 1) {
+    if (threadIdx.x == 0) finish_all(a, r.n > 0 ? r.bal : 0.f, r.z, r.n, r.n > 0 ? 1 : 0, r.flags);
+    return;
+  }
   if (threadIdx.x == 0) {
-    float b = 0.f;
-    for (int w = 0; w < 8; ++w) b += s_w[w];
-    SeqSum r = s_seq;
-    r.bal = b * static_cast<float>(E) / static_cast<float>(a.k) * inv_n;
-    a.tokens[s] = r.n;
     a.pseq[s] = r;
     __threadfence();
     s_last = atomicAdd(a.ticket, 1) == a.S - 1;
@@ -297,14 +337,10 @@ __global__ void __launch_bounds__(kFinThreads) balance_finish_kernel(const BalAr
   n = __reduce_add_sync(0xffffffffu, n);
   used = __reduce_add_sync(0xffffffffu, used);
   flags = __reduce_or_sync(0xffffffffu, flags);
-  if (threadIdx.x == 0) {
-    a.loss[0] = used > 0 ? bal / static_cast<float>(used) : 0.f;
-    a.loss[1] = n > 0 ? z / static_cast<float>(n) : 0.f;
-    *a.status = flags;
-  }
+  if (threadIdx.x == 0) finish_all(a, bal, z, n, used, flags);
 }
 
-template <bool VEC, int NV, bool ADD>
+template <int W, int NV, bool ADD>
 __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(const BalArgs a) {
   griddep_wait();  // the previous kernel in the stream has completed
   __shared__ int s_n[kWarps], s_used[kWarps];
@@ -313,80 +349,70 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(const BalArgs a) 
   const int seq = blockIdx.x / a.nbs, blk = blockIdx.x - seq * a.nbs;
   const int i0 = blk * a.per, i1 = min(i0 + a.per, a.L);
   const size_t tbase = static_cast<size_t>(seq) * a.L;
-  int n = 0, used = 0;
-  for (int q = threadIdx.x; q < a.S; q += kThreads) {
-    const int t = a.tokens[q];
-    n += t;
-    used += t > 0;
-  }
-  n = __reduce_add_sync(0xffffffffu, n);
-  used = __reduce_add_sync(0xffffffffu, used);
-  if (l32 == 0) {
-    s_n[warp] = n;
-    s_used[warp] = used;
-  }
-  __syncthreads();
-  n = used = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    n += s_n[w];
-    used += s_used[w];
-  }
+  const int step = kWarps * tpw;
+  float next[NV], old[NV], lse_next;
+  int ib = i0 + warp * tpw;
+  auto fetch = [&](int i) {  // the next token's logits, before this one is worked on
+    load_row<W>(a.logits + (tbase + i) * E, E, G, lane, i < i1, -INFINITY, next);
+    lse_next = i < i1 ? a.lse_in[tbase + i] : INFINITY;
+  };
+  fetch(ib + sub);
   const int ns = a.tokens[seq];
+  int n = ns, used = ns > 0 ? 1 : 0;
+  if (a.S > 1) {
+    n = used = 0;
+    for (int q = threadIdx.x; q < a.S; q += kThreads) {
+      const int t = a.tokens[q];
+      n += t;
+      used += t > 0;
+    }
+    n = __reduce_add_sync(0xffffffffu, n);
+    used = __reduce_add_sync(0xffffffffu, used);
+    if (l32 == 0) {
+      s_n[warp] = n;
+      s_used[warp] = used;
+    }
+    __syncthreads();
+    n = used = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      n += s_n[w];
+      used += s_used[w];
+    }
+  }
   const float inv = ns > 0 ? 1.f / static_cast<float>(ns) : 0.f;
   const float cb = used > 0 ? a.g_bal * static_cast<float>(E) / static_cast<float>(used) * inv : 0.f;
   const float cz = n > 0 ? 2.f * a.g_z / static_cast<float>(n) : 0.f;
   float f[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int e = col_of<VEC>(j, lane, G);
+    const int e = col_of<W>(j, lane, G);
     f[j] = e < E ? static_cast<float>(a.counts[static_cast<size_t>(seq) * E + e]) * inv / static_cast<float>(a.k) : 0.f;
   }
-  const int step = kWarps * tpw;
-  constexpr int U = kUnroll / 2;
-  for (int ib = i0 + warp * tpw; ib < i1; ib += step * U) {
-    float v[U][NV], old[U][NV], lse[U];
+  for (; ib < i1; ib += step) {
+    const int i = ib + sub;
+    float p[NV];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = ib + u * step + sub;
-      const bool in = i < i1;
-      load_row<VEC>(a.logits + (tbase + i) * E, E, G, lane, in, -INFINITY, v[u]);
-      if (ADD) load_row<VEC>(a.d_logits + (tbase + i) * E, E, G, lane, in, 0.f, old[u]);
-      lse[u] = in ? a.lse_in[tbase + i] : INFINITY;
+    for (int j = 0; j < NV; ++j) p[j] = next[j];
+    const float lse = lse_next;
+    float *row = a.d_logits + (tbase + i) * E;
+    if (ADD) load_row<W>(row, E, G, lane, i < i1, 0.f, old);
+    fetch(i + step);
+    const bool some = lse != INFINITY;  // the token has a part in the losses
+    float dot = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      p[j] = some ? expf(p[j] - lse) : 0.f;
+      dot = fmaf(f[j], p[j], dot);
     }
+    dot = group_sum(dot, G);
+    const float zt = some ? cz * lse : 0.f;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = ib + u * step + sub;
-      const bool some = lse[u] != INFINITY;  // the token has a part in the losses
-      float p[NV], dot = 0.f;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        p[j] = some ? expf(v[u][j] - lse[u]) : 0.f;
-        dot = fmaf(f[j], p[j], dot);
-      }
-      dot = group_sum(dot, G);
-      const float zt = some ? cz * lse[u] : 0.f;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const float d = p[j] * fmaf(cb, f[j] - dot, zt);
-        p[j] = ADD ? old[u][j] + d : d;
-      }
-      if (i < i1 && (some || !ADD)) {
-        float *row = a.d_logits + (tbase + i) * E;
-        if constexpr (VEC) {
-#pragma unroll
-          for (int j = 0; j < NV / 4; ++j) {
-            const int c = (j * G + lane) * 4;
-            if (c < E)
-              *reinterpret_cast<float4 *>(row + c) = make_float4(p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < NV; ++j)
-            if (j * G + lane < E) row[j * G + lane] = p[j];
-        }
-      }
+    for (int j = 0; j < NV; ++j) {
+      const float d = p[j] * fmaf(cb, f[j] - dot, zt);
+      p[j] = ADD ? old[j] + d : d;
     }
+    if (i < i1 && (some || !ADD)) store_row<W>(row, E, G, lane, p);
   }
 }
 
@@ -395,19 +421,34 @@ bool bal_ok(const moe_balance_config *c) {
          c->k <= c->E && c->sequences >= 1 && c->T % c->sequences == 0;
 }
 
-int lanes_per_token(int E) {
-  const int units = E % 4 == 0 ? E / 4 : E;
+// Values per lane and lanes per token.  Whole float4s: up to `most` values per
+// lane, so that few lanes share a token and its sums take few shuffles; narrower
+// vectors: 8, so that the lanes of a warp read whole lines.
+int width_of(int E) { return E % 4 == 0 ? 4 : (E % 2 == 0 ? 2 : 1); }
+int values_per_lane(int E, int most) {
+  if (E % 4 != 0) most = 8;
+  int nv = width_of(E);
+  while (nv < most && nv * 32 < (E % 4 == 0 ? 32 * E : E)) nv *= 2;
+  return nv;
+}
+int lanes_per_token(int E, int most) {
+  const int nv = values_per_lane(E, most);
   int G = 1;
-  while (G < units && G < 32) G *= 2;
+  while (G * nv < E) G *= 2;
   return G;
 }
+constexpr int kFwdValues = 16, kBwdValues = 8;  // (the backward's 16 took 110 registers: 12.5 against 9 us)
 
-// Blocks per sequence and tokens per block: enough blocks to fill the part, but
-// none with less than two passes of its warps.
-void split(const moe_balance_config *c, int *nbs, int *per) {
-  const int L = c->T / c->sequences, pass = kWarps * (32 / lanes_per_token(c->E));
-  int n = (L + 2 * pass - 1) / (2 * pass);
-  const int most = kMaxBlocks / c->sequences > 1 ? kMaxBlocks / c->sequences : 1;
+// Blocks per sequence (at most `most` over all of them, at least one each) and
+// tokens per block, whole passes of its warps.
+// A single sequence of up to kSoloPasses goes to one block, which needs no
+// second kernel.
+constexpr int kSoloPasses = 4;
+void split(const moe_balance_config *c, int most, int G, bool solo, int *nbs, int *per) {
+  const int L = c->T / c->sequences, pass = kWarps * (32 / G);
+  int n = (L + pass - 1) / pass;
+  if (solo && c->sequences == 1 && n <= kSoloPasses) n = 1;
+  most = most / c->sequences > 1 ? most / c->sequences : 1;
   if (n > most) n = most;
   if (n < 1) n = 1;
   *per = ((L + n - 1) / n + pass - 1) / pass * pass;
@@ -419,7 +460,7 @@ struct BalLayout {
 };
 BalLayout bal_layout(const moe_balance_config *c) {
   int nbs, per;
-  split(c, &nbs, &per);
+  split(c, kMaxBlocks, lanes_per_token(c->E, kFwdValues), true, &nbs, &per);
   const size_t rows = static_cast<size_t>(c->sequences) * nbs;
   BalLayout L;
   L.ticket = 64;  // inside the header
@@ -431,32 +472,46 @@ BalLayout bal_layout(const moe_balance_config *c) {
   return L;
 }
 
-BalArgs bal_args(const moe_balance_config *c) {
+BalArgs bal_args(const moe_balance_config *c, int most, int values, bool solo) {
   BalArgs a{};
   a.T = c->T;
   a.E = c->E;
   a.k = c->k;
   a.S = c->sequences;
   a.L = c->T / c->sequences;
-  a.G = lanes_per_token(c->E);
-  split(c, &a.nbs, &a.per);
+  a.G = lanes_per_token(c->E, values);
+  split(c, most, a.G, solo, &a.nbs, &a.per);
   return a;
 }
 
-template <bool VEC, int NV>
+template <int W, int NV>
 cudaError_t launch_fwd(const BalArgs &a, cudaStream_t s) {
-  return launch_pdl(balance_fwd_kernel<VEC, NV>, dim3(a.S * a.nbs), dim3(kThreads), 0, s, 1, a);
-}
-template <bool VEC, int NV>
-cudaError_t launch_bwd(const BalArgs &a, bool add, cudaStream_t s) {
-  return launch_pdl(add ? balance_bwd_kernel<VEC, NV, true> : balance_bwd_kernel<VEC, NV, false>, dim3(a.S * a.nbs),
+  const bool solo = a.S * a.nbs == 1;
+  return launch_pdl(solo ? balance_fwd_kernel<W, NV, true> : balance_fwd_kernel<W, NV, false>, dim3(a.S * a.nbs),
                     dim3(kThreads), 0, s, 1, a);
 }
-// Values per lane: float4s where rows are whole ones, else single columns.
-template <class Vec4, class Vec8, class S1, class S2, class S4, class S8>
-cudaError_t by_width(int E, Vec4 &&v4, Vec8 &&v8, S1 &&s1, S2 &&s2, S4 &&s4, S8 &&s8) {
-  if (E % 4 == 0) return E <= 128 ? v4() : v8();
-  return E <= 32 ? s1() : E <= 64 ? s2() : E <= 128 ? s4() : s8();
+template <int W, int NV>
+cudaError_t launch_bwd(const BalArgs &a, bool add, cudaStream_t s) {
+  return launch_pdl(add ? balance_bwd_kernel<W, NV, true> : balance_bwd_kernel<W, NV, false>, dim3(a.S * a.nbs),
+                    dim3(kThreads), 0, s, 1, a);
+}
+template <int MOST, class F>
+cudaError_t by_width(int E, F &&f) {
+  const int nv = values_per_lane(E, MOST);
+  auto narrow = [&](auto w) {
+    if (nv == 8) return f(w, std::integral_constant<int, 8>{});
+    if (nv == 4) return f(w, std::integral_constant<int, 4>{});
+    return f(w, std::integral_constant<int, 2>{});
+  };
+  if (E % 4 == 0) {
+    if constexpr (MOST == 16)
+      if (nv == 16) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 16>{});
+    if (nv == 8) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 8>{});
+    return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 4>{});
+  }
+  if (E % 2 == 0) return narrow(std::integral_constant<int, 2>{});
+  if (nv == 1) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
+  return narrow(std::integral_constant<int, 1>{});
 }
 
 }  // namespace
@@ -487,7 +542,7 @@ moe_status moe_balance_forward(const moe_balance_config *cfg, const float *logit
   MOE_TRY(device_info(&di));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t *sc = static_cast<uint8_t *>(scratch);
-  BalArgs a = bal_args(cfg);
+  BalArgs a = bal_args(cfg, kMaxBlocks, kFwdValues, true);
   a.logits = logits;
   a.topk_idx = topk_idx;
   a.mask = mask;
@@ -504,11 +559,11 @@ moe_status moe_balance_forward(const moe_balance_config *cfg, const float *logit
   a.status = reinterpret_cast<int32_t *>(sc);
   // with no tokens the blocks find empty sequences and write zeros
   MOE_TRY(timed("balance_forward", s, [&] {
-    return by_width(
-        a.E, [&] { return launch_fwd<true, 4>(a, s); }, [&] { return launch_fwd<true, 8>(a, s); },
-        [&] { return launch_fwd<false, 1>(a, s); }, [&] { return launch_fwd<false, 2>(a, s); },
-        [&] { return launch_fwd<false, 4>(a, s); }, [&] { return launch_fwd<false, 8>(a, s); });
+    return by_width<kFwdValues>(a.E, [&](auto w, auto nv) {
+      return launch_fwd<decltype(w)::value, decltype(nv)::value>(a, s);
+    });
   }));
+  if (a.S * a.nbs == 1) return MOE_OK;
   return timed("balance_finish", s, [&] {
     return launch_pdl(balance_finish_kernel, dim3(a.S), dim3(kFinThreads), 0, s, 1, a);
   });
@@ -524,7 +579,7 @@ moe_status moe_balance_backward(const moe_balance_config *cfg, const float *logi
   MOE_TRY(device_info(&di));
   if (cfg->T == 0) return MOE_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  BalArgs a = bal_args(cfg);
+  BalArgs a = bal_args(cfg, di.sms * kBwdBlocksPerSm, kBwdValues, false);
   a.logits = logits;
   a.counts = const_cast<int32_t *>(counts);
   a.tokens = const_cast<int32_t *>(tokens);
@@ -534,10 +589,9 @@ moe_status moe_balance_backward(const moe_balance_config *cfg, const float *logi
   a.d_logits = d_logits;
   const bool add = accumulate != 0;
   return timed("balance_backward", s, [&] {
-    return by_width(
-        a.E, [&] { return launch_bwd<true, 4>(a, add, s); }, [&] { return launch_bwd<true, 8>(a, add, s); },
-        [&] { return launch_bwd<false, 1>(a, add, s); }, [&] { return launch_bwd<false, 2>(a, add, s); },
-        [&] { return launch_bwd<false, 4>(a, add, s); }, [&] { return launch_bwd<false, 8>(a, add, s); });
+    return by_width<kBwdValues>(a.E, [&](auto w, auto nv) {
+      return launch_bwd<decltype(w)::value, decltype(nv)::value>(a, add, s);
+    });
   });
 }
 
