@@ -15,9 +15,17 @@
 // entries (about 1 / sqrt(n m) at first) clear of fp16's subnormals.  a I is part
 // of P, so the update is one plain product.
 //
+// Steps in pairs: S, P and everything made of them commute, so with S the second
+// step's S is P S P, and both steps are one product with X by P' P.  A call of five
+// steps makes three passes over X instead of five.  What the pair's products round
+// stays as small beside a I as what a step rounds; longer runs were less exact
+// (three steps at once: 1.4 times the bf16 rounding against 1.25).
+//
 // No transposes: the tensor core reads either operand with its reduction axis
-// contiguous or strided (K-major or MN-major boxes), S and P are symmetric, and
-// only S's and P's upper tiles are computed (the lower ones are stored mirrored).
+// contiguous or strided (K-major or MN-major boxes).  S and P are symmetric: only
+// their tiles on and above the diagonal are computed and stored, and where a
+// product needs a tile below it, it loads the stored one with the axes exchanged
+// (the majorness of an operand is chosen for every 64 of the reduction).
 //
 // The products run on CTA pairs (tcgen05 cta_group::2, 256 x 256 tiles, fp32
 // accumulators double-buffered in TMEM), persistent over all matrices' tiles:
@@ -29,6 +37,8 @@
 // its copies and MMAs, frees TMEM and returns.
 #include <cuda.h>
 #include <cuda_fp16.h>
+
+#include <algorithm>
 
 #include "abi.h"
 #include "common.cuh"
@@ -197,8 +207,12 @@ __global__ void __launch_bounds__(kPrepThreads) ortho_scale_kernel(const PrepArg
 
 // ---------------------------------------------------------------- products
 
-constexpr int BM = 128;               // rows per CTA of a 256-row tile
-constexpr int BN = 256;               // tile columns; 128 of B per CTA
+// CG CTAs work on a tile of 128 CG rows and columns: a pair (tcgen05 cta_group::2)
+// or one alone, each with 128 rows of A and 128 columns of B in its shared memory.
+// A tile of a pair takes half the operand bytes per operation; where a product has
+// too few tiles for the part, one of a single CTA takes half the time.
+constexpr int BM = 128;
+constexpr int tile_size(int cg) { return BM * cg; }
 constexpr int BK = 64;                // reduction elements per box: one 128-byte swizzle row
 constexpr int kHalf = 128 * BK * 2;   // one operand's box (or two 64 x 64 boxes) per CTA: 16 KB
 constexpr int kBox = 64 * 64 * 2;
@@ -207,7 +221,6 @@ constexpr int kStageBytes = 4 * kHalf;  // two K blocks: [A k0 | A k1 | B k0 | B
 constexpr int kEpiWarps = 8;
 constexpr int kGemmThreads = 64 + 32 * kEpiWarps;
 constexpr int kTileBytes = 32 * 32 * 2;  // an epilogue warp's staging tile
-constexpr uint32_t kTmemCols = 2 * BN;
 constexpr int kEpiOff = kStages * kStageBytes + 256;
 constexpr int kGemmSmem = kEpiOff + kEpiWarps * kTileBytes + 1024 /*align*/;
 static_assert(kGemmSmem <= 227 * 1024, "shared memory budget");
@@ -221,7 +234,7 @@ enum Product : int {
 
 struct ProductArgs {
   int batch, M, N, K;
-  int nm, nn;             // tiles of 256 rows, of 256 columns
+  int nm, nn;             // tiles along the rows, along the columns
   int per;                // tiles per matrix (symmetric: mt <= nt)
   float a, b, c;          // kSquare; c also the factor of the other products
   const uint16_t *s;      // kSquare: S
@@ -233,25 +246,23 @@ struct ProductArgs {
 
 struct TileAt {
   int b, m0, n0;
-  bool mirror;  // symmetric, off the diagonal: stored transposed as well
 };
 
-template <int KIND>
+template <int KIND, int CG>
 __device__ __forceinline__ TileAt tile_of(int tile, const ProductArgs &p) {
+  constexpr int TS = tile_size(CG);
   TileAt t;
   t.b = tile / p.per;
   int r = tile - t.b * p.per;
   if constexpr (KIND == kGram || KIND == kSquare) {
     int nt = 0;
     while (r > nt) r -= ++nt;
-    t.m0 = r * 2 * BM;
-    t.n0 = nt * BN;
-    t.mirror = r != nt;
+    t.m0 = r * TS;
+    t.n0 = nt * TS;
   } else {
     const int mt = r / p.nn;
-    t.m0 = mt * 2 * BM;
-    t.n0 = (r - mt * p.nn) * BN;
-    t.mirror = false;
+    t.m0 = mt * TS;
+    t.n0 = (r - mt * p.nn) * TS;
   }
   return t;
 }
@@ -260,6 +271,11 @@ __device__ __forceinline__ TileAt tile_of(int tile, const ProductArgs &p) {
 // rows written by lanes and pieces read by rows free of bank conflicts.
 __device__ __forceinline__ uint32_t swz(int r, int q) {
   return static_cast<uint32_t>(r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
+}
+
+// The same for rows of 128 bytes as the tensor core reads them (128B swizzle).
+__device__ __forceinline__ uint32_t swz128(int r, int q) {
+  return static_cast<uint32_t>(r * 128 + ((q ^ (r & 7)) << 4));
 }
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
@@ -281,51 +297,47 @@ __device__ __forceinline__ void tile_to_rows(const uint8_t *tile, uint16_t *g0, 
   }
 }
 
-constexpr int kChunks = BN / 64;  // 32-column chunks of a warp's half of the columns
+constexpr int chunks_of(int cg) { return tile_size(cg) / 64; }  // 32-column chunks of a warp's half of the columns
 
-// kSquare: S under the warp's 32 rows and half of the tile's columns, in the
-// order its coalesced loads bring it.
+// kSquare: S under the warp's 32 rows and half of the tile's columns, a row per
+// lane as the accumulator comes: its 64-byte pieces are whole sectors.
+template <int CG>
 struct SChunks {
+  static constexpr int kChunks = chunks_of(CG), TS = tile_size(CG);
   uint4 v[kChunks][4];
   __device__ __forceinline__ void load(const TileAt &t, int row0, int part, const ProductArgs &p) {
-    const int lane = threadIdx.x & 31, nrows = min(32, p.M - row0);
-    const uint16_t *s = p.s + t.b * p.stride;
+    const int lane = threadIdx.x & 31;
+    const uint16_t *s = p.s + t.b * p.stride + (row0 + lane) * static_cast<int64_t>(p.ld) + t.n0 + part * (TS / 2);
 #pragma unroll
     for (int j = 0; j < kChunks; ++j) {
-      const int c0 = t.n0 + part * (BN / 2) + 32 * j;
+      const bool in = row0 + lane < p.M && t.n0 + part * (TS / 2) + 32 * j < p.N;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 8 * i + (lane >> 2);
-        v[j][i] = r < nrows && c0 < p.N ? *reinterpret_cast<const uint4 *>(
-                                              s + (row0 + r) * static_cast<int64_t>(p.ld) + c0 + (lane & 3) * 8)
-                                        : make_uint4(0, 0, 0, 0);
-      }
+      for (int i = 0; i < 4; ++i)
+        v[j][i] = in ? *reinterpret_cast<const uint4 *>(s + 32 * j + 8 * i) : make_uint4(0, 0, 0, 0);
     }
   }
 };
 
 // One warp's 32 rows of half a tile's columns.
-template <int KIND>
+template <int KIND, int CG>
 __device__ __forceinline__ void epilogue(const TileAt &t, uint32_t tb, int row0, int part, const ProductArgs &p,
-                                         uint8_t *tile, const SChunks &sc) {
+                                         uint8_t *tile, const SChunks<CG> &sc) {
+  constexpr int kChunks = chunks_of(CG), TS = tile_size(CG);
   const int lane = threadIdx.x & 31;
   const int nrows = min(32, p.M - row0);
   uint16_t *out = p.out + t.b * p.stride;
 #pragma unroll KIND == kSquare ? kChunks : 1
   for (int j = 0; j < kChunks; ++j) {
-    const int cc = part * (BN / 2) + 32 * j, c0 = t.n0 + cc;
+    const int cc = part * (TS / 2) + 32 * j, c0 = t.n0 + cc;
     if (c0 >= p.N || nrows <= 0) break;
     uint32_t acc[32];
     tmem_ld32(tb + cc, acc);
     float v[32];
     if constexpr (KIND == kSquare) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(tile + swz(8 * i + (lane >> 2), lane & 3)) = sc.v[j][i];
-      __syncwarp();
       tmem_ld_wait();
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(tile + swz(lane, q));
+        const uint4 w = sc.v[j][q];
         const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
@@ -342,7 +354,6 @@ __device__ __forceinline__ void epilogue(const TileAt &t, uint32_t tb, int row0,
         for (int e = 0; e < 32; ++e)
           if (e == lane) v[e] += p.a;
       }
-      __syncwarp();
     } else {
       tmem_ld_wait();
 #pragma unroll
@@ -375,37 +386,50 @@ __device__ __forceinline__ void epilogue(const TileAt &t, uint32_t tb, int row0,
       __syncwarp();
       tile_to_rows(tile, out + row0 * static_cast<int64_t>(p.ld) + c0, p.ld, nrows, 32);
       __syncwarp();
-      if constexpr (KIND == kGram || KIND == kSquare) {
-        if (t.mirror) {  // column e of the chunk is row c0 + e of the transpose
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            *reinterpret_cast<uint16_t *>(tile + swz(e, lane >> 3) + (lane & 7) * 2) =
-                __half_as_ushort(__float2half_rn(v[e]));
-          __syncwarp();
-          tile_to_rows(tile, out + c0 * static_cast<int64_t>(p.ld) + row0, p.ld, min(32, p.N - c0), 32);
-          __syncwarp();
-        }
-      }
     }
   }
 }
 
+// How one operand is read.  kK: its reduction axis is contiguous; kMN: its other
+// axis is; kSym: it is symmetric and stored on and above the diagonal of its
+// tiles, so contiguous from the diagonal tile on, the other way before it.
+enum Major : int { kK = 0, kMN = 1, kSym = 2 };
+template <int MAJOR>
+__device__ __forceinline__ bool mn_major(int k0, int tile0) {
+  return MAJOR == kMN || (MAJOR == kSym && k0 < tile0);
+}
+
 // One K block of one operand into this CTA's half of the stage: 128 rows x 64 of
-// K (K-major), or 64 of K x 128 columns in two boxes (MN-major).
-template <int MN>
-__device__ __forceinline__ void load_operand(uint8_t *dst, const CUtensorMap *map, uint32_t bar, int k0, int r0, int b) {
-  if constexpr (MN) {
-    tma_load_3d_pair(dst, map, bar, r0, k0, b);
-    tma_load_3d_pair(dst + kBox, map, bar, r0 + 64, k0, b);
+// K (one box), or 64 of K x 128 columns in two boxes.
+template <int MAJOR, int CG>
+__device__ __forceinline__ void load_operand(uint8_t *dst, const CUtensorMap *map, const CUtensorMap *map_mn,
+                                             uint64_t *bar, uint32_t bar0, int k0, int tile0, int r0, int b) {
+  auto load = [&](uint8_t *to, const CUtensorMap *m, int x, int y) {
+    if constexpr (CG == 2)
+      tma_load_3d_pair(to, m, bar0, x, y, b);
+    else
+      tma_load_3d(to, m, bar, x, y, b);
+  };
+  if (mn_major<MAJOR>(k0, tile0)) {
+    load(dst, map_mn, r0, k0);
+    load(dst + kBox, map_mn, r0 + 64, k0);
   } else {
-    tma_load_3d_pair(dst, map, bar, k0, r0, b);
+    load(dst, map, k0, r0);
   }
 }
 
-template <int KIND, int AMN, int BMN>
+// Descriptor of the j-th 16 of K of a block at shared address s.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t s, int j, bool mn) {
+  return mn ? smem_desc_sw128(s + j * 2048, kBox, 1024) : smem_desc_sw128(s + j * 32, 16, 1024);
+}
+
+template <int KIND, int AM, int BMAJ, int CG>
 __global__ void __launch_bounds__(kGemmThreads, 1)
-    ortho_product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+    ortho_product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmAmn,
+                         const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmBmn,
                          const ProductArgs p) {
+  constexpr int TS = tile_size(CG);
+  constexpr uint32_t kTmemCols = 2 * TS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem =
       reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -419,8 +443,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint8_t *epi_tiles = smem + kEpiOff;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = static_cast<int>(cluster_ctarank());
-  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int rank = CG == 2 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int group = blockIdx.x / CG, ngroups = gridDim.x / CG;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -428,21 +452,26 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 2 * kEpiWarps);
+      mbar_init(&tempty[b], CG * kEpiWarps);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tmA);
-    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(AM == kMN ? &tmAmn : &tmA);
+    tma_prefetch_desc(BMAJ == kMN ? &tmBmn : &tmB);
   }
-  if (warp == 1) tmem_alloc_pair(tmem_slot, kTmemCols);
+  if (warp == 1) {
+    if constexpr (CG == 2)
+      tmem_alloc_pair(tmem_slot, kTmemCols);
+    else
+      tmem_alloc(tmem_slot, kTmemCols);
+  }
   griddep_wait();  // the set-up above overlaps the previous kernel's end; its outputs are read below
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // both CTAs' barriers initialised before any remote arrival
+  if constexpr (CG == 2) cluster_sync();  // both CTAs' barriers initialised before any remote arrival
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int total = p.batch * p.per;
@@ -450,25 +479,27 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      const uint32_t full0 = peer_smem_addr(&full[0], 0);
+      const uint32_t full0 = CG == 2 ? peer_smem_addr(&full[0], 0) : 0;
       int stage = 0;
       uint32_t phase = 0, armed = 0, arm_par = 0;
       bool ok = true;
-      for (int tile = pair; tile < total && ok; tile += npairs) {
-        const TileAt t = tile_of<KIND>(tile, p);
+      for (int tile = group; tile < total && ok; tile += ngroups) {
+        const TileAt t = tile_of<KIND, CG>(tile, p);
         for (int ks = 0; ks < nstage; ++ks) {
           if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) {
             ok = false;
             break;
           }
           uint8_t *sa = smem + stage * kStageBytes;
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);  // both CTAs' bytes
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], CG * kStageBytes);  // the group's bytes
           // a K block past the end is zero fill, and no MMA reads it
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int k0 = (ks * 2 + h) * BK;
-            load_operand<AMN>(sa + h * kHalf, &tmA, full0 + 8u * stage, k0, t.m0 + BM * rank, t.b);
-            load_operand<BMN>(sa + (2 + h) * kHalf, &tmB, full0 + 8u * stage, k0, t.n0 + (BN / 2) * rank, t.b);
+            load_operand<AM, CG>(sa + h * kHalf, &tmA, &tmAmn, &full[stage], full0 + 8u * stage, k0, t.m0,
+                                 t.m0 + BM * rank, t.b);
+            load_operand<BMAJ, CG>(sa + (2 + h) * kHalf, &tmB, &tmBmn, &full[stage], full0 + 8u * stage, k0, t.n0,
+                                   t.n0 + BM * rank, t.b);
           }
           armed |= 1u << stage;
           arm_par = (arm_par & ~(1u << stage)) | (phase << stage);
@@ -490,14 +521,27 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
+      auto mma = [](uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+        if constexpr (CG == 2)
+          tc_mma_f16_pair(d, a, b, idesc, acc);
+        else
+          tc_mma_f16_one(d, a, b, idesc, acc);
+      };
+      auto commit = [](uint64_t *bar) {
+        if constexpr (CG == 2)
+          tc_commit_pair(bar);
+        else
+          tc_commit(bar);
+      };
       int stage = 0, it = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int tile = pair; tile < total && ok; tile += npairs, ++it) {
+      for (int tile = group; tile < total && ok; tile += ngroups, ++it) {
+        const TileAt t = tile_of<KIND, CG>(tile, p);
         const int buf = it & 1;
         if (!mbar_wait(&tempty[buf], ((it >> 1) & 1) ^ 1, abort_flag)) break;
         tc_fence_after();
-        const uint32_t d = tmem_base + buf * BN;
+        const uint32_t d = tmem_base + buf * TS;
         for (int ks = 0; ks < nstage; ++ks) {
           if (!mbar_wait(&full[stage], phase, abort_flag)) {
             ok = false;
@@ -505,30 +549,30 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           }
           tc_fence_after();
           const uint32_t ab = smem_addr(smem + stage * kStageBytes), bb = ab + 2 * kHalf;
-          const int nk16 = (BK / 16) * min(2, nkb - ks * 2);
+          const int nblk = min(2, nkb - ks * 2);  // K blocks inside K
 #pragma unroll
-          for (int k16 = 0; k16 < 2 * (BK / 16); ++k16) {
-            if (k16 < nk16) {
-              const int h = k16 / (BK / 16), j = k16 % (BK / 16);
-              const uint32_t ao = ab + h * kHalf, bo = bb + h * kHalf;
-              const uint64_t ad =
-                  AMN ? smem_desc_sw128(ao + j * 2048, kBox, 1024) : smem_desc_sw128(ao + j * 32, 16, 1024);
-              const uint64_t bd =
-                  BMN ? smem_desc_sw128(bo + j * 2048, kBox, 1024) : smem_desc_sw128(bo + j * 32, 16, 1024);
-              tc_mma_f16_pair(d, ad, bd, idesc_f16(2 * BM, BN, AMN, BMN), (ks | k16) != 0 ? 1u : 0u);
+          for (int h = 0; h < 2; ++h) {
+            if (h < nblk) {
+              const int k0 = (ks * 2 + h) * BK;
+              const bool amn = mn_major<AM>(k0, t.m0), bmn = mn_major<BMAJ>(k0, t.n0);
+              const uint32_t idesc = idesc_f16(TS, TS, amn, bmn);
+#pragma unroll
+              for (int j = 0; j < BK / 16; ++j)
+                mma(d, operand_desc(ab + h * kHalf, j, amn), operand_desc(bb + h * kHalf, j, bmn), idesc,
+                    (ks | h | j) != 0 ? 1u : 0u);
             }
           }
-          tc_commit_pair(&empty[stage]);
+          commit(&empty[stage]);
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1;
           }
         }
         if (!ok) break;
-        tc_commit_pair(&tfull[buf]);
+        commit(&tfull[buf]);
       }
       if (*abort_flag) {  // wait for the pair's MMAs before TMEM is freed
-        tc_commit_pair(drain);
+        commit(drain);
         for (int i = 0; i < (1 << 22) && !mbar_try_wait(drain, 0); ++i) {
         }
       }
@@ -537,31 +581,383 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   } else {
     const int q = warp & 3;               // TMEM lane quarter
     const int part = (warp - 2) >> 2;     // column half
-    const uint32_t tempty0 = peer_smem_addr(&tempty[0], 0), tempty1 = peer_smem_addr(&tempty[1], 0);
+    const uint32_t tempty0 = CG == 2 ? peer_smem_addr(&tempty[0], 0) : 0;
     uint8_t *stile = epi_tiles + (warp - 2) * kTileBytes;
     int it = 0;
-    for (int tile = pair; tile < total; tile += npairs, ++it) {
-      const TileAt t = tile_of<KIND>(tile, p);
+    for (int tile = group; tile < total; tile += ngroups, ++it) {
+      const TileAt t = tile_of<KIND, CG>(tile, p);
       const int buf = it & 1, row0 = t.m0 + BM * rank + q * 32;
-      SChunks sc;
+      SChunks<CG> sc;
       if constexpr (KIND == kSquare) sc.load(t, row0, part, p);  // while the product runs
       if (!wait_lane0(&tfull[buf], (it >> 1) & 1, abort_flag)) break;
       __syncwarp();
       tc_fence_after();
-      epilogue<KIND>(t, tmem_base + buf * BN + (static_cast<uint32_t>(q * 32) << 16), row0, part, p, stile, sc);
+      epilogue<KIND, CG>(t, tmem_base + buf * TS + (static_cast<uint32_t>(q * 32) << 16), row0, part, p, stile, sc);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(buf ? tempty1 : tempty0);
+      if (lane == 0) {
+        if constexpr (CG == 2)
+          mbar_arrive_cluster(tempty0 + 8u * buf);
+        else
+          mbar_arrive(&tempty[buf]);
+      }
     }
   }
 
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0 && *abort_flag) flag_status(p.status, kDevWaitTimeout);
-  cluster_sync();  // the pair is done with each other's barriers and TMEM
+  if constexpr (CG == 2) cluster_sync();  // the pair is done with each other's barriers and TMEM
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem_base, kTmemCols);
+    if constexpr (CG == 2)
+      tmem_dealloc_pair(tmem_base, kTmemCols);
+    else
+      tmem_dealloc(tmem_base, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------- small matrices
+//
+// n <= 128: a cluster of CTAs keeps a whole matrix in shared memory from the first
+// read to the last write, one launch for the call.  Each CTA holds all n rows (of X,
+// or of its transpose when R > C) of up to 256 of the m columns, in blocks of 64
+// columns (128 rows of 128 bytes, 128B-swizzled).  Such a block is a K-major operand
+// of the Gram product and, unchanged, an MN-major one of the update.  The Gram
+// product's partial sums meet through distributed shared memory, each CTA adding a
+// share of the rows in the order of the CTAs; S, P and the update are then each
+// CTA's own.  What bounds it is the chain of dependent steps: three products, three
+// passes TMEM -> registers -> shared memory and two cluster barriers per step.
+
+constexpr int kSmallN = 128, kSlab = 256;     // rows, and columns per CTA at most
+constexpr int kSmallCluster = 16;             // CTAs per matrix at most
+constexpr int kSmallThreads = 256;
+constexpr int kBlk = 128 * 128;               // bytes of a block
+constexpr int kPartStride = kSmallN + 4;      // floats of a row of partial sums
+constexpr int kSmallS = (kSlab / 64) * kBlk;  // S, then P: two blocks
+constexpr int kSmallPart = kSmallS + 2 * kBlk;
+constexpr int small_smem(int cluster) {
+  return kSmallPart + (cluster > 1 ? kSmallN * kPartStride * 4 : 0) + 1024 /*align*/;
+}
+static_assert(small_smem(2) <= 227 * 1024, "shared memory budget");
+
+struct SmallArgs {
+  const void *g;
+  float *mom;
+  uint16_t *out;
+  int R, C, n, m;
+  int cluster, nblk;  // CTAs per matrix, blocks of 64 columns per CTA
+  bool tall, vec;     // R > C; rows of g are whole groups of eight
+  float beta, eps, scale;
+  bool nesterov;
+  int steps;
+  int32_t *status;
+  float coefs[3 * kMaxSteps];
+};
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster_u32x2(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// Byte of element (row, column c) in blocks of 64 columns.
+__device__ __forceinline__ uint32_t blk_byte(int row, int c) {
+  return static_cast<uint32_t>((c >> 6) * kBlk) + swz128(row, (c >> 3) & 7) + (c & 7) * 2;
+}
+
+template <class El>
+__global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const __grid_constant__ SmallArgs p) {
+  griddep_wait();  // the previous kernel in the stream has completed
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t s_bar;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  __shared__ float s_red[kSmallThreads / 32], s_sq;
+  uint8_t *smem =
+      reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t *xs = smem, *ss = smem + kSmallS;
+  float *part = reinterpret_cast<float *>(smem + kSmallPart);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = p.cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int b = blockIdx.x / p.cluster;
+  const int c0 = rank * p.nblk * 64, cols = max(0, min(p.nblk * 64, p.m - c0));  // this CTA's columns
+  const int64_t numel = static_cast<int64_t>(p.R) * p.C;
+  const El *g = static_cast<const El *>(p.g) + b * numel;
+  float *mom = p.mom ? p.mom + b * numel : nullptr;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&s_bar, 1);
+    s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) tmem_alloc(&s_tmem, kSlab);
+  // rows past n and columns past m stay zero
+  for (int i = threadIdx.x; i < kSmallPart / 16; i += kSmallThreads)
+    reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0, 0, 0, 0);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+
+  // this CTA's elements in memory order: rows of `width` elements, `stride` apart
+  const int rows = p.tall ? cols : p.n, width = p.tall ? p.n : cols;
+  const int64_t base = p.tall ? static_cast<int64_t>(c0) * p.C : c0;
+  // pass 0: advance the momentum and sum the squares; pass 1: store the scaled elements
+  auto each = [&](int pass, float f0) {
+    float acc = 0.f;
+    const int unit = p.vec ? 8 : 1, per = width / unit, total = rows * per;
+    for (int i0 = threadIdx.x; i0 < total; i0 += kSmallThreads * 4) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * kSmallThreads;
+        if (i >= total) break;
+        const int r = i / per, c = (i - r * per) * unit;
+        const int64_t at = base + static_cast<int64_t>(r) * p.C + c;
+        float f[8], mm[8];
+        if (p.vec) {
+          load_el<El, true>(g + at, f);
+          if (mom) load_el<float, true>(mom + at, mm);
+        } else {
+          f[0] = to_f(g[at]);
+          if (mom) mm[0] = mom[at];
+        }
+        if (mom) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (k < unit) {
+              if (pass == 0) mom[at + k] = mm[k] = fmaf(p.beta, mm[k], f[k]);
+              f[k] = update_of(f[k], mm[k], p.beta, p.nesterov);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < unit) {
+            if (pass == 0)
+              acc = fmaf(f[k], f[k], acc);
+            else
+              *reinterpret_cast<uint16_t *>(xs + (p.tall ? blk_byte(c + k, r) : blk_byte(r, c + k))) =
+                  __half_as_ushort(__float2half_rn(f[k] * f0));
+          }
+      }
+    }
+    return acc;
+  };
+  float sq = warp_sum(each(0, 0.f));
+  if (lane == 0) s_red[warp] = sq;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kSmallThreads / 32; ++w) sq += s_red[w];
+    s_sq = sq;
+  }
+  __syncthreads();
+  if (p.cluster > 1) {
+    cluster_sync();
+    sq = 0.f;
+    for (int r = 0; r < p.cluster; ++r) sq += ld_cluster_f32(peer_smem_addr(&s_sq, r));
+  } else {
+    sq = s_sq;
+  }
+  const bool fine = isfinite(sq);
+  if (!fine && rank == 0 && threadIdx.x == 0) flag_status(p.status, kDevNonfiniteUpdate);
+  const float norm = fmaxf(sqrtf(sq), p.eps);
+  each(1, fine ? (norm > 0.f ? kSigma / norm : 0.f) : NAN);
+  fence_async();
+  __syncthreads();
+
+  // a product's MMAs by one thread, and the wait for them by all (a wait that runs
+  // out is flagged; the kernel goes on, so that no barrier misses a thread)
+  uint32_t phase = 0;
+  auto product = [&](auto &&issue) {
+    if (threadIdx.x == 0) {
+      tc_fence_after();
+      issue();
+      tc_commit(&s_bar);
+    }
+    if (!mbar_wait(&s_bar, phase, &s_abort) && lane == 0) flag_status(p.status, kDevWaitTimeout);
+    phase ^= 1;
+    __syncwarp();
+    tc_fence_after();
+  };
+  const int kn = p.n <= 64 ? 1 : 2;  // blocks of 64 that hold n
+  const uint32_t xa = smem_addr(xs), sa = smem_addr(ss);
+  const int q = warp & 3, half = warp >> 2, row = q * 32 + lane;
+  const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16);
+
+  for (int step = 0; step < p.steps; ++step) {
+    const float ca = p.coefs[3 * step], cb = p.coefs[3 * step + 1], cc = p.coefs[3 * step + 2];
+    // S = X X^T / sigma^2
+    product([&] {
+      for (int k = 0; k < p.nblk; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t d = smem_desc_sw128(xa + k * kBlk + j * 32, 16, 1024);
+          tc_mma_f16_one(tmem, d, d, idesc_f16(128, 128, 0, 0), (k | j) != 0 ? 1u : 0u);
+        }
+    });
+    constexpr float inv = 1.f / (kSigma * kSigma);
+    if (half < kn) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t acc[32];
+        tmem_ld32(tq + half * 64 + h * 32, acc);
+        tmem_ld_wait();
+        if (p.cluster > 1) {
+          float4 *dst = reinterpret_cast<float4 *>(part + row * kPartStride + half * 64 + h * 32);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            dst[e] = make_float4(__uint_as_float(acc[4 * e]), __uint_as_float(acc[4 * e + 1]),
+                                 __uint_as_float(acc[4 * e + 2]), __uint_as_float(acc[4 * e + 3]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = pack_half2(__uint_as_float(acc[8 * e + 2 * k]) * inv, __uint_as_float(acc[8 * e + 2 * k + 1]) * inv);
+            *reinterpret_cast<uint4 *>(ss + half * kBlk + swz128(row, h * 4 + e)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+    }
+    tc_fence_before();
+    if (p.cluster > 1) {
+      cluster_sync();  // every CTA's partial sums are there
+      // this CTA's share of the rows: 128 / cluster, four columns per thread
+      const int share = kSmallN / p.cluster, groups = kn * 16;
+      for (int i = threadIdx.x; i < share * groups; i += kSmallThreads) {
+        const int r = rank * share + i / groups, c = i % groups * 4;
+        float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int o0 = 0; o0 < p.cluster; o0 += 8) {  // eight CTAs' sums in flight
+          float4 v[8];
+#pragma unroll
+          for (int o = 0; o < 8; ++o)
+            v[o] = o0 + o < p.cluster ? ld_cluster_f32x4(peer_smem_addr(part + r * kPartStride + c, o0 + o))
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int o = 0; o < 8; ++o) t.x += v[o].x, t.y += v[o].y, t.z += v[o].z, t.w += v[o].w;
+        }
+        const uint32_t lo = pack_half2(t.x * inv, t.y * inv), hi = pack_half2(t.z * inv, t.w * inv);
+        for (int o = 0; o < p.cluster; ++o) st_cluster_u32x2(peer_smem_addr(ss + blk_byte(r, c), o), lo, hi);
+      }
+      fence_async();
+      cluster_sync();
+    }
+    fence_async();
+    __syncthreads();
+    // P = a I + b S + c S S, in S's place
+    product([&] {
+      for (int k = 0; k < kn; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t d = smem_desc_sw128(sa + k * kBlk + j * 32, 16, 1024);
+          tc_mma_f16_one(tmem, d, d, idesc_f16(128, 128, 0, 0), (k | j) != 0 ? 1u : 0u);
+        }
+    });
+    if (half < kn) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t acc[32];
+        tmem_ld32(tq + half * 64 + h * 32, acc);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint4 *at = reinterpret_cast<uint4 *>(ss + half * kBlk + swz128(row, h * 4 + e));
+          const uint4 sv = *at;
+          const uint32_t sw[4] = {sv.x, sv.y, sv.z, sv.w};
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            __half2 hh;
+            memcpy(&hh, &sw[k], 4);
+            const float2 f = __half22float2(hh);
+            const int c = half * 64 + h * 32 + 8 * e + 2 * k;
+            const float v0 = fmaf(cc, __uint_as_float(acc[8 * e + 2 * k]), cb * f.x) + (c == row ? ca : 0.f);
+            const float v1 = fmaf(cc, __uint_as_float(acc[8 * e + 2 * k + 1]), cb * f.y) + (c + 1 == row ? ca : 0.f);
+            w[k] = pack_half2(v0, v1);
+          }
+          *at = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+    tc_fence_before();
+    fence_async();
+    __syncthreads();
+    // X <- P X
+    product([&] {
+      for (int k = 0; k < kn; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          tc_mma_f16_one(tmem, smem_desc_sw128(sa + k * kBlk + j * 32, 16, 1024),
+                         smem_desc_sw128(xa + (k * 64 + j * 16) * 128, kBlk, 1024),
+                         idesc_f16(128, 64 * p.nblk, 0, 1), (k | j) != 0 ? 1u : 0u);
+    });
+    const bool last = step + 1 == p.steps;
+    for (int k = half; k < p.nblk; k += 2) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t acc[32];
+        tmem_ld32(tq + k * 64 + h * 32, acc);
+        tmem_ld_wait();
+        if (!last) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[i] = pack_half2(__uint_as_float(acc[8 * e + 2 * i]), __uint_as_float(acc[8 * e + 2 * i + 1]));
+            *reinterpret_cast<uint4 *>(xs + k * kBlk + swz128(row, h * 4 + e)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else if (row < p.n) {
+          const float f = p.scale / kSigma;
+          const int c = c0 + k * 64 + h * 32;  // column of X
+          uint16_t *out = p.out + b * numel;
+          if (p.tall) {  // row c + e of out, column `row`: contiguous over the lanes
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (c + e < p.m)
+                out[static_cast<int64_t>(c + e) * p.C + row] =
+                    __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(acc[e]) * f));
+          } else {
+            uint16_t *o = out + static_cast<int64_t>(row) * p.C + c;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                w[i] = pack_bf16x2(__uint_as_float(acc[8 * e + 2 * i]) * f, __uint_as_float(acc[8 * e + 2 * i + 1]) * f);
+              if (p.vec) {
+                if (c + 8 * e < p.m) *reinterpret_cast<uint4 *>(o + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  if (c + 8 * e + i < p.m) o[8 * e + i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+              }
+            }
+          }
+        }
+      }
+    }
+    tc_fence_before();
+    fence_async();
+    __syncthreads();
+  }
+  if (p.cluster > 1) cluster_sync();  // no CTA leaves while another may read it
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kSlab);
   }
 }
 
@@ -585,21 +981,26 @@ bool map3(CUtensorMap *m, const void *ptr, int inner, int rows, int batch, int l
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int KIND, int AMN, int BMN>
-cudaError_t launch_product(const CUtensorMap &a, const CUtensorMap &b, ProductArgs p, int sms, cudaStream_t s) {
-  static DeviceOnce once;  // the shared-memory opt-in, and how many CTA pairs fit at once
-  auto kernel = ortho_product_kernel<KIND, AMN, BMN>;
-  int pairs = 0;
-  cudaError_t e = once.get(
+// A matrix's maps: boxes of 128 rows x 64 columns (K-major) and of 64 x 64 (MN-major).
+struct Maps {
+  CUtensorMap k, mn;
+};
+
+template <int KIND, int AM, int BMAJ, int CG>
+cudaError_t launch_groups(const Maps &a, const Maps &b, ProductArgs p, int sms, cudaStream_t s) {
+  static DeviceOnce once;  // the shared-memory opt-in, and how many groups of CTAs fit at once
+  auto kernel = ortho_product_kernel<KIND, AM, BMAJ, CG>;
+  int groups = 0;
+  const cudaError_t e = once.get(
       [&](int *out) {
         cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
         if (r != cudaSuccess) return r;
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = 2;
+        attr.val.clusterDim.x = CG;
         attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
         cudaLaunchConfig_t q = {};
-        q.gridDim = dim3(sms & ~1);
+        q.gridDim = dim3(sms / CG * CG);
         q.blockDim = dim3(kGemmThreads);
         q.dynamicSmemBytes = kGemmSmem;
         q.attrs = &attr;
@@ -608,16 +1009,44 @@ cudaError_t launch_product(const CUtensorMap &a, const CUtensorMap &b, ProductAr
         r = cudaOccupancyMaxActiveClusters(&n, kernel, &q);
         if (r != cudaSuccess) return r;
         if (n < 1) return cudaErrorInvalidConfiguration;
-        *out = n < sms / 2 ? n : sms / 2;
+        *out = n < sms / CG ? n : sms / CG;
         return cudaSuccess;
       },
-      &pairs);
+      &groups);
   if (e != cudaSuccess) return e;
-  p.nm = (p.M + 2 * BM - 1) / (2 * BM);
-  p.nn = (p.N + BN - 1) / BN;
+  constexpr int TS = tile_size(CG);
+  p.nm = (p.M + TS - 1) / TS;
+  p.nn = (p.N + TS - 1) / TS;
   p.per = KIND == kGram || KIND == kSquare ? p.nn * (p.nn + 1) / 2 : p.nm * p.nn;
-  const int tiles = p.per * p.batch;
-  return launch_pdl(kernel, dim3(2 * (tiles < pairs ? tiles : pairs)), dim3(kGemmThreads), kGemmSmem, s, 2, a, b, p);
+  const int64_t tiles = static_cast<int64_t>(p.per) * p.batch;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(CG * (tiles < groups ? tiles : groups))), dim3(kGemmThreads),
+                    kGemmSmem, s, CG, a.k, a.mn, b.k, b.mn, p);
+}
+
+template <int KIND, int AM, int BMAJ>
+cudaError_t launch_product(const Maps &a, const Maps &b, const ProductArgs &p, bool pair, int sms, cudaStream_t s) {
+  return pair ? launch_groups<KIND, AM, BMAJ, 2>(a, b, p, sms, s) : launch_groups<KIND, AM, BMAJ, 1>(a, b, p, sms, s);
+}
+
+// Pairs of CTAs or single ones, by the rounds of tiles that a step's products take
+// on 152 SMs.  A round's length in units of 128 of the reduction, from timings: K + 4
+// for pairs, 0.8 K + 2 for single CTAs (half the MMA and epilogue work, but nearly
+// the same operand stream).  Both measured: 3 x 1000 x 333 144 us in pairs, 110 in
+// single CTAs; 100 x 256 x 256 183 and 131; 4 x 768 x 1536 188 and 157; but
+// 8 x 768 x 1536 216 and 244, 24 x 1024 x 1024 538 and 652, 128 x 2048 x 768 2.0 and
+// 2.4 ms.
+bool use_pairs(int batch, int R, int C) {
+  const int n = R < C ? R : C, m = R < C ? C : R;
+  double cost[2];
+  for (int cg = 1; cg <= 2; ++cg) {
+    const int ts = tile_size(cg), groups = 152 / cg;
+    auto tiles = [&](int x) { return static_cast<int64_t>((x + ts - 1) / ts); };
+    auto rounds = [&](int64_t per) { return static_cast<double>((per * batch + groups - 1) / groups); };
+    auto length = [&](int k) { return cg == 2 ? k / 128.0 + 4 : 0.8 * k / 128.0 + 2; };
+    const double sym = rounds(tiles(n) * (tiles(n) + 1) / 2), apply = rounds(tiles(R) * tiles(C));
+    cost[cg - 1] = sym * length(m) + (sym + apply) * length(n);
+  }
+  return cost[1] <= cost[0];
 }
 
 bool ortho_ok(const moe_ortho_config *c) {
@@ -627,19 +1056,43 @@ bool ortho_ok(const moe_ortho_config *c) {
   return c->dtype == MOE_DTYPE_BF16 || c->dtype == MOE_DTYPE_FP32;
 }
 
+// Whether clusters hold the matrices on chip.
+bool is_small(const moe_ortho_config *c) {
+  const int n = std::min(c->R, c->C), m = std::max(c->R, c->C), cluster = (m + kSlab - 1) / kSlab;
+  // up to two CTAs per matrix any number of matrices (608 x 128 x 256: 100 against 444
+  // us, 304 x 128 x 512: 222 against 305); more only while all matrices are on the part
+  // at once (38 x 128 x 1024: 110 against 125 us, but 76 of them 163 against 154)
+  return n <= kSmallN && (cluster <= 2 || (cluster <= kSmallCluster && c->batch * cluster <= 152));
+}
+
+// Steps in pairs, where X is long enough and there is enough to save.  A pair
+// replaces one Gram product (n^2 m) and one update (2 n^2 m) by three symmetric
+// products (n^3 each), which have launches of their own.  Measured against single
+// steps: 128 x 2048 x 768 2.01 against 2.33 ms, 24 x 1024 x 1536 668 against 680 us,
+// but 24 x 1024 x 1280 626 against 610, and where launches count, 3 x 1000 x 333
+// (1.3e9 operations less) 153 against 144; 5 x 500 x 2600 (1.6e10) 191 against 200.
+bool fuse_steps(int batch, int n, int m) {
+  const double saved = 6.0 * n * n * (m - n) * batch;
+  return 2 * m >= 3 * n && saved >= 1e10;
+}
+
 inline int pad64(int x) { return (x + 63) / 64 * 64; }
 
 struct OrthoLayout {
   int chunks, ldx, lds;
-  size_t part, x0, x1, s, p, total;
+  size_t part, x0, x1, n[3], total;
 };
 OrthoLayout ortho_layout(const moe_ortho_config *c) {
-  OrthoLayout L;
+  OrthoLayout L{};
   const size_t B = c->batch, n = c->R < c->C ? c->R : c->C;
   L.chunks = static_cast<int>((static_cast<int64_t>(c->R) * c->C + kChunk - 1) / kChunk);
   L.ldx = pad64(c->C);
   L.lds = pad64(static_cast<int>(n));
   size_t o = kHeader;
+  if (is_small(c)) {
+    L.total = o;
+    return L;
+  }
   auto take = [&o](size_t bytes) {
     const size_t at = o;
     o += align256(bytes);
@@ -648,10 +1101,28 @@ OrthoLayout ortho_layout(const moe_ortho_config *c) {
   L.part = take(B * L.chunks * 4);
   L.x0 = take(B * c->R * L.ldx * 2);
   L.x1 = take(c->steps > 1 ? B * c->R * L.ldx * 2 : 0);
-  L.s = take(B * n * L.lds * 2);
-  L.p = take(B * n * L.lds * 2);
+  const size_t square = B * n * L.lds * 2;
+  L.n[0] = take(square);
+  L.n[1] = take(square);
+  L.n[2] = take(fuse_steps(c->batch, static_cast<int>(n), c->R < c->C ? c->C : c->R) ? square : 0);
   L.total = o;
   return L;
+}
+
+template <class El>
+cudaError_t launch_small(SmallArgs &a, int batch, cudaStream_t s) {
+  static DeviceOnce once;
+  auto kernel = ortho_small_kernel<El>;
+  const cudaError_t e = once.get([&](int *) {
+    const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, small_smem(2));
+    return r != cudaSuccess ? r : cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  });
+  if (e != cudaSuccess) return e;
+  const int blocks = (a.m + 63) / 64;  // of 64 columns
+  a.cluster = 1;
+  while (a.cluster * (kSlab / 64) < blocks) a.cluster *= 2;
+  a.nblk = (blocks + a.cluster - 1) / a.cluster;
+  return launch_pdl(kernel, dim3(batch * a.cluster), dim3(kSmallThreads), small_smem(a.cluster), s, a.cluster, a);
 }
 
 template <class El>
@@ -704,6 +1175,28 @@ moe_status moe_ortho_update(const moe_ortho_config *cfg, const float *coefs, con
   const bool tall = R > C;
   const int n = tall ? C : R, m = tall ? R : C;
   int32_t *status = reinterpret_cast<int32_t *>(sc);
+  if (is_small(cfg)) {
+    SmallArgs q{};
+    q.g = g;
+    q.mom = momentum;
+    q.out = static_cast<uint16_t *>(out);
+    q.R = R;
+    q.C = C;
+    q.n = n;
+    q.m = m;
+    q.tall = tall;
+    q.vec = C % 8 == 0;
+    q.beta = beta;
+    q.eps = cfg->eps;
+    q.scale = scale;
+    q.nesterov = nesterov != 0;
+    q.steps = cfg->steps;
+    q.status = status;
+    for (int i = 0; i < 3 * cfg->steps; ++i) q.coefs[i] = coefs[i];
+    return timed("ortho_small", st, [&] {
+      return cfg->dtype == MOE_DTYPE_BF16 ? launch_small<uint16_t>(q, B, st) : launch_small<float>(q, B, st);
+    });
+  }
   PrepArgs a{};
   a.g = g;
   a.mom = momentum;
@@ -723,47 +1216,86 @@ moe_status moe_ortho_update(const moe_ortho_config *cfg, const float *coefs, con
   }));
   // X's rows along C with C contiguous: the Gram product reduces over m, the
   // update over n, so one of them reads X K-major and the other MN-major
-  uint8_t *xb[2] = {sc + L.x0, sc + L.x1};
-  CUtensorMap xk[2], xm[2], ms, mp;
+  const bool pairs = fuse_steps(B, n, m), pair = use_pairs(B, R, C);
+  uint8_t *xb[2] = {sc + L.x0, sc + L.x1}, *nb[3] = {sc + L.n[0], sc + L.n[1], sc + L.n[2]};
+  Maps mx[2], mn[3];
+  auto make = [&](Maps *mm, const void *ptr, int inner, int rows, int ld) {
+    return map3(&mm->k, ptr, inner, rows, B, ld, 128) && map3(&mm->mn, ptr, inner, rows, B, ld, 64);
+  };
   for (int i = 0; i < (cfg->steps > 1 ? 2 : 1); ++i)
-    if (!map3(&xk[i], xb[i], C, R, B, L.ldx, 128) || !map3(&xm[i], xb[i], C, R, B, L.ldx, 64)) return MOE_ERR_CUDA;
-  if (!map3(&ms, sc + L.s, n, n, B, L.lds, 128) || !map3(&mp, sc + L.p, n, n, B, L.lds, 128)) return MOE_ERR_CUDA;
-  for (int i = 0; i < cfg->steps; ++i) {
-    const int cur = i & 1;
-    ProductArgs p{};
-    p.batch = B;
-    p.status = status;
-    p.M = p.N = n;
+    if (!make(&mx[i], xb[i], C, R, L.ldx)) return MOE_ERR_CUDA;
+  for (int i = 0; i < (pairs ? 3 : 2); ++i)
+    if (!make(&mn[i], nb[i], n, n, L.lds)) return MOE_ERR_CUDA;
+  ProductArgs sym{};  // of the products into an n x n matrix
+  sym.batch = B;
+  sym.status = status;
+  sym.M = sym.N = n;
+  sym.ld = L.lds;
+  sym.stride = static_cast<int64_t>(n) * L.lds;
+  auto gram = [&](int x) {  // nb[0] <- S
+    ProductArgs p = sym;
     p.K = m;
-    p.ld = L.lds;
-    p.stride = static_cast<int64_t>(n) * L.lds;
     p.c = 1.f / (kSigma * kSigma);
-    p.out = reinterpret_cast<uint16_t *>(sc + L.s);
-    MOE_TRY(timed("ortho_gram", st, [&] {
-      return tall ? launch_product<kGram, 1, 1>(xm[cur], xm[cur], p, di.sms, st)
-                  : launch_product<kGram, 0, 0>(xk[cur], xk[cur], p, di.sms, st);
-    }));
+    p.out = reinterpret_cast<uint16_t *>(nb[0]);
+    return timed("ortho_gram", st, [&] {
+      return tall ? launch_product<kGram, kMN, kMN>(mx[x], mx[x], p, pair, di.sms, st)
+                  : launch_product<kGram, kK, kK>(mx[x], mx[x], p, pair, di.sms, st);
+    });
+  };
+  auto polynomial = [&](int step, int in, int to) {  // nb[to] <- a I + b S + c S S
+    ProductArgs p = sym;
     p.K = n;
-    p.a = coefs[3 * i];
-    p.b = coefs[3 * i + 1];
-    p.c = coefs[3 * i + 2];
-    p.s = reinterpret_cast<const uint16_t *>(sc + L.s);
-    p.out = reinterpret_cast<uint16_t *>(sc + L.p);
-    MOE_TRY(timed("ortho_polynomial", st, [&] { return launch_product<kSquare, 0, 0>(ms, ms, p, di.sms, st); }));
-    const bool last = i + 1 == cfg->steps;
+    p.a = coefs[3 * step];
+    p.b = coefs[3 * step + 1];
+    p.c = coefs[3 * step + 2];
+    p.s = reinterpret_cast<const uint16_t *>(nb[in]);
+    p.out = reinterpret_cast<uint16_t *>(nb[to]);
+    return timed("ortho_polynomial", st,
+                 [&] { return launch_product<kSquare, kSym, kSym>(mn[in], mn[in], p, pair, di.sms, st); });
+  };
+  auto commuting = [&](int x, int y, int to) {  // nb[to] <- nb[x] nb[y], symmetric as they commute
+    ProductArgs p = sym;
+    p.K = n;
+    p.c = 1.f;
+    p.out = reinterpret_cast<uint16_t *>(nb[to]);
+    return timed("ortho_commuting", st,
+                 [&] { return launch_product<kGram, kSym, kSym>(mn[x], mn[y], p, pair, di.sms, st); });
+  };
+  auto apply = [&](int poly, int x, bool last) {  // X (or out) <- nb[poly] X
+    ProductArgs p = sym;
     p.M = R;
     p.N = C;
+    p.K = n;
     p.ld = last ? C : L.ldx;
     p.stride = static_cast<int64_t>(R) * p.ld;
     p.c = last ? scale / kSigma : 1.f;
-    p.out = last ? static_cast<uint16_t *>(out) : reinterpret_cast<uint16_t *>(xb[cur ^ 1]);
-    MOE_TRY(timed("ortho_apply", st, [&] {
+    p.out = last ? static_cast<uint16_t *>(out) : reinterpret_cast<uint16_t *>(xb[x ^ 1]);
+    return timed("ortho_apply", st, [&] {
       if (last)
-        return tall ? launch_product<kLast, 0, 0>(xk[cur], mp, p, di.sms, st)
-                    : launch_product<kLast, 0, 1>(mp, xm[cur], p, di.sms, st);
-      return tall ? launch_product<kUpdate, 0, 0>(xk[cur], mp, p, di.sms, st)
-                  : launch_product<kUpdate, 0, 1>(mp, xm[cur], p, di.sms, st);
-    }));
+        return tall ? launch_product<kLast, kK, kSym>(mx[x], mn[poly], p, pair, di.sms, st)
+                    : launch_product<kLast, kSym, kMN>(mn[poly], mx[x], p, pair, di.sms, st);
+      return tall ? launch_product<kUpdate, kK, kSym>(mx[x], mn[poly], p, pair, di.sms, st)
+                  : launch_product<kUpdate, kSym, kMN>(mn[poly], mx[x], p, pair, di.sms, st);
+    });
+  };
+  int cur = 0;
+  for (int i = 0; i < cfg->steps;) {
+    MOE_TRY(gram(cur));
+    MOE_TRY(polynomial(i, 0, 1));  // P
+    int poly = 1, taken = 1;
+    // steps go in pairs, an odd one by itself in the middle
+    const bool alone = cfg->steps % 2 == 1 && i == cfg->steps / 2 / 2 * 2;
+    if (pairs && !alone && i + 1 < cfg->steps) {
+      MOE_TRY(commuting(1, 0, 2));       // P S
+      MOE_TRY(commuting(2, 1, 0));       // P S P: the S of P X
+      MOE_TRY(polynomial(i + 1, 0, 2));  // the next P
+      MOE_TRY(commuting(2, 1, 0));       // both steps at once
+      poly = 0;
+      taken = 2;
+    }
+    i += taken;
+    MOE_TRY(apply(poly, cur, i == cfg->steps));
+    cur ^= 1;
   }
   return MOE_OK;
 }

@@ -68,6 +68,21 @@ def test_sizes(B, R, C, dtype):
     assert torch.equal(out, o.update(g))  # the same bits every time
 
 
+# matrices that a cluster of CTAs holds on chip: 1 to 16 CTAs, ragged slabs, CTAs without columns, both orientations
+@pytest.mark.parametrize("B,R,C", [(1, 128, 4096), (2, 4096, 96), (3, 100, 3000), (2, 1100, 128), (5, 64, 264),
+                                   (2, 520, 33), (300, 16, 40), (1, 2, 4096), (40, 128, 1024), (1, 4097, 128),
+                                   (2, 129, 300)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_narrow(B, R, C, dtype):
+    g = grad(B, R, C, dtype, 31)
+    m = grad(B, R, C, "fp32", 32)
+    u = g.double() + 0.95 * (0.95 * m.double() + g.double())
+    o = moe.Orthogonaliser(B, R, C, dtype=dtype)
+    near(o.update(g), reference(g, moe.MUON_COEFS))
+    near(o.update(g, momentum=m), reference(u, moe.MUON_COEFS))
+    assert o.status() == {"update": 0}
+
+
 def test_singular_values_end_near_one():
     g = grad(2, 384, 700, "fp32", 2)
     s = torch.linalg.svdvals(moe.Orthogonaliser(2, 384, 700, dtype="fp32").update(g).float())

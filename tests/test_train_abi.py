@@ -42,10 +42,10 @@ def test_balance_configurations(L, bad):
                                  dict(C=16385), dict(steps=0), dict(steps=65), dict(dtype=2), dict(eps=-1.0),
                                  dict(eps=float("nan"))])
 def test_ortho_configurations(L, bad):
-    good = dict(batch=4, R=64, C=48, steps=5, dtype=0, eps=1e-7)
+    good = dict(batch=4, R=640, C=480, steps=5, dtype=0, eps=1e-7)
     n = ctypes.c_size_t()
     assert L.moe_ortho_workspace(ctypes.byref(moe.OrthoConfig(**good)), ctypes.byref(n)) == 0
-    assert n.value >= 256 + 4 * (2 * 64 * 48 + 2 * 48 * 48) * 2
+    assert n.value >= 256 + 4 * (2 * 640 * 480 + 2 * 480 * 480) * 2
     assert L.moe_ortho_workspace(ctypes.byref(moe.OrthoConfig(**{**good, **bad})), ctypes.byref(n)) == -1
 
 
