@@ -50,10 +50,21 @@ constexpr float kSigma = 256.f;  // X is stored times this
 constexpr int kMaxDim = 16384, kMaxBatch = 65535, kMaxSteps = 64;  // (at most 2^28 tiles in a product)
 
 // ---------------------------------------------------------------- norms and the first X
+//
+// One pass over the update: the momentum is advanced, the squares are summed and X
+// is written, before the norm is known: times a power of two taken from a sample of
+// the gradient that every block reads, so that X's root mean square comes out near 1.
+// The norm's factor enters the first step's products, where it is exact in fp32.
+// Where the sample misled (X's root mean square is not within 2^-6 .. 2^10 of 1, or a
+// value does not fit fp16), the second kernel, which otherwise only adds the
+// sums, writes X again with a power of two from the norm.  Two passes over 128 x
+// 2048 x 768 took 189 us, 16 x 1536 x 4096 with momentum 281; this one 131 and 194.
 
 constexpr int kPrepThreads = 256;
-constexpr int kPrepVecs = 8;                                  // 8-element groups per thread
-constexpr int kChunk = kPrepThreads * kPrepVecs * 8;          // elements of one block
+constexpr int kPrepVecs = 8;        // 8-element groups a thread has in flight
+constexpr int kPrepSingles = 16;    // or elements, where rows are not whole groups
+constexpr int kRescaleBlocks = 4;   // blocks per matrix of the second kernel
+constexpr float kFits = 60000.f;    // the largest value stored
 
 struct PrepArgs {
   const void *g;
@@ -63,8 +74,10 @@ struct PrepArgs {
   float eps;
   int64_t numel;  // R * C
   int C, ld;      // columns, and X's row stride
+  int chunk;      // elements per block
   int chunks;     // blocks per matrix
-  float *part;    // [B][chunks] sums of squares
+  float *part;    // [B][chunks] sums of squares; infinite where a value does not fit
+  float *fac;     // [B] what X is to be multiplied with
   uint16_t *x;    // [B][R][ld] fp16
   int64_t x_stride;
   int32_t *status;
@@ -98,19 +111,76 @@ __device__ __forceinline__ float update_of(float g, float m, float beta, bool ne
   return nesterov ? fmaf(beta, m, g) : m;
 }
 
-// Sum of squares of one chunk of one matrix's update; the momentum is advanced
-// on the way.  VEC: a matrix's elements are whole groups of eight.
+__device__ __forceinline__ float block_sum(float v, float *s_w) {
+  v = warp_sum(v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) s_w[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = s_w[0];
+#pragma unroll
+  for (int w = 1; w < kPrepThreads / 32; ++w) v += s_w[w];
+  return v;
+}
+
+// The power of two that brings a root mean square of sqrt(sum / count) to 1 .. 2
+// (1 where there is nothing to go by).
+__device__ __forceinline__ float power_for(float sum, float count) {
+  const float ms = sum / count;
+  if (!(ms > 1e-36f && ms < 1e36f)) return 1.f;
+  return exp2f(-floorf(0.5f * log2f(ms)));
+}
+
+// u times f0 into X at element `at` of the matrix (8 elements or one).
+template <bool VEC>
+__device__ __forceinline__ void store_x(const PrepArgs &a, uint16_t *x, int64_t at, const float *u, float f0) {
+  const int row = static_cast<int>(static_cast<uint32_t>(at) / static_cast<uint32_t>(a.C));  // R * C <= 2^28
+  const int64_t dst = static_cast<int64_t>(row) * a.ld + (at - static_cast<int64_t>(row) * a.C);
+  if constexpr (VEC) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 h = __floats2half2_rn(u[2 * i] * f0, u[2 * i + 1] * f0);
+      memcpy(&w[i], &h, 4);
+    }
+    *reinterpret_cast<uint4 *>(x + dst) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    x[dst] = __half_as_ushort(__float2half_rn(u[0] * f0));
+  }
+}
+
+// The scale that a matrix's blocks take from the sample: 8 elements per thread,
+// spread evenly (or the whole matrix, where it is smaller).
+template <class El, bool VEC>
+__device__ __forceinline__ float sample_scale(const El *g, int64_t numel, float *s_w) {
+  constexpr int N = VEC ? 8 : 1;
+  const int64_t groups = numel / N;
+  const int64_t at = groups > kPrepThreads ? groups * threadIdx.x / kPrepThreads : threadIdx.x;
+  float f[N], sum = 0.f;
+  const bool in = at < groups;
+  if (in) {
+    load_el<El, VEC>(g + at * N, f);
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum = fmaf(f[i], f[i], sum);
+  }
+  const int64_t used = groups < kPrepThreads ? groups : kPrepThreads;
+  return power_for(block_sum(sum, s_w), static_cast<float>(used * N));
+}
+
+// One chunk of one matrix.  VEC: rows are whole groups of eight.
 template <class El, bool VEC, bool MOM>
-__global__ void __launch_bounds__(kPrepThreads) ortho_norm_kernel(const PrepArgs a) {
+__global__ void __launch_bounds__(kPrepThreads) ortho_prepare_kernel(const PrepArgs a) {
   griddep_wait();  // the previous kernel in the stream has completed
   __shared__ float s_w[kPrepThreads / 32];
-  constexpr int N = VEC ? 8 : 1, IT = kChunk / (kPrepThreads * N), U = VEC ? kPrepVecs : 16;
+  constexpr int N = VEC ? 8 : 1, U = VEC ? (MOM ? kPrepVecs / 2 : kPrepVecs) : kPrepSingles;
   const El *g = static_cast<const El *>(a.g) + blockIdx.y * a.numel;
   float *mom = MOM ? a.mom + blockIdx.y * a.numel : nullptr;
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * kChunk + threadIdx.x * N;
-  float acc = 0.f;
+  uint16_t *x = a.x + blockIdx.y * a.x_stride;
+  const float f0 = sample_scale<El, VEC>(g, a.numel, s_w);
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * a.chunk + threadIdx.x * N;
+  float acc = 0.f, most = 0.f;
 #pragma unroll 1
-  for (int it = 0; it < IT; it += U) {
+  for (int it = 0; it < a.chunk / (kPrepThreads * N); it += U) {
+    if (base + static_cast<int64_t>(it) * kPrepThreads * N >= a.numel) break;
     float f[U][N], m[U][N];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -141,67 +211,62 @@ __global__ void __launch_bounds__(kPrepThreads) ortho_norm_kernel(const PrepArgs
         for (int i = 0; i < N; ++i) f[u][i] = update_of(f[u][i], m[u][i], a.beta, a.nesterov);
       }
 #pragma unroll
-      for (int i = 0; i < N; ++i) acc = fmaf(f[u][i], f[u][i], acc);
+      for (int i = 0; i < N; ++i) {
+        acc = fmaf(f[u][i], f[u][i], acc);
+        most = fmaxf(most, fabsf(f[u][i]));
+      }
+      if (at < a.numel) store_x<VEC>(a, x, at, f[u], f0);
     }
   }
-  acc = warp_sum(acc);
-  if ((threadIdx.x & 31) == 0) s_w[threadIdx.x >> 5] = acc;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kPrepThreads / 32; ++w) acc += s_w[w];
-    a.part[static_cast<size_t>(blockIdx.y) * a.chunks + blockIdx.x] = acc;
-  }
+  acc = block_sum(acc, s_w);
+  // a value past fp16's range, marked by the sign (the sum itself is not negative)
+  const bool fits = __syncthreads_and(!(most * f0 > kFits));
+  if (threadIdx.x == 0)
+    a.part[static_cast<size_t>(blockIdx.y) * a.chunks + blockIdx.x] = fits ? acc : -fmaxf(acc, 1e-38f);
 }
 
-// X = kSigma u / max(|u|, eps) in fp16, rows padded to ld.  VEC: rows are whole
-// groups of eight.
+// A matrix's factor from its sums; X again, by the blocks of the matrix, where the
+// sample misled.
 template <class El, bool VEC, bool MOM>
-__global__ void __launch_bounds__(kPrepThreads) ortho_scale_kernel(const PrepArgs a) {
+__global__ void __launch_bounds__(kPrepThreads) ortho_rescale_kernel(const PrepArgs a) {
   griddep_wait();  // the previous kernel in the stream has completed
   __shared__ float s_w[kPrepThreads / 32];
-  constexpr int N = VEC ? 8 : 1, IT = kChunk / (kPrepThreads * N);
-  float sq = 0.f;  // the matrix's chunks in a fixed order
-  for (int i = threadIdx.x; i < a.chunks; i += kPrepThreads)
-    sq += a.part[static_cast<size_t>(blockIdx.y) * a.chunks + i];
-  sq = warp_sum(sq);
-  if ((threadIdx.x & 31) == 0) s_w[threadIdx.x >> 5] = sq;
-  __syncthreads();
-  sq = s_w[0];
-#pragma unroll
-  for (int w = 1; w < kPrepThreads / 32; ++w) sq += s_w[w];
-  const bool fine = isfinite(sq);
-  if (!fine && blockIdx.x == 0 && threadIdx.x == 0) flag_status(a.status, kDevNonfiniteUpdate);
-  const float norm = fmaxf(sqrtf(sq), a.eps);
-  const float f0 = fine ? (norm > 0.f ? kSigma / norm : 0.f) : NAN;
+  constexpr int N = VEC ? 8 : 1;
   const El *g = static_cast<const El *>(a.g) + blockIdx.y * a.numel;
-  const float *mom = MOM ? a.mom + blockIdx.y * a.numel : nullptr;
-  uint16_t *x = a.x + blockIdx.y * a.x_stride;
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * kChunk + threadIdx.x * N;
-#pragma unroll 4
-  for (int it = 0; it < IT; ++it) {
-    const int64_t at = base + static_cast<int64_t>(it) * kPrepThreads * N;
-    if (at >= a.numel) break;
-    float f[N];
-    load_el<El, VEC>(g + at, f);
-    if constexpr (MOM) {
-      float m[N];
-      load_el<float, VEC>(mom + at, m);
+  const float *part = a.part + static_cast<size_t>(blockIdx.y) * a.chunks;
+  float sq = 0.f;  // the chunks in a fixed order
+  bool fits = true;
+  for (int i = threadIdx.x; i < a.chunks; i += kPrepThreads) {
+    const float v = part[i];
+    sq += fabsf(v);
+    fits = fits && !(v < 0.f);
+  }
+  sq = block_sum(sq, s_w);
+  fits = __syncthreads_and(fits);
+  float f0 = sample_scale<El, VEC>(g, a.numel, s_w);
+  const bool fine = isfinite(sq);
+  const float rms = sqrtf(sq / static_cast<float>(a.numel)) * f0;
+  if (fine && sq > 0.f && !(fits && rms >= 0x1p-6f && rms <= 0x1p10f)) {
+    f0 = power_for(sq, static_cast<float>(a.numel));
+    const float *mom = MOM ? a.mom + blockIdx.y * a.numel : nullptr;
+    uint16_t *x = a.x + blockIdx.y * a.x_stride;
+    for (int64_t at = (static_cast<int64_t>(blockIdx.x) * kPrepThreads + threadIdx.x) * N; at < a.numel;
+         at += static_cast<int64_t>(gridDim.x) * kPrepThreads * N) {
+      float f[N];
+      load_el<El, VEC>(g + at, f);
+      if constexpr (MOM) {
+        float m[N];
+        load_el<float, VEC>(mom + at, m);
 #pragma unroll
-      for (int i = 0; i < N; ++i) f[i] = update_of(f[i], m[i], a.beta, a.nesterov);
-    }
-    const int row = static_cast<int>(static_cast<uint32_t>(at) / static_cast<uint32_t>(a.C));  // R * C <= 2^28
-    const int64_t dst = static_cast<int64_t>(row) * a.ld + (at - static_cast<int64_t>(row) * a.C);
-    if constexpr (VEC) {
-      uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __half2 h = __floats2half2_rn(f[2 * i] * f0, f[2 * i + 1] * f0);
-        memcpy(&w[i], &h, 4);
+        for (int i = 0; i < N; ++i) f[i] = update_of(f[i], m[i], a.beta, a.nesterov);
       }
-      *reinterpret_cast<uint4 *>(x + dst) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-      x[dst] = __half_as_ushort(__float2half_rn(f[0] * f0));
+      store_x<VEC>(a, x, at, f, f0);
     }
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (!fine) flag_status(a.status, kDevNonfiniteUpdate);
+    const float norm = fmaxf(sqrtf(sq), a.eps);
+    a.fac[blockIdx.y] = fine ? (norm > 0.f ? kSigma / (norm * f0) : 0.f) : NAN;
   }
 }
 
@@ -237,6 +302,7 @@ struct ProductArgs {
   int nm, nn;             // tiles along the rows, along the columns
   int per;                // tiles per matrix (symmetric: mt <= nt)
   float a, b, c;          // kSquare; c also the factor of the other products
+  const float *fac;       // a matrix's factor besides c (the first step's X), or null
   const uint16_t *s;      // kSquare: S
   uint16_t *out;
   int ld;                 // row stride of s and out
@@ -326,6 +392,11 @@ __device__ __forceinline__ void epilogue(const TileAt &t, uint32_t tb, int row0,
   const int lane = threadIdx.x & 31;
   const int nrows = min(32, p.M - row0);
   uint16_t *out = p.out + t.b * p.stride;
+  float c = p.c;
+  if (KIND != kSquare && p.fac) {
+    const float f = p.fac[t.b];
+    c *= KIND == kGram ? f * f : f;
+  }
 #pragma unroll KIND == kSquare ? kChunks : 1
   for (int j = 0; j < kChunks; ++j) {
     const int cc = part * (TS / 2) + 32 * j, c0 = t.n0 + cc;
@@ -357,7 +428,7 @@ __device__ __forceinline__ void epilogue(const TileAt &t, uint32_t tb, int row0,
     } else {
       tmem_ld_wait();
 #pragma unroll
-      for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(acc[e]) * p.c;
+      for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(acc[e]) * c;
     }
     if constexpr (KIND == kLast) {  // out [M,N] itself, bf16
       const int ncols = min(32, p.N - c0);
@@ -1079,13 +1150,18 @@ bool fuse_steps(int batch, int n, int m) {
 inline int pad64(int x) { return (x + 63) / 64 * 64; }
 
 struct OrthoLayout {
-  int chunks, ldx, lds;
-  size_t part, x0, x1, n[3], total;
+  int chunk, chunks, ldx, lds;
+  size_t part, fac, x0, x1, n[3], total;
 };
 OrthoLayout ortho_layout(const moe_ortho_config *c) {
   OrthoLayout L{};
   const size_t B = c->batch, n = c->R < c->C ? c->R : c->C;
-  L.chunks = static_cast<int>((static_cast<int64_t>(c->R) * c->C + kChunk - 1) / kChunk);
+  // a block's share: one round of its threads' loads, or four where that leaves
+  // several blocks for every place on the part
+  const int64_t numel = static_cast<int64_t>(c->R) * c->C;
+  L.chunk = kPrepThreads * (c->C % 8 == 0 ? kPrepVecs * 8 : kPrepSingles);
+  if (numel * c->batch >= static_cast<int64_t>(L.chunk) * 4 * 152 * 8) L.chunk *= 4;
+  L.chunks = static_cast<int>((numel + L.chunk - 1) / L.chunk);
   L.ldx = pad64(c->C);
   L.lds = pad64(static_cast<int>(n));
   size_t o = kHeader;
@@ -1099,6 +1175,7 @@ OrthoLayout ortho_layout(const moe_ortho_config *c) {
     return at;
   };
   L.part = take(B * L.chunks * 4);
+  L.fac = take(B * 4);
   L.x0 = take(B * c->R * L.ldx * 2);
   L.x1 = take(c->steps > 1 ? B * c->R * L.ldx * 2 : 0);
   const size_t square = B * n * L.lds * 2;
@@ -1125,23 +1202,18 @@ cudaError_t launch_small(SmallArgs &a, int batch, cudaStream_t s) {
   return launch_pdl(kernel, dim3(batch * a.cluster), dim3(kSmallThreads), small_smem(a.cluster), s, a.cluster, a);
 }
 
-template <class El>
-cudaError_t launch_prep(const PrepArgs &a, int batch, int C, cudaStream_t s) {
-  const dim3 grid(a.chunks, batch), block(kPrepThreads);
-  const bool whole = a.numel % 8 == 0, rows = C % 8 == 0;
-  cudaError_t e;
-  if (a.mom)
-    e = launch_pdl(whole ? ortho_norm_kernel<El, true, true> : ortho_norm_kernel<El, false, true>, grid, block, 0, s, 1,
-                   a);
-  else
-    e = launch_pdl(whole ? ortho_norm_kernel<El, true, false> : ortho_norm_kernel<El, false, false>, grid, block, 0, s,
-                   1, a);
+template <class El, bool VEC, bool MOM>
+cudaError_t launch_prep(const PrepArgs &a, int batch, cudaStream_t s) {
+  cudaError_t e =
+      launch_pdl(ortho_prepare_kernel<El, VEC, MOM>, dim3(a.chunks, batch), dim3(kPrepThreads), 0, s, 1, a);
   if (e != cudaSuccess) return e;
-  if (a.mom)
-    return launch_pdl(rows ? ortho_scale_kernel<El, true, true> : ortho_scale_kernel<El, false, true>, grid, block, 0,
-                      s, 1, a);
-  return launch_pdl(rows ? ortho_scale_kernel<El, true, false> : ortho_scale_kernel<El, false, false>, grid, block, 0,
-                    s, 1, a);
+  const int blocks = a.chunks < kRescaleBlocks ? a.chunks : kRescaleBlocks;
+  return launch_pdl(ortho_rescale_kernel<El, VEC, MOM>, dim3(blocks, batch), dim3(kPrepThreads), 0, s, 1, a);
+}
+template <class El>
+cudaError_t launch_prep(const PrepArgs &a, int batch, cudaStream_t s) {
+  if (a.C % 8 == 0) return a.mom ? launch_prep<El, true, true>(a, batch, s) : launch_prep<El, true, false>(a, batch, s);
+  return a.mom ? launch_prep<El, false, true>(a, batch, s) : launch_prep<El, false, false>(a, batch, s);
 }
 
 }  // namespace
@@ -1206,13 +1278,15 @@ moe_status moe_ortho_update(const moe_ortho_config *cfg, const float *coefs, con
   a.numel = static_cast<int64_t>(R) * C;
   a.C = C;
   a.ld = L.ldx;
+  a.chunk = L.chunk;
   a.chunks = L.chunks;
   a.part = reinterpret_cast<float *>(sc + L.part);
+  a.fac = reinterpret_cast<float *>(sc + L.fac);
   a.x = reinterpret_cast<uint16_t *>(sc + L.x0);
   a.x_stride = static_cast<int64_t>(R) * L.ldx;
   a.status = status;
   MOE_TRY(timed("ortho_norm_scale", st, [&] {
-    return cfg->dtype == MOE_DTYPE_BF16 ? launch_prep<uint16_t>(a, B, C, st) : launch_prep<float>(a, B, C, st);
+    return cfg->dtype == MOE_DTYPE_BF16 ? launch_prep<uint16_t>(a, B, st) : launch_prep<float>(a, B, st);
   }));
   // X's rows along C with C contiguous: the Gram product reduces over m, the
   // update over n, so one of them reads X K-major and the other MN-major
@@ -1232,10 +1306,12 @@ moe_status moe_ortho_update(const moe_ortho_config *cfg, const float *coefs, con
   sym.M = sym.N = n;
   sym.ld = L.lds;
   sym.stride = static_cast<int64_t>(n) * L.lds;
+  const float *fac = a.fac;  // of the first X
   auto gram = [&](int x) {  // nb[0] <- S
     ProductArgs p = sym;
     p.K = m;
     p.c = 1.f / (kSigma * kSigma);
+    p.fac = fac;
     p.out = reinterpret_cast<uint16_t *>(nb[0]);
     return timed("ortho_gram", st, [&] {
       return tall ? launch_product<kGram, kMN, kMN>(mx[x], mx[x], p, pair, di.sms, st)
@@ -1269,6 +1345,7 @@ moe_status moe_ortho_update(const moe_ortho_config *cfg, const float *coefs, con
     p.ld = last ? C : L.ldx;
     p.stride = static_cast<int64_t>(R) * p.ld;
     p.c = last ? scale / kSigma : 1.f;
+    p.fac = fac;
     p.out = last ? static_cast<uint16_t *>(out) : reinterpret_cast<uint16_t *>(xb[x ^ 1]);
     return timed("ortho_apply", st, [&] {
       if (last)
@@ -1296,6 +1373,7 @@ moe_status moe_ortho_update(const moe_ortho_config *cfg, const float *coefs, con
     i += taken;
     MOE_TRY(apply(poly, cur, i == cfg->steps));
     cur ^= 1;
+    fac = nullptr;
   }
   return MOE_OK;
 }

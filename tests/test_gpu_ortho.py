@@ -119,6 +119,37 @@ def test_size_of_the_update_has_no_part():
         near(moe.Orthogonaliser(1, 96, 160, eps=0.0).update(g), reference(g, moe.MUON_COEFS, eps=0.0))
 
 
+@pytest.mark.parametrize("R,C", [(256, 304), (203, 301)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_updates_of_uneven_size(R, C, dtype):
+    """Matrices whose parts differ widely in size: rows of zeros, one large value among small ones, sizes that change
+    by 1e8 on the way, momentum without a gradient and a gradient that cancels it."""
+    g = grad(6, R, C, dtype, 33, 1.0)
+    g[1, :, : C - 1] = 0                                   # one column
+    g[2] *= 1e-9
+    g[2, R // 2, C // 3] = 1e3                             # one value
+    g[3, : R // 2] *= 1e-8
+    g[4, ::3] = 0
+    g[5] = 0
+    ref = reference(g, moe.MUON_COEFS)
+    o = moe.Orthogonaliser(6, R, C, dtype=dtype)
+    out = o.update(g).view(torch.bfloat16).double()
+    assert o.status() == {"update": 0} and float(out[5].abs().max()) == 0
+    near(out[[0, 4]].to(torch.bfloat16), ref[[0, 4]])
+    for b in (1, 2, 3):
+        # rank one, or half of the singular values 1e-8 of the others: what is small against the norm has no more
+        # than its absolute exactness, 2^-12 per rounding and step, grown by at most 3.4445 a step
+        err = torch.linalg.matrix_norm(out[b] - ref[b], ord=2)
+        assert float(err) <= 0.05, (b, float(err))
+    m = grad(6, R, C, "fp32", 34, 10.0)
+    m[0] = -m[0].abs() * 0 - g[0].float() / 0.95           # cancels but for the nesterov term
+    u = g.double() + 0.95 * (0.95 * m.double() + g.double())
+    out = o.update(g, momentum=m)
+    near(out[[5]], reference(u[[5]], moe.MUON_COEFS))
+    near(out[[4]], reference(u[[4]], moe.MUON_COEFS))
+    near(out[[0]], reference(u[[0]], moe.MUON_COEFS))
+
+
 def test_zeros_and_bad_matrices_stay_their_own():
     g = grad(5, 136, 200, "bf16", 6)
     g[1] = 0
