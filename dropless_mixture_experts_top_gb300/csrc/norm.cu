@@ -207,28 +207,32 @@ __device__ __forceinline__ void row_dx(F2 (&o2)[kPairs], const F2 (&gw)[kPairs],
   for (int i = 0; i < kPairs; ++i) o2[i] = f2_fma(r2, f2_fma(xh[i], c1, f2_sub(gw[i], c2)), o2[i]);
 }
 
-// The block's column sums: its rows' threads add theirs in order, one row group
-// after another, the last into the block's partial row.  col(j): the column of
-// a thread's element j (one below 0 or past H: none).  s_col: [2][H] in shared memory, used when
-// several rows share the block (H <= 2048 then).
+// The block's column sums into its partial row, its row groups added in order.
+// col(j): the column of a thread's element j (one below 0 or past H: none).  s_col:
+// [rows][2][H] in shared memory (at most 128 bytes a thread), used when several rows
+// share the block.
 template <class Col>
 __device__ __forceinline__ void block_colsum(const NormArgs &a, const Place &pl, const F2 (&aw)[kPairs],
                                              const F2 (&ab)[kPairs], float *s_col, Col &&col) {
   float cw[kElems], cb[kElems];
   unpair(aw, cw);
   unpair(ab, cb);
-  float *part = a.part + static_cast<size_t>(blockIdx.x) * 2 * a.H;
-  for (int q = 0; q < pl.rows; ++q) {
-    if (q > 0) __syncthreads();
-    if (pl.g != q) continue;
-    float *out = q == pl.rows - 1 ? part : s_col;
+  const int H = a.H;
+  float *part = a.part + static_cast<size_t>(blockIdx.x) * 2 * H;
+  float *mine = pl.rows > 1 ? s_col + pl.g * 2 * H : part;
 #pragma unroll
-    for (int j = 0; j < kElems; ++j) {
-      const int c = col(j);
-      if (c < 0 || c >= a.H) continue;
-      out[c] = q > 0 ? s_col[c] + cw[j] : cw[j];
-      out[a.H + c] = q > 0 ? s_col[a.H + c] + cb[j] : cb[j];
-    }
+  for (int j = 0; j < kElems; ++j) {
+    const int c = col(j);
+    if (c < 0 || c >= H) continue;
+    mine[c] = cw[j];
+    mine[H + c] = cb[j];
+  }
+  if (pl.rows == 1) return;
+  __syncthreads();
+  for (int c = threadIdx.x; c < 2 * H; c += blockDim.x) {
+    float v = s_col[c];
+    for (int q = 1; q < pl.rows; ++q) v += s_col[q * 2 * H + c];
+    part[c] = v;
   }
 }
 
