@@ -343,9 +343,9 @@ struct Ring {
     for (int u = 0; u < V; ++u)
       if (ln.tpr * u < ln.left) {
         int bytes = 16;
-        if (SPAN && t == ln.T - 1) {  // nothing past the end of the last row is read
-          const int over = ln.col(N * u) + N - ln.H;
-          bytes = over > 0 ? 16 - over * static_cast<int>(sizeof(El)) : 16;
+        if (SPAN && ln.T - t <= N) {  // nothing past the end of the last row is read
+          const int64_t rest = static_cast<int64_t>(ln.T - t) * ln.H - ln.col(N * u);  // elements from the vector on
+          bytes = rest < N ? static_cast<int>(rest) * static_cast<int>(sizeof(El)) : 16;
         }
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
