@@ -14,11 +14,17 @@
 // sum; its lse is stored as +inf, by which the backward knows it.
 //
 // Both directions read the logits once, in fp32, G lanes (a power of two) per
-// token holding its row in registers.  The forward's blocks stay inside one
-// sequence and leave their column sums, counts and z sums as one partial row
-// each; a second kernel (one block per sequence, the last to finish adds the
-// sequences) reduces them in a fixed order, so losses are the same bits every
-// time.  Counts are integers, added in any order.
+// token holding its row in registers, the next token's loads issued before this
+// one is worked on.  The forward's blocks stay inside one sequence and leave their
+// column sums, counts and z sums as one partial row each; a second kernel reduces
+// them in a fixed order, so losses are the same bits every time (counts are
+// integers, added in any order).  A single short sequence is one block and one
+// kernel.
+//
+// Bounds, measured: the backward moves 12 bytes per logit at 88% of the copy rate
+// (131072 x 250: 66 us); the forward of as many (4 bytes per logit, 20 us at that
+// rate) takes 43 to 55 us, for its exponentials, shuffles and column sums; below
+// some 10,000 tokens it is the latency of its two kernels (16384 x 128: 14 us).
 #include <math.h>
 
 #include <type_traits>
@@ -31,8 +37,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBwdBlocksPerSm = 8;  // backward blocks at most
-constexpr int kMaxBlocks = 304;  // forward blocks over all sequences at most, unless there are more sequences
+constexpr int kBwdBlocksPerSm = 4;  // backward blocks at most (eight: 16384 x 128 10.3 us against 8.2)
+// forward blocks over all sequences at most, unless there are more sequences: three per SM
+// (131072 x 250 in 32 sequences 55 us against 66 with two; four are no faster)
+constexpr int kMaxBlocks = 456;
 
 struct SeqSum {  // one sequence, or one block's share of it
   float bal, z;
@@ -115,9 +123,9 @@ __device__ __forceinline__ float group_max(float v, int G) {
   return v;
 }
 
-// One sequence's outputs, by a block's first 256 threads: thread e holds expert e's
-// probability sum and count (0 past E).  r: its z sum, tokens and flags; thread 0
-// gets the sequence's balance term in r.bal.  Every thread of the block calls it.
+// One sequence's outputs by its only block: thread e holds expert e's probability
+// sum and count (0 past E).  r: its z sum, tokens and flags; thread 0 gets the
+// sequence's balance term in r.bal.  Every thread of the block calls it.
 __device__ __forceinline__ void finish_seq(const BalArgs &a, int s, float sum, int cnt, SeqSum &r, float *s_w) {
   const float inv_n = r.n > 0 ? 1.f / static_cast<float>(r.n) : 0.f;
   const int e = threadIdx.x;
@@ -158,9 +166,24 @@ __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(const BalArgs a) 
   const int i0 = blk * a.per, i1 = min(i0 + a.per, a.L);  // tokens of the sequence
   const size_t tbase = static_cast<size_t>(seq) * a.L;
   const int step = kWarps * tpw;  // tokens of one pass of the block
+  // the next token's logits, mask and first slots are loaded before this one is
+  // worked on
+  constexpr int kAhead = 2;  // slots per lane that are loaded ahead
   float v[NV], next[NV];
+  int slot[kAhead], next_slot[kAhead];
+  bool next_ok;
+  auto fetch = [&](int i) {
+    const bool in = i < i1;
+    load_row<W>(a.logits + (tbase + i) * E, E, G, lane, in, -INFINITY, next);
+    next_ok = in && (!a.mask || a.mask[tbase + i] != 0);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int q = lane + G * u;
+      next_slot[u] = in && q < a.k ? a.topk_idx[(tbase + i) * a.k + q] : -1;
+    }
+  };
   int ib = i0 + warp * tpw;
-  load_row<W>(a.logits + (tbase + ib + sub) * E, E, G, lane, ib + sub < i1, -INFINITY, next);
+  fetch(ib + sub);
   if (!SOLO && blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
   for (int e = threadIdx.x; e < E; e += kThreads) s_cnt[e] = 0;
   __syncthreads();
@@ -173,8 +196,10 @@ __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(const BalArgs a) 
     const int i = ib + sub;
 #pragma unroll
     for (int j = 0; j < NV; ++j) v[j] = next[j];
-    load_row<W>(a.logits + (tbase + i + step) * E, E, G, lane, i + step < i1, -INFINITY, next);
-    bool ok = i < i1 && (!a.mask || a.mask[tbase + i] != 0);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) slot[u] = next_slot[u];
+    bool ok = next_ok;
+    fetch(i + step);
     float mx = v[0];
 #pragma unroll
     for (int j = 1; j < NV; ++j) mx = fmaxf(mx, v[j]);
@@ -189,7 +214,7 @@ __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(const BalArgs a) 
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      v[j] = expf(v[j] - mx);
+      v[j] = __expf(v[j] - mx);
       sum += v[j];
     }
     sum = group_sum(sum, G);
@@ -203,13 +228,16 @@ __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(const BalArgs a) 
         n += 1;
         if (lse != lse) flags |= kDevNonfiniteLogit;
       }
-      for (int q = lane; q < a.k; q += G) {
-        const int e = a.topk_idx[(tbase + i) * a.k + q];
+      auto count = [&](int e) {
         if (static_cast<unsigned>(e) < static_cast<unsigned>(E))
           atomicAdd(&s_cnt[e], 1);
         else
           flags |= kDevBadIndex;
-      }
+      };
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (lane + G * u < a.k) count(slot[u]);
+      for (int q = lane + G * kAhead; q < a.k; q += G) count(a.topk_idx[(tbase + i) * a.k + q]);
     }
     if (lane == 0 && i < i1) a.lse[tbase + i] = ok ? lse : INFINITY;
   }
@@ -253,29 +281,32 @@ __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(const BalArgs a) 
   }
 }
 
-// One block per sequence; the last one to finish adds the sequences.
-constexpr int kFinThreads = 1024;
+// The blocks' partial rows added: a cluster of blocks per sequence, 32 experts per
+// block (a warp of columns, 32 interleaved runs of rows); the first block of the
+// cluster gets the others' part of the balance term through distributed shared
+// memory.  Of several sequences, the last cluster to finish (a ticket) adds them.
+constexpr int kFinThreads = 1024, kFinCols = 32, kFinRuns = kFinThreads / kFinCols;
 __global__ void __launch_bounds__(kFinThreads) balance_finish_kernel(const BalArgs a) {
   griddep_wait();  // the previous kernel in the stream has completed
-  __shared__ float s_sum[kFinThreads];
-  __shared__ int s_cnt[kFinThreads];
-  __shared__ SeqSum s_seq;
-  __shared__ float s_w[8];
+  __shared__ float s_sum[kFinRuns][kFinCols + 1];
+  __shared__ int s_cnt[kFinRuns][kFinCols + 1];
+  __shared__ SeqSum s_warp[kFinRuns];
+  __shared__ float s_bal[kMaxExperts / kFinCols];
   __shared__ int s_last;
-  const int E = a.E, s = blockIdx.x;
-  int ep = 32;
-  while (ep < E) ep *= 2;
-  const int e = threadIdx.x & (ep - 1), run = threadIdx.x / ep, runs = kFinThreads / ep;
+  const int E = a.E, groups = (E + kFinCols - 1) / kFinCols;
+  const int s = blockIdx.x / groups, cg = blockIdx.x - s * groups;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int e = cg * kFinCols + lane;
   const size_t row0 = static_cast<size_t>(s) * a.nbs;
   float sum = 0.f;
   int cnt = 0;
-  constexpr int U = 16;  // loads of each kind in flight
-  for (int b0 = run; b0 < a.nbs; b0 += runs * U) {
+  constexpr int U = 10;  // loads of each kind in flight
+  for (int b0 = warp; b0 < a.nbs; b0 += kFinRuns * U) {
     float v[U];
     int c[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int b = b0 + runs * u;
+      const int b = b0 + kFinRuns * u;
       const bool in = b < a.nbs && e < E;
       v[u] = in ? a.psum[(row0 + b) * E + e] : 0.f;
       c[u] = in ? a.pcnt[(row0 + b) * E + e] : 0;
@@ -286,40 +317,56 @@ __global__ void __launch_bounds__(kFinThreads) balance_finish_kernel(const BalAr
       cnt += c[u];
     }
   }
-  s_sum[threadIdx.x] = sum;
-  s_cnt[threadIdx.x] = cnt;
-  if (threadIdx.x < 32) {
-    SeqSum r{0.f, 0.f, 0, 0};
-    for (int b = threadIdx.x; b < a.nbs; b += 32) {
-      const SeqSum q = a.pblk[row0 + b];
-      r.z += q.z;
-      r.n += q.n;
-      r.flags |= q.flags;
-    }
+  SeqSum r{0.f, 0.f, 0, 0};
+  for (int b = threadIdx.x; b < a.nbs; b += kFinThreads) {
+    const SeqSum q = a.pblk[row0 + b];
+    r.z += q.z;
+    r.n += q.n;
+    r.flags |= q.flags;
+  }
+  r.z = warp_sum(r.z);
+  r.n = __reduce_add_sync(0xffffffffu, r.n);
+  r.flags = __reduce_or_sync(0xffffffffu, r.flags);
+  s_sum[warp][lane] = sum;
+  s_cnt[warp][lane] = cnt;
+  if (lane == 0) s_warp[warp] = r;
+  __syncthreads();
+  if (warp == 0) {  // lane = expert
+    r = s_warp[lane];  // kFinRuns == 32
     r.z = warp_sum(r.z);
     r.n = __reduce_add_sync(0xffffffffu, r.n);
     r.flags = __reduce_or_sync(0xffffffffu, r.flags);
-    if (threadIdx.x == 0) s_seq = r;
+#pragma unroll
+    for (int q = 1; q < kFinRuns; ++q) {
+      sum += s_sum[q][lane];
+      cnt += s_cnt[q][lane];
+    }
+    const float inv_n = r.n > 0 ? 1.f / static_cast<float>(r.n) : 0.f;
+    const float P = sum * inv_n;
+    if (e < E) {
+      a.counts[static_cast<size_t>(s) * E + e] = cnt;
+      a.probs[static_cast<size_t>(s) * E + e] = P;
+    }
+    const float fp = warp_sum(static_cast<float>(cnt) * P);
+    if (lane == 0) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer_smem_addr(s_bal + cg, 0)), "f"(fp) : "memory");
   }
-  __syncthreads();
-  SeqSum r = s_seq;
-  if (threadIdx.x < E) {
-    for (int q = 1; q < runs; ++q) {
-      sum += s_sum[q * ep + threadIdx.x];
-      cnt += s_cnt[q * ep + threadIdx.x];
+  cluster_sync();
+  if (cg != 0) return;
+  if (threadIdx.x == 0) {
+    float b = 0.f;
+    for (int q = 0; q < groups; ++q) b += s_bal[q];
+    r.bal = r.n > 0 ? b * static_cast<float>(E) / static_cast<float>(a.k) / static_cast<float>(r.n) : 0.f;
+    a.tokens[s] = r.n;
+    if (a.S == 1) {
+      finish_all(a, r.bal, r.z, r.n, r.n > 0 ? 1 : 0, r.flags);
+    } else {
+      a.pseq[s] = r;
+      __threadfence();
+      s_last = atomicAdd(a.ticket, 1) == a.S - 1;
+      if (s_last) __threadfence();
     }
   }
-  finish_seq(a, s, sum, cnt, r, s_w);
-  if (a.S == 1) {
-    if (threadIdx.x == 0) finish_all(a, r.n > 0 ? r.bal : 0.f, r.z, r.n, r.n > 0 ? 1 : 0, r.flags);
-    return;
-  }
-  if (threadIdx.x == 0) {
-    a.pseq[s] = r;
-    __threadfence();
-    s_last = atomicAdd(a.ticket, 1) == a.S - 1;
-    if (s_last) __threadfence();
-  }
+  if (a.S == 1) return;
   __syncthreads();
   if (!s_last || threadIdx.x >= 32) return;
   float bal = 0.f, z = 0.f;
@@ -402,7 +449,7 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(const BalArgs a) 
     float dot = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      p[j] = some ? expf(p[j] - lse) : 0.f;
+      p[j] = some ? __expf(p[j] - lse) : 0.f;
       dot = fmaf(f[j], p[j], dot);
     }
     dot = group_sum(dot, G);
@@ -565,7 +612,8 @@ moe_status moe_balance_forward(const moe_balance_config *cfg, const float *logit
   }));
   if (a.S * a.nbs == 1) return MOE_OK;
   return timed("balance_finish", s, [&] {
-    return launch_pdl(balance_finish_kernel, dim3(a.S), dim3(kFinThreads), 0, s, 1, a);
+    const int groups = (a.E + kFinCols - 1) / kFinCols;
+    return launch_pdl(balance_finish_kernel, dim3(a.S * groups), dim3(kFinThreads), 0, s, groups, a);
   });
 }
 
