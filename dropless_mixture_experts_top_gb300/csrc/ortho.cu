@@ -1032,6 +1032,136 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const __grid
   }
 }
 
+// ---------------------------------------------------------------- Gram products of few tiles
+//
+// A Gram product reduces over the long side and has only the short side's tiles: two
+// 520 x 2452 matrices are 30 tiles of 20 stages each on 152 SMs.  Here a cluster of
+// `split` CTAs works on one tile of 128 x 128, each on a share of the reduction; the
+// partial sums (in the operand ring, free by then) meet through distributed shared
+// memory, each CTA adding a share of the rows in the order of the CTAs.
+constexpr int kSplitThreads = 256, kMaxSplit = 8;
+constexpr int kSplitStride = BM + 4;  // floats of a row of partial sums
+static_assert(BM * kSplitStride * 4 <= kStages * kStageBytes, "the partial sums fit the ring");
+constexpr int kSplitSmem = kStages * kStageBytes + 1024 /*align*/;
+
+template <int MAJOR>
+__global__ void __launch_bounds__(kSplitThreads, 1)
+    ortho_gram_split_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm_mn,
+                            const ProductArgs p, int split) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_done;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  uint8_t *smem =
+      reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  float *part = reinterpret_cast<float *>(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], 1);
+    }
+    mbar_init(&s_done, 1);
+    s_abort = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(MAJOR == kMN ? &tm_mn : &tm);
+  }
+  if (warp == 1) tmem_alloc(&s_tmem, BM);
+  griddep_wait();  // the set-up above overlaps the previous kernel's end; its outputs are read below
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const TileAt t = tile_of<kGram, 1>(static_cast<int>(blockIdx.x) / split, p);
+  const int nkb = (p.K + BK - 1) / BK, nst = (nkb + 1) / 2;
+  const int st0 = nst * rank / split, st1 = nst * (rank + 1) / split;  // this CTA's stages
+  // (a wait that runs out is flagged; the kernel goes on, so that no barrier misses a thread)
+  if (warp == 0 && lane == 0) {
+    for (int st = st0; st < st1; ++st) {
+      const int i = (st - st0) % kStages;
+      if (!mbar_wait(&s_empty[i], (((st - st0) / kStages) & 1) ^ 1, &s_abort)) break;
+      mbar_arrive_expect_tx(&s_full[i], kStageBytes);
+      uint8_t *sa = smem + i * kStageBytes;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k0 = (st * 2 + h) * BK;
+        load_operand<MAJOR, 1>(sa + h * kHalf, &tm, &tm_mn, &s_full[i], 0, k0, t.m0, t.m0, t.b);
+        load_operand<MAJOR, 1>(sa + (2 + h) * kHalf, &tm, &tm_mn, &s_full[i], 0, k0, t.n0, t.n0, t.b);
+      }
+    }
+  } else if (warp == 1 && lane == 0) {
+    for (int st = st0; st < st1; ++st) {
+      const int i = (st - st0) % kStages;
+      if (!mbar_wait(&s_full[i], ((st - st0) / kStages) & 1, &s_abort)) break;
+      tc_fence_after();
+      const uint32_t ab = smem_addr(smem + i * kStageBytes), bb = ab + 2 * kHalf;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (st * 2 + h < nkb) {
+#pragma unroll
+          for (int j = 0; j < BK / 16; ++j)
+            tc_mma_f16_one(tmem, operand_desc(ab + h * kHalf, j, MAJOR == kMN),
+                           operand_desc(bb + h * kHalf, j, MAJOR == kMN),
+                           idesc_f16(BM, BM, MAJOR == kMN, MAJOR == kMN), ((st - st0) | h | j) != 0 ? 1u : 0u);
+        }
+      tc_commit(&s_empty[i]);
+    }
+    tc_commit(&s_done);
+  }
+  __syncwarp();
+  if (!mbar_wait(&s_done, 0, &s_abort) && lane == 0) flag_status(p.status, kDevWaitTimeout);
+  __syncwarp();
+  tc_fence_after();
+  {
+    const int q = warp & 3, half = warp >> 2, row = q * 32 + lane;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t acc[32];
+      tmem_ld32(tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 64 + h * 32, acc);
+      tmem_ld_wait();
+      float4 *dst = reinterpret_cast<float4 *>(part + row * kSplitStride + half * 64 + h * 32);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        dst[e] = make_float4(__uint_as_float(acc[4 * e]), __uint_as_float(acc[4 * e + 1]),
+                             __uint_as_float(acc[4 * e + 2]), __uint_as_float(acc[4 * e + 3]));
+    }
+  }
+  tc_fence_before();
+  cluster_sync();  // every CTA's partial sums are there
+  float c = p.c;
+  if (p.fac) c *= p.fac[t.b] * p.fac[t.b];
+  uint16_t *out = p.out + t.b * p.stride;
+  const int share = BM / split;
+  for (int i = threadIdx.x; i < share * (BM / 8); i += kSplitThreads) {
+    const int r = rank * share + i / (BM / 8), c8 = i % (BM / 8) * 8;
+    if (t.m0 + r >= p.M || t.n0 + c8 >= p.ld) continue;
+    float4 v[kMaxSplit][2];
+#pragma unroll
+    for (int o = 0; o < kMaxSplit; ++o)
+      if (o < split) {
+        const uint32_t at = peer_smem_addr(part + r * kSplitStride + c8, o);
+        v[o][0] = ld_cluster_f32x4(at);
+        v[o][1] = ld_cluster_f32x4(at + 16);
+      }
+#pragma unroll
+    for (int o = 1; o < kMaxSplit; ++o)
+      if (o < split) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          v[0][h].x += v[o][h].x, v[0][h].y += v[o][h].y, v[0][h].z += v[o][h].z, v[0][h].w += v[o][h].w;
+      }
+    *reinterpret_cast<uint4 *>(out + (t.m0 + r) * static_cast<int64_t>(p.ld) + t.n0 + c8) =
+        make_uint4(pack_half2(v[0][0].x * c, v[0][0].y * c), pack_half2(v[0][0].z * c, v[0][0].w * c),
+                   pack_half2(v[0][1].x * c, v[0][1].y * c), pack_half2(v[0][1].z * c, v[0][1].w * c));
+  }
+  cluster_sync();  // no CTA leaves while another reads its sums
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, BM);
+  }
+}
+
 // ---------------------------------------------------------------- host side
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -1092,6 +1222,33 @@ cudaError_t launch_groups(const Maps &a, const Maps &b, ProductArgs p, int sms, 
   const int64_t tiles = static_cast<int64_t>(p.per) * p.batch;
   return launch_pdl(kernel, dim3(static_cast<unsigned>(CG * (tiles < groups ? tiles : groups))), dim3(kGemmThreads),
                     kGemmSmem, s, CG, a.k, a.mn, b.k, b.mn, p);
+}
+
+// CTAs per tile of a Gram product; 1: no split.  The exchange costs about 5 us, so
+// only reductions from kSplitStages stages of 128 on are split, over the CTAs that
+// the tiles leave idle.  Measured, split and not: 1 x 4000 x 400 134 and 161 us,
+// 1 x 1024 x 4096 184 and 200, 2 x 520 x 2452 156 and 163; but 3 x 1000 x 333 110 and
+// 102, 1 x 768 x 768 120 and 113 (both sides of 1 x 2048 x 768 the same).
+constexpr int kSplitStages = 17;
+int gram_split(int batch, int n, int m) {
+  const int64_t t = (n + BM - 1) / BM, tiles = batch * t * (t + 1) / 2;
+  int split = 1;
+  if ((m + 2 * BK - 1) / (2 * BK) >= kSplitStages)
+    while (split < kMaxSplit && 2 * split * tiles <= 152) split *= 2;
+  return split;
+}
+
+template <int MAJOR>
+cudaError_t launch_gram_split(const Maps &x, ProductArgs p, int split, cudaStream_t s) {
+  static DeviceOnce once;
+  auto kernel = ortho_gram_split_kernel<MAJOR>;
+  const cudaError_t e = once.get(
+      [&](int *) { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSplitSmem); });
+  if (e != cudaSuccess) return e;
+  p.nm = p.nn = (p.N + BM - 1) / BM;
+  p.per = p.nn * (p.nn + 1) / 2;
+  return launch_pdl(kernel, dim3(p.per * p.batch * split), dim3(kSplitThreads), kSplitSmem, s, split, x.k, x.mn, p,
+                    split);
 }
 
 template <int KIND, int AM, int BMAJ>
@@ -1313,7 +1470,10 @@ moe_status moe_ortho_update(const moe_ortho_config *cfg, const float *coefs, con
     p.c = 1.f / (kSigma * kSigma);
     p.fac = fac;
     p.out = reinterpret_cast<uint16_t *>(nb[0]);
+    const int split = pair ? 1 : gram_split(B, n, m);
     return timed("ortho_gram", st, [&] {
+      if (split > 1)
+        return tall ? launch_gram_split<kMN>(mx[x], p, split, st) : launch_gram_split<kK>(mx[x], p, split, st);
       return tall ? launch_product<kGram, kMN, kMN>(mx[x], mx[x], p, pair, di.sms, st)
                   : launch_product<kGram, kK, kK>(mx[x], mx[x], p, pair, di.sms, st);
     });

@@ -83,6 +83,17 @@ def test_narrow(B, R, C, dtype):
     assert o.status() == {"update": 0}
 
 
+# long sides that split the Gram product's reduction over clusters of 2 to 8 CTAs, in both orientations
+@pytest.mark.parametrize("B,R,C", [(1, 2200, 160), (2, 200, 3000), (3, 2501, 333), (1, 900, 2320), (7, 300, 2200)])
+def test_long_reductions(B, R, C):
+    g = grad(B, R, C, "bf16", 41)
+    o = moe.Orthogonaliser(B, R, C)
+    out = o.update(g)
+    assert o.status() == {"update": 0}
+    near(out, reference(g, moe.MUON_COEFS))
+    assert torch.equal(out, o.update(g))
+
+
 def test_singular_values_end_near_one():
     g = grad(2, 384, 700, "fp32", 2)
     s = torch.linalg.svdvals(moe.Orthogonaliser(2, 384, 700, dtype="fp32").update(g).float())
