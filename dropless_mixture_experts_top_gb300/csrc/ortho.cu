@@ -303,6 +303,7 @@ struct ProductArgs {
   int per;                // tiles per matrix (symmetric: mt <= nt)
   float a, b, c;          // kSquare; c also the factor of the other products
   const float *fac;       // a matrix's factor besides c (the first step's X), or null
+  bool sectors;           // kLast: every row of out starts on 32 bytes
   const uint16_t *s;      // kSquare: S
   uint16_t *out;
   int ld;                 // row stride of s and out
@@ -363,6 +364,20 @@ __device__ __forceinline__ void tile_to_rows(const uint8_t *tile, uint16_t *g0, 
   }
 }
 
+// One 32-byte sector (32-byte aligned) to or from a lane: whole sectors, although
+// every lane has a row of its own.
+__device__ __forceinline__ void ld_sector(const void *p, uint4 &a, uint4 &b) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void st_sector(void *p, const uint4 &a, const uint4 &b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
+               "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
 constexpr int chunks_of(int cg) { return tile_size(cg) / 64; }  // 32-column chunks of a warp's half of the columns
 
 // kSquare: S under the warp's 32 rows and half of the tile's columns, a row per
@@ -378,8 +393,10 @@ struct SChunks {
     for (int j = 0; j < kChunks; ++j) {
       const bool in = row0 + lane < p.M && t.n0 + part * (TS / 2) + 32 * j < p.N;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        v[j][i] = in ? *reinterpret_cast<const uint4 *>(s + 32 * j + 8 * i) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < 4; i += 2) {
+        v[j][i] = v[j][i + 1] = make_uint4(0, 0, 0, 0);
+        if (in) ld_sector(s + 32 * j + 8 * i, v[j][i], v[j][i + 1]);
+      }
     }
   }
 };
@@ -433,11 +450,21 @@ __device__ __forceinline__ void epilogue(const TileAt &t, uint32_t tb, int row0,
     if constexpr (KIND == kLast) {  // out [M,N] itself, bf16
       const int ncols = min(32, p.N - c0);
       uint16_t *g0 = out + row0 * static_cast<int64_t>(p.ld) + c0;
+      uint4 w[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<uint4 *>(tile + swz(lane, q)) =
-            make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
-                       pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+        w[q] = make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                          pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+      if (p.sectors) {
+        if (lane < nrows) {
+          uint16_t *row = g0 + lane * static_cast<int64_t>(p.ld);
+          st_sector(row, w[0], w[1]);
+          if (ncols > 16) st_sector(row + 16, w[2], w[3]);
+        }
+        continue;
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4 *>(tile + swz(lane, q)) = w[q];
       __syncwarp();
       if ((p.ld & 7) == 0) {
         tile_to_rows(tile, g0, p.ld, nrows, ncols);
@@ -448,15 +475,15 @@ __device__ __forceinline__ void epilogue(const TileAt &t, uint32_t tb, int row0,
                 *reinterpret_cast<const uint16_t *>(tile + swz(r, lane >> 3) + (lane & 7) * 2);
       }
       __syncwarp();
-    } else {  // padded rows: whole chunks
+    } else if (lane < nrows) {  // padded rows: whole chunks, a row per lane
+      uint16_t *g0 = out + (row0 + lane) * static_cast<int64_t>(p.ld) + c0;
+      uint4 w[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<uint4 *>(tile + swz(lane, q)) =
-            make_uint4(pack_half2(v[8 * q], v[8 * q + 1]), pack_half2(v[8 * q + 2], v[8 * q + 3]),
-                       pack_half2(v[8 * q + 4], v[8 * q + 5]), pack_half2(v[8 * q + 6], v[8 * q + 7]));
-      __syncwarp();
-      tile_to_rows(tile, out + row0 * static_cast<int64_t>(p.ld) + c0, p.ld, nrows, 32);
-      __syncwarp();
+        w[q] = make_uint4(pack_half2(v[8 * q], v[8 * q + 1]), pack_half2(v[8 * q + 2], v[8 * q + 3]),
+                          pack_half2(v[8 * q + 4], v[8 * q + 5]), pack_half2(v[8 * q + 6], v[8 * q + 7]));
+      st_sector(g0, w[0], w[1]);
+      st_sector(g0 + 16, w[2], w[3]);
     }
   }
 }
@@ -1321,11 +1348,11 @@ OrthoLayout ortho_layout(const moe_ortho_config *c) {
   L.chunks = static_cast<int>((numel + L.chunk - 1) / L.chunk);
   L.ldx = pad64(c->C);
   L.lds = pad64(static_cast<int>(n));
-  size_t o = kHeader;
   if (is_small(c)) {
-    L.total = o;
+    L.total = kHeader;
     return L;
   }
+  size_t o = 0;  // from the first multiple of 256 bytes past the header on
   auto take = [&o](size_t bytes) {
     const size_t at = o;
     o += align256(bytes);
@@ -1339,7 +1366,7 @@ OrthoLayout ortho_layout(const moe_ortho_config *c) {
   L.n[0] = take(square);
   L.n[1] = take(square);
   L.n[2] = take(fuse_steps(c->batch, static_cast<int>(n), c->R < c->C ? c->C : c->R) ? square : 0);
-  L.total = o;
+  L.total = kHeader + 256 + o;
   return L;
 }
 
@@ -1426,6 +1453,9 @@ moe_status moe_ortho_update(const moe_ortho_config *cfg, const float *coefs, con
       return cfg->dtype == MOE_DTYPE_BF16 ? launch_small<uint16_t>(q, B, st) : launch_small<float>(q, B, st);
     });
   }
+  // (sectors are stored, which need 32-byte alignment; the scratch has 16)
+  uint8_t *body = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(sc) + kHeader + 255) &
+                                              ~static_cast<uintptr_t>(255));
   PrepArgs a{};
   a.g = g;
   a.mom = momentum;
@@ -1437,9 +1467,9 @@ moe_status moe_ortho_update(const moe_ortho_config *cfg, const float *coefs, con
   a.ld = L.ldx;
   a.chunk = L.chunk;
   a.chunks = L.chunks;
-  a.part = reinterpret_cast<float *>(sc + L.part);
-  a.fac = reinterpret_cast<float *>(sc + L.fac);
-  a.x = reinterpret_cast<uint16_t *>(sc + L.x0);
+  a.part = reinterpret_cast<float *>(body + L.part);
+  a.fac = reinterpret_cast<float *>(body + L.fac);
+  a.x = reinterpret_cast<uint16_t *>(body + L.x0);
   a.x_stride = static_cast<int64_t>(R) * L.ldx;
   a.status = status;
   MOE_TRY(timed("ortho_norm_scale", st, [&] {
@@ -1448,7 +1478,7 @@ moe_status moe_ortho_update(const moe_ortho_config *cfg, const float *coefs, con
   // X's rows along C with C contiguous: the Gram product reduces over m, the
   // update over n, so one of them reads X K-major and the other MN-major
   const bool pairs = fuse_steps(B, n, m), pair = use_pairs(B, R, C);
-  uint8_t *xb[2] = {sc + L.x0, sc + L.x1}, *nb[3] = {sc + L.n[0], sc + L.n[1], sc + L.n[2]};
+  uint8_t *xb[2] = {body + L.x0, body + L.x1}, *nb[3] = {body + L.n[0], body + L.n[1], body + L.n[2]};
   Maps mx[2], mn[3];
   auto make = [&](Maps *mm, const void *ptr, int inner, int rows, int ld) {
     return map3(&mm->k, ptr, inner, rows, B, ld, 128) && map3(&mm->mn, ptr, inner, rows, B, ld, 64);
@@ -1505,6 +1535,7 @@ moe_status moe_ortho_update(const moe_ortho_config *cfg, const float *coefs, con
     p.ld = last ? C : L.ldx;
     p.stride = static_cast<int64_t>(R) * p.ld;
     p.c = last ? scale / kSigma : 1.f;
+    p.sectors = last && C % 16 == 0 && (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
     p.fac = fac;
     p.out = last ? static_cast<uint16_t *>(out) : reinterpret_cast<uint16_t *>(xb[x ^ 1]);
     return timed("ortho_apply", st, [&] {

@@ -83,6 +83,30 @@ def test_narrow(B, R, C, dtype):
     assert o.status() == {"update": 0}
 
 
+# every kind of row of the result: whole sectors (C % 16), whole vectors (C % 8), neither; results, inputs and scratch
+# that start on a multiple of 16 bytes and not of 32
+@pytest.mark.parametrize("C", [304, 312, 315, 64])
+@pytest.mark.parametrize("R", [200, 650])
+@pytest.mark.parametrize("first", [16, 8])
+def test_result_rows(R, C, first):
+    n = 2 * R * C
+    g = torch.zeros(n + first, device="cuda", dtype=torch.bfloat16)[first:].view(2, R, C)
+    g.copy_(grad(2, R, C, "bf16", 42))
+    m = torch.zeros(n + first // 2, device="cuda")[first // 2:].view(2, R, C)
+    base = torch.full((first + n + 16,), 7.0, device="cuda", dtype=torch.bfloat16)
+    out = base[first:first + n].view(2, R, C)
+    o = moe.Orthogonaliser(2, R, C)
+    o.scratch = torch.empty(o.scratch.numel() + 2 * first, dtype=torch.uint8, device="cuda")[2 * first:]
+    o._scratch = o.scratch.data_ptr()
+    assert out.data_ptr() % 32 == 2 * first % 32 and o._scratch % 32 == 2 * first % 32
+    o.update(g, out=out)
+    near(out, reference(g, moe.MUON_COEFS))
+    o.update(g, momentum=m, out=out)
+    near(out, reference(g, moe.MUON_COEFS))
+    assert o.status() == {"update": 0}
+    assert bool((base[:first] == 7).all()) and bool((base[first + n:] == 7).all())
+
+
 # long sides that split the Gram product's reduction over clusters of 2 to 8 CTAs, in both orientations
 @pytest.mark.parametrize("B,R,C", [(1, 2200, 160), (2, 200, 3000), (3, 2501, 333), (1, 900, 2320), (7, 300, 2200)])
 def test_long_reductions(B, R, C):
