@@ -301,6 +301,7 @@ struct ProductArgs {
   int batch, M, N, K;
   int nm, nn;             // tiles along the rows, along the columns
   int per;                // tiles per matrix (symmetric: mt <= nt)
+  bool back;              // the matrices from the last one to the first
   float a, b, c;          // kSquare; c also the factor of the other products
   const float *fac;       // a matrix's factor besides c (the first step's X), or null
   bool sectors;           // kLast: every row of out starts on 32 bytes
@@ -321,6 +322,7 @@ __device__ __forceinline__ TileAt tile_of(int tile, const ProductArgs &p) {
   TileAt t;
   t.b = tile / p.per;
   int r = tile - t.b * p.per;
+  if (p.back) t.b = p.batch - 1 - t.b;
   if constexpr (KIND == kGram || KIND == kSquare) {
     int nt = 0;
     while (r > nt) r -= ++nt;
@@ -715,6 +717,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
 }
 
+// After a wait has run out: time (bounded) for copies and MMAs in flight to end
+// before shared memory and TMEM are given up.
+__device__ __forceinline__ void settle() {
+  const long long t0 = clock64();
+  while (clock64() - t0 < 20000000LL) {
+  }
+}
+
 // ---------------------------------------------------------------- small matrices
 //
 // n <= 128: a cluster of CTAs keeps a whole matrix in shared memory from the first
@@ -1052,6 +1062,8 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const __grid
     fence_async();
     __syncthreads();
   }
+  if (threadIdx.x == 0 && s_abort) settle();
+  __syncthreads();
   if (p.cluster > 1) cluster_sync();  // no CTA leaves while another may read it
   if (warp == 0) {
     tc_fence_after();
@@ -1182,6 +1194,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
         make_uint4(pack_half2(v[0][0].x * c, v[0][0].y * c), pack_half2(v[0][0].z * c, v[0][0].w * c),
                    pack_half2(v[0][1].x * c, v[0][1].y * c), pack_half2(v[0][1].z * c, v[0][1].w * c));
   }
+  if (threadIdx.x == 0 && s_abort) settle();
   cluster_sync();  // no CTA leaves while another reads its sums
   if (warp == 1) {
     tc_fence_after();
@@ -1487,6 +1500,13 @@ moe_status moe_ortho_update(const moe_ortho_config *cfg, const float *coefs, con
     if (!make(&mx[i], xb[i], C, R, L.ldx)) return MOE_ERR_CUDA;
   for (int i = 0; i < (pairs ? 3 : 2); ++i)
     if (!make(&mn[i], nb[i], n, n, L.lds)) return MOE_ERR_CUDA;
+  // Every launch goes through the matrices the other way round, so that it starts with
+  // those that the last one left in the L2.
+  bool back = true;
+  auto turn = [&back] {
+    back = !back;
+    return !back;
+  };
   ProductArgs sym{};  // of the products into an n x n matrix
   sym.batch = B;
   sym.status = status;
@@ -1499,6 +1519,7 @@ moe_status moe_ortho_update(const moe_ortho_config *cfg, const float *coefs, con
     p.K = m;
     p.c = 1.f / (kSigma * kSigma);
     p.fac = fac;
+    p.back = turn();
     p.out = reinterpret_cast<uint16_t *>(nb[0]);
     const int split = pair ? 1 : gram_split(B, n, m);
     return timed("ortho_gram", st, [&] {
@@ -1512,6 +1533,7 @@ moe_status moe_ortho_update(const moe_ortho_config *cfg, const float *coefs, con
     ProductArgs p = sym;
     p.K = n;
     p.a = coefs[3 * step];
+    p.back = turn();
     p.b = coefs[3 * step + 1];
     p.c = coefs[3 * step + 2];
     p.s = reinterpret_cast<const uint16_t *>(nb[in]);
@@ -1524,6 +1546,7 @@ moe_status moe_ortho_update(const moe_ortho_config *cfg, const float *coefs, con
     p.K = n;
     p.c = 1.f;
     p.out = reinterpret_cast<uint16_t *>(nb[to]);
+    p.back = turn();
     return timed("ortho_commuting", st,
                  [&] { return launch_product<kGram, kSym, kSym>(mn[x], mn[y], p, pair, di.sms, st); });
   };
@@ -1533,6 +1556,7 @@ moe_status moe_ortho_update(const moe_ortho_config *cfg, const float *coefs, con
     p.N = C;
     p.K = n;
     p.ld = last ? C : L.ldx;
+    p.back = turn();
     p.stride = static_cast<int64_t>(R) * p.ld;
     p.c = last ? scale / kSigma : 1.f;
     p.sectors = last && C % 16 == 0 && (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
