@@ -392,6 +392,14 @@ class Norm:
 _F32, _I32, _U8 = (torch.float32,), (torch.int32,), (torch.uint8, torch.bool)
 
 
+def _status_scratch(n, device):
+    """A scratch buffer whose status reads 0 before its first call, ready for use on any stream."""
+    s = torch.empty(n, dtype=torch.uint8, device=device)
+    s[:256] = 0
+    torch.cuda.current_stream(device).synchronize()
+    return s
+
+
 class BalanceLoss:
     """The router's balance loss and z loss over `sequences` equal parts of T
     tokens, with per-expert counts, and their gradient for the logits."""
@@ -404,7 +412,7 @@ class BalanceLoss:
         self._dev, self._fwd, self._bwd = self.device.index, lib().moe_balance_forward, lib().moe_balance_backward
         self._te, self._tk, self._t, self._se, self._s, self._two = (
             torch.Size(s) for s in ((T, E), (T, k), (T,), (sequences, E), (sequences,), (2,)))
-        self.fwd_scratch = torch.empty(n.value, dtype=torch.uint8, device=self.device)
+        self.fwd_scratch = _status_scratch(n.value, self.device)
         self._scratch = self.fwd_scratch.data_ptr()
 
     def forward(self, logits, topk_idx, mask=None, out=None, stream=None) -> dict:
@@ -464,7 +472,7 @@ class Orthogonaliser:
         self._shape = torch.Size((batch, R, C))
         self._dev, self._update = self.device.index, lib().moe_ortho_update
         self._coefs = (ctypes.c_float * len(coefs))(*coefs)
-        self.scratch = torch.empty(n.value, dtype=torch.uint8, device=self.device)
+        self.scratch = _status_scratch(n.value, self.device)
         self._scratch = self.scratch.data_ptr()
 
     def update(self, g, momentum=None, beta=0.95, nesterov=True, scale=1.0, out=None, stream=None):

@@ -241,3 +241,10 @@ def test_arguments_are_checked():
                dict(logits=torch.empty(8, 64, device="cuda").t())):
         with pytest.raises(ValueError):
             b.forward(**{**dict(logits=lg, topk_idx=idx), **kw})
+
+
+def test_status_is_clear_before_the_first_call():
+    size = moe.BalanceLoss(512, 8, 2, 1).fwd_scratch.numel()
+    used = torch.full((size,), 0x5A, dtype=torch.uint8, device="cuda")
+    del used  # the allocator hands the same memory out again
+    assert moe.BalanceLoss(512, 8, 2, 1).status() == {"forward": 0}

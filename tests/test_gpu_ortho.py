@@ -274,3 +274,10 @@ def test_arguments_are_checked():
     for coefs in ((), ((1.0, 2.0),)):
         with pytest.raises(ValueError):
             moe.Orthogonaliser(2, 64, 96, coefs=coefs)
+
+
+def test_status_is_clear_before_the_first_call():
+    size = moe.Orthogonaliser(2, 300, 200).scratch.numel()
+    used = torch.full((size,), 0x5A, dtype=torch.uint8, device="cuda")
+    del used  # the allocator hands the same memory out again
+    assert moe.Orthogonaliser(2, 300, 200).status() == {"update": 0}
