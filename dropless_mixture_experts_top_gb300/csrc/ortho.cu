@@ -76,7 +76,7 @@ struct PrepArgs {
   int C, ld;      // columns, and X's row stride
   int chunk;      // elements per block
   int chunks;     // blocks per matrix
-  float *part;    // [B][chunks] sums of squares; infinite where a value does not fit
+  float *part;    // [B][chunks] sums of squares; negative where a value does not fit
   float *fac;     // [B] what X is to be multiplied with
   uint16_t *x;    // [B][R][ld] fp16
   int64_t x_stride;
@@ -219,10 +219,11 @@ __global__ void __launch_bounds__(kPrepThreads) ortho_prepare_kernel(const PrepA
     }
   }
   acc = block_sum(acc, s_w);
-  // a value past fp16's range, marked by the sign (the sum itself is not negative)
+  // a value past fp16's range, marked by the sign (the sum itself is not negative,
+  // and a NaN stays one)
   const bool fits = __syncthreads_and(!(most * f0 > kFits));
   if (threadIdx.x == 0)
-    a.part[static_cast<size_t>(blockIdx.y) * a.chunks + blockIdx.x] = fits ? acc : -fmaxf(acc, 1e-38f);
+    a.part[static_cast<size_t>(blockIdx.y) * a.chunks + blockIdx.x] = fits ? acc : -(acc < 1e-38f ? 1e-38f : acc);
 }
 
 // A matrix's factor from its sums; X again, by the blocks of the matrix, where the

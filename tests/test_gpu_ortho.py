@@ -202,6 +202,17 @@ def test_zeros_and_bad_matrices_stay_their_own():
     assert o.status() == {"update": 0}  # nothing of the last call is left
 
 
+@pytest.mark.parametrize("R,C", [(136, 200), (136, 201), (64, 200)])
+@pytest.mark.parametrize("momentum", [False, True])
+def test_an_infinity_beside_a_nan_is_reported(R, C, momentum):
+    g = grad(3, R, C, "bf16", 9)
+    g[1, 3, 4], g[1, 3, 6], g[1, 3, 5] = float("nan"), float("nan"), float("inf")
+    o = moe.Orthogonaliser(3, R, C)
+    out = o.update(g, momentum=torch.zeros(3, R, C, device="cuda") if momentum else None).float()
+    assert o.status() == {"update": moe.DEV_NONFINITE_UPDATE}
+    assert bool(torch.isnan(out[1]).all()) and bool(torch.isfinite(out[[0, 2]]).all())
+
+
 def test_nothing_past_a_matrix_is_read_or_written():
     """Matrices of odd sizes between guard values: the neighbours of out, g and momentum keep theirs, and NaNs around
     g have no part."""
