@@ -21,10 +21,11 @@
 // integers, added in any order).  A single short sequence is one block and one
 // kernel.
 //
-// Bounds, measured: the backward moves 12 bytes per logit at 88% of the copy rate
-// (131072 x 250: 66 us); the forward of as many (4 bytes per logit, 20 us at that
-// rate) takes 43 to 55 us, for its exponentials, shuffles and column sums; below
-// some 10,000 tokens it is the latency of its two kernels (16384 x 128: 14 us).
+// Bounds, measured: the backward moves 12 bytes per logit at 96% of the copy rate
+// (131072 x 250: 60 us); the forward of as many (4 bytes per logit, 20 us at that
+// rate) takes 38 to 51 us, for the latency of a token's chain of load, maximum,
+// exponentials and sum with the registers that its columns need; below some 20,000 tokens it is the latency of its two kernels
+// (16384 x 128 in four sequences: 12 us) or its one (512 x 8: 6).
 #include <math.h>
 
 #include <type_traits>
@@ -123,6 +124,58 @@ __device__ __forceinline__ float group_max(float v, int G) {
   return v;
 }
 
+// v = exp(v - at) in pairs: 2^((v - at) log2 e) with the difference taken first, so
+// that rows of the type's lowest value stay exact; what is below 2^-126 is zero.
+// The compiler's exponential scales such values instead, three operations more each:
+// with it 131072 x 256 forward took 43 us, 38 with this; 131072 x 250 55 and 51.
+constexpr float kLog2e = 1.44269504f;
+__device__ __forceinline__ float exp2_flush(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <int NV>
+__device__ __forceinline__ void exp_row(float (&v)[NV], float at) {
+  if constexpr (NV == 1) {
+    v[0] = exp2_flush((v[0] - at) * kLog2e);
+  } else {
+    const F2 a2 = f2(at, at), l2 = f2(kLog2e, kLog2e);
+#pragma unroll
+    for (int j = 0; j < NV; j += 2) {
+      const float2 x = f2_get(f2_mul(f2_sub(f2(v[j], v[j + 1]), a2), l2));
+      v[j] = exp2_flush(x.x);
+      v[j + 1] = exp2_flush(x.y);
+    }
+  }
+}
+// a = v s + a, and the sum of v.
+template <int NV>
+__device__ __forceinline__ void add_scaled(float (&a)[NV], const float (&v)[NV], float s) {
+  if constexpr (NV == 1) {
+    a[0] = fmaf(v[0], s, a[0]);
+  } else {
+    const F2 s2 = f2(s, s);
+#pragma unroll
+    for (int j = 0; j < NV; j += 2) {
+      const float2 x = f2_get(f2_fma(f2(v[j], v[j + 1]), s2, f2(a[j], a[j + 1])));
+      a[j] = x.x;
+      a[j + 1] = x.y;
+    }
+  }
+}
+template <int NV>
+__device__ __forceinline__ float row_sum(const float (&v)[NV]) {
+  if constexpr (NV == 1) {
+    return v[0];
+  } else {
+    F2 t = f2(v[0], v[1]);
+#pragma unroll
+    for (int j = 2; j < NV; j += 2) t = f2_add(t, f2(v[j], v[j + 1]));
+    const float2 x = f2_get(t);
+    return x.x + x.y;
+  }
+}
+
 // One sequence's outputs by its only block: thread e holds expert e's probability
 // sum and count (0 past E).  r: its z sum, tokens and flags; thread 0 gets the
 // sequence's balance term in r.bal.  Every thread of the block calls it.
@@ -211,18 +264,11 @@ __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(const BalArgs a) 
       nan = group_max(nan, G);  // by every lane of the warp: its shuffles name them all
       if (mx == -INFINITY && nan == 0.f) ok = false;
     }
-    float sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      v[j] = __expf(v[j] - mx);
-      sum += v[j];
-    }
-    sum = group_sum(sum, G);
+    exp_row(v, mx);
+    const float sum = group_sum(row_sum(v), G);
     const float lse = mx + logf(sum);  // NaN with a NaN or +inf logit
     if (ok) {
-      const float inv = 1.f / sum;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) col[j] = fmaf(v[j], inv, col[j]);
+      add_scaled(col, v, 1.f / sum);
       if (lane == 0) {
         z = fmaf(lse, lse, z);
         n += 1;
@@ -446,10 +492,11 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(const BalArgs a) 
     if (ADD) load_row<W>(row, E, G, lane, i < i1, 0.f, old);
     fetch(i + step);
     const bool some = lse != INFINITY;  // the token has a part in the losses
+    exp_row(p, lse);
     float dot = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      p[j] = some ? __expf(p[j] - lse) : 0.f;
+      p[j] = some ? p[j] : 0.f;
       dot = fmaf(f[j], p[j], dot);
     }
     dot = group_sum(dot, G);

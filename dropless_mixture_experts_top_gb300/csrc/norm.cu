@@ -9,6 +9,10 @@
 //   dx = r (g - mean g - xh mean(g xh)) (+ d_sum)      (RMS: no mean g)
 //   dw = sum_t dy xh,  db = sum_t dy
 // Both are bound by memory: every input is read and every output written once.
+// Measured as called, bf16: forward with residual 16384 x 4096 80.6 us, 98% of what a
+// copy moves in that time; backward with d_sum 16384 x 2048 47.8 us, 83% (the kernel
+// 41.5 and the sums of its blocks' partial rows the rest).  512 x 128 takes 5.0 us,
+// the launch.
 //
 // Layout: a row is shared by TPR threads (a power of two, 8 to 512), each
 // holding kElems elements, in vectors of 16 bytes that lie TPR vectors apart, so
