@@ -53,6 +53,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "abi.h"
 #include "common.cuh"
@@ -802,7 +803,7 @@ __device__ __forceinline__ uint32_t blk_byte(int row, int c) {
 }
 
 template <class El>
-__global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const __grid_constant__ SmallArgs p) {
+__global__ void __launch_bounds__(kSmallThreads, 2) ortho_small_kernel(const __grid_constant__ SmallArgs p) {
   griddep_wait();  // the previous kernel in the stream has completed
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t s_bar;
@@ -838,45 +839,63 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const __grid
   // this CTA's elements in memory order: rows of `width` elements, `stride` apart
   const int rows = p.tall ? cols : p.n, width = p.tall ? p.n : cols;
   const int64_t base = p.tall ? static_cast<int64_t>(c0) * p.C : c0;
-  // pass 0: advance the momentum and sum the squares; pass 1: store the scaled elements
-  auto each = [&](int pass, float f0) {
+  // i / d for i < 2^15 and d <= 256, from 1 / d: what the half keeps from a whole
+  // number, 2^-9 at least, is above what i / d rounds away
+  auto quotient = [](int i, float inv_d) { return static_cast<int>((static_cast<float>(i) + 0.5f) * inv_d); };
+  // pass 0: advance the momentum and sum the squares; pass 1: store the scaled
+  // elements.  Groups of eight or, in rows that are not whole groups, single elements,
+  // 16 of them in flight (20 x 100 x 252: 75 us, of which 36 are these passes; with one
+  // in flight and rows stored by their lanes 102)
+  auto pass_over = [&](auto vec, int pass, float f0) {
+    constexpr int N = decltype(vec)::value ? 8 : 1, U = decltype(vec)::value ? 4 : 16;  // U loads in flight
     float acc = 0.f;
-    const int unit = p.vec ? 8 : 1, per = width / unit, total = rows * per;
-    for (int i0 = threadIdx.x; i0 < total; i0 += kSmallThreads * 4) {
+    const int per = width / N, total = rows * per;
+    const float inv_per = 1.f / static_cast<float>(per);
+    for (int i0 = threadIdx.x; i0 < total; i0 += kSmallThreads * U) {
+      float f[U][N], mm[U][N];
+      int rr[U];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < U; ++u) {
         const int i = i0 + u * kSmallThreads;
         if (i >= total) break;
-        const int r = i / per, c = (i - r * per) * unit;
-        const int64_t at = base + static_cast<int64_t>(r) * p.C + c;
-        float f[8], mm[8];
-        if (p.vec) {
-          load_el<El, true>(g + at, f);
-          if (mom) load_el<float, true>(mom + at, mm);
-        } else {
-          f[0] = to_f(g[at]);
-          if (mom) mm[0] = mom[at];
-        }
+        rr[u] = quotient(i, inv_per);
+        const int64_t at = base + static_cast<int64_t>(rr[u]) * p.C + (i - rr[u] * per) * N;
+        load_el<El, N == 8>(g + at, f[u]);
+        if (mom) load_el<float, N == 8>(mom + at, mm[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * kSmallThreads;
+        if (i >= total) break;
+        const int r = rr[u], c = (i - r * per) * N;
         if (mom) {
+          float *m = mom + base + static_cast<int64_t>(r) * p.C + c;
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (k < unit) {
-              if (pass == 0) mom[at + k] = mm[k] = fmaf(p.beta, mm[k], f[k]);
-              f[k] = update_of(f[k], mm[k], p.beta, p.nesterov);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (k < unit) {
-            if (pass == 0)
-              acc = fmaf(f[k], f[k], acc);
-            else
-              *reinterpret_cast<uint16_t *>(xs + (p.tall ? blk_byte(c + k, r) : blk_byte(r, c + k))) =
-                  __half_as_ushort(__float2half_rn(f[k] * f0));
+          for (int k = 0; k < N; ++k) {
+            if (pass == 0) m[k] = mm[u][k] = fmaf(p.beta, mm[u][k], f[u][k]);
+            f[u][k] = update_of(f[u][k], mm[u][k], p.beta, p.nesterov);
           }
+        }
+        if (pass == 0) {
+#pragma unroll
+          for (int k = 0; k < N; ++k) acc = fmaf(f[u][k], f[u][k], acc);
+        } else if (N == 1 || p.tall) {
+#pragma unroll
+          for (int k = 0; k < N; ++k)
+            *reinterpret_cast<uint16_t *>(xs + (p.tall ? blk_byte(c + k, r) : blk_byte(r, c + k))) =
+                __half_as_ushort(__float2half_rn(f[u][k] * f0));
+        } else {  // eight columns are one piece of 16 bytes
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[k] = pack_half2(f[u][2 * k % N] * f0, f[u][(2 * k + 1) % N] * f0);
+          *reinterpret_cast<uint4 *>(xs + blk_byte(r, c)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
       }
     }
     return acc;
+  };
+  auto each = [&](int pass, float f0) {
+    return p.vec ? pass_over(std::true_type{}, pass, f0) : pass_over(std::false_type{}, pass, f0);
   };
   float sq = warp_sum(each(0, 0.f));
   if (lane == 0) s_red[warp] = sq;
@@ -921,6 +940,7 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const __grid
 
   for (int step = 0; step < p.steps; ++step) {
     const float ca = p.coefs[3 * step], cb = p.coefs[3 * step + 1], cc = p.coefs[3 * step + 2];
+    const float own = 0.5f * ca;  // X's own part of the update, which P leaves out
     // S = X X^T / sigma^2
     product([&] {
       for (int k = 0; k < p.nblk; ++k)
@@ -958,29 +978,60 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const __grid
     tc_fence_before();
     if (p.cluster > 1) {
       cluster_sync();  // every CTA's partial sums are there
-      // this CTA's share of the rows: 128 / cluster, four columns per thread
-      const int share = kSmallN / p.cluster, groups = kn * 16;
-      for (int i = threadIdx.x; i < share * groups; i += kSmallThreads) {
-        const int r = rank * share + i / groups, c = i % groups * 4;
-        float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int o0 = 0; o0 < p.cluster; o0 += 8) {  // eight CTAs' sums in flight
-          float4 v[8];
+      // this CTA's share of the rows: 128 / cluster, four columns at a time, 16 loads
+      // in flight (20 x 128 x 512: 52 us; one row at a time 58)
+      auto add_parts = [&](auto ctas, auto rows_at_once) {
+        constexpr int CC = decltype(ctas)::value, U = decltype(rows_at_once)::value;
+        const int groups = kn * 16, total = kSmallN / p.cluster * groups;
+        for (int i0 = threadIdx.x; i0 < total; i0 += kSmallThreads * U) {
+          float4 t[U];
 #pragma unroll
-          for (int o = 0; o < 8; ++o)
-            v[o] = o0 + o < p.cluster ? ld_cluster_f32x4(peer_smem_addr(part + r * kPartStride + c, o0 + o))
-                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int u = 0; u < U; ++u) t[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int o0 = 0; o0 < p.cluster; o0 += CC) {
+            float4 v[U][CC];
 #pragma unroll
-          for (int o = 0; o < 8; ++o) t.x += v[o].x, t.y += v[o].y, t.z += v[o].z, t.w += v[o].w;
+            for (int u = 0; u < U; ++u) {
+              const int i = min(i0 + u * kSmallThreads, total - 1);
+              const int r = rank * (kSmallN / p.cluster) + i / groups, c = i % groups * 4;
+#pragma unroll
+              for (int o = 0; o < CC; ++o) v[u][o] = ld_cluster_f32x4(peer_smem_addr(part + r * kPartStride + c, o0 + o));
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+              for (int o = 0; o < CC; ++o)
+                t[u].x += v[u][o].x, t[u].y += v[u][o].y, t[u].z += v[u][o].z, t[u].w += v[u][o].w;
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * kSmallThreads;
+            if (i >= total) break;
+            const int r = rank * (kSmallN / p.cluster) + i / groups, c = i % groups * 4;
+            const uint32_t lo = pack_half2(t[u].x * inv, t[u].y * inv), hi = pack_half2(t[u].z * inv, t[u].w * inv);
+            for (int o = 0; o < p.cluster; ++o) st_cluster_u32x2(peer_smem_addr(ss + blk_byte(r, c), o), lo, hi);
+          }
         }
-        const uint32_t lo = pack_half2(t.x * inv, t.y * inv), hi = pack_half2(t.z * inv, t.w * inv);
-        for (int o = 0; o < p.cluster; ++o) st_cluster_u32x2(peer_smem_addr(ss + blk_byte(r, c), o), lo, hi);
-      }
+      };
+      const std::integral_constant<int, 1> one;
+      const std::integral_constant<int, 2> two;
+      const std::integral_constant<int, 4> four;
+      const std::integral_constant<int, 8> eight;
+      if (p.cluster == 2)
+        add_parts(two, eight);
+      else if (p.cluster == 4)
+        add_parts(four, four);
+      else if (p.cluster == 8)
+        add_parts(eight, two);
+      else
+        add_parts(eight, one);
       fence_async();
       cluster_sync();
     }
     fence_async();
     __syncthreads();
-    // P = a I + b S + c S S, in S's place
+    // P = a/2 I + b S + c S S, in S's place: P's diagonal runs from a down to about 1, so
+    // that its rounding is smaller with half of a taken out (the result of 13 x 94 x 33
+    // is off by 2.1e-3 instead of 2.5e-3 of itself, bf16 alone by 1.7e-3, for 1 us)
     product([&] {
       for (int k = 0; k < kn; ++k)
 #pragma unroll
@@ -1007,8 +1058,8 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const __grid
             memcpy(&hh, &sw[k], 4);
             const float2 f = __half22float2(hh);
             const int c = half * 64 + h * 32 + 8 * e + 2 * k;
-            const float v0 = fmaf(cc, __uint_as_float(acc[8 * e + 2 * k]), cb * f.x) + (c == row ? ca : 0.f);
-            const float v1 = fmaf(cc, __uint_as_float(acc[8 * e + 2 * k + 1]), cb * f.y) + (c + 1 == row ? ca : 0.f);
+            const float v0 = fmaf(cc, __uint_as_float(acc[8 * e + 2 * k]), cb * f.x) + (c == row ? ca - own : 0.f);
+            const float v1 = fmaf(cc, __uint_as_float(acc[8 * e + 2 * k + 1]), cb * f.y) + (c + 1 == row ? ca - own : 0.f);
             w[k] = pack_half2(v0, v1);
           }
           *at = make_uint4(w[0], w[1], w[2], w[3]);
@@ -1018,7 +1069,7 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const __grid
     tc_fence_before();
     fence_async();
     __syncthreads();
-    // X <- P X
+    // X <- a/2 X + P X
     product([&] {
       for (int k = 0; k < kn; ++k)
 #pragma unroll
@@ -1034,6 +1085,19 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const __grid
         uint32_t acc[32];
         tmem_ld32(tq + k * 64 + h * 32, acc);
         tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint4 xv = *reinterpret_cast<const uint4 *>(xs + k * kBlk + swz128(row, h * 4 + e));
+          const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            __half2 hh;
+            memcpy(&hh, &xw[i], 4);
+            const float2 f = __half22float2(hh);
+            acc[8 * e + 2 * i] = __float_as_uint(fmaf(own, f.x, __uint_as_float(acc[8 * e + 2 * i])));
+            acc[8 * e + 2 * i + 1] = __float_as_uint(fmaf(own, f.y, __uint_as_float(acc[8 * e + 2 * i + 1])));
+          }
+        }
         if (!last) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -1061,13 +1125,10 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const __grid
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 w[i] = pack_bf16x2(__uint_as_float(acc[8 * e + 2 * i]) * f, __uint_as_float(acc[8 * e + 2 * i + 1]) * f);
-              if (p.vec) {
-                if (c + 8 * e < p.m) *reinterpret_cast<uint4 *>(o + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
-              } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  if (c + 8 * e + i < p.m) o[8 * e + i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
-              }
+              if (!p.vec)  // rows that start anywhere: through X's place, below
+                *reinterpret_cast<uint4 *>(xs + k * kBlk + swz128(row, h * 4 + e)) = make_uint4(w[0], w[1], w[2], w[3]);
+              else if (c + 8 * e < p.m)
+                *reinterpret_cast<uint4 *>(o + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
         }
@@ -1076,6 +1137,15 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const __grid
     tc_fence_before();
     fence_async();
     __syncthreads();
+  }
+  if (!p.vec && !p.tall) {
+    uint16_t *out = p.out + b * numel + c0;
+    const float inv_cols = 1.f / static_cast<float>(cols);
+#pragma unroll 8
+    for (int i = threadIdx.x; i < p.n * cols; i += kSmallThreads) {
+      const int r = quotient(i, inv_cols), c = i - r * cols;
+      out[static_cast<int64_t>(r) * p.C + c] = *reinterpret_cast<const uint16_t *>(xs + blk_byte(r, c));
+    }
   }
   if (threadIdx.x == 0 && s_abort) settle();
   __syncthreads();
