@@ -46,7 +46,7 @@
 // to back this update meets the cap too and takes 2.13 ms).  Symmetric products of
 // few tiles lose the most: 70 us each at n = 768, with 300 MB moved.  Small calls
 // are chains of dependent products of 4 to 6 us: 3 x 1000 x 333 takes 97 us, 8 x
-// 128 x 64 on chip 23.
+// 128 x 64 on chip 25.
 // Every wait is bounded; on a timeout the kernel flags the status word, drains
 // its copies and MMAs, frees TMEM and returns.
 #include <cuda.h>
@@ -844,8 +844,8 @@ __global__ void __launch_bounds__(kSmallThreads, 2) ortho_small_kernel(const __g
   auto quotient = [](int i, float inv_d) { return static_cast<int>((static_cast<float>(i) + 0.5f) * inv_d); };
   // pass 0: advance the momentum and sum the squares; pass 1: store the scaled
   // elements.  Groups of eight or, in rows that are not whole groups, single elements,
-  // 16 of them in flight (20 x 100 x 252: 75 us, of which 36 are these passes; with one
-  // in flight and rows stored by their lanes 102)
+  // 16 of them in flight (20 x 100 x 252: 75 us, against 39 for 20 x 128 x 256 in groups;
+  // with few in flight, and rows stored by the lanes that hold them, 102)
   auto pass_over = [&](auto vec, int pass, float f0) {
     constexpr int N = decltype(vec)::value ? 8 : 1, U = decltype(vec)::value ? 4 : 16;  // U loads in flight
     float acc = 0.f;
