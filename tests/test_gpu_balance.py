@@ -248,3 +248,23 @@ def test_status_is_clear_before_the_first_call():
     used = torch.full((size,), 0x5A, dtype=torch.uint8, device="cuda")
     del used  # the allocator hands the same memory out again
     assert moe.BalanceLoss(512, 8, 2, 1).status() == {"forward": 0}
+
+
+def test_more_logits_than_32_bits_count():
+    """Two sequences whose logits pass the 2^31st element: rows there and the last ones, and whole counts."""
+    E, k, base = 256, 2, 4096
+    T = 2 ** 31 // E + 2 * base
+    part, idx, _ = make(base, E, k, 12)
+    lg, ix = part.repeat(T // base, 1), idx.repeat(T // base, 1)
+    b = moe.BalanceLoss(T, E, k, sequences=2)
+    out = b.forward(lg, ix)
+    assert b.status() == {"forward": 0} and out["tokens"].tolist() == [T // 2, T // 2]
+    counts = torch.bincount(idx.flatten().long(), minlength=E) * (T // base // 2)
+    assert torch.equal(out["counts"].long(), counts.expand(2, E))
+    r = reference(part, idx, None, E, k, 1, 0.3, 0.05)
+    for at in (0, 2 ** 31 // E - base, 2 ** 31 // E, T - base):  # the same rows everywhere
+        near("lse", out["lse"][at:at + base], r["lse"])
+    d = b.backward(lg, out["counts"], out["tokens"], out["lse"], 0.3, 0.05, d_logits=None)
+    # the gradient of the mean over all tokens is that of the part's mean, spread over T / base copies
+    for at in (0, 2 ** 31 // E - base, 2 ** 31 // E, T - base):
+        near("d_logits", d[at:at + base] * (T // base), r["d"])

@@ -210,3 +210,25 @@ def test_arguments_are_checked():
     with pytest.raises(moe.MoEError) as e:  # 8 bytes past a 16-byte boundary
         n.forward(buf[4:].view(8, 64), t["w"], t["b"])
     assert e.value.code == -2
+
+
+@pytest.mark.parametrize("H", [8192, 8189])
+def test_more_elements_than_32_bits_count(H):
+    """Rows before and after the 2^31st element, and the last ones, whole vectors and not."""
+    T = 2 ** 31 // H + 3000
+    t = tensors(1500, H, "bf16", 11)
+
+    def longer(v):
+        return v.repeat((T + 1499) // 1500, 1)[:T].contiguous()
+    x, res, dy = longer(t["x"]), longer(t["res"]), longer(t["dy"])
+    n = moe.Norm(T, H, kind="layer", dtype="bf16")
+    out = n.forward(x, t["w"], t["b"], residual=res)
+    g = n.backward(dy, out["sum"], t["w"], out["stats"], d_sum=res)
+    cross = 2 ** 31 // H
+    for r in (slice(0, 8), slice(cross - 8, cross + 8), slice(T - 8, T)):
+        h = (x[r].float() + res[r].float()).to(torch.bfloat16)
+        assert torch.equal(out["sum"][r], h)
+        y, _, _ = ref_forward(h, t["w"], t["b"], "layer", 1e-5)
+        near_rows("y", out["y"][r], y, "bf16")
+        st = out["stats"][r].double()
+        near_rows("dx", g["dx"][r], ref_backward(dy[r], h, t["w"], st[:, 0], st[:, 1], "layer", res[r])[0], "bf16")

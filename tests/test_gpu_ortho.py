@@ -292,3 +292,16 @@ def test_status_is_clear_before_the_first_call():
     used = torch.full((size,), 0x5A, dtype=torch.uint8, device="cuda")
     del used  # the allocator hands the same memory out again
     assert moe.Orthogonaliser(2, 300, 200).status() == {"update": 0}
+
+
+@pytest.mark.parametrize("B,R,C", [(8200, 512, 512), (65535, 128, 264)])
+def test_more_elements_than_32_bits_count(B, R, C):
+    """Batches whose elements pass 2^31, in scratch and on chip: the first matrices, those there, and the last."""
+    few = grad(9, R, C, "bf16", 13)
+    g = few.repeat((B + 8) // 9, 1, 1)[:B].contiguous()
+    o = moe.Orthogonaliser(B, R, C)
+    out = o.update(g)
+    assert o.status() == {"update": 0}
+    cross = 2 ** 31 // (R * C)
+    for b in (0, cross - 1, cross, cross + 1, B - 1):
+        near(out[[b]], reference(g[[b]], moe.MUON_COEFS))
