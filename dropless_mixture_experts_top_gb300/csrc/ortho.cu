@@ -9,7 +9,7 @@
 //
 // Number format: X, S and P are held in fp16 between products (fp32 accumulation
 // throughout).  All three are bounded by about 3.5, so fp16's range suffices and
-// its 2^-12 rounding is eight times finer than bf16's: the result is within 1.3
+// its 2^-12 rounding is eight times finer than bf16's: the result is within 1.4
 // times the error that rounding the exact result to bf16 makes anyway (bf16
 // operands: four to seven times).  X carries a factor of 256 that keeps its
 // entries (about 1 / sqrt(n m) at first) clear of fp16's subnormals.  a I is part
@@ -19,7 +19,7 @@
 // step's S is P S P, and both steps are one product with X by P' P.  A call of five
 // steps makes three passes over X instead of five.  What the pair's products round
 // stays as small beside a I as what a step rounds; longer runs were less exact
-// (three steps at once: 1.4 times the bf16 rounding against 1.25).
+// (simulated, three steps at once: 1.44 times the bf16 rounding against 1.25).
 //
 // No transposes: the tensor core reads either operand with its reduction axis
 // contiguous or strided (K-major or MN-major boxes).  S and P are symmetric: only
@@ -1421,12 +1421,15 @@ bool is_small(const moe_ortho_config *c) {
 // Steps in pairs, where X is long enough and there is enough to save.  A pair
 // replaces one Gram product (n^2 m) and one update (2 n^2 m) by three symmetric
 // products (n^3 each), which have launches of their own.  Measured against single
-// steps: 128 x 2048 x 768 2.01 against 2.33 ms, 24 x 1024 x 1536 668 against 680 us,
+// steps: 128 x 2048 x 768 2.01 against 2.33 ms, 24 x 1024 x 1856 722 against 772 us,
 // but 24 x 1024 x 1280 626 against 610, and where launches count, 3 x 1000 x 333
 // (1.3e9 operations less) 153 against 144; 5 x 500 x 2600 (1.6e10) 191 against 200.
+// The nearer the matrices are to square, the more the pairs' roundings show: the error
+// is 2.2e-3 at 1024 x 1856 and 2.4e-3 at 1024 x 1536 (651 against 661 us), 2.0e-3 in
+// single steps, 1.7e-3 of rounding the result alone; so from m = 1.75 n on.
 bool fuse_steps(int batch, int n, int m) {
   const double saved = 6.0 * n * n * (m - n) * batch;
-  return 2 * m >= 3 * n && saved >= 1e10;
+  return 4 * m >= 7 * n && saved >= 1e10;
 }
 
 inline int pad64(int x) { return (x + 63) / 64 * 64; }
