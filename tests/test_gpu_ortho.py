@@ -305,3 +305,22 @@ def test_more_elements_than_32_bits_count(B, R, C):
     cross = 2 ** 31 // (R * C)
     for b in (0, cross - 1, cross, cross + 1, B - 1):
         near(out[[b]], reference(g[[b]], moe.MUON_COEFS))
+
+
+# enough work, and long enough sides, that two steps are taken at once: both orientations, whole and odd sizes, tiles of
+# one CTA and of two; every number of steps up to five (an odd one by itself in the middle) and steps of other kinds
+@pytest.mark.parametrize("B,R,C,steps", [(6, 600, 1500, 5), (6, 1507, 601, 5), (40, 300, 1100, 5), (2, 2100, 1024, 5),
+                                         (6, 600, 1500, 1), (6, 1500, 600, 2), (6, 600, 1500, 3), (6, 1500, 600, 4)])
+@pytest.mark.parametrize("mixed", [False, True])
+def test_steps_in_pairs(B, R, C, steps, mixed):
+    g, m = grad(B, R, C, "bf16", 51), grad(B, R, C, "fp32", 52)
+    coefs = moe.MUON_COEFS[:steps]
+    if mixed:
+        coefs = [(1.5, -0.5, 0.0) if i % 2 else c for i, c in enumerate(coefs)]
+    n, k = min(R, C), max(R, C)
+    assert 4 * k >= 7 * n and 6 * n * n * (k - n) * B >= 1e10
+    u = g.double() + 0.95 * (0.95 * m.double() + g.double())
+    o = moe.Orthogonaliser(B, R, C, coefs=coefs)
+    out = o.update(g, momentum=m)
+    assert o.status() == {"update": 0}
+    near(out, reference(u, coefs))
