@@ -333,6 +333,7 @@ __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(const BalArgs a) 
 // memory.  Of several sequences, the last cluster to finish (a ticket) adds them.
 constexpr int kFinThreads = 1024, kFinCols = 32, kFinRuns = kFinThreads / kFinCols;
 __global__ void __launch_bounds__(kFinThreads) balance_finish_kernel(const BalArgs a) {
+  cluster_arrive();  // waited for below, before the first block's shared memory is written
   griddep_wait();  // the previous kernel in the stream has completed
   __shared__ float s_sum[kFinRuns][kFinCols + 1];
   __shared__ int s_cnt[kFinRuns][kFinCols + 1];
@@ -377,6 +378,7 @@ __global__ void __launch_bounds__(kFinThreads) balance_finish_kernel(const BalAr
   s_cnt[warp][lane] = cnt;
   if (lane == 0) s_warp[warp] = r;
   __syncthreads();
+  cluster_wait();  // every block of the cluster runs: its shared memory may be reached
   if (warp == 0) {  // lane = expert
     r = s_warp[lane];  // kFinRuns == 32
     r.z = warp_sum(r.z);
@@ -395,6 +397,7 @@ __global__ void __launch_bounds__(kFinThreads) balance_finish_kernel(const BalAr
     }
     const float fp = warp_sum(static_cast<float>(cnt) * P);
     if (lane == 0) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer_smem_addr(s_bal + cg, 0)), "f"(fp) : "memory");
+    __syncwarp();
   }
   cluster_sync();
   if (cg != 0) return;
