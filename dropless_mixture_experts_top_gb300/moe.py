@@ -11,6 +11,7 @@ buffers one configuration needs.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -269,6 +270,28 @@ def router_workspace(cfg: Config):
     return int(f.value), int(b.value)
 
 
+def _device(device):
+    d = torch.device(device)
+    if d.type != "cuda":
+        raise ValueError(f"device: {d}, expected a GPU")
+    return torch.device("cuda", torch.cuda.current_device()) if d.index is None else d
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)  # (without its Python layers)
+
+
+def _on_own_device(call):
+    """A plan's method, run with the plan's GPU current: the library launches on the current one.  The three plans
+    whose smallest calls are a few microseconds ask for themselves: this wrapper costs 0.4 of one."""
+    @functools.wraps(call)
+    def on_own_device(self, *args, **kwargs):
+        if _current_device() == self._dev:
+            return call(self, *args, **kwargs)
+        with torch.cuda.device(self._dev):
+            return call(self, *args, **kwargs)
+    return on_own_device
+
+
 class Router:
     """The router projection logits = x . W_r (bf16 in, fp32 logits) and its
     backward, over scratch buffers sized for one configuration."""
@@ -279,8 +302,9 @@ class Router:
         fs, bs = router_workspace(self.cfg)
         self.fwd_scratch = torch.empty(fs, dtype=torch.uint8, device=device)
         self.bwd_scratch = torch.empty(bs, dtype=torch.uint8, device=device)
-        self.device = device
+        self.device, self._dev = device, _device(device).index
 
+    @_on_own_device
     def forward(self, x, W_r, logits=None, stream=None):
         if logits is None:
             logits = torch.empty((self.shape.T, self.shape.E), dtype=torch.float32, device=self.device)
@@ -289,6 +313,7 @@ class Router:
                "moe_router_forward")
         return logits
 
+    @_on_own_device
     def backward(self, x, W_r, d_logits, dx, dW_r=None, stream=None):
         """dx (bf16 [T,H]) is updated in place; returns dW_r (fp32 [H,E])."""
         if dW_r is None:
@@ -298,6 +323,7 @@ class Router:
                                          _stream(stream)), "moe_router_backward")
         return dW_r
 
+    @_on_own_device
     def status(self, stream=None) -> dict:
         return {n: get_device_status(b, stream) for n, b in (("forward", self.fwd_scratch),
                                                              ("backward", self.bwd_scratch))}
@@ -321,13 +347,6 @@ def _addr(t, name, shape, dtypes, dev):
         return t.data_ptr()
     raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, {'' if t.is_contiguous() else 'not '}"
                      f"contiguous; expected one of {dtypes}, {tuple(shape)}, on GPU {dev}, contiguous")
-
-
-def _device(device):
-    d = torch.device(device)
-    if d.type != "cuda":
-        raise ValueError(f"device: {d}, expected a GPU")
-    return torch.device("cuda", torch.cuda.current_device()) if d.index is None else d
 
 
 def _raw_stream(stream, dev):
@@ -356,6 +375,9 @@ class Norm:
     def forward(self, x, weight, bias=None, residual=None, out=None, stream=None) -> dict:
         """{"y", "sum" (x + residual, or None), "stats" [T, 2]: mean and 1 / deviation}"""
         d, ty, rows, cols = self._dev, self._types, self._rows, self._cols
+        if _current_device() != d:
+            with torch.cuda.device(d):
+                return self.forward(x, weight, bias, residual, out, stream)
         if (bias is not None) != self.bias:
             raise ValueError("bias: given to a norm without one" if bias is not None else "bias: missing")
         if out is None:
@@ -374,6 +396,9 @@ class Norm:
         """{"dx", "dweight", "dbias" (None without a bias)} from the forward's
         stats and h, its sum (x where there was no residual)."""
         d, ty, rows, cols = self._dev, self._types, self._rows, self._cols
+        if _current_device() != d:
+            with torch.cuda.device(d):
+                return self.backward(dy, h, weight, stats, d_sum, grads, stream)
         if grads is None:
             f32 = dict(dtype=torch.float32, device=self.device)
             grads = {"dx": torch.empty_like(dy), "dweight": torch.empty(cols, **f32),
@@ -419,6 +444,9 @@ class BalanceLoss:
         """{"loss" [2]: balance, z; "counts" and "probs" [sequences, E]; "tokens"
         [sequences]; "lse" [T]}.  mask [T]: zero for padding."""
         d = self._dev
+        if _current_device() != d:
+            with torch.cuda.device(d):
+                return self.forward(logits, topk_idx, mask, out, stream)
         if out is None:
             f32, i32 = (dict(dtype=t, device=self.device) for t in (torch.float32, torch.int32))
             out = {"loss": torch.empty(self._two, **f32), "counts": torch.empty(self._se, **i32),
@@ -438,6 +466,9 @@ class BalanceLoss:
         """The gradient of g_balance * loss[0] + g_z * loss[1], added to d_logits in
         place where that is given (as the layer's backward left it)."""
         d, add = self._dev, d_logits is not None
+        if _current_device() != d:
+            with torch.cuda.device(d):
+                return self.backward(logits, counts, tokens, lse, g_balance, g_z, d_logits, stream)
         if not add:
             d_logits = torch.empty(self._te, dtype=torch.float32, device=self.device)
         rc = self._bwd(
@@ -448,6 +479,7 @@ class BalanceLoss:
             raise MoEError("moe_balance_backward", rc)
         return d_logits
 
+    @_on_own_device
     def status(self, stream=None) -> dict:
         return {"forward": get_device_status(self.fwd_scratch, stream)}
 
@@ -479,6 +511,9 @@ class Orthogonaliser:
         """scale times the orthogonalised update, bf16 [batch, R, C]; momentum (fp32)
         is advanced in place."""
         d, s = self._dev, self._shape
+        if _current_device() != d:
+            with torch.cuda.device(d):
+                return self.update(g, momentum, beta, nesterov, scale, out, stream)
         if out is None:
             out = torch.empty(s, dtype=g.dtype if g.dtype in _BF16 else torch.bfloat16, device=self.device)
         rc = self._update(
@@ -489,6 +524,7 @@ class Orthogonaliser:
             raise MoEError("moe_ortho_update", rc)
         return out
 
+    @_on_own_device
     def status(self, stream=None) -> dict:
         return {"update": get_device_status(self.scratch, stream)}
 
@@ -537,7 +573,7 @@ class MoELayer:
     def __init__(self, shape, precision="bf16", device="cuda"):
         self.shape = shape
         self.cfg = make_config(shape, precision)
-        self.device = torch.device(device)
+        self.device, self._dev = torch.device(device), _device(device).index
         T, H, I, E, k = shape.T, shape.H, shape.I, shape.E, shape.k
         rs, sv, fs, bs = query_workspace(self.cfg)
         dev = self.device
@@ -609,9 +645,11 @@ class MoELayer:
         R, K = rows_k[name]
         return buf[off:off + R * K].view(R, K)
 
+    @_on_own_device
     def route(self, logits, stream=None):
         route(self.cfg, logits, self.routing, self.route_scratch, stream)
 
+    @_on_own_device
     def forward(self, x, W_gate, W_up, W_down, out=None, stream=None, save=True):
         """save=False: a checkpointed layer's first pass (out only; call recompute
         before backward)."""
@@ -621,10 +659,12 @@ class MoELayer:
                 save=save)
         return out
 
+    @_on_own_device
     def recompute(self, x, W_gate, W_up, W_down, stream=None):
         """What backward reads, rebuilt from the same inputs (no out)."""
         forward_recompute(self.cfg, x, self.routing, W_gate, W_up, W_down, self.saved, self.fwd_scratch, stream)
 
+    @_on_own_device
     def backward(self, dy, x, W_gate, W_up, W_down, grads=None, stream=None):
         s = self.shape
         dev = self.device
@@ -642,6 +682,7 @@ class MoELayer:
                  grads.get("d_topk_w"), self.bwd_scratch, stream)
         return grads
 
+    @_on_own_device
     def status(self, stream=None) -> dict:
         return {n: get_device_status(b, stream) for n, b in
                 (("route", self.route_scratch), ("forward", self.fwd_scratch), ("backward", self.bwd_scratch))}
