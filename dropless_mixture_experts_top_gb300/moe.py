@@ -10,6 +10,7 @@ buffers one configuration needs.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -292,6 +293,12 @@ def _on_own_device(call):
     return on_own_device
 
 
+def _on_stream(stream):
+    """Where the results of a call on this stream (None: the current one) are allocated: memory is handed out again in
+    the order of the stream that it was taken on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 class Router:
     """The router projection logits = x . W_r (bf16 in, fp32 logits) and its
     backward, over scratch buffers sized for one configuration."""
@@ -307,7 +314,8 @@ class Router:
     @_on_own_device
     def forward(self, x, W_r, logits=None, stream=None):
         if logits is None:
-            logits = torch.empty((self.shape.T, self.shape.E), dtype=torch.float32, device=self.device)
+            with _on_stream(stream):
+                logits = torch.empty((self.shape.T, self.shape.E), dtype=torch.float32, device=self.device)
         _check(lib().moe_router_forward(ctypes.byref(self.cfg), _ptr(x), _ptr(W_r), _ptr(logits),
                                         _ptr(self.fwd_scratch), self.fwd_scratch.numel(), _stream(stream)),
                "moe_router_forward")
@@ -317,7 +325,8 @@ class Router:
     def backward(self, x, W_r, d_logits, dx, dW_r=None, stream=None):
         """dx (bf16 [T,H]) is updated in place; returns dW_r (fp32 [H,E])."""
         if dW_r is None:
-            dW_r = torch.empty((self.shape.H, self.shape.E), dtype=torch.float32, device=self.device)
+            with _on_stream(stream):
+                dW_r = torch.empty((self.shape.H, self.shape.E), dtype=torch.float32, device=self.device)
         _check(lib().moe_router_backward(ctypes.byref(self.cfg), _ptr(x), _ptr(W_r), _ptr(d_logits), _ptr(dx),
                                          _ptr(dW_r), _ptr(self.bwd_scratch), self.bwd_scratch.numel(),
                                          _stream(stream)), "moe_router_backward")
@@ -353,7 +362,27 @@ def _raw_stream(stream, dev):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-class Norm:
+class _Plan:
+    """A plan's scratch and the streams that work with it."""
+
+    def _take_scratch(self, n):
+        """A scratch buffer whose status reads 0 before its first call, ready for use on any stream."""
+        s = torch.empty(n, dtype=torch.uint8, device=self.device)
+        s[:256] = 0
+        torch.cuda.current_stream(self.device).synchronize()
+        self._home = _raw_stream(None, self._dev)
+        return s
+
+    def _working(self, scratch, stream):
+        """The handle of the stream that a call works on.  The allocator is told where that is not the stream that the
+        scratch was taken on: a plan may be dropped while its last call runs."""
+        raw = _raw_stream(stream, self._dev)
+        if raw != self._home:
+            scratch.record_stream(torch.cuda.current_stream(self._dev) if stream is None else stream)
+        return raw
+
+
+class Norm(_Plan):
     """Layer norm (kind "layer") or RMS norm ("rms") over [T, H] of one type
     ("bf16" or "fp32"), with the residual sum in front of it, and its backward.
 
@@ -369,7 +398,7 @@ class Norm:
         self._dev, self._fwd, self._bwd = self.device.index, lib().moe_norm_forward, lib().moe_norm_backward
         self._cfg, self._types = ctypes.byref(self.cfg), _TORCH_DTYPES[dtype]
         self._rows, self._cols, self._stats = (torch.Size(s) for s in ((T, H), (H,), (T, 2)))
-        self.bwd_scratch = torch.empty(n.value, dtype=torch.uint8, device=self.device)
+        self.bwd_scratch = self._take_scratch(n.value)
         self._scratch = self.bwd_scratch.data_ptr()
 
     def forward(self, x, weight, bias=None, residual=None, out=None, stream=None) -> dict:
@@ -381,8 +410,9 @@ class Norm:
         if (bias is not None) != self.bias:
             raise ValueError("bias: given to a norm without one" if bias is not None else "bias: missing")
         if out is None:
-            out = {"y": torch.empty_like(x), "sum": torch.empty_like(x) if residual is not None else None,
-                   "stats": torch.empty(self._stats, dtype=torch.float32, device=self.device)}
+            with _on_stream(stream):
+                out = {"y": torch.empty_like(x), "sum": torch.empty_like(x) if residual is not None else None,
+                       "stats": torch.empty(self._stats, dtype=torch.float32, device=self.device)}
         rc = self._fwd(
             self._cfg, _addr(x, "x", rows, ty, d), _addr(residual, "residual", rows, ty, d),
             _addr(weight, "weight", cols, ty, d), _addr(bias, "bias", cols, ty, d), _addr(out["y"], "y", rows, ty, d),
@@ -401,14 +431,15 @@ class Norm:
                 return self.backward(dy, h, weight, stats, d_sum, grads, stream)
         if grads is None:
             f32 = dict(dtype=torch.float32, device=self.device)
-            grads = {"dx": torch.empty_like(dy), "dweight": torch.empty(cols, **f32),
-                     "dbias": torch.empty(cols, **f32) if self.bias else None}
+            with _on_stream(stream):
+                grads = {"dx": torch.empty_like(dy), "dweight": torch.empty(cols, **f32),
+                         "dbias": torch.empty(cols, **f32) if self.bias else None}
         rc = self._bwd(
             self._cfg, _addr(dy, "dy", rows, ty, d), _addr(h, "h", rows, ty, d),
             _addr(weight, "weight", cols, ty, d), _addr(stats, "stats", self._stats, _F32, d),
             _addr(d_sum, "d_sum", rows, ty, d), _addr(grads["dx"], "dx", rows, ty, d),
             _addr(grads["dweight"], "dweight", cols, _F32, d), _addr(grads["dbias"], "dbias", cols, _F32, d),
-            self._scratch, self.bwd_scratch.numel(), _raw_stream(stream, d))
+            self._scratch, self.bwd_scratch.numel(), self._working(self.bwd_scratch, stream))
         if rc:
             raise MoEError("moe_norm_backward", rc)
         return grads
@@ -417,15 +448,7 @@ class Norm:
 _F32, _I32, _U8 = (torch.float32,), (torch.int32,), (torch.uint8, torch.bool)
 
 
-def _status_scratch(n, device):
-    """A scratch buffer whose status reads 0 before its first call, ready for use on any stream."""
-    s = torch.empty(n, dtype=torch.uint8, device=device)
-    s[:256] = 0
-    torch.cuda.current_stream(device).synchronize()
-    return s
-
-
-class BalanceLoss:
+class BalanceLoss(_Plan):
     """The router's balance loss and z loss over `sequences` equal parts of T
     tokens, with per-expert counts, and their gradient for the logits."""
 
@@ -437,7 +460,7 @@ class BalanceLoss:
         self._dev, self._fwd, self._bwd = self.device.index, lib().moe_balance_forward, lib().moe_balance_backward
         self._te, self._tk, self._t, self._se, self._s, self._two = (
             torch.Size(s) for s in ((T, E), (T, k), (T,), (sequences, E), (sequences,), (2,)))
-        self.fwd_scratch = _status_scratch(n.value, self.device)
+        self.fwd_scratch = self._take_scratch(n.value)
         self._scratch = self.fwd_scratch.data_ptr()
 
     def forward(self, logits, topk_idx, mask=None, out=None, stream=None) -> dict:
@@ -449,15 +472,16 @@ class BalanceLoss:
                 return self.forward(logits, topk_idx, mask, out, stream)
         if out is None:
             f32, i32 = (dict(dtype=t, device=self.device) for t in (torch.float32, torch.int32))
-            out = {"loss": torch.empty(self._two, **f32), "counts": torch.empty(self._se, **i32),
-                   "probs": torch.empty(self._se, **f32), "tokens": torch.empty(self._s, **i32),
-                   "lse": torch.empty(self._t, **f32)}
+            with _on_stream(stream):
+                out = {"loss": torch.empty(self._two, **f32), "counts": torch.empty(self._se, **i32),
+                       "probs": torch.empty(self._se, **f32), "tokens": torch.empty(self._s, **i32),
+                       "lse": torch.empty(self._t, **f32)}
         rc = self._fwd(
             self._cfg, _addr(logits, "logits", self._te, _F32, d), _addr(topk_idx, "topk_idx", self._tk, _I32, d),
             _addr(mask, "mask", self._t, _U8, d), _addr(out["loss"], "loss", self._two, _F32, d),
             _addr(out["counts"], "counts", self._se, _I32, d), _addr(out["probs"], "probs", self._se, _F32, d),
             _addr(out["tokens"], "tokens", self._s, _I32, d), _addr(out["lse"], "lse", self._t, _F32, d),
-            self._scratch, self.fwd_scratch.numel(), _raw_stream(stream, d))
+            self._scratch, self.fwd_scratch.numel(), self._working(self.fwd_scratch, stream))
         if rc:
             raise MoEError("moe_balance_forward", rc)
         return out
@@ -470,7 +494,8 @@ class BalanceLoss:
             with torch.cuda.device(d):
                 return self.backward(logits, counts, tokens, lse, g_balance, g_z, d_logits, stream)
         if not add:
-            d_logits = torch.empty(self._te, dtype=torch.float32, device=self.device)
+            with _on_stream(stream):
+                d_logits = torch.empty(self._te, dtype=torch.float32, device=self.device)
         rc = self._bwd(
             self._cfg, _addr(logits, "logits", self._te, _F32, d), _addr(counts, "counts", self._se, _I32, d),
             _addr(tokens, "tokens", self._s, _I32, d), _addr(lse, "lse", self._t, _F32, d), g_balance, g_z,
@@ -488,7 +513,7 @@ class BalanceLoss:
 MUON_COEFS = ((3.4445, -4.7750, 2.0315),) * 5
 
 
-class Orthogonaliser:
+class Orthogonaliser(_Plan):
     """The orthogonalised update of `batch` matrices [R, C] by Newton-Schulz
     products, optionally through a momentum, over a scratch buffer of its own.
     coefs: one (a, b, c) per step."""
@@ -504,7 +529,7 @@ class Orthogonaliser:
         self._shape = torch.Size((batch, R, C))
         self._dev, self._update = self.device.index, lib().moe_ortho_update
         self._coefs = (ctypes.c_float * len(coefs))(*coefs)
-        self.scratch = _status_scratch(n.value, self.device)
+        self.scratch = self._take_scratch(n.value)
         self._scratch = self.scratch.data_ptr()
 
     def update(self, g, momentum=None, beta=0.95, nesterov=True, scale=1.0, out=None, stream=None):
@@ -515,11 +540,12 @@ class Orthogonaliser:
             with torch.cuda.device(d):
                 return self.update(g, momentum, beta, nesterov, scale, out, stream)
         if out is None:
-            out = torch.empty(s, dtype=g.dtype if g.dtype in _BF16 else torch.bfloat16, device=self.device)
+            with _on_stream(stream):
+                out = torch.empty(s, dtype=g.dtype if g.dtype in _BF16 else torch.bfloat16, device=self.device)
         rc = self._update(
             self._cfg, self._coefs, _addr(g, "g", s, self._types, d), _addr(momentum, "momentum", s, _F32, d), beta,
             nesterov, scale, _addr(out, "out", s, _BF16, d), self._scratch, self.scratch.numel(),
-            _raw_stream(stream, d))
+            self._working(self.scratch, stream))
         if rc:
             raise MoEError("moe_ortho_update", rc)
         return out
@@ -654,7 +680,8 @@ class MoELayer:
         """save=False: a checkpointed layer's first pass (out only; call recompute
         before backward)."""
         if out is None:
-            out = torch.empty((self.shape.T, self.shape.H), dtype=torch.int16, device=self.device)
+            with _on_stream(stream):
+                out = torch.empty((self.shape.T, self.shape.H), dtype=torch.int16, device=self.device)
         forward(self.cfg, x, self.routing, W_gate, W_up, W_down, out, self.saved, self.fwd_scratch, stream,
                 save=save)
         return out
@@ -669,14 +696,15 @@ class MoELayer:
         s = self.shape
         dev = self.device
         if grads is None:
-            grads = {
-                "dx": torch.empty((s.T, s.H), dtype=torch.int16, device=dev),
-                "dW_gate": torch.empty((s.E, s.H, s.I), dtype=torch.int16, device=dev),
-                "dW_up": torch.empty((s.E, s.H, s.I), dtype=torch.int16, device=dev),
-                "dW_down": torch.empty((s.E, s.I, s.H), dtype=torch.int16, device=dev),
-                "d_logits": torch.empty((s.T, s.E), dtype=torch.float32, device=dev),
-                "d_topk_w": torch.empty((s.T, s.k), dtype=torch.float32, device=dev),
-            }
+            with _on_stream(stream):
+                grads = {
+                    "dx": torch.empty((s.T, s.H), dtype=torch.int16, device=dev),
+                    "dW_gate": torch.empty((s.E, s.H, s.I), dtype=torch.int16, device=dev),
+                    "dW_up": torch.empty((s.E, s.H, s.I), dtype=torch.int16, device=dev),
+                    "dW_down": torch.empty((s.E, s.I, s.H), dtype=torch.int16, device=dev),
+                    "d_logits": torch.empty((s.T, s.E), dtype=torch.float32, device=dev),
+                    "d_topk_w": torch.empty((s.T, s.k), dtype=torch.float32, device=dev),
+                }
         backward(self.cfg, dy, x, self.routing, W_gate, W_up, W_down, self.saved, grads["dx"],
                  grads["dW_gate"], grads["dW_up"], grads["dW_down"], grads["d_logits"],
                  grads.get("d_topk_w"), self.bwd_scratch, stream)
