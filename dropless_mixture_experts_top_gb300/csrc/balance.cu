@@ -125,9 +125,11 @@ __device__ __forceinline__ float group_max(float v, int G) {
 }
 
 // v = exp(v - at) in pairs: 2^((v - at) log2 e) with the difference taken first, so
-// that rows of the type's lowest value stay exact; what is below 2^-126 is zero.
-// The compiler's exponential scales such values instead, three operations more each:
-// with it 131072 x 256 forward took 43 us, 38 with this; 131072 x 250 55 and 51.
+// that rows of the type's lowest value stay exact.  The product with log2 e is rounded,
+// which at a distance of d from `at` is 2^-24 d log2 e of the result (5e-7 at 10, 4e-6 at
+// 80, where the result is 2e-35), and what is below 2^-126 is zero: both far below the
+// last place of a sum that has 1 in it.  131072 x 256 forward takes 38 us with it, 43 with
+// expf; 131072 x 250 51 and 55.
 constexpr float kLog2e = 1.44269504f;
 __device__ __forceinline__ float exp2_flush(float x) {
   float y;
@@ -495,18 +497,24 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(const BalArgs a) 
     if (ADD) load_row<W>(row, E, G, lane, i < i1, 0.f, old);
     fetch(i + step);
     const bool some = lse != INFINITY;  // the token has a part in the losses
+    // softmax from the row itself: lse only keeps the exponentials in range (they are at
+    // most e^6, where its last place is as much as log E).  exp(v - lse) alone would carry
+    // lse's rounding into p, 5e-4 of it at 1e4.  The sum rides along with the dot product.
     exp_row(p, lse);
-    float dot = 0.f;
+    float dot = 0.f, sum = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       p[j] = some ? p[j] : 0.f;
       dot = fmaf(f[j], p[j], dot);
+      sum += p[j];
     }
     dot = group_sum(dot, G);
-    const float zt = some ? cz * lse : 0.f;
+    sum = group_sum(sum, G);
+    const float r = some ? 1.f / sum : 0.f, cbr = cb * r, zt = some ? cz * lse * r : 0.f;
+    dot *= r;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const float d = p[j] * fmaf(cb, f[j] - dot, zt);
+      const float d = p[j] * fmaf(cbr, f[j] - dot, zt);
       p[j] = ADD ? old[j] + d : d;
     }
     if (i < i1 && (some || !ADD)) store_row<W>(row, E, G, lane, p);
