@@ -438,24 +438,31 @@ __global__ void __launch_bounds__(kFinThreads) balance_finish_kernel(const BalAr
   if (threadIdx.x == 0) finish_all(a, bal, z, n, used, flags);
 }
 
-template <int W, int NV, bool ADD>
+// MANY: as many blocks as run at once, each going through several sequences.  A block
+// adds up the tokens of all sequences, so with a block per sequence that is S^2 reads.
+// Measured with a block per sequence and with this, one token each: 131072 sequences 3230
+// and 957 us, 32768 322 and 249, 16384 130 and 131, 4096 31 and 36; of 16 tokens, 32768
+// 401 and 420, 16384 170 and 210.  So from kManySequences on.  Without MANY the loop around
+// the sequences is not there: with it 131072 x 250 in 32 sequences took 81 us instead of 59.
+constexpr int kManySequences = 32768;
+template <int W, int NV, bool ADD, bool MANY>
 __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(const BalArgs a) {
   griddep_wait();  // the previous kernel in the stream has completed
   __shared__ int s_n[kWarps], s_used[kWarps];
   const int warp = threadIdx.x >> 5, l32 = threadIdx.x & 31;
   const int E = a.E, G = a.G, lane = l32 & (G - 1), sub = l32 / G, tpw = 32 / G;
-  const int seq = blockIdx.x / a.nbs, blk = blockIdx.x - seq * a.nbs;
+  int seq = blockIdx.x / a.nbs;
+  const int blk = blockIdx.x - seq * a.nbs;
   const int i0 = blk * a.per, i1 = min(i0 + a.per, a.L);
-  const size_t tbase = static_cast<size_t>(seq) * a.L;
-  const int step = kWarps * tpw;
+  const int step = kWarps * tpw, i_first = i0 + warp * tpw;
   float next[NV], old[NV], lse_next;
-  int ib = i0 + warp * tpw;
+  size_t tbase = static_cast<size_t>(seq) * a.L;
   auto fetch = [&](int i) {  // the next token's logits, before this one is worked on
     load_row<W>(a.logits + (tbase + i) * E, E, G, lane, i < i1, -INFINITY, next);
     lse_next = i < i1 ? a.lse_in[tbase + i] : INFINITY;
   };
-  fetch(ib + sub);
-  const int ns = a.tokens[seq];
+  fetch(i_first + sub);
+  int ns = a.tokens[seq];
   int n = ns, used = ns > 0 ? 1 : 0;
   if (a.S > 1) {
     n = used = 0;
@@ -478,46 +485,54 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(const BalArgs a) 
       used += s_used[w];
     }
   }
-  const float inv = ns > 0 ? 1.f / static_cast<float>(ns) : 0.f;
-  const float cb = used > 0 ? a.g_bal * static_cast<float>(E) / static_cast<float>(used) * inv : 0.f;
   const float cz = n > 0 ? 2.f * a.g_z / static_cast<float>(n) : 0.f;
-  float f[NV];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int e = col_of<W>(j, lane, G);
-    f[j] = e < E ? static_cast<float>(a.counts[static_cast<size_t>(seq) * E + e]) * inv / static_cast<float>(a.k) : 0.f;
-  }
-  for (; ib < i1; ib += step) {
-    const int i = ib + sub;
-    float p[NV];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) p[j] = next[j];
-    const float lse = lse_next;
-    float *row = a.d_logits + (tbase + i) * E;
-    if (ADD) load_row<W>(row, E, G, lane, i < i1, 0.f, old);
-    fetch(i + step);
-    const bool some = lse != INFINITY;  // the token has a part in the losses
-    // softmax from the row itself: lse only keeps the exponentials in range (they are at
-    // most e^6, where its last place is as much as log E).  exp(v - lse) alone would carry
-    // lse's rounding into p, 5e-4 of it at 1e4.  The sum rides along with the dot product.
-    exp_row(p, lse);
-    float dot = 0.f, sum = 0.f;
+  while (true) {
+    const float inv = ns > 0 ? 1.f / static_cast<float>(ns) : 0.f;
+    const float cb = used > 0 ? a.g_bal * static_cast<float>(E) / static_cast<float>(used) * inv : 0.f;
+    float f[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      p[j] = some ? p[j] : 0.f;
-      dot = fmaf(f[j], p[j], dot);
-      sum += p[j];
+      const int e = col_of<W>(j, lane, G);
+      f[j] = e < E ? static_cast<float>(a.counts[static_cast<size_t>(seq) * E + e]) * inv / static_cast<float>(a.k) : 0.f;
     }
-    dot = group_sum(dot, G);
-    sum = group_sum(sum, G);
-    const float r = some ? 1.f / sum : 0.f, cbr = cb * r, zt = some ? cz * lse * r : 0.f;
-    dot *= r;
+    for (int ib = i_first; ib < i1; ib += step) {
+      const int i = ib + sub;
+      float p[NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const float d = p[j] * fmaf(cbr, f[j] - dot, zt);
-      p[j] = ADD ? old[j] + d : d;
+      for (int j = 0; j < NV; ++j) p[j] = next[j];
+      const float lse = lse_next;
+      float *row = a.d_logits + (tbase + i) * E;
+      if (ADD) load_row<W>(row, E, G, lane, i < i1, 0.f, old);
+      fetch(i + step);
+      const bool some = lse != INFINITY;  // the token has a part in the losses
+      // softmax from the row itself: lse only keeps the exponentials in range (they are at
+      // most e^6, where its last place is as much as log E).  exp(v - lse) alone would carry
+      // lse's rounding into p, 5e-4 of it at 1e4.  The sum rides along with the dot product.
+      exp_row(p, lse);
+      float dot = 0.f, sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        p[j] = some ? p[j] : 0.f;
+        dot = fmaf(f[j], p[j], dot);
+        sum += p[j];
+      }
+      dot = group_sum(dot, G);
+      sum = group_sum(sum, G);
+      const float r = some ? 1.f / sum : 0.f, cbr = cb * r, zt = some ? cz * lse * r : 0.f;
+      dot *= r;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const float d = p[j] * fmaf(cbr, f[j] - dot, zt);
+        p[j] = ADD ? old[j] + d : d;
+      }
+      if (i < i1 && (some || !ADD)) store_row<W>(row, E, G, lane, p);
     }
-    if (i < i1 && (some || !ADD)) store_row<W>(row, E, G, lane, p);
+    if (!MANY) break;
+    seq += gridDim.x;
+    if (seq >= a.S) break;
+    tbase = static_cast<size_t>(seq) * a.L;
+    fetch(i_first + sub);
+    ns = a.tokens[seq];
   }
 }
 
@@ -596,9 +611,11 @@ cudaError_t launch_fwd(const BalArgs &a, cudaStream_t s) {
                     dim3(kThreads), 0, s, 1, a);
 }
 template <int W, int NV>
-cudaError_t launch_bwd(const BalArgs &a, bool add, cudaStream_t s) {
-  return launch_pdl(add ? balance_bwd_kernel<W, NV, true> : balance_bwd_kernel<W, NV, false>, dim3(a.S * a.nbs),
-                    dim3(kThreads), 0, s, 1, a);
+cudaError_t launch_bwd(const BalArgs &a, int most, bool add, cudaStream_t s) {
+  const bool many = a.S >= kManySequences && a.S > most;  // then nbs is 1
+  auto kernel = many ? (add ? balance_bwd_kernel<W, NV, true, true> : balance_bwd_kernel<W, NV, false, true>)
+                     : (add ? balance_bwd_kernel<W, NV, true, false> : balance_bwd_kernel<W, NV, false, false>);
+  return launch_pdl(kernel, dim3(many ? most : a.S * a.nbs), dim3(kThreads), 0, s, 1, a);
 }
 template <int MOST, class F>
 cudaError_t by_width(int E, F &&f) {
@@ -685,7 +702,8 @@ moe_status moe_balance_backward(const moe_balance_config *cfg, const float *logi
   MOE_TRY(device_info(&di));
   if (cfg->T == 0) return MOE_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  BalArgs a = bal_args(cfg, di.sms * kBwdBlocksPerSm, kBwdValues, false);
+  const int most = di.sms * kBwdBlocksPerSm;
+  BalArgs a = bal_args(cfg, most, kBwdValues, false);
   a.logits = logits;
   a.counts = const_cast<int32_t *>(counts);
   a.tokens = const_cast<int32_t *>(tokens);
@@ -696,7 +714,7 @@ moe_status moe_balance_backward(const moe_balance_config *cfg, const float *logi
   const bool add = accumulate != 0;
   return timed("balance_backward", s, [&] {
     return by_width<kBwdValues>(a.E, [&](auto w, auto nv) {
-      return launch_bwd<decltype(w)::value, decltype(nv)::value>(a, add, s);
+      return launch_bwd<decltype(w)::value, decltype(nv)::value>(a, most, add, s);
     });
   });
 }

@@ -89,3 +89,42 @@ def test_z_gradient_of_large_logits():
     b = moe.BalanceLoss(T, E, k)
     out = b.forward(lg, idx)
     near(b.backward(lg, out["counts"], out["tokens"], out["lse"], 0.0, 0.1), reference(lg, idx, k, 1, 0.0, 0.1)[0])
+
+
+def test_many_sequences():
+    """More sequences than blocks run at once, of one token and of a few."""
+    for L, S, E, k in ((1, 5000, 8, 2), (3, 1700, 40, 4), (1, 1217, 256, 8), (300, 700, 5, 1),
+                       (1, 40001, 8, 2), (2, 33333, 33, 4), (40, 32768, 4, 1), (1, 32769, 130, 3)):
+        lg, idx = make(L * S, E, k, 4)
+        b = moe.BalanceLoss(L * S, E, k, sequences=S)
+        out = b.forward(lg, idx)
+        d, P, f = reference(lg, idx, k, S, 0.5, 0.1)
+        near(out["probs"], P)
+        assert torch.equal(out["counts"], (f * k * L).round().int())
+        assert bool((out["tokens"] == L).all())
+        near(out["loss"][:1], (E * f * P).sum(1).mean()[None])
+        near(b.backward(lg, out["counts"], out["tokens"], out["lse"], 0.5, 0.1), d)
+        old = torch.randn(L * S, E, device="cuda") * 1e-3
+        acc = old.clone()
+        b.backward(lg, out["counts"], out["tokens"], out["lse"], 0.5, 0.1, d_logits=acc)
+        near(acc, old.double() + d)
+
+
+def test_the_backward_s_time_grows_with_the_sequences_alone():
+    """Four times the sequences, one token each, take four times as long: less than eight, where each block going
+    through every sequence would take sixteen."""
+    def time(S):
+        lg, idx = make(S, 8, 2, 5)
+        b = moe.BalanceLoss(S, 8, 2, sequences=S)
+        out = b.forward(lg, idx)
+        d = torch.empty_like(lg)
+        best = math.inf
+        for _ in range(5):
+            t0, t1 = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            t0.record()
+            b.backward(lg, out["counts"], out["tokens"], out["lse"], 0.5, 0.1, d_logits=d)
+            t1.record()
+            torch.cuda.synchronize()
+            best = min(best, t0.elapsed_time(t1))
+        return best
+    assert time(1 << 17) < 8 * time(1 << 15)
