@@ -138,11 +138,11 @@ __device__ __forceinline__ float block_sum(float v, float *s_w) {
 }
 
 // The power of two that brings a root mean square of sqrt(sum / count) to 1 .. 2
-// (1 where there is nothing to go by).
+// (1 where there is nothing to go by).  The quotient itself may be below fp32's range;
+// the power is between 2^-64 and 2^89 for every finite sum.
 __device__ __forceinline__ float power_for(float sum, float count) {
-  const float ms = sum / count;
-  if (!(ms > 1e-36f && ms < 1e36f)) return 1.f;
-  return exp2f(-floorf(0.5f * log2f(ms)));
+  if (!(sum > 0.f && sum < INFINITY)) return 1.f;
+  return exp2f(-floorf(0.5f * (log2f(sum) - log2f(count))));
 }
 
 // u times f0 into X at element `at` of the matrix (8 elements or one).
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kPrepThreads) ortho_prepare_kernel(const PrepA
   // and a NaN stays one)
   const bool fits = __syncthreads_and(!(most * f0 > kFits));
   if (threadIdx.x == 0)
-    a.part[static_cast<size_t>(blockIdx.y) * a.chunks + blockIdx.x] = fits ? acc : -(acc < 1e-38f ? 1e-38f : acc);
+    a.part[static_cast<size_t>(blockIdx.y) * a.chunks + blockIdx.x] = fits ? acc : -(acc == 0.f ? 1e-45f : acc);
 }
 
 // A matrix's factor from its sums; X again, by the blocks of the matrix, where the
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kPrepThreads) ortho_rescale_kernel(const PrepA
   fits = __syncthreads_and(fits);
   float f0 = sample_scale<El, VEC>(g, a.numel, s_w);
   const bool fine = isfinite(sq);
-  const float rms = sqrtf(sq / static_cast<float>(a.numel)) * f0;
+  const float rms = sqrtf(sq) * f0 / sqrtf(static_cast<float>(a.numel));
   if (fine && sq > 0.f && !(fits && rms >= 0x1p-6f && rms <= 0x1p10f)) {
     f0 = power_for(sq, static_cast<float>(a.numel));
     const float *mom = MOM ? a.mom + blockIdx.y * a.numel : nullptr;

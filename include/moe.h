@@ -355,8 +355,9 @@ moe_status moe_balance_backward(const moe_balance_config *cfg, const float *logi
  * 3.4445 -4.7750 2.0315 five times, keeps them below 1.3).  Singular values far below
  * |u|_F / 1000 grow out of the roundings as they do out of a bf16 gradient's own.
  * 1 <= R, C <= 16384, 0 <= batch <= 65535, 1 <= steps <= 64, any alignment of rows
- * (multiples of 8 columns are fastest).  out may not overlap g or momentum.  A
- * matrix of zeros gives zeros; one whose sum of squares is not finite gives NaN
+ * (multiples of 8 columns are fastest).  out may not overlap g or momentum.  The
+ * sum of squares is formed in fp32: values of u below about 1e-22 have no part in
+ * it.  A matrix of zeros gives zeros; one whose sum of squares is not finite gives NaN
  * and sets MOE_DEV_NONFINITE_UPDATE (status word at the start of the scratch), and
  * no other matrix is touched by it. */
 typedef struct {

@@ -1,0 +1,78 @@
+"""The orthogonalised update at the ends of its ranges: updates of any size, workspaces full of NaN, coefficients that
+leave fp16's range.
+
+Tolerances as derived for the update: bf16's rounding, 1.7e-3 of the result, and the fp16 roundings between products,
+1.9e-3 at most: together 2.5e-3, held to 4e-3."""
+import pytest
+import torch
+
+from dropless_mixture_experts_top_gb300 import moe
+
+pytestmark = pytest.mark.gpu
+
+REL = 4e-3
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _build():
+    from dropless_mixture_experts_top_gb300 import _build as B
+    B.build()
+
+
+def grad(B, R, C, dtype, seed, scale=1.0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    x = torch.randn(B, R, C, generator=g, device="cuda") * scale
+    return x.to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+
+
+def reference(u, coefs=moe.MUON_COEFS):
+    x = u.double()
+    tall = x.shape[1] > x.shape[2]
+    x = x.transpose(1, 2) if tall else x
+    x = x / torch.linalg.vector_norm(x, dim=(1, 2), keepdim=True)
+    for a, b, c in coefs:
+        s = x @ x.transpose(1, 2)
+        x = a * x + (b * s + c * (s @ s)) @ x
+    return x.transpose(1, 2) if tall else x
+
+
+def near(got, ref):
+    got = got.view(torch.bfloat16).double()
+    assert bool(torch.isfinite(got).all())
+    for b in range(len(ref)):
+        err, size = torch.linalg.vector_norm(got[b] - ref[b]), torch.linalg.vector_norm(ref[b])
+        assert float(err) <= REL * float(size), (b, float(err / size))
+
+
+# in scratch: rows in vectors and single elements, both orientations, a split Gram product, steps in pairs; on chip
+SIZES = [(2, 256, 304), (2, 203, 301), (2, 301, 203), (1, 200, 3000), (6, 600, 1500), (2, 96, 160), (2, 100, 252)]
+
+
+@pytest.mark.parametrize("B,R,C", SIZES)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("scale", [1e-21, 1e-20, 1e-18, 1e-9, 1e9, 1e15])
+def test_the_size_of_the_update_has_no_part(B, R, C, dtype, scale):
+    """eps = 0, with and without momentum; the sum of the squares is inside fp32's range, the mean square (1e-42 at
+    the least) need not be."""
+    g, m = grad(B, R, C, dtype, 61, scale), grad(B, R, C, "fp32", 62, scale)
+    o = moe.Orthogonaliser(B, R, C, dtype=dtype, eps=0.0)
+    out = o.update(g)
+    assert o.status() == {"update": 0}
+    near(out, reference(g))
+    u = g.double() + 0.95 * (0.95 * m.double() + g.double())
+    out = o.update(g, momentum=m)
+    assert o.status() == {"update": 0}
+    near(out, reference(u))
+
+
+@pytest.mark.parametrize("B,R,C", [(2, 256, 304), (2, 203, 301)])
+def test_small_values_that_the_sample_misses(B, R, C):
+    """No gradient, or one far smaller than the momentum, both tiny: X's first power of two is taken from the norm."""
+    for scale in (0.0, 1e-30, 1e-24):
+        g, m = grad(B, R, C, "fp32", 63, scale), grad(B, R, C, "fp32", 64, 1e-19)
+        o = moe.Orthogonaliser(B, R, C, dtype="fp32", eps=0.0)
+        u = g.double() + 0.95 * (0.95 * m.double() + g.double())
+        out = o.update(g, momentum=m)
+        assert o.status() == {"update": 0}
+        near(out, reference(u))
