@@ -8,18 +8,22 @@
 // With the usual coefficients every singular value ends near 1.
 //
 // Number format: X, S and P are held in fp16 between products (fp32 accumulation
-// throughout).  All three are bounded by about 3.5, so fp16's range suffices and
-// its 2^-12 rounding is eight times finer than bf16's: the result is within 1.4
-// times the error that rounding the exact result to bf16 makes anyway (bf16
+// throughout).  With the usual coefficients none is above 3.5, so fp16's range
+// suffices and its 2^-12 rounding is eight times finer than bf16's: the result is
+// within 1.4 times the error that rounding the exact result to bf16 makes anyway (bf16
 // operands: four to seven times).  X carries a factor of 256 that keeps its
 // entries (about 1 / sqrt(n m) at first) clear of fp16's subnormals.  a I is part
-// of P, so the update is one plain product.
+// of P, so the update is one plain product.  Coefficients with which X passes 255, or
+// P (for pairs of steps: P S, P' P) 65504, leave the range: infinities, which reach the
+// result and are reported there.
 //
 // Steps in pairs: S, P and everything made of them commute, so with S the second
 // step's S is P S P, and both steps are one product with X by P' P.  A call of five
-// steps makes three passes over X instead of five.  What the pair's products round
-// stays as small beside a I as what a step rounds; longer runs were less exact
-// (simulated, three steps at once: 1.44 times the bf16 rounding against 1.25).
+// steps makes three passes over X instead of five.  P' P reaches a' a = 11.9, where
+// fp16's last place is four times that at a: rounding it moves the singular values that a
+// pair leaves near 1 by up to that much more, and the result's error is 2.2e-3 of itself
+// instead of 2.0e-3.  Longer runs were less exact still (simulated, three steps at once:
+// 1.44 times the bf16 rounding against 1.25).
 //
 // No transposes: the tensor core reads either operand with its reduction axis
 // contiguous or strided (K-major or MN-major boxes).  S and P are symmetric: only
@@ -419,6 +423,16 @@ struct SChunks {
   }
 };
 
+// Flags a result that is not finite.  What left fp16's range on the way is infinite
+// there and reaches the result: every product multiplies it with something, if only
+// with zero.  v times 0 is 0 of a finite value and a NaN of any other.
+__device__ __forceinline__ void report_bad(const float (&v)[32], int32_t *status) {
+  float bad = 0.f;
+#pragma unroll
+  for (int e = 0; e < 32; ++e) bad = fmaf(v[e], 0.f, bad);
+  if (bad != bad) flag_status(status, kDevNonfiniteUpdate);
+}
+
 // One warp's 32 rows of half a tile's columns.
 template <int KIND, int CG>
 __device__ __forceinline__ void epilogue(const TileAt &t, uint32_t tb, int row0, int part, const ProductArgs &p,
@@ -466,6 +480,7 @@ __device__ __forceinline__ void epilogue(const TileAt &t, uint32_t tb, int row0,
       for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(acc[e]) * c;
     }
     if constexpr (KIND == kLast) {  // out [M,N] itself, bf16
+      report_bad(v, p.status);
       const int ncols = min(32, p.N - c0);
       uint16_t *g0 = out + row0 * static_cast<int64_t>(p.ld) + c0;
       uint4 w[4];
@@ -1110,13 +1125,17 @@ __global__ void __launch_bounds__(kSmallThreads, 2) ortho_small_kernel(const __g
         } else if (row < p.n) {
           const float f = p.scale / kSigma;
           const int c = c0 + k * 64 + h * 32;  // column of X
+          float v[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(acc[e]) * f;
+          report_bad(v, p.status);
           uint16_t *out = p.out + b * numel;
           if (p.tall) {  // row c + e of out, column `row`: contiguous over the lanes
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (c + e < p.m)
                 out[static_cast<int64_t>(c + e) * p.C + row] =
-                    __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(acc[e]) * f));
+                    __bfloat16_as_ushort(__float2bfloat16_rn(v[e]));
           } else {
             uint16_t *o = out + static_cast<int64_t>(row) * p.C + c;
 #pragma unroll
@@ -1124,7 +1143,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) ortho_small_kernel(const __g
               uint32_t w[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                w[i] = pack_bf16x2(__uint_as_float(acc[8 * e + 2 * i]) * f, __uint_as_float(acc[8 * e + 2 * i + 1]) * f);
+                w[i] = pack_bf16x2(v[8 * e + 2 * i], v[8 * e + 2 * i + 1]);
               if (!p.vec)  // rows that start anywhere: through X's place, below
                 *reinterpret_cast<uint4 *>(xs + k * kBlk + swz128(row, h * 4 + e)) = make_uint4(w[0], w[1], w[2], w[3]);
               else if (c + 8 * e < p.m)

@@ -78,7 +78,7 @@ typedef enum {
 /* Device status flags (moe_get_device_status *host_code). */
 #define MOE_DEV_NONFINITE_LOGIT 0x1 /* a logit was NaN or +-Inf; routing outputs unspecified */
 #define MOE_DEV_WAIT_TIMEOUT 0x2    /* a pipeline wait exceeded its bound; outputs unspecified */
-#define MOE_DEV_NONFINITE_UPDATE 0x4 /* moe_ortho_update: a matrix's sum of squares is not finite; it becomes NaN */
+#define MOE_DEV_NONFINITE_UPDATE 0x4 /* moe_ortho_update: a matrix's sum of squares, or its result, is not finite */
 #define MOE_DEV_BAD_INDEX 0x8       /* moe_balance_forward: an expert index outside [0, E); that slot is not counted */
 
 typedef struct {
@@ -350,9 +350,12 @@ moe_status moe_balance_backward(const moe_balance_config *cfg, const float *logi
  *   during the call):  S = X X^T (R <= C) or X^T X,  P = a I + b S + c S^2,
  *   X <- P X or X P;
  *   out = scale X, bf16 [batch,R,C].
- * X, S and P are rounded to fp16 between products, whose sums are fp32; the
- * coefficients are to keep X's singular values below about 100 (the usual quintic,
- * 3.4445 -4.7750 2.0315 five times, keeps them below 1.3).  Singular values far below
+ * X, S and P are rounded to fp16 between products, whose sums are fp32.  The
+ * coefficients are to keep it all in fp16's range: with s a singular value of X in
+ * front of a step and p = |a + b s^2 + c s^4|, s has to stay below 255, and p, p s^2
+ * and the product of two steps' p in succession below 65504 (the usual quintic,
+ * 3.4445 -4.7750 2.0315 five times, keeps s below 1.3 and p below 3.5).  A result that
+ * is not finite sets MOE_DEV_NONFINITE_UPDATE.  Singular values far below
  * |u|_F / 1000 grow out of the roundings as they do out of a bf16 gradient's own.
  * 1 <= R, C <= 16384, 0 <= batch <= 65535, 1 <= steps <= 64, any alignment of rows
  * (multiples of 8 columns are fastest).  out may not overlap g or momentum.  The

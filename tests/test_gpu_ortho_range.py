@@ -76,3 +76,26 @@ def test_small_values_that_the_sample_misses(B, R, C):
         out = o.update(g, momentum=m)
         assert o.status() == {"update": 0}
         near(out, reference(u))
+
+
+# P past 65504 from a step on that finds s = 14; X past 255; the product of two steps' P past 65504 (steps in pairs)
+@pytest.mark.parametrize("coefs", [((14.0, 0.0, 0.0), (3.4445, -4.7750, 2.0315)), ((400.0, 0.0, 0.0), (1.5, -0.5, 0.0)),
+                                   ((1.0, 299.0, 0.0), (1.0, 0.01, 0.0))])
+@pytest.mark.parametrize("B,R,C", [(2, 256, 304), (2, 301, 203), (6, 600, 1500), (6, 1500, 600), (2, 96, 160),
+                                   (1, 128, 1000), (2, 100, 252), (2, 252, 100)])
+def test_coefficients_that_leave_the_range_are_reported(coefs, B, R, C):
+    """One value in a matrix is one singular value of 1.  The other matrices, of one value as well or of zeros, show
+    that a finite result is not reported."""
+    g = torch.zeros(B, R, C, device="cuda", dtype=torch.bfloat16)
+    g[0, R // 2, C // 3] = 2.0
+    o = moe.Orthogonaliser(B, R, C, coefs=coefs)
+    out = o.update(g).float()
+    assert o.status() == {"update": moe.DEV_NONFINITE_UPDATE}
+    assert not bool(torch.isfinite(out[0]).all())
+    assert B == 1 or float(out[1:].abs().max()) == 0
+    # in range: the second P at 4647 and both together at 32529, and X at 200
+    for fine in (((7.0, 0.0, 0.0), (3.4445, -4.7750, 2.0315)), ((200.0, 0.0, 0.0), (1.0, 0.0, 0.0))):
+        o = moe.Orthogonaliser(B, R, C, coefs=fine)
+        out = o.update(g)
+        assert o.status() == {"update": 0}
+        near(out[:1], reference(g[:1], fine))
