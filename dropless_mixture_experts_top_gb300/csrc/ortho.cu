@@ -1374,11 +1374,11 @@ cudaError_t launch_groups(const Maps &a, const Maps &b, ProductArgs p, int sms, 
 // 1 x 1024 x 4096 184 and 200, 2 x 520 x 2452 156 and 163; but 3 x 1000 x 333 110 and
 // 102, 1 x 768 x 768 120 and 113 (both sides of 1 x 2048 x 768 the same).
 constexpr int kSplitStages = 17;
-int gram_split(int batch, int n, int m) {
+int gram_split(int batch, int n, int m, int sms) {
   const int64_t t = (n + BM - 1) / BM, tiles = batch * t * (t + 1) / 2;
   int split = 1;
   if ((m + 2 * BK - 1) / (2 * BK) >= kSplitStages)
-    while (split < kMaxSplit && 2 * split * tiles <= 152) split *= 2;
+    while (split < kMaxSplit && 2 * split * tiles <= sms) split *= 2;
   return split;
 }
 
@@ -1401,17 +1401,17 @@ cudaError_t launch_product(const Maps &a, const Maps &b, const ProductArgs &p, b
 }
 
 // Pairs of CTAs or single ones, by the rounds of tiles that a step's products take
-// on 152 SMs.  A round's length in units of 128 of the reduction, from timings: K + 4
+// on the part's SMs.  A round's length in units of 128 of the reduction, from timings: K + 4
 // for pairs, 0.8 K + 2 for single CTAs (half the MMA and epilogue work, but nearly
 // the same operand stream).  Both measured: 3 x 1000 x 333 144 us in pairs, 110 in
 // single CTAs; 100 x 256 x 256 183 and 131; 4 x 768 x 1536 188 and 157; but
 // 8 x 768 x 1536 216 and 244, 24 x 1024 x 1024 538 and 652, 128 x 2048 x 768 2.0 and
 // 2.4 ms.
-bool use_pairs(int batch, int R, int C) {
+bool use_pairs(int batch, int R, int C, int sms) {
   const int n = R < C ? R : C, m = R < C ? C : R;
   double cost[2];
   for (int cg = 1; cg <= 2; ++cg) {
-    const int ts = tile_size(cg), groups = 152 / cg;
+    const int ts = tile_size(cg), groups = sms / cg;
     auto tiles = [&](int x) { return static_cast<int64_t>((x + ts - 1) / ts); };
     auto rounds = [&](int64_t per) { return static_cast<double>((per * batch + groups - 1) / groups); };
     auto length = [&](int k) { return cg == 2 ? k / 128.0 + 4 : 0.8 * k / 128.0 + 2; };
@@ -1428,13 +1428,17 @@ bool ortho_ok(const moe_ortho_config *c) {
   return c->dtype == MOE_DTYPE_BF16 || c->dtype == MOE_DTYPE_FP32;
 }
 
+// The workspace's size goes by the rules below, and must be known without a GPU: they
+// take GB300's SMs as they were measured, not the present part's.
+constexpr int kRuleSms = 152;
+
 // Whether clusters hold the matrices on chip.
 bool is_small(const moe_ortho_config *c) {
   const int n = std::min(c->R, c->C), m = std::max(c->R, c->C), cluster = (m + kSlab - 1) / kSlab;
   // up to two CTAs per matrix any number of matrices (608 x 128 x 256: 100 against 444
   // us, 304 x 128 x 512: 222 against 305); more only while all matrices are on the part
   // at once (38 x 128 x 1024: 110 against 125 us, but 76 of them 163 against 154)
-  return n <= kSmallN && (cluster <= 2 || (cluster <= kSmallCluster && c->batch * cluster <= 152));
+  return n <= kSmallN && (cluster <= 2 || (cluster <= kSmallCluster && c->batch * cluster <= kRuleSms));
 }
 
 // Steps in pairs, where X is long enough and there is enough to save.  A pair
@@ -1464,7 +1468,7 @@ OrthoLayout ortho_layout(const moe_ortho_config *c) {
   // several blocks for every place on the part
   const int64_t numel = static_cast<int64_t>(c->R) * c->C;
   L.chunk = kPrepThreads * (c->C % 8 == 0 ? kPrepVecs * 8 : kPrepSingles);
-  if (numel * c->batch >= static_cast<int64_t>(L.chunk) * 4 * 152 * 8) L.chunk *= 4;
+  if (numel * c->batch >= static_cast<int64_t>(L.chunk) * 4 * kRuleSms * 8) L.chunk *= 4;
   L.chunks = static_cast<int>((numel + L.chunk - 1) / L.chunk);
   L.ldx = pad64(c->C);
   L.lds = pad64(static_cast<int>(n));
@@ -1597,7 +1601,7 @@ moe_status moe_ortho_update(const moe_ortho_config *cfg, const float *coefs, con
   }));
   // X's rows along C with C contiguous: the Gram product reduces over m, the
   // update over n, so one of them reads X K-major and the other MN-major
-  const bool pairs = fuse_steps(B, n, m), pair = use_pairs(B, R, C);
+  const bool pairs = fuse_steps(B, n, m), pair = use_pairs(B, R, C, di.sms);
   uint8_t *xb[2] = {body + L.x0, body + L.x1}, *nb[3] = {body + L.n[0], body + L.n[1], body + L.n[2]};
   Maps mx[2], mn[3];
   auto make = [&](Maps *mm, const void *ptr, int inner, int rows, int ld) {
@@ -1628,7 +1632,7 @@ moe_status moe_ortho_update(const moe_ortho_config *cfg, const float *coefs, con
     p.fac = fac;
     p.back = turn();
     p.out = reinterpret_cast<uint16_t *>(nb[0]);
-    const int split = pair ? 1 : gram_split(B, n, m);
+    const int split = pair ? 1 : gram_split(B, n, m, di.sms);
     return timed("ortho_gram", st, [&] {
       if (split > 1)
         return tall ? launch_gram_split<kMN>(mx[x], p, split, st) : launch_gram_split<kK>(mx[x], p, split, st);
