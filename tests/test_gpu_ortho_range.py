@@ -99,3 +99,31 @@ def test_coefficients_that_leave_the_range_are_reported(coefs, B, R, C):
         out = o.update(g)
         assert o.status() == {"update": 0}
         near(out[:1], reference(g[:1], fine))
+
+
+# in scratch, where the padding of X, S and P is never written and read as zeros: both orientations, rows in vectors and
+# single elements, a split Gram product, steps in pairs, a side just past a tile
+@pytest.mark.parametrize("B,R,C", [(2, 203, 301), (2, 301, 203), (2, 129, 136), (1, 200, 3000), (1, 2501, 333),
+                                   (6, 600, 1500), (6, 1507, 601), (2, 257, 300)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_nans_around_have_no_part(B, R, C, dtype):
+    """A workspace full of NaN, NaN on either side of the gradient and the momentum, and guards around what is written."""
+    pad, n = 64, B * R * C
+    g, m0 = grad(B, R, C, dtype, 71), grad(B, R, C, "fp32", 72)
+    gb = torch.full((n + 2 * pad,), float("nan"), device="cuda", dtype=g.dtype)
+    mb = torch.full((n + 2 * pad,), float("nan"), device="cuda")
+    ob = torch.full((n + 2 * pad,), 7.0, device="cuda", dtype=torch.bfloat16)
+    gb[pad:pad + n], mb[pad:pad + n] = g.flatten(), m0.flatten()
+    o = moe.Orthogonaliser(B, R, C, dtype=dtype)
+    assert o.scratch.numel() > 4 * n  # the matrices are in it
+    for momentum in (None, mb[pad:pad + n].view(B, R, C)):
+        o.scratch.fill_(255)
+        o.update(gb[pad:pad + n].view(B, R, C), momentum=momentum, out=ob[pad:pad + n].view(B, R, C))
+        u = g.double()
+        if momentum is not None:
+            u = u + 0.95 * (0.95 * m0.double() + u)
+        assert o.status() == {"update": 0}
+        near(ob[pad:pad + n].view(B, R, C), reference(u))
+    assert bool((ob[:pad] == 7).all()) and bool((ob[pad + n:] == 7).all())
+    assert bool(torch.isnan(mb[:pad]).all()) and bool(torch.isnan(mb[pad + n:]).all())
+    assert bool(torch.isnan(gb[:pad]).all()) and bool(torch.isnan(gb[pad + n:]).all())
