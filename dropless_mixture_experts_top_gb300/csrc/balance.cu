@@ -21,11 +21,13 @@
 // integers, added in any order).  A single short sequence is one block and one
 // kernel.
 //
-// Bounds, measured: the backward moves 12 bytes per logit at 96% of the copy rate
-// (131072 x 250: 60 us); the forward of as many (4 bytes per logit, 20 us at that
-// rate) takes 38 to 51 us, for the latency of a token's chain of load, maximum,
-// exponentials and sum with the registers that its columns need; below some 20,000 tokens it is the latency of its two kernels
-// (16384 x 128 in four sequences: 12 us) or its one (512 x 8: 6).
+// Bounds, measured: the backward moves 12 bytes per logit at 98% of the copy rate
+// (131072 x 250: 59 us).  The forward of as many (4 bytes per logit, 20 us at that
+// rate) takes 35 to 51 us and is bound by its instructions: 72% of the issue slots are
+// taken at 57% of DRAM's rate, and of the 7.6 cycles between two instructions of a warp
+// 0.4 are waits for memory (3.1 for earlier results, 2.1 for a free slot or pipe).  Below
+// some 20,000 tokens it is the latency of its two kernels (16384 x 128 in four
+// sequences: 12 us) or its one (512 x 8: 6).
 #include <math.h>
 
 #include <type_traits>

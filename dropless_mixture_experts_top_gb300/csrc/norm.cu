@@ -11,8 +11,13 @@
 // Both are bound by memory: every input is read and every output written once.
 // Measured as called, bf16: forward with residual 16384 x 4096 80.6 us, 98% of what a
 // copy moves in that time; backward with d_sum 16384 x 2048 47.8 us, 83% (the kernel
-// 41.5 and the sums of its blocks' partial rows the rest).  512 x 128 takes 5.0 us,
-// the launch.
+// 41.5 and the sums of its blocks' partial rows the rest).  512 x 128 takes 5.2 us,
+// the launch.  Forward without residual 16384 x 2048 26.9 us, 74%: 1024 threads per SM
+// leave 64 registers, which also hold the weight and the bias, and 8 to 100 bytes a
+// thread are spilled.  fp32 16384 x 4096: forward with residual 176 us, 90%, without 96,
+// 82%.  Widths far from a power of two leave threads without elements (5120 with
+// residual 176 us, 56%), and ragged rows within a vector of 8192 take 1024 threads a
+// block, whose kernels spill 40 to 184 bytes a thread forward and 428 to 676 backward.
 //
 // Layout: a row is shared by TPR threads (a power of two, 8 to 512), each
 // holding kElems elements, in vectors of 16 bytes that lie TPR vectors apart, so
@@ -410,7 +415,7 @@ __device__ __forceinline__ void unpack_all(const uint4 *r, float (&f)[kElems]) {
 // Threads per SM that the kernels are built for.  Forward: 1024, or 512 with a
 // residual, whose two reads and two writes run faster from fewer rows at once
 // (16384 x 4096 bf16: 84 against 102 us; without one, 16384 x 2048: 28 against
-// 34 us the other way).  Backward: 512 (its column sums take the registers).
+// 34 us the other way, although 64 registers are too few there).  Backward: 512 (its column sums take the registers).
 constexpr int fwd_threads(bool res) { return res ? 512 : 1024; }
 constexpr int at_least_1(int x) { return x > 0 ? x : 1; }
 

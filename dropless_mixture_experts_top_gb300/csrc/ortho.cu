@@ -44,10 +44,11 @@
 //
 // What bounds it, measured (five steps, graph replays): 128 x 2048 x 768 takes 1.90
 // ms and 16 x 1536 x 4096 with momentum 1.63, of which the first pass over the
-// gradient is 131 and 193 us at the copy rate; the products execute 2.4e12
-// operations in the rest, 1.35e15 per second, against a library's 1.9e15 for one
+// gradient is 131 and 193 us at the copy rate.  The steps in pairs need 2.03e12
+// operations; with tiles that reach past the diagonal the products execute 2.4e12, in
+// the rest of the time 1.35e15 per second, against a library's 1.9e15 for one
 // large product (1.7e15 once the part's power cap holds the clock near 1.5 GHz; back
-// to back this update meets the cap too and takes 2.13 ms).  Symmetric products of
+// to back this update meets the cap too and takes 2.09 to 2.16 ms).  Symmetric products of
 // few tiles lose the most: 70 us each at n = 768, with 300 MB moved.  Small calls
 // are chains of dependent products of 4 to 6 us: 3 x 1000 x 333 takes 97 us, 8 x
 // 128 x 64 on chip 25.
@@ -66,7 +67,7 @@ namespace moe {
 namespace {
 
 constexpr float kSigma = 256.f;  // X is stored times this
-constexpr int kMaxDim = 16384, kMaxBatch = 65535, kMaxSteps = 64;  // (at most 2^28 tiles in a product)
+constexpr int kMaxDim = 16384, kMaxBatch = 65535, kMaxSteps = 64;  // (at most 2^30 tiles of 128 x 128 in a product)
 
 // ---------------------------------------------------------------- norms and the first X
 //

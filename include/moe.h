@@ -356,7 +356,9 @@ moe_status moe_balance_backward(const moe_balance_config *cfg, const float *logi
  * and the product of two steps' p in succession below 65504 (the usual quintic,
  * 3.4445 -4.7750 2.0315 five times, keeps s below 1.3 and p below 3.5).  A result that
  * is not finite sets MOE_DEV_NONFINITE_UPDATE.  Singular values far below
- * |u|_F / 1000 grow out of the roundings as they do out of a bf16 gradient's own.
+ * |u|_F / 1000 grow out of the roundings as they do out of a bf16 gradient's own; where
+ * eps is above |u|_F, values of u / eps below about 1e-7 lose exactness, those below
+ * 1e-10 become zero.
  * 1 <= R, C <= 16384, 0 <= batch <= 65535, 1 <= steps <= 64, any alignment of rows
  * (multiples of 8 columns are fastest).  out may not overlap g or momentum.  The
  * sum of squares is formed in fp32: values of u below about 1e-22 have no part in

@@ -127,3 +127,22 @@ def test_nans_around_have_no_part(B, R, C, dtype):
     assert bool((ob[:pad] == 7).all()) and bool((ob[pad + n:] == 7).all())
     assert bool(torch.isnan(mb[:pad]).all()) and bool(torch.isnan(mb[pad + n:]).all())
     assert bool(torch.isnan(gb[:pad]).all()) and bool(torch.isnan(gb[pad + n:]).all())
+
+
+@pytest.mark.parametrize("B,R,C", [(2, 256, 304), (2, 301, 203), (6, 600, 1500), (2, 96, 160), (2, 100, 252)])
+@pytest.mark.parametrize("size", [1e-5, 1e-6])
+def test_updates_below_eps(B, R, C, size):
+    """u / eps then, and what the steps make of it; its values (times 256 in fp16) are above the subnormals."""
+    eps = 1e-4
+    g = grad(B, R, C, "fp32", 91, size * eps)
+    x = g.double() / eps
+    assert float(torch.linalg.vector_norm(g.double(), dim=(1, 2)).max()) < eps
+    tall = R > C
+    x = x.transpose(1, 2) if tall else x
+    for a, b, c in moe.MUON_COEFS:
+        s = x @ x.transpose(1, 2)
+        x = a * x + (b * s + c * (s @ s)) @ x
+    o = moe.Orthogonaliser(B, R, C, dtype="fp32", eps=eps)
+    out = o.update(g)
+    assert o.status() == {"update": 0}
+    near(out, x.transpose(1, 2) if tall else x)
