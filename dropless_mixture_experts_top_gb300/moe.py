@@ -38,6 +38,7 @@ EXPORTED = [
     "moe_norm_workspace", "moe_norm_forward", "moe_norm_backward",
     "moe_balance_workspace", "moe_balance_forward", "moe_balance_backward",
     "moe_ortho_workspace", "moe_ortho_update",
+    "moe_gate_workspace", "moe_gate_forward", "moe_gate_backward", "moe_gate_update_bias",
 ]
 
 
@@ -62,6 +63,11 @@ class BalanceConfig(ctypes.Structure):
 
 class OrthoConfig(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("batch", "R", "C", "steps", "dtype")] + [("eps", ctypes.c_float)]
+
+
+class GateConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "E", "k", "score", "groups", "top_groups", "group_best",
+                                              "renormalise")] + [("scale", ctypes.c_float)]
 
 
 class SavedLayout(ctypes.Structure):
@@ -125,6 +131,12 @@ def lib():
         L.moe_balance_backward.argtypes = [P] * 5 + [ctypes.c_float, ctypes.c_float, P, ctypes.c_int32, P]
         L.moe_ortho_workspace.argtypes = [P, P]
         L.moe_ortho_update.argtypes = [P, P, P, P, ctypes.c_float, ctypes.c_int32, ctypes.c_float, P, P, sz, P]
+        L.moe_gate_workspace.argtypes = [P, P]
+        L.moe_gate_forward.argtypes = [P] * 5 + [sz, P]
+        L.moe_gate_backward.argtypes = [P] * 7
+        L.moe_gate_update_bias.argtypes = [P, P, P, ctypes.c_int32, ctypes.c_float, P]
+        for f in ("moe_gate_workspace", "moe_gate_forward", "moe_gate_backward", "moe_gate_update_bias"):
+            getattr(L, f).restype = ctypes.c_int
         for f in ("moe_ortho_workspace", "moe_ortho_update", "moe_norm_workspace", "moe_norm_forward", "moe_norm_backward", "moe_balance_workspace",
                   "moe_balance_forward", "moe_balance_backward"):
             getattr(L, f).restype = ctypes.c_int
@@ -553,6 +565,94 @@ class Orthogonaliser(_Plan):
     @_on_own_device
     def status(self, stream=None) -> dict:
         return {"update": get_device_status(self.scratch, stream)}
+
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+class Gate(_Plan):
+    """A routing from the router's logits: softmax or sigmoid scores, a bias for the
+    choice, groups of experts of which a token may use a few, weights renormalised
+    or not, and scaled; its gradient, and the step of the bias.
+
+    The routing is what MoELayer.route leaves: forward(..., out=layer.routing) routes
+    a layer.  After the layer's backward, backward(..., grads["d_topk_w"],
+    d_logits=grads["d_logits"]) replaces the gradient of the layer's own routing."""
+
+    def __init__(self, T, E, k, score="softmax", groups=1, top_groups=1, group_best=1, renormalise=True, scale=1.0,
+                 device="cuda"):
+        self.cfg = GateConfig(int(T), int(E), int(k), SCORES[score], int(groups), int(top_groups), int(group_best),
+                              bool(renormalise), float(scale))
+        n = ctypes.c_size_t()
+        _check(lib().moe_gate_workspace(ctypes.byref(self.cfg), ctypes.byref(n)), "moe_gate_workspace")
+        self.device, self._cfg = _device(device), ctypes.byref(self.cfg)
+        self._dev, self._fwd, self._bwd = self.device.index, lib().moe_gate_forward, lib().moe_gate_backward
+        self._te, self._tk, self._m, self._e, self._off = (
+            torch.Size(s) for s in ((T, E), (T, k), (T * k,), (E,), (E + 1,)))
+        self.fwd_scratch = self._take_scratch(n.value)
+        self._scratch = self.fwd_scratch.data_ptr()
+
+    def forward(self, logits, bias=None, out=None, stream=None) -> dict:
+        """{"topk_idx", "topk_w", "row_of_slot" [T, k]; "counts" [E]; "offsets" [E + 1]; "slot_of_row", "w_row"
+        [T k]}.  bias: fp32 [E], added to the scores that choose."""
+        d = self._dev
+        if _current_device() != d:
+            with torch.cuda.device(d):
+                return self.forward(logits, bias, out, stream)
+        if out is None:
+            f32, i32 = (dict(dtype=t, device=self.device) for t in (torch.float32, torch.int32))
+            with _on_stream(stream):
+                out = {"topk_idx": torch.empty(self._tk, **i32), "topk_w": torch.empty(self._tk, **f32),
+                       "counts": torch.empty(self._e, **i32), "offsets": torch.empty(self._off, **i32),
+                       "row_of_slot": torch.empty(self._tk, **i32), "slot_of_row": torch.empty(self._m, **i32),
+                       "w_row": torch.empty(self._m, **f32)}
+        rt = Routing(_addr(out["topk_idx"], "topk_idx", self._tk, _I32, d),
+                     _addr(out["topk_w"], "topk_w", self._tk, _F32, d), _addr(out["counts"], "counts", self._e, _I32, d),
+                     _addr(out["offsets"], "offsets", self._off, _I32, d),
+                     _addr(out["row_of_slot"], "row_of_slot", self._tk, _I32, d),
+                     _addr(out["slot_of_row"], "slot_of_row", self._m, _I32, d),
+                     _addr(out["w_row"], "w_row", self._m, _F32, d))
+        rc = self._fwd(self._cfg, _addr(logits, "logits", self._te, _F32, d), _addr(bias, "bias", self._e, _F32, d),
+                       ctypes.byref(rt), self._scratch, self.fwd_scratch.numel(),
+                       self._working(self.fwd_scratch, stream))
+        if rc:
+            raise MoEError("moe_gate_forward", rc)
+        return out
+
+    def backward(self, logits, topk_idx, topk_w, d_topk_w, d_logits=None, stream=None):
+        """The gradient for the logits (d_logits is overwritten where it is given)."""
+        d = self._dev
+        if _current_device() != d:
+            with torch.cuda.device(d):
+                return self.backward(logits, topk_idx, topk_w, d_topk_w, d_logits, stream)
+        if d_logits is None:
+            with _on_stream(stream):
+                d_logits = torch.empty(self._te, dtype=torch.float32, device=self.device)
+        rc = self._bwd(self._cfg, _addr(logits, "logits", self._te, _F32, d),
+                       _addr(topk_idx, "topk_idx", self._tk, _I32, d), _addr(topk_w, "topk_w", self._tk, _F32, d),
+                       _addr(d_topk_w, "d_topk_w", self._tk, _F32, d), _addr(d_logits, "d_logits", self._te, _F32, d),
+                       _raw_stream(stream, d))
+        if rc:
+            raise MoEError("moe_gate_backward", rc)
+        return d_logits
+
+    @_on_own_device
+    def update_bias(self, bias, counts, rate, stream=None):
+        """bias (fp32 [E], in place) one step of `rate` towards even loads.  counts: int32 [E], a routing's, or
+        [rows, E], added up (BalanceLoss's, which leave padding out)."""
+        E = self._e[0]
+        rows = counts.shape[0] if counts.dim() == 2 else 1
+        shape = torch.Size((rows, E)) if counts.dim() == 2 else self._e
+        rc = lib().moe_gate_update_bias(self._cfg, _addr(bias, "bias", self._e, _F32, self._dev),
+                                        _addr(counts, "counts", shape, _I32, self._dev), rows, float(rate),
+                                        _raw_stream(stream, self._dev))
+        if rc:
+            raise MoEError("moe_gate_update_bias", rc)
+        return bias
+
+    @_on_own_device
+    def status(self, stream=None) -> dict:
+        return {"forward": get_device_status(self.fwd_scratch, stream)}
 
 
 def selftest_wait_timeout(status, stream=None):

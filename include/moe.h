@@ -377,6 +377,55 @@ moe_status moe_ortho_update(const moe_ortho_config *cfg, const float *coefs, con
                             float beta, int32_t nesterov, float scale, void *out, void *scratch,
                             size_t scratch_bytes, void *stream);
 
+/* The gate: a routing from the router's logits [T,E] fp32, in the forms that moe_route does not have.
+ * Per token, with l its logits:
+ *   s = softmax(l) or sigmoid(l);   c = s + bias (fp32 [E], or NULL: the order of l)
+ *   groups: the E experts are `groups` equal runs; a group's score is the sum of its group_best (1 or 2)
+ *   largest c; the top_groups best groups stay (ties: the lower group)
+ *   S = the k largest c among the experts of those groups (ties: the lower expert)
+ *   w_j = scale s_{S_j} / sum_i s_{S_i}   (renormalise), or scale s_{S_j}
+ * The bias enters the choice alone, not the weights.  topk_idx is ordered by (c desc, index asc), and all
+ * fields of *routing are written as moe_route writes them, so that moe_forward and moe_backward take it.
+ * The choice is that of exact scores: tokens whose scores lie closer together than fp32 resolves are
+ * chosen again from scores in 64 bits, so that a recomputed forward, or another program, chooses the same.
+ * (A bias that is far larger than the scores, 1e3 and more, makes that every token, at some hundred times
+ * the cost.)
+ * A logit of -inf, or a bias of -inf or NaN, is an expert that may not be chosen; a group's score goes over
+ * the others, and a group without any comes last.  Slots that no expert is left for are filled with the
+ * remaining experts by index, at weight zero.  A NaN logit counts as -inf, +inf as the largest float, and
+ * both set MOE_DEV_NONFINITE_LOGIT (status word at the start of the scratch).
+ * 0 <= T <= 2^30, T * k < 2^31, 1 <= E <= 256, 1 <= k <= min(E, 16), 1 <= groups <= 32, a divisor of E,
+ * 1 <= top_groups <= groups, top_groups * (E / groups) >= k, 0 < scale, finite.
+ * Backward: d_logits [T,E] (overwritten) from d_topk_w [T,k], the gradient of the weights (moe_backward's
+ * d_topk_w; its d_logits are those of moe_route's weights and not used), and the routing's topk_idx and
+ * topk_w.  A token's indices are distinct; a slot whose index is outside [0, E), or whose weight is zero,
+ * has no part.  The bias has no gradient; its step
+ *   bias_e += rate * sign(mean over experts of the load - load_e)
+ * takes the load from counts [rows,E], added up over the rows: a routing's counts (rows = 1), or
+ * moe_balance_forward's (rows = sequences), which leave padding out.  d_logits may not overlap an input. */
+typedef enum {
+  MOE_SCORE_SOFTMAX = 0,
+  MOE_SCORE_SIGMOID = 1
+} moe_score;
+typedef struct {
+  int32_t T;           /* tokens */
+  int32_t E;           /* experts */
+  int32_t k;           /* experts per token */
+  int32_t score;       /* moe_score */
+  int32_t groups;      /* groups of E / groups experts; 1: none */
+  int32_t top_groups;  /* groups that a token may use */
+  int32_t group_best;  /* scores that a group is judged by: 1 or 2 */
+  int32_t renormalise; /* nonzero: the weights of a token add up to scale */
+  float scale;         /* factor of the weights */
+} moe_gate_config;
+moe_status moe_gate_workspace(const moe_gate_config *cfg, size_t *fwd_scratch);
+moe_status moe_gate_forward(const moe_gate_config *cfg, const float *logits, const float *bias,
+                            const moe_routing *routing, void *scratch, size_t scratch_bytes, void *stream);
+moe_status moe_gate_backward(const moe_gate_config *cfg, const float *logits, const int32_t *topk_idx,
+                             const float *topk_w, const float *d_topk_w, float *d_logits, void *stream);
+moe_status moe_gate_update_bias(const moe_gate_config *cfg, float *bias, const int32_t *counts, int32_t rows,
+                                float rate, void *stream);
+
 /* Routing without a caller-provided scratch buffer.  The paper has no
  * counterpart: it exists for callers that cannot allocate device memory --
  * code running while a CUDA graph is captured (cudaMalloc is not allowed
