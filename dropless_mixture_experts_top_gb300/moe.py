@@ -38,6 +38,7 @@ EXPORTED = [
     "moe_norm_workspace", "moe_norm_forward", "moe_norm_backward",
     "moe_balance_workspace", "moe_balance_forward", "moe_balance_backward",
     "moe_ortho_workspace", "moe_ortho_update",
+    "moe_adamw_state_elements", "moe_adamw_step",
     "moe_gate_workspace", "moe_gate_forward", "moe_gate_backward", "moe_gate_update_bias",
 ]
 
@@ -68,6 +69,15 @@ class OrthoConfig(ctypes.Structure):
 class GateConfig(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "E", "k", "score", "groups", "top_groups", "group_best",
                                               "renormalise")] + [("scale", ctypes.c_float)]
+
+
+class AdamWConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("tensors", "param_dtype", "grad_dtype", "state_bits")] + \
+               [(n, ctypes.c_double) for n in ("beta1", "beta2", "eps")]
+
+
+class AdamWState(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("m", "v", "m_scale", "v_scale", "step")]
 
 
 class SavedLayout(ctypes.Structure):
@@ -135,7 +145,9 @@ def lib():
         L.moe_gate_forward.argtypes = [P] * 5 + [sz, P]
         L.moe_gate_backward.argtypes = [P] * 7
         L.moe_gate_update_bias.argtypes = [P, P, P, ctypes.c_int32, ctypes.c_float, P]
-        for f in ("moe_gate_workspace", "moe_gate_forward", "moe_gate_backward", "moe_gate_update_bias"):
+        L.moe_adamw_state_elements.argtypes = [P, P, P]
+        L.moe_adamw_step.argtypes = [P] * 7 + [ctypes.c_double, P, P, P]
+        for f in ("moe_adamw_state_elements", "moe_adamw_step", "moe_gate_workspace", "moe_gate_forward", "moe_gate_backward", "moe_gate_update_bias"):
             getattr(L, f).restype = ctypes.c_int
         for f in ("moe_ortho_workspace", "moe_ortho_update", "moe_norm_workspace", "moe_norm_forward", "moe_norm_backward", "moe_balance_workspace",
                   "moe_balance_forward", "moe_balance_backward"):
@@ -565,6 +577,87 @@ class Orthogonaliser(_Plan):
     @_on_own_device
     def status(self, stream=None) -> dict:
         return {"update": get_device_status(self.scratch, stream)}
+
+
+class AdamW:
+    """An AdamW step over tensors of these shapes, all at once: parameters of one type
+    ("fp32", with bf16 copies of them if wanted, or "bf16"), gradients of one, states
+    of 32 bits ("fp32") or 8 ("8bit": e4m3 values with an fp32 scale per 256).
+    weight_decay: one number, or one for each tensor."""
+
+    def __init__(self, shapes, param="fp32", grad="bf16", state="fp32", weight_decay=0.01, beta1=0.9, beta2=0.999,
+                 eps=1e-8, device="cuda"):
+        self._shapes = [torch.Size(s) for s in shapes]
+        count = len(self._shapes)
+        decay = [float(d) for d in weight_decay] if isinstance(weight_decay, (list, tuple)) else [float(weight_decay)] * count
+        if len(decay) != count:
+            raise ValueError(f"weight_decay: {len(decay)} numbers for {count} tensors")
+        if any(not 0 <= d < float("inf") for d in decay):
+            raise ValueError("weight_decay: numbers of at least 0")
+        self.bits = {"fp32": 32, "8bit": 8}[state]
+        self.cfg = AdamWConfig(count, DTYPES[param], DTYPES[grad], self.bits, float(beta1), float(beta2), float(eps))
+        self._n = (ctypes.c_int64 * count)(*[s.numel() for s in self._shapes])
+        self._decay, self._array = (ctypes.c_double * count)(*decay), ctypes.c_void_p * count
+        n = ctypes.c_int64()
+        _check(lib().moe_adamw_state_elements(ctypes.byref(self.cfg), self._n, ctypes.byref(n)),
+               "moe_adamw_state_elements")
+        self.device, self._cfg, self._step = _device(device), ctypes.byref(self.cfg), lib().moe_adamw_step
+        self._dev, self._ptypes, self._gtypes = self.device.index, _TORCH_DTYPES[param], _TORCH_DTYPES[grad]
+        self._codes = _F32 if self.bits == 32 else _E4M3
+        self._all, self._blocks = torch.Size((n.value,)), torch.Size((n.value // 256,))
+
+    def new_state(self) -> dict:
+        """States before the first step: {"m", "v" [elements], with 8 bits "m_scale", "v_scale" [elements / 256], "step" [4]}.
+        A tensor's states start at a multiple of 256 elements, in the order of the shapes."""
+        zeros = lambda s, t: torch.zeros(s, dtype=t, device=self.device)  # noqa: E731
+        st = {"m": zeros(self._all, self._codes[0]), "v": zeros(self._all, self._codes[0])}
+        if self.bits == 8:
+            st.update(m_scale=zeros(self._blocks, torch.float32), v_scale=zeros(self._blocks, torch.float32))
+        st["step"] = zeros((4,), torch.int32)
+        return st
+
+    def step(self, params, grads, state, lr, copies=None, grad_scale=None, stream=None):
+        """Advances params, state and copies (a list of bf16 tensors, or None) in place.  lr: a number, or a device
+        fp32 tensor of one element; grad_scale: such a tensor that the gradients are multiplied with (of a value
+        that is not finite: the step is left out)."""
+        d, shapes = self._dev, self._shapes
+        if _current_device() != d:
+            with torch.cuda.device(d):
+                return self.step(params, grads, state, lr, copies, grad_scale, stream)
+        for what, ts in (("params", params), ("grads", grads), ("copies", copies)):
+            if ts is not None and len(ts) != len(shapes):
+                raise ValueError(f"{what}: {len(ts)} tensors, expected {len(shapes)}")
+        pt, gt, ct = self._ptypes, self._gtypes, self._codes
+        on_device = isinstance(lr, torch.Tensor)
+        eight = self.bits == 8
+        st = AdamWState(_addr(state["m"], "m", self._all, ct, d), _addr(state["v"], "v", self._all, ct, d),
+                        _addr(state["m_scale"], "m_scale", self._blocks, _F32, d) if eight else None,
+                        _addr(state["v_scale"], "v_scale", self._blocks, _F32, d) if eight else None,
+                        _addr(state["step"], "step", _STEP, _I32, d))
+        rc = self._step(
+            self._cfg, self._n, self._decay, self._array(*[_addr(p, "params", s, pt, d) for p, s in zip(params, shapes)]),
+            self._array(*[_addr(g, "grads", s, gt, d) for g, s in zip(grads, shapes)]),
+            None if copies is None else self._array(*[_addr(c, "copies", s, _BF16, d) for c, s in zip(copies, shapes)]),
+            ctypes.byref(st), 0.0 if on_device else lr, _one(lr, "lr", d) if on_device else None,
+            _one(grad_scale, "grad_scale", d), _raw_stream(stream, d))
+        if rc:
+            raise MoEError("moe_adamw_step", rc)
+
+    def status(self, state, stream=None) -> dict:
+        with torch.cuda.device(self._dev):
+            return {"step": get_device_status(state["step"], stream)}
+
+
+_E4M3, _STEP = (torch.float8_e4m3fn,), torch.Size((4,))
+
+
+def _one(t, name, dev):
+    """The address of a device number (fp32, of any shape with one element), or None."""
+    if t is None:
+        return None
+    if t.numel() != 1:
+        raise ValueError(f"{name}: {tuple(t.shape)}, expected one element")
+    return _addr(t, name, t.shape, _F32, dev)
 
 
 SCORES = {"softmax": 0, "sigmoid": 1}

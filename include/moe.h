@@ -426,6 +426,46 @@ moe_status moe_gate_backward(const moe_gate_config *cfg, const float *logits, co
 moe_status moe_gate_update_bias(const moe_gate_config *cfg, float *bias, const int32_t *counts, int32_t rows,
                                 float rate, void *stream);
 
+/* One AdamW step over a list of tensors (for parameters that are no expert matrices: norms, router,
+ * embeddings; or for all of them).  Tensor i has n[i] >= 0 elements (at most 2^40 in all): params[i] of
+ * param_dtype, updated in place; grads[i] of grad_dtype; copies (NULL: none; fp32 parameters only)
+ * with copies[i], or NULL, a bf16 copy of the new parameter; decay[i] >= 0 its weight decay (decay NULL: 0).
+ * The arrays of sizes, decays and addresses are host memory, read during the call.  In fp32,
+ *   g = grads * *grad_scale (device fp32; NULL: 1),   t = the step's number, from 1
+ *   m <- beta1 m + (1 - beta1) g,   v <- beta2 v + (1 - beta2) g^2
+ *   p <- p (1 - lr decay) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * with lr from *lr_device (device fp32) where that is given, so that a captured step follows a schedule.
+ * States, in one array each over all tensors, a tensor's from a multiple of 256 elements on
+ * (moe_adamw_state_elements gives the elements of an array; the padding is not touched):
+ *   state_bits 32: m, v fp32;
+ *   state_bits 8: m and the root of v as e4m3 codes, m_scale and v_scale fp32, one per 256 elements: a value
+ *   is its code's times the scale, which is the block's largest (1e-30 at least) / 448; rounded to
+ *   nearest even, a root above zero to 2^-9 of the scale at least.  This step uses m and v from before the rounding.
+ *   step: int32 [4]: the status word, the number of steps so far, and two words that are zero between
+ *   calls.  A call adds one to the steps.
+ * All of it starts as zeros.  A step after which a parameter or v is not finite sets MOE_DEV_NONFINITE_UPDATE
+ * in the status word (of the last call; moe_get_device_status reads it from step); such an element is stored as
+ * e4m3's NaN and leaves the scale of its block alone.  Where *grad_scale is not finite the step
+ * is left out: nothing changes but the status word, which gets that flag.
+ * Tensors overlap neither each other nor the states.  Calls of up to 64 tensors with elements are one launch. */
+typedef struct {
+  int32_t tensors;
+  int32_t param_dtype; /* moe_dtype */
+  int32_t grad_dtype;  /* moe_dtype */
+  int32_t state_bits;  /* 8 or 32 */
+  double beta1, beta2; /* in [0, 1) */
+  double eps;          /* >= 0 */
+} moe_adamw_config;
+typedef struct {
+  void *m, *v;              /* device [elements], fp32 or e4m3 */
+  float *m_scale, *v_scale; /* device [elements / 256]; state_bits 8 only */
+  int32_t *step;            /* device [4] */
+} moe_adamw_state;
+moe_status moe_adamw_state_elements(const moe_adamw_config *cfg, const int64_t *n, int64_t *elements);
+moe_status moe_adamw_step(const moe_adamw_config *cfg, const int64_t *n, const double *decay, void *const *params,
+                          const void *const *grads, void *const *copies, const moe_adamw_state *state, double lr,
+                          const float *lr_device, const float *grad_scale, void *stream);
+
 /* Routing without a caller-provided scratch buffer.  The paper has no
  * counterpart: it exists for callers that cannot allocate device memory --
  * code running while a CUDA graph is captured (cudaMalloc is not allowed
