@@ -1,0 +1,840 @@
+// linear.cu -- a dense layer: a matrix product with bias, activation and residual
+// in its epilogue, and its backward pass.
+//
+//   forward   z = x W + bias,   y = act(z) + residual        x [T,K], W [K,N]
+//   backward  dz = dy act'(z),  dx = dz W^T,  dW = x^T dz,  dbias = sum_t dz
+// x, W, bias, residual, z, y, dy, dx and dW are bf16, sums fp32; dz is rounded to
+// bf16 as an operand of the two products (dbias adds it up unrounded).
+//
+// Activations, in fp32:  relu;  silu z s(z);  gelu z s(2 sqrt(2/pi) (z + 0.044715 z^3)), the
+// tanh form written with the sigmoid s, which takes one exponential and one reciprocal.
+//
+// No transposes: the tensor core reads either operand with its reduction axis
+// contiguous (K-major boxes) or strided (MN-major): x . W reads W strided, dz . W^T
+// contiguous, x^T . dz both strided.
+//
+// The products run on CTA pairs (tcgen05 cta_group::2, 256 x 256 tiles) or single
+// CTAs (128 x 128), persistent over tiles, fp32 accumulators double-buffered in TMEM:
+//   warp 0     TMA producer (each CTA): 128B-swizzled boxes, zeros past the ends
+//   warp 1     MMA issuer (of a pair: CTA 0's)
+//   warps 2-9  epilogue: tcgen05.ld, bias, activation, residual, bf16 rows
+// Tiles that do not fill a last round are split along the reduction, so that the round
+// is full: their parts leave fp32 sums in the workspace, which a second kernel adds in
+// a fixed order before the same epilogue.
+// Every wait is bounded; on a timeout the kernel flags the status word, drains its
+// copies and MMAs, frees TMEM and returns.
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "abi.h"
+#include "common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxDim = 65536;
+constexpr int BM = 128;
+constexpr int tile_size(int cg) { return BM * cg; }
+constexpr int BK = 64;                // reduction elements per box: one 128-byte swizzle row
+constexpr int kHalf = 128 * BK * 2;   // one operand's box (or two 64 x 64 boxes) per CTA: 16 KB
+constexpr int kBox = 64 * 64 * 2;
+constexpr int kStages = 3;
+constexpr int kStageBytes = 4 * kHalf;  // two K blocks: [A k0 | A k1 | B k0 | B k1]
+constexpr int kEpiWarps = 8;
+constexpr int kGemmThreads = 64 + 32 * kEpiWarps;
+constexpr int kGemmSmem = kStages * kStageBytes + 256 + 1024 /*align*/;
+static_assert(kGemmSmem <= 227 * 1024, "shared memory budget");
+constexpr int kRuleSms = 152;         // the workspace's size is known without a GPU
+constexpr int kMaxSplit = 8;
+constexpr int kLeastStages = 4;       // of a part of a split reduction
+
+enum Product : int { kFwd = 0, kDx = 1, kDw = 2 };
+
+struct Ends {  // what an epilogue adds and writes
+  const uint16_t *bias, *res;
+  uint16_t *y, *z;
+  int act;
+  bool sectors;  // every row of res, y and z starts on 32 bytes
+};
+struct ProductArgs {
+  int M, N, K;    // rows, columns, reduction
+  int nm, nn;     // tiles along both
+  int full;       // tiles that are computed whole; the others in `split` parts
+  int split;
+  int units;      // tiles and parts in all
+  float *part;    // [parts][tile][tile]
+  Ends e;
+  int32_t *status;
+  bool first;     // of the call's kernels: clears the status word
+};
+
+// The k-th unit of work: its tile, and its stages of the reduction.
+struct Unit {
+  int m0, n0, ks0, ks1, part;  // part: index of the sums it leaves, or -1
+};
+template <int CG>
+__device__ __forceinline__ Unit unit_of(int u, const ProductArgs &p, int nstage) {
+  constexpr int TS = tile_size(CG);
+  Unit t;
+  int tile = u;
+  t.ks0 = 0;
+  t.ks1 = nstage;
+  t.part = -1;
+  if (u >= p.full && p.split > 1) {
+    t.part = u - p.full;
+    const int s = t.part % p.split;
+    tile = p.full + t.part / p.split;
+    t.ks0 = static_cast<int>(static_cast<int64_t>(nstage) * s / p.split);
+    t.ks1 = static_cast<int>(static_cast<int64_t>(nstage) * (s + 1) / p.split);
+  }
+  const int mt = tile / p.nn;
+  t.m0 = mt * TS;
+  t.n0 = (tile - mt * p.nn) * TS;
+  return t;
+}
+
+// A lane's 32 columns of a row (64 bytes, eight columns a piece), of which ncols (a multiple of
+// eight) exist.
+__device__ __forceinline__ void ld_row(const uint16_t *p, int ncols, bool sectors, uint4 (&w)[4]) {
+  if (sectors) {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2)
+      if (8 * i < ncols)
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w), "=r"(w[i + 1].x), "=r"(w[i + 1].y),
+                       "=r"(w[i + 1].z), "=r"(w[i + 1].w)
+                     : "l"(p + 8 * i)
+                     : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (8 * i < ncols) w[i] = *reinterpret_cast<const uint4 *>(p + 8 * i);
+  }
+}
+__device__ __forceinline__ void st_row(uint16_t *p, int ncols, bool sectors, const float (&v)[32]) {
+  uint4 w[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    w[q] = make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                      pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+  if (sectors) {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2)
+      if (8 * i < ncols)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + 8 * i), "r"(w[i].x), "r"(w[i].y),
+                     "r"(w[i].z), "r"(w[i].w), "r"(w[i + 1].x), "r"(w[i + 1].y), "r"(w[i + 1].z), "r"(w[i + 1].w)
+                     : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (8 * i < ncols) *reinterpret_cast<uint4 *>(p + 8 * i) = w[i];
+  }
+}
+__device__ __forceinline__ void unpack_row(const uint4 (&w)[4], float (&v)[32]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t x[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      v[8 * q + 2 * h] = bf16_lo(x[h]);
+      v[8 * q + 2 * h + 1] = bf16_hi(x[h]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- activations
+
+// The sigmoid by the part's exponential and reciprocal: within a few fp32 ulp, far below the
+// bf16 rounding of what it enters.
+__device__ __forceinline__ float sigmoid_(float a) { return __fdividef(1.f, 1.f + __expf(-a)); }
+constexpr float kGelu1 = 1.5957691216057308f;   // 2 sqrt(2 / pi)
+constexpr float kGelu3 = 0.071354816272600252f; // times 0.044715
+// Past 20 gelu's sigmoid is 0 or 1 to the last bit, and its slope's polynomial would overflow first.
+__device__ __forceinline__ float gelu_arg(float z) {
+  const float c = fminf(fmaxf(z, -20.f), 20.f);
+  return c * fmaf(kGelu3 * c, c, kGelu1);
+}
+__device__ __forceinline__ float activate(float z, int act) {
+  switch (act) {
+    case MOE_ACT_RELU: return fmaxf(z, 0.f);
+    case MOE_ACT_SILU: return z * sigmoid_(z);
+    case MOE_ACT_GELU: return z * sigmoid_(gelu_arg(z));
+    default: return z;
+  }
+}
+__device__ __forceinline__ float slope(float z, int act) {
+  switch (act) {
+    case MOE_ACT_RELU: return z > 0.f ? 1.f : 0.f;
+    case MOE_ACT_SILU: {
+      const float s = sigmoid_(z);
+      return fmaf(z * s, 1.f - s, s);
+    }
+    case MOE_ACT_GELU: {
+      const float c = fminf(fmaxf(z, -20.f), 20.f), s = sigmoid_(gelu_arg(z));
+      return fmaf(c * s * (1.f - s), fmaf(3.f * kGelu3 * c, c, kGelu1), s);
+    }
+    default: return 1.f;
+  }
+}
+
+// A row's 32 columns from c0 on: bias, activation, residual, and what is stored.  res: the residual's
+// 64 bytes where there is one.
+template <int KIND>
+__device__ __forceinline__ void finish_row(float (&v)[32], const Ends &e, const uint4 (&res)[4], int64_t at, int c0, int ncols) {
+  if constexpr (KIND == kFwd) {
+    if (e.bias) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (8 * q < ncols) {
+          const uint4 b = __ldg(reinterpret_cast<const uint4 *>(e.bias + c0 + 8 * q));
+          const uint32_t x[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            v[8 * q + 2 * h] += bf16_lo(x[h]);
+            v[8 * q + 2 * h + 1] += bf16_hi(x[h]);
+          }
+        }
+      }
+    }
+    if (e.z) st_row(e.z + at, ncols, e.sectors, v);
+    if (e.act == MOE_ACT_RELU) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = activate(v[i], MOE_ACT_RELU);
+    } else if (e.act == MOE_ACT_SILU) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = activate(v[i], MOE_ACT_SILU);
+    } else if (e.act == MOE_ACT_GELU) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = activate(v[i], MOE_ACT_GELU);
+    }
+    if (e.res) {
+      float r[32];
+      unpack_row(res, r);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] += r[i];
+    }
+  }
+  st_row(e.y + at, ncols, e.sectors, v);
+}
+
+// ---------------------------------------------------------------- the product
+
+template <bool MN, int CG>
+__device__ __forceinline__ void load_operand(uint8_t *dst, const CUtensorMap *map, uint64_t *bar, uint32_t bar0, int k0,
+                                             int r0) {
+  auto load = [&](uint8_t *to, int x, int y) {
+    if constexpr (CG == 2)
+      tma_load_2d_pair(to, map, bar0, x, y);
+    else
+      tma_load_2d(to, map, bar, x, y);
+  };
+  if constexpr (MN) {
+    load(dst, r0, k0);
+    load(dst + kBox, r0 + 64, k0);
+  } else {
+    load(dst, k0, r0);
+  }
+}
+// Descriptor of the j-th 16 of K of a block at shared address s.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t s, int j, bool mn) {
+  return mn ? smem_desc_sw128(s + j * 2048, kBox, 1024) : smem_desc_sw128(s + j * 32, 16, 1024);
+}
+
+template <int KIND, int CG>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    linear_product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const ProductArgs p) {
+  constexpr int TS = tile_size(CG);
+  constexpr uint32_t kTmemCols = 2 * TS;
+  constexpr bool AMN = KIND == kDw, BMN = KIND != kDx;
+  constexpr int kChunks = TS / 64;  // 32-column chunks of a warp's half of the columns
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem =
+      reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + kStages * kStageBytes);  // [kStages] CTA 0: both CTAs' copies
+  uint64_t *empty = full + kStages;      // [kStages] the pair's MMAs are done with the stage
+  uint64_t *tfull = empty + kStages;     // [2] accumulator ready (both CTAs)
+  uint64_t *tempty = tfull + 2;          // [2] CTA 0: both CTAs' epilogues done
+  uint64_t *drain = tempty + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = CG == 2 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int group = blockIdx.x / CG, ngroups = gridDim.x / CG;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], CG * kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 1) {
+    if constexpr (CG == 2)
+      tmem_alloc_pair(tmem_slot, kTmemCols);
+    else
+      tmem_alloc(tmem_slot, kTmemCols);
+  }
+  griddep_wait();  // the set-up above overlaps the previous kernel's end; its outputs are read below
+  // (a wait that runs out takes two seconds: no block flags one before this)
+  if (p.first && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();  // both CTAs' barriers initialised before any remote arrival
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int nkb = (p.K + BK - 1) / BK, nstage = (nkb + 1) / 2;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint32_t full0 = CG == 2 ? peer_smem_addr(&full[0], 0) : 0;
+      int stage = 0;
+      uint32_t phase = 0, armed = 0, arm_par = 0;
+      bool ok = true;
+      for (int u = group; u < p.units && ok; u += ngroups) {
+        const Unit t = unit_of<CG>(u, p, nstage);
+        for (int ks = t.ks0; ks < t.ks1; ++ks) {
+          if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          uint8_t *sa = smem + stage * kStageBytes;
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], CG * kStageBytes);  // the group's bytes
+          // a K block past the end is zero fill, and no MMA reads it
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int k0 = (ks * 2 + h) * BK;
+            load_operand<AMN, CG>(sa + h * kHalf, &tmA, &full[stage], full0 + 8u * stage, k0, t.m0 + BM * rank);
+            load_operand<BMN, CG>(sa + (2 + h) * kHalf, &tmB, &full[stage], full0 + 8u * stage, k0, t.n0 + BM * rank);
+          }
+          armed |= 1u << stage;
+          arm_par = (arm_par & ~(1u << stage)) | (phase << stage);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      griddep_launch_dependents();  // all loads issued: the next kernel may be launched
+      if (*abort_flag && rank == 0) {  // let the pair's copies land before exit
+        for (int s = 0; s < kStages; ++s) {
+          if (!((armed >> s) & 1u)) continue;
+          for (int i = 0; i < (1 << 22) && !mbar_try_wait(&full[s], (arm_par >> s) & 1u); ++i) {
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      auto mma = [](uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+        if constexpr (CG == 2)
+          tc_mma_f16_pair(d, a, b, idesc, acc);
+        else
+          tc_mma_f16_one(d, a, b, idesc, acc);
+      };
+      auto commit = [](uint64_t *bar) {
+        if constexpr (CG == 2)
+          tc_commit_pair(bar);
+        else
+          tc_commit(bar);
+      };
+      constexpr uint32_t idesc = idesc_bf16(TS, TS, AMN, BMN);
+      int stage = 0, it = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int u = group; u < p.units && ok; u += ngroups, ++it) {
+        const Unit t = unit_of<CG>(u, p, nstage);
+        const int buf = it & 1;
+        if (!mbar_wait(&tempty[buf], ((it >> 1) & 1) ^ 1, abort_flag)) break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + buf * TS;
+        for (int ks = t.ks0; ks < t.ks1; ++ks) {
+          if (!mbar_wait(&full[stage], phase, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t ab = smem_addr(smem + stage * kStageBytes), bb = ab + 2 * kHalf;
+          const int nblk = min(2, nkb - ks * 2);  // K blocks inside K
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (h < nblk) {
+#pragma unroll
+              for (int j = 0; j < BK / 16; ++j)
+                mma(d, operand_desc(ab + h * kHalf, j, AMN), operand_desc(bb + h * kHalf, j, BMN), idesc,
+                    (ks != t.ks0 || (h | j) != 0) ? 1u : 0u);
+            }
+          }
+          commit(&empty[stage]);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        commit(&tfull[buf]);
+      }
+      if (*abort_flag) {  // wait for the pair's MMAs before TMEM is freed
+        commit(drain);
+        for (int i = 0; i < (1 << 22) && !mbar_try_wait(drain, 0); ++i) {
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    const int q = warp & 3;               // TMEM lane quarter
+    const int half = (warp - 2) >> 2;     // column half
+    const uint32_t tempty0 = CG == 2 ? peer_smem_addr(&tempty[0], 0) : 0;
+    int it = 0;
+    for (int u = group; u < p.units; u += ngroups, ++it) {
+      const Unit t = unit_of<CG>(u, p, nstage);
+      const int buf = it & 1, row = t.m0 + BM * rank + q * 32 + lane, cols0 = t.n0 + half * (TS / 2);
+      const int64_t row_at = static_cast<int64_t>(row) * p.N;
+      uint4 res[KIND == kFwd ? kChunks : 1][4];
+      if constexpr (KIND == kFwd) {  // while the product runs
+        if (p.e.res && t.part < 0 && row < p.M) {
+#pragma unroll
+          for (int j = 0; j < kChunks; ++j)
+            if (cols0 + 32 * j < p.N) ld_row(p.e.res + row_at + cols0 + 32 * j, p.N - (cols0 + 32 * j), p.e.sectors, res[j]);
+        }
+      }
+      if (!wait_lane0(&tfull[buf], (it >> 1) & 1, abort_flag)) break;
+      __syncwarp();
+      tc_fence_after();
+      const uint32_t tb = tmem_base + buf * TS + (static_cast<uint32_t>(q * 32) << 16) + half * (TS / 2);
+#pragma unroll(KIND == kFwd ? kChunks : 1)
+      for (int j = 0; j < kChunks; ++j) {
+        const int c0 = cols0 + 32 * j;
+        if (c0 >= p.N) break;
+        uint32_t acc[32];
+        tmem_ld32(tb + 32 * j, acc);
+        tmem_ld_wait();
+        if (t.part >= 0) {  // sums of a part: the whole tile, rows and columns past the ends among it
+          float *to = p.part + (static_cast<int64_t>(t.part) * TS + BM * rank + q * 32 + lane) * TS + half * (TS / 2) + 32 * j;
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<uint4 *>(to + i) = make_uint4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+        } else if (row < p.M) {
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(acc[i]);
+          finish_row<KIND>(v, p.e, res[KIND == kFwd ? j : 0], row_at + c0, c0, min(32, p.N - c0));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CG == 2)
+          mbar_arrive_cluster(tempty0 + 8u * buf);
+        else
+          mbar_arrive(&tempty[buf]);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) flag_status(p.status, kDevWaitTimeout);
+  if constexpr (CG == 2) cluster_sync();  // the pair is done with each other's barriers and TMEM
+  if (warp == 1) {
+    tc_fence_after();
+    if constexpr (CG == 2)
+      tmem_dealloc_pair(tmem_base, kTmemCols);
+    else
+      tmem_dealloc(tmem_base, kTmemCols);
+  }
+}
+
+// The tiles in parts: their sums in the order of the parts, then the epilogue.  A thread has eight
+// columns of a row.
+constexpr int kFinishThreads = 256;
+template <int KIND, int CG>
+__global__ void __launch_bounds__(kFinishThreads) linear_finish_kernel(const ProductArgs p) {
+  constexpr int TS = tile_size(CG), kPer = TS / 8;
+  griddep_wait();  // the previous kernel in the stream has completed
+  griddep_launch_dependents();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kFinishThreads + threadIdx.x;
+  const int r = static_cast<int>(i / (TS * kPer)), in = static_cast<int>(i % (TS * kPer));
+  const int tile = p.full + r;
+  if (tile >= p.nm * p.nn) return;
+  const int mt = tile / p.nn, row = mt * TS + in / kPer, c0 = (tile - mt * p.nn) * TS + in % kPer * 8;
+  if (row >= p.M || c0 >= p.N) return;
+  const float *from = p.part + (static_cast<int64_t>(r) * p.split * TS + in / kPer) * TS + in % kPer * 8;
+  float v[8] = {};
+  float4 a[kMaxSplit][2];
+#pragma unroll
+  for (int s = 0; s < kMaxSplit; ++s) {
+    if (s < p.split) {
+      const float4 *f = reinterpret_cast<const float4 *>(from + static_cast<int64_t>(s) * TS * TS);
+      a[s][0] = __ldcg(f);
+      a[s][1] = __ldcg(f + 1);
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < kMaxSplit; ++s) {
+    if (s < p.split) {
+      v[0] += a[s][0].x, v[1] += a[s][0].y, v[2] += a[s][0].z, v[3] += a[s][0].w;
+      v[4] += a[s][1].x, v[5] += a[s][1].y, v[6] += a[s][1].z, v[7] += a[s][1].w;
+    }
+  }
+  const int64_t at = static_cast<int64_t>(row) * p.N + c0;
+  auto pack = [&] {
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  };
+  auto add = [&](const uint4 &w) {
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      v[2 * h] += bf16_lo(x[h]);
+      v[2 * h + 1] += bf16_hi(x[h]);
+    }
+  };
+  if constexpr (KIND == kFwd) {
+    if (p.e.bias) add(__ldg(reinterpret_cast<const uint4 *>(p.e.bias + c0)));
+    if (p.e.z) *reinterpret_cast<uint4 *>(p.e.z + at) = pack();
+#pragma unroll
+    for (int h = 0; h < 8; ++h) v[h] = activate(v[h], p.e.act);
+    if (p.e.res) add(*reinterpret_cast<const uint4 *>(p.e.res + at));
+  }
+  *reinterpret_cast<uint4 *>(p.e.y + at) = pack();
+}
+
+// ---------------------------------------------------------------- dz and dbias
+//
+// dz = dy act'(z) in bf16 (where there is an activation), and the column sums of it unrounded.  A block
+// takes 64 columns and every `split`-th run of rows: 8 threads a row, 32 rows at once; its sums over
+// those go to a partial row, which the second kernel adds in order.
+
+constexpr int kDzThreads = 256, kDzCols = 64, kDzRows = kDzThreads / 8;
+constexpr int kDzSplit = 64;  // partial rows at most
+struct DzArgs {
+  const uint16_t *dy, *z;
+  uint16_t *dz;    // null: no activation, dy itself
+  float *part;     // [split][N], or null: no bias
+  float *dbias;
+  int T, N, act, split;
+  int32_t *status;
+};
+__global__ void __launch_bounds__(kDzThreads) linear_dz_kernel(const DzArgs a) {
+  __shared__ float s_sum[kDzRows / 4][kDzCols];
+  griddep_wait();  // the previous kernel in the stream has completed
+  griddep_launch_dependents();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.status = 0;
+  const int c = blockIdx.x * kDzCols + (threadIdx.x & 7) * 8;
+  const int step = kDzRows * a.split;
+  float sum[8] = {};
+  if (c < a.N) {
+    constexpr int kAhead = 4;
+    for (int64_t t0 = blockIdx.y * kDzRows + (threadIdx.x >> 3); t0 < a.T; t0 += static_cast<int64_t>(step) * kAhead) {
+      uint4 dy[kAhead], z[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int64_t t = t0 + static_cast<int64_t>(i) * step;
+        if (t < a.T) {
+          dy[i] = __ldg(reinterpret_cast<const uint4 *>(a.dy + t * a.N + c));
+          if (a.dz) z[i] = __ldg(reinterpret_cast<const uint4 *>(a.z + t * a.N + c));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int64_t t = t0 + static_cast<int64_t>(i) * step;
+        if (t >= a.T) break;
+        const uint32_t y[4] = {dy[i].x, dy[i].y, dy[i].z, dy[i].w};
+        float v[8];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          v[2 * h] = bf16_lo(y[h]);
+          v[2 * h + 1] = bf16_hi(y[h]);
+        }
+        if (a.dz) {
+          const uint32_t x[4] = {z[i].x, z[i].y, z[i].z, z[i].w};
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            v[2 * h] *= slope(bf16_lo(x[h]), a.act);
+            v[2 * h + 1] *= slope(bf16_hi(x[h]), a.act);
+          }
+          *reinterpret_cast<uint4 *>(a.dz + t * a.N + c) =
+              make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+        }
+#pragma unroll
+        for (int h = 0; h < 8; ++h) sum[h] += v[h];
+      }
+    }
+  }
+  if (!a.part) return;
+  // over the four rows of a warp, then over the warps
+#pragma unroll
+  for (int h = 0; h < 8; ++h) {
+    sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 8);
+    sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 16);
+  }
+  if ((threadIdx.x & 31) < 8) {
+#pragma unroll
+    for (int h = 0; h < 8; ++h) s_sum[threadIdx.x >> 5][(threadIdx.x & 7) * 8 + h] = sum[h];
+  }
+  __syncthreads();
+  const int col = blockIdx.x * kDzCols + threadIdx.x;
+  if (threadIdx.x < kDzCols && col < a.N) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kDzThreads / 32; ++w) s += s_sum[w][threadIdx.x];
+    (a.split == 1 ? a.dbias : a.part + static_cast<int64_t>(blockIdx.y) * a.N)[col] = s;
+  }
+}
+__global__ void __launch_bounds__(128) linear_dbias_kernel(const float *part, int split, int N, float *dbias) {
+  griddep_wait();  // the previous kernel in the stream has completed
+  griddep_launch_dependents();
+  const int c = blockIdx.x * 128 + threadIdx.x;
+  if (c >= N) return;
+  float s = 0.f;
+#pragma unroll 16
+  for (int i = 0; i < split; ++i) s += __ldcg(part + static_cast<int64_t>(i) * N + c);
+  dbias[c] = s;
+}
+
+// ---------------------------------------------------------------- host side
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// A row-major bf16 matrix [rows, inner]: boxes of 64 x box_rows, 128-byte swizzle, zeros outside.
+bool map2(CUtensorMap *m, const void *ptr, int inner, int rows, int box_rows) {
+  auto fn = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
+  if (!fn) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(inner) * 2};
+  cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// How a product is cut: the whole tiles, and the parts of those that are left.
+struct Cut {
+  int cg, nm, nn, full, split, units;
+  double cost;
+};
+Cut cut_with(int64_t M, int64_t N, int64_t K, int cg, int sms) {
+  const int ts = tile_size(cg), groups = sms / cg;
+  Cut c;
+  c.cg = cg;
+  c.nm = static_cast<int>((M + ts - 1) / ts);
+  c.nn = static_cast<int>((N + ts - 1) / ts);
+  const int64_t tiles = static_cast<int64_t>(c.nm) * c.nn;
+  const int nstage = static_cast<int>((K + 2 * BK - 1) / (2 * BK));
+  const int left = static_cast<int>(tiles % groups);
+  c.split = 1;
+  if (left) c.split = std::max(1, std::min({groups / left, kMaxSplit, nstage / kLeastStages}));
+  c.full = static_cast<int>(c.split > 1 ? tiles - left : tiles);
+  c.units = static_cast<int>(c.split > 1 ? c.full + left * c.split : tiles);
+  const int64_t rounds = c.split > 1 ? c.full / groups : (tiles + groups - 1) / groups;
+  const double stage = cg == 2 ? 1.0 : 0.8, extra = cg == 2 ? 4 : 2;
+  c.cost = rounds * (nstage * stage + extra);
+  if (c.split > 1) c.cost += (nstage + c.split - 1) / c.split * stage + extra + 5;
+  return c;
+}
+Cut cut_of(int64_t M, int64_t N, int64_t K, int sms) {
+  const Cut one = cut_with(M, N, K, 1, sms), two = cut_with(M, N, K, 2, sms);
+  return two.cost <= one.cost ? two : one;
+}
+constexpr size_t kPartBytes = static_cast<size_t>(kRuleSms) * BM * BM * 4 * 2;  // parts of a round of pairs (or singles)
+
+template <int KIND, int CG>
+cudaError_t launch_cut(const CUtensorMap &a, const CUtensorMap &b, ProductArgs p, const Cut &c, int sms, cudaStream_t s) {
+  static DeviceOnce once;  // the shared-memory opt-in, and how many groups of CTAs fit at once
+  auto kernel = linear_product_kernel<KIND, CG>;
+  int groups = 0;
+  cudaError_t e = once.get(
+      [&](int *out) {
+        cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
+        if (r != cudaSuccess) return r;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = CG;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cudaLaunchConfig_t q = {};
+        q.gridDim = dim3(sms / CG * CG);
+        q.blockDim = dim3(kGemmThreads);
+        q.dynamicSmemBytes = kGemmSmem;
+        q.attrs = &attr;
+        q.numAttrs = 1;
+        int n = 0;
+        r = cudaOccupancyMaxActiveClusters(&n, kernel, &q);
+        if (r != cudaSuccess) return r;
+        if (n < 1) return cudaErrorInvalidConfiguration;
+        *out = n < sms / CG ? n : sms / CG;
+        return cudaSuccess;
+      },
+      &groups);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kernel, dim3(static_cast<unsigned>(CG * std::min(c.units, groups))), dim3(kGemmThreads), kGemmSmem, s, CG, a,
+                 b, p);
+  if (e != cudaSuccess || c.split == 1) return e;
+  constexpr int TS = tile_size(CG);
+  const int64_t threads = static_cast<int64_t>(c.nm * c.nn - c.full) * TS * (TS / 8);
+  return launch_pdl(linear_finish_kernel<KIND, CG>, dim3(static_cast<unsigned>((threads + kFinishThreads - 1) / kFinishThreads)),
+                    dim3(kFinishThreads), 0, s, 1, p);
+}
+
+// One product [M,N] over K of a (its rows contiguous along K, or along M where KIND is kDw) and b.
+template <int KIND>
+moe_status product(const char *label, const void *a, const void *b, int M, int N, int K, const Ends &ends, float *part,
+                   int32_t *status, bool first, int sms, cudaStream_t s) {
+  const Cut c = cut_of(M, N, K, std::min(sms, kRuleSms));
+  CUtensorMap ma, mb;
+  const bool ok = (KIND == kDw ? map2(&ma, a, M, K, 64) : map2(&ma, a, K, M, 128)) &&
+                  (KIND == kDx ? map2(&mb, b, K, N, 128) : map2(&mb, b, N, K, 64));
+  if (!ok) return MOE_ERR_CUDA;
+  ProductArgs p{};
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.nm = c.nm;
+  p.nn = c.nn;
+  p.full = c.full;
+  p.split = c.split;
+  p.units = c.units;
+  p.part = part;
+  p.e = ends;
+  auto al32 = [](const void *q) { return (reinterpret_cast<uintptr_t>(q) & 31) == 0; };
+  p.e.sectors = N % 16 == 0 && al32(ends.res) && al32(ends.y) && al32(ends.z);
+  p.status = status;
+  p.first = first;
+  return timed(label, s, [&] {
+    return c.cg == 2 ? launch_cut<KIND, 2>(ma, mb, p, c, sms, s) : launch_cut<KIND, 1>(ma, mb, p, c, sms, s);
+  });
+}
+
+bool linear_ok(const moe_linear_config *c) {
+  if (!c || c->T < 0 || c->T > (1 << 30)) return false;
+  if (c->K < 8 || c->K > kMaxDim || c->K % 8 || c->N < 8 || c->N > kMaxDim || c->N % 8) return false;
+  if (static_cast<int64_t>(c->T) * std::max(c->K, c->N) >= int64_t{1} << 40) return false;  // (tiles are counted in 32 bits)
+  return c->act >= MOE_ACT_NONE && c->act <= MOE_ACT_GELU;
+}
+
+struct LinearLayout {
+  size_t part, fwd, dz, sums, bwd;
+};
+LinearLayout linear_layout(const moe_linear_config *c) {
+  LinearLayout L;
+  L.part = kHeader;
+  L.fwd = L.part + kPartBytes;
+  L.dz = L.fwd;
+  L.sums = L.dz + (c->act == MOE_ACT_NONE ? 0 : align256(static_cast<size_t>(c->T) * c->N * 2));
+  L.bwd = L.sums + align256(static_cast<size_t>(kDzSplit) * c->N * 4);
+  return L;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status moe_linear_workspace(const moe_linear_config *cfg, size_t *fwd_scratch, size_t *bwd_scratch) {
+  if (!linear_ok(cfg)) return MOE_ERR_INVALID_ARG;
+  const LinearLayout L = linear_layout(cfg);
+  if (fwd_scratch) *fwd_scratch = L.fwd;
+  if (bwd_scratch) *bwd_scratch = L.bwd;
+  return MOE_OK;
+}
+
+moe_status moe_linear_forward(const moe_linear_config *cfg, const void *x, const void *W, const void *bias,
+                              const void *residual, void *y, void *z, void *scratch, size_t scratch_bytes, void *stream) {
+  if (!linear_ok(cfg)) return MOE_ERR_INVALID_ARG;
+  if (!W || !scratch || (cfg->T > 0 && (!x || !y)) || (z && cfg->act == MOE_ACT_NONE)) return MOE_ERR_INVALID_ARG;
+  if (!al16(x) || !al16(W) || !al16(bias) || !al16(residual) || !al16(y) || !al16(z) || !al16(scratch)) return MOE_ERR_ALIGNMENT;
+  const LinearLayout L = linear_layout(cfg);
+  if (scratch_bytes < L.fwd) return MOE_ERR_WORKSPACE;
+  DevInfo di;
+  MOE_TRY(device_info(&di));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t *sc = static_cast<uint8_t *>(scratch);
+  if (cfg->T == 0) return cudaMemsetAsync(sc, 0, kHeader, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  Ends e{};
+  e.bias = static_cast<const uint16_t *>(bias);
+  e.res = static_cast<const uint16_t *>(residual);
+  e.y = static_cast<uint16_t *>(y);
+  e.z = static_cast<uint16_t *>(z);
+  e.act = cfg->act;
+  return product<kFwd>("linear_forward", x, W, cfg->T, cfg->N, cfg->K, e, reinterpret_cast<float *>(sc + L.part),
+                       reinterpret_cast<int32_t *>(sc), true, di.sms, s);
+}
+
+moe_status moe_linear_backward(const moe_linear_config *cfg, const void *dy, const void *x, const void *W, const void *z,
+                               void *dx, void *dW, float *dbias, void *scratch, size_t scratch_bytes, void *stream) {
+  if (!linear_ok(cfg)) return MOE_ERR_INVALID_ARG;
+  const bool act = cfg->act != MOE_ACT_NONE;
+  if (!scratch || (!dx && !dW && !dbias) || (dx && !W)) return MOE_ERR_INVALID_ARG;
+  if (cfg->T > 0 && (!dy || (dW && !x) || (act != (z != nullptr)))) return MOE_ERR_INVALID_ARG;
+  if (!al16(dy) || !al16(x) || !al16(W) || !al16(z) || !al16(dx) || !al16(dW) || !al16(dbias) || !al16(scratch))
+    return MOE_ERR_ALIGNMENT;
+  const LinearLayout L = linear_layout(cfg);
+  if (scratch_bytes < L.bwd) return MOE_ERR_WORKSPACE;
+  DevInfo di;
+  MOE_TRY(device_info(&di));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t *sc = static_cast<uint8_t *>(scratch);
+  int32_t *status = reinterpret_cast<int32_t *>(sc);
+  const int T = cfg->T, K = cfg->K, N = cfg->N;
+  if (T == 0) {
+    if (cudaMemsetAsync(sc, 0, kHeader, s) != cudaSuccess) return MOE_ERR_CUDA;
+    if (dW && cudaMemsetAsync(dW, 0, static_cast<size_t>(K) * N * 2, s) != cudaSuccess) return MOE_ERR_CUDA;
+    if (dbias && cudaMemsetAsync(dbias, 0, static_cast<size_t>(N) * 4, s) != cudaSuccess) return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
+  float *part = reinterpret_cast<float *>(sc + L.part);
+  const void *dz = dy;
+  bool first = true;
+  if (act || dbias) {
+    DzArgs a{};
+    a.dy = static_cast<const uint16_t *>(dy);
+    a.z = static_cast<const uint16_t *>(z);
+    a.dz = act ? reinterpret_cast<uint16_t *>(sc + L.dz) : nullptr;
+    a.dbias = dbias;
+    a.part = dbias ? reinterpret_cast<float *>(sc + L.sums) : nullptr;
+    a.T = T;
+    a.N = N;
+    a.act = cfg->act;
+    a.status = status;
+    // enough blocks for four on each SM, of at least four rows a thread
+    const int cols = (N + kDzCols - 1) / kDzCols, rounds = (T + kDzRows * 4 - 1) / (kDzRows * 4);
+    a.split = std::max(1, std::min({(4 * di.sms + cols - 1) / cols, rounds, kDzSplit}));
+    MOE_TRY(timed("linear_dz", s, [&] { return launch_pdl(linear_dz_kernel, dim3(cols, a.split), dim3(kDzThreads), 0, s, 1, a); }));
+    if (dbias && a.split > 1)
+      MOE_TRY(timed("linear_dbias", s, [&] {
+        return launch_pdl(linear_dbias_kernel, dim3((N + 127) / 128), dim3(128), 0, s, 1, static_cast<const float *>(a.part),
+                          a.split, N, dbias);
+      }));
+    if (act) dz = a.dz;
+    first = false;
+  }
+  if (dx) {
+    Ends e{};
+    e.y = static_cast<uint16_t *>(dx);
+    MOE_TRY(product<kDx>("linear_dx", dz, W, T, K, N, e, part, status, first, di.sms, s));
+    first = false;
+  }
+  if (dW) {
+    Ends e{};
+    e.y = static_cast<uint16_t *>(dW);
+    MOE_TRY(product<kDw>("linear_dW", x, dz, K, N, T, e, part, status, first, di.sms, s));
+  }
+  return MOE_OK;
+}
+
+}  // extern "C"

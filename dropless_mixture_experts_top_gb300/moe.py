@@ -38,6 +38,7 @@ EXPORTED = [
     "moe_norm_workspace", "moe_norm_forward", "moe_norm_backward",
     "moe_balance_workspace", "moe_balance_forward", "moe_balance_backward",
     "moe_ortho_workspace", "moe_ortho_update",
+    "moe_linear_workspace", "moe_linear_forward", "moe_linear_backward",
     "moe_adamw_state_elements", "moe_adamw_step",
     "moe_gate_workspace", "moe_gate_forward", "moe_gate_backward", "moe_gate_update_bias",
 ]
@@ -78,6 +79,10 @@ class AdamWConfig(ctypes.Structure):
 
 class AdamWState(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("m", "v", "m_scale", "v_scale", "step")]
+
+
+class LinearConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "K", "N", "act")]
 
 
 class SavedLayout(ctypes.Structure):
@@ -147,7 +152,10 @@ def lib():
         L.moe_gate_update_bias.argtypes = [P, P, P, ctypes.c_int32, ctypes.c_float, P]
         L.moe_adamw_state_elements.argtypes = [P, P, P]
         L.moe_adamw_step.argtypes = [P] * 7 + [ctypes.c_double, P, P, P]
-        for f in ("moe_adamw_state_elements", "moe_adamw_step", "moe_gate_workspace", "moe_gate_forward", "moe_gate_backward", "moe_gate_update_bias"):
+        L.moe_linear_workspace.argtypes = [P, P, P]
+        L.moe_linear_forward.argtypes = [P] * 8 + [sz, P]
+        L.moe_linear_backward.argtypes = [P] * 9 + [sz, P]
+        for f in ("moe_linear_workspace", "moe_linear_forward", "moe_linear_backward", "moe_adamw_state_elements", "moe_adamw_step", "moe_gate_workspace", "moe_gate_forward", "moe_gate_backward", "moe_gate_update_bias"):
             getattr(L, f).restype = ctypes.c_int
         for f in ("moe_ortho_workspace", "moe_ortho_update", "moe_norm_workspace", "moe_norm_forward", "moe_norm_backward", "moe_balance_workspace",
                   "moe_balance_forward", "moe_balance_backward"):
@@ -658,6 +666,75 @@ def _one(t, name, dev):
     if t.numel() != 1:
         raise ValueError(f"{name}: {tuple(t.shape)}, expected one element")
     return _addr(t, name, t.shape, _F32, dev)
+
+
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
+
+
+class Linear(_Plan):
+    """A dense layer over [T, K]: y = act(x W + bias) + residual, W [K, N], and its
+    backward, all in bf16 with fp32 sums (the bias' gradient is fp32).
+
+    Dictionaries that a call returned may be handed to the next one, which then
+    writes into the same tensors."""
+
+    def __init__(self, T, K, N, activation="none", bias=True, device="cuda"):
+        self.cfg = LinearConfig(int(T), int(K), int(N), ACTIVATIONS[activation])
+        f, b = ctypes.c_size_t(), ctypes.c_size_t()
+        _check(lib().moe_linear_workspace(ctypes.byref(self.cfg), ctypes.byref(f), ctypes.byref(b)),
+               "moe_linear_workspace")
+        self.device, self._cfg, self.bias, self._act = _device(device), ctypes.byref(self.cfg), bool(bias), activation != "none"
+        self._dev, self._fwd, self._bwd = self.device.index, lib().moe_linear_forward, lib().moe_linear_backward
+        self._tk, self._tn, self._kn, self._cols = (torch.Size(s) for s in ((T, K), (T, N), (K, N), (N,)))
+        self._fwd_bytes = f.value
+        # one buffer for both: the backward starts with what the forward uses
+        self.scratch = self._take_scratch(b.value)
+        self._scratch = self.scratch.data_ptr()
+
+    def forward(self, x, W, bias=None, residual=None, out=None, save=True, stream=None) -> dict:
+        """{"y", "z" (in front of the activation, for backward; None without one, or with save=False)}"""
+        d, tn = self._dev, self._tn
+        if _current_device() != d:
+            with torch.cuda.device(d):
+                return self.forward(x, W, bias, residual, out, save, stream)
+        if (bias is not None) != self.bias:
+            raise ValueError("bias: given to a layer without one" if bias is not None else "bias: missing")
+        if out is None:
+            with _on_stream(stream):
+                made = dict(dtype=x.dtype if x.dtype in _BF16 else torch.bfloat16, device=self.device)
+                out = {"y": torch.empty(tn, **made), "z": torch.empty(tn, **made) if self._act and save else None}
+        rc = self._fwd(self._cfg, _addr(x, "x", self._tk, _BF16, d), _addr(W, "W", self._kn, _BF16, d),
+                       _addr(bias, "bias", self._cols, _BF16, d), _addr(residual, "residual", tn, _BF16, d),
+                       _addr(out["y"], "y", tn, _BF16, d), _addr(out["z"], "z", tn, _BF16, d), self._scratch,
+                       self._fwd_bytes, self._working(self.scratch, stream))
+        if rc:
+            raise MoEError("moe_linear_forward", rc)
+        return out
+
+    def backward(self, dy, x, W, z=None, grads=None, stream=None) -> dict:
+        """{"dx", "dW", "dbias" (None without a bias)} from the forward's z (None without an activation).  In a grads
+        that is given, a None in their place leaves a gradient out."""
+        d = self._dev
+        if _current_device() != d:
+            with torch.cuda.device(d):
+                return self.backward(dy, x, W, z, grads, stream)
+        if grads is None:
+            with _on_stream(stream):
+                made = dict(dtype=dy.dtype if dy.dtype in _BF16 else torch.bfloat16, device=self.device)
+                grads = {"dx": torch.empty(self._tk, **made), "dW": torch.empty(self._kn, **made),
+                         "dbias": torch.empty(self._cols, dtype=torch.float32, device=self.device) if self.bias else None}
+        rc = self._bwd(self._cfg, _addr(dy, "dy", self._tn, _BF16, d), _addr(x, "x", self._tk, _BF16, d),
+                       _addr(W, "W", self._kn, _BF16, d), _addr(z, "z", self._tn, _BF16, d),
+                       _addr(grads["dx"], "dx", self._tk, _BF16, d), _addr(grads["dW"], "dW", self._kn, _BF16, d),
+                       _addr(grads["dbias"], "dbias", self._cols, _F32, d), self._scratch, self.scratch.numel(),
+                       self._working(self.scratch, stream))
+        if rc:
+            raise MoEError("moe_linear_backward", rc)
+        return grads
+
+    @_on_own_device
+    def status(self, stream=None) -> dict:
+        return {"last": get_device_status(self.scratch, stream)}
 
 
 SCORES = {"softmax": 0, "sigmoid": 1}

@@ -466,6 +466,38 @@ moe_status moe_adamw_step(const moe_adamw_config *cfg, const int64_t *n, const d
                           const void *const *grads, void *const *copies, const moe_adamw_state *state, double lr,
                           const float *lr_device, const float *grad_scale, void *stream);
 
+/* A dense layer (a shared expert beside the routed ones, a projection): a matrix product with bias, activation
+ * and residual in its epilogue, and its backward.  bf16 tensors, dense rows; sums in fp32.
+ * Forward:   z = x W + bias,  y = act(z) + residual
+ *   x [T,K], W [K,N], bias [N] (may be NULL), residual [T,N] (may be NULL), y [T,N]; z [T,N], which the
+ *   backward reads, is written where it is not NULL (never without an activation).  y may be residual
+ *   itself and overlaps nothing else.
+ * Backward:  dz = dy act'(z),  dx = dz W^T,  dW = x^T dz,  dbias = sum_t dz
+ *   dx [T,K], dW [K,N] bf16 and dbias [N] fp32, overwritten; each may be NULL (not all three) and is then
+ *   not computed (W is only read for dx, x for dW).  z as the forward left it; NULL without an
+ *   activation.  dz enters the products rounded to bf16, dbias as it is.  The residual's gradient is dy itself.
+ *   Outputs overlap no input.
+ * Activations: relu, silu z / (1 + e^-z), gelu in its tanh form.  Sums run in a fixed order: the same bits every
+ * time.  0 <= T <= 2^30; K and N multiples of 8, 8 to 65536; T times either below 2^40.  With T == 0 the weight gradients are zeroed.
+ * Status word at the start of each scratch. */
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_SILU = 2,
+  MOE_ACT_GELU = 3
+} moe_act;
+typedef struct {
+  int32_t T;   /* rows */
+  int32_t K;   /* inputs of a row */
+  int32_t N;   /* outputs */
+  int32_t act; /* moe_act */
+} moe_linear_config;
+moe_status moe_linear_workspace(const moe_linear_config *cfg, size_t *fwd_scratch, size_t *bwd_scratch);
+moe_status moe_linear_forward(const moe_linear_config *cfg, const void *x, const void *W, const void *bias,
+                              const void *residual, void *y, void *z, void *scratch, size_t scratch_bytes, void *stream);
+moe_status moe_linear_backward(const moe_linear_config *cfg, const void *dy, const void *x, const void *W, const void *z,
+                               void *dx, void *dW, float *dbias, void *scratch, size_t scratch_bytes, void *stream);
+
 /* Routing without a caller-provided scratch buffer.  The paper has no
  * counterpart: it exists for callers that cannot allocate device memory --
  * code running while a CUDA graph is captured (cudaMalloc is not allowed
