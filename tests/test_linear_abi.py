@@ -96,5 +96,7 @@ def test_the_binding_s_refusals(monkeypatch):
         lin.forward(bf(4, 8).float(), bf(8, 16), bf(16))
     with pytest.raises(ValueError, match="dy:"):
         lin.backward(bf(4, 8), bf(4, 8), bf(8, 16), bf(4, 16))
+    lin = moe.Linear(4, 8, 16, bias=False)
+    lin._dev = -1
     with pytest.raises(ValueError, match="bias: given"):
-        moe.Linear(4, 8, 16, bias=False).forward(bf(4, 8), bf(8, 16), bf(16))
+        lin.forward(bf(4, 8), bf(8, 16), bf(16))
