@@ -1,0 +1,682 @@
+// gate.cuh -- the gate's choice: from the router's logits to the chosen experts, their
+// weights and their places.  gate_logit.cu, gate_sigmoid.cu and gate_softmax.cu hold the
+// kernel's variants (apart, so that they compile side by side), gate.cu the rest of the gate.
+//
+// Per token, l = its E logits:
+//   s = softmax(l) or sigmoid(l),  c = s + bias  (no bias: the order of l)
+//   a group's score: the sum of its 1 or 2 largest c;  the best `top_groups` groups
+//   S = the k largest c in those groups (ties: lower expert)
+//   w_j = scale s_{S_j} / (sum_i s_{S_i} or 1)
+//
+// Exact choice.  Two scores can be closer than fp32 resolves, and a choice that
+// depends on the roundings of an exponential differs from program to program.  The
+// choice made here is that of the exact scores: fp32 scores carry an error that
+// is bounded (kNearSigmoid, kNearSoftmax below), and a token whose order is not
+// decided by more than that is chosen again from scores in 64 bits.  Without a bias the
+// logits themselves are compared.
+//
+// One warp per token, a few experts per lane.  A score becomes a 23-bit fixed-point
+// number above the expert's index in one 32-bit key, so that keys are unique and one
+// warp-wide maximum (redux) gives both the next score and whose it is.  Each lane sorts
+// its keys once and hands out its largest.  Without a bias the key is the upper 24 bits
+// of the logit.  Where 32 lanes hold all experts in whole vectors, a lane's experts are
+// neighbours (VEC): one load per token, and groups are runs of lanes.
+#pragma once
+
+#include <float.h>
+#include <limits.h>
+#include <math.h>
+
+#include "abi.h"
+#include "common.cuh"
+
+namespace moe {
+
+struct GateArgs {
+  const float *logits;  // [T,E]
+  const float *bias;    // [E] or null
+  int T, E, k;
+  int groups, top_groups, group_best, group_size;
+  bool sigmoid, renormalise;
+  float scale;
+  int32_t *topk_idx;
+  float *topk_w;
+  int32_t *counts, *offsets, *row_of_slot, *slot_of_row;
+  float *w_row;
+  int chunks;           // chunk c: the tokens [c T / chunks, (c + 1) T / chunks)
+  int cluster;          // chunks per cluster
+  int32_t *before;      // [chunks][E]: the slots of expert e in the cluster's earlier chunks
+  int32_t *total;       // [clusters][E]
+  int32_t *flags;       // [clusters]
+  int32_t *status;
+};
+
+constexpr int kGateThreads = 256;
+constexpr int kGateTok = 256;      // tokens of one round of a block at most
+constexpr int kGateCluster = 8;    // blocks of a cluster at most
+
+enum GateKey : int { kKeyLogit = 0, kKeySigmoid = 1, kKeySoftmax = 2 };
+// The choice, by the key that orders the experts; one cluster: everything.
+template <int KEY>
+cudaError_t launch_gate_select(const GateArgs &a, cudaStream_t s);
+
+__device__ __forceinline__ int gate_first(const GateArgs &a, int chunk) {
+  return static_cast<int>(static_cast<int64_t>(a.T) * min(chunk, a.chunks) / a.chunks);
+}
+
+__device__ __forceinline__ int32_t ld_peer(const int32_t *p, int rank) {
+  int32_t v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(peer_smem_addr(p, rank)) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float clean_logit(float l, bool &bad) {
+  bad |= !(l <= FLT_MAX);
+  return l != l ? -INFINITY : fminf(l, FLT_MAX);
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// Exclusive prefix of v over the block's first kMaxExperts threads (thread = expert); the
+// total to *total.  s_w: 8 ints.
+__device__ __forceinline__ int expert_prefix(int v, int *s_w, int *total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31 && warp < kMaxExperts / 32) s_w[warp] = incl;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kMaxExperts / 32; ++w) {
+    before += w < warp ? s_w[w] : 0;
+    all += s_w[w];
+  }
+  *total = all;
+  return before + incl - v;
+}
+
+}  // namespace moe
+
+#ifdef MOE_GATE_SELECT
+namespace moe {
+namespace {
+
+constexpr int kWarps = kGateThreads / 32;
+
+// Fixed point: c in [-B, 1 + B], B the largest finite |bias|, as 8 + O + c * scale in
+// 23 bits, O = ceil(B scale).  A unit is (1 + 2B) 2^-23 or a little more.
+// How far the number may be from that of the exact c, in units:
+//   sigmoid: 1 / (1 + e), e = 2^(-l log2 e) by the part's ex2: off by 2^-22 of itself, and by |l| 2^-23 for the
+//   rounded argument, of which s (1 - s) reaches s (at most 1/4, with the |l| 0.23); the sum by half an ulp, the
+//   reciprocal by one: 2^-24 + 0.23 2^-23 + s (2^-24 + 2^-23), 2.2 units; bias * scale + base rounded,
+//   half a unit, the product rounded, half: 3.2.  Two numbers that differ by more than 7 are in the order
+//   of the exact ones; 10 leaves room.
+//   softmax: e = 2^((l - m) log2 e) off by 2^-22 of itself and by |l - m| 2^-22 for the rounded difference and
+//   argument, which with the e^-|l - m| of its size is at most 0.37 2^-22; the sum Z by 13 roundings and its
+//   terms, 1.3e-6; the quotient by 2 ulp: 1.9e-6 in all, 16 units, with the roundings 17: 35, and 40 with room.
+constexpr int kNearSigmoid = 10, kNearSoftmax = 40;
+constexpr float kFixOne = 8388608.f;       // 2^23
+constexpr float kFixLeast = 8.f;           // the least number of an expert that may be chosen; 0: it may not
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float sigmoid_fast(float l) { return rcp(1.f + ex2(-kLog2e * l)); }
+
+// A logit's order as an unsigned number (both zeros alike).
+__device__ __forceinline__ uint32_t order_of(float l) {
+  const uint32_t u = __float_as_uint(l + 0.f);
+  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
+
+// Sorts NV keys, largest first.
+template <int NV>
+__device__ __forceinline__ void sort_keys(uint32_t (&v)[NV]) {
+  auto cas = [&](int a, int b) {
+    const uint32_t hi = max(v[a], v[b]), lo = min(v[a], v[b]);
+    v[a] = hi;
+    v[b] = lo;
+  };
+  if constexpr (NV == 2) {
+    cas(0, 1);
+  } else if constexpr (NV == 4) {
+    cas(0, 1), cas(2, 3), cas(0, 2), cas(1, 3), cas(1, 2);
+  } else if constexpr (NV == 8) {
+    cas(0, 1), cas(2, 3), cas(4, 5), cas(6, 7);
+    cas(0, 2), cas(1, 3), cas(4, 6), cas(5, 7);
+    cas(1, 2), cas(5, 6), cas(0, 4), cas(3, 7);
+    cas(1, 5), cas(2, 6);
+    cas(1, 4), cas(3, 6);
+    cas(2, 4), cas(3, 5);
+    cas(3, 4);
+  }
+}
+
+// What the block keeps of the bias.
+struct BiasInfo {
+  float scale;  // units per 1
+  float base;   // 2^23 + 8 + O
+  int off;      // 8 + O: the number of c = 0
+  bool odd;     // some entry is not finite
+};
+
+// A token whose order fp32 does not decide.  runs: which runs of `run` experts may be used
+// (bit e / run), or 0 to choose the groups as well; only experts whose fp32 number is at least
+// `least` can be among the chosen (0: every one).
+struct Undecided {
+  uint32_t runs;
+  int least;
+};
+
+// Its choice from 64-bit scores, by one warp.  val: E doubles of this warp, list: E bytes; slot: its k
+// slots, bit 15 set where an expert had no score.
+template <int KEY>
+__device__ __noinline__ void resolve_token(const GateArgs &a, const float *row, const float *s_bias, BiasInfo bi, Undecided u,
+                                           int run, double *val, uint8_t *list, uint16_t *slot) {
+  const int lane = threadIdx.x & 31, E = a.E;
+  const bool biased = a.bias != nullptr;
+  bool bad = false;
+  double top = -DBL_MAX, z = 1.0;
+  float top32 = -FLT_MAX, z32 = 1.f;
+  if (KEY == kKeySoftmax) {
+    for (int e = lane; e < E; e += 32) top32 = fmaxf(top32, clean_logit(__ldg(row + e), bad));
+    top32 = warp_max(top32);
+    top = top32;
+    z = 0.0;
+    for (int e = lane; e < E; e += 32) z += exp(static_cast<double>(clean_logit(__ldg(row + e), bad)) - top);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    z32 = static_cast<float>(z);
+  }
+  // the score of an expert in the order of the experts (order) or of the groups; a lane keeps the last
+  // exponential, which serves rows of equal logits
+  float last_l = NAN;
+  double last_s = 0.0;
+  auto exact = [&](float l, float b, bool order) -> double {
+    if (KEY == kKeyLogit || (order && !biased)) return static_cast<double>(l);
+    if (l != last_l) {
+      last_l = l;
+      last_s = KEY == kKeySigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(l))) : exp(static_cast<double>(l) - top) / z;
+    }
+    return biased ? last_s + static_cast<double>(b) : last_s;
+  };
+  auto scored = [&](float l, float b) { return l >= -FLT_MAX && b > -INFINITY; };  // (not where b is NaN)
+  if (u.runs == 0) {
+    for (int e = lane; e < E; e += 32) {
+      const float l = clean_logit(__ldg(row + e), bad), b = biased ? s_bias[e] : 0.f;
+      val[e] = scored(l, b) ? exact(l, b, false) : -INFINITY;
+    }
+    __syncwarp();
+    double g1 = -INFINITY, g2 = -INFINITY;
+    if (lane < a.groups)
+      for (int m = 0; m < a.group_size; ++m) {
+        const double v = val[lane * a.group_size + m];
+        g2 = fmax(g2, fmin(g1, v));
+        g1 = fmax(g1, v);
+      }
+    const double gv = a.group_best == 2 && g2 > -INFINITY ? g1 + g2 : g1;
+    int before = 0;
+    for (int h = 0; h < a.groups; ++h) {
+      const double o = __shfl_sync(0xffffffffu, gv, h);
+      before += (o > gv || (o == gv && h < lane)) ? 1 : 0;
+    }
+    u.runs = __ballot_sync(0xffffffffu, lane < a.groups && before < a.top_groups);
+    u.least = 0;
+    run = a.group_size;
+    __syncwarp();
+  }
+  // the experts in question, by index
+  int n = 0;
+  for (int e0 = 0; e0 < E; e0 += 32) {
+    const int e = e0 + lane;
+    bool use = false;
+    if (e < E) {
+      const float l = clean_logit(__ldg(row + e), bad), b = biased ? s_bias[e] : 0.f;
+      use = scored(l, b) && ((u.runs >> (e / run)) & 1u);
+      if (KEY != kKeyLogit && use && u.least > 0) {
+        // the fp32 number once more, with the distance that decides off for safety
+        const float s = KEY == kKeySigmoid ? sigmoid_fast(l) : ex2((l - top32) * kLog2e) * rcp(z32);
+        use = fmaf(s + b, bi.scale, static_cast<float>(bi.off)) >= static_cast<float>(u.least) - kNearSoftmax;
+      }
+    }
+    const uint32_t set = __ballot_sync(0xffffffffu, use);
+    if (use) list[n + __popc(set & ((1u << lane) - 1u))] = static_cast<uint8_t>(e);
+    n += __popc(set);
+  }
+  __syncwarp();
+  for (int i = lane; i < n; i += 32) {
+    const int e = list[i];
+    val[i] = exact(clean_logit(__ldg(row + e), bad), biased ? s_bias[e] : 0.f, true);
+  }
+  __syncwarp();
+  // k times the best of what is left; taken ones become NaN, which no comparison prefers
+  const int found = min(n, a.k);
+  for (int j = 0; j < found; ++j) {
+    double best = -INFINITY;
+    int at = INT_MAX;
+    for (int i = lane; i < n; i += 32) {
+      const double v = val[i];
+      if (v > best || (v == best && i < at)) best = v, at = i;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const double ov = __shfl_xor_sync(0xffffffffu, best, o);
+      const int oa = __shfl_xor_sync(0xffffffffu, at, o);
+      if (ov > best || (ov == best && oa < at)) best = ov, at = oa;
+    }
+    if ((at & 31) == lane) {
+      val[at] = NAN;
+      slot[j] = list[at];
+    }
+    __syncwarp();
+  }
+  if (lane == 0) {  // fewer than k: the others by index
+    int i = 0, e = 0;
+    for (int j = found; j < a.k; ++e) {
+      if (i < n && list[i] == e)
+        ++i;
+      else
+        slot[j++] = static_cast<uint16_t>(e | 0x8000);
+    }
+  }
+  __syncwarp();
+}
+
+// NV experts per lane: e = lane + 32 i, or NV lane + i (VEC; E = 32 NV).  KMAX: k at most.
+template <int NV, bool VEC, int KEY, bool GROUPS, int KMAX>
+__global__ void __launch_bounds__(kGateThreads, NV == 8 ? 3 : 4) gate_select_kernel(const GateArgs a) {
+  constexpr int kNear = KEY == kKeyLogit ? 0 : (KEY == kKeySigmoid ? kNearSigmoid : kNearSoftmax);
+  constexpr bool KEYS = GROUPS && !VEC;
+  constexpr int kWords = kGateTok / 32;
+  __shared__ union {                                     // one after the other:
+    uint32_t keys[KEYS ? kWarps : 1][KEYS ? kMaxExperts : 1];  // the choice's
+    double val[kWarps][kMaxExperts];                     // for undecided tokens
+    struct {
+      uint32_t emask[kWords][kMaxExperts];               // tokens of this round that chose expert e
+      uint16_t before[kWords][kMaxExperts];              // how many in the words in front
+    } rank;
+  } sh;
+  __shared__ float s_bias[kMaxExperts];
+  __shared__ int32_t s_run[kMaxExperts];                 // the chunk's slots of expert e in earlier rounds
+  __shared__ uint16_t s_slot[kGateTok * KMAX];           // expert of each slot; bit 15: without a score
+  __shared__ float2 s_soft[kGateTok];                    // softmax weights: a token's largest logit, and its sum
+  __shared__ Undecided s_und[kGateTok];
+  __shared__ uint8_t s_list[kGateTok];                   // undecided tokens
+  __shared__ uint8_t s_cand[kWarps][kMaxExperts];
+  __shared__ int32_t s_count, s_flag, s_bodd;
+  __shared__ float s_bmax[kWarps];
+  __shared__ int32_t s_base[kMaxExperts];
+  __shared__ int s_w[kMaxExperts / 32];
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int E = a.E, k = a.k;
+  const int first = gate_first(a, blockIdx.x), last = min(a.T, gate_first(a, blockIdx.x + 1));
+  if (tid == 0) s_count = 0, s_flag = 0, s_bodd = 0;
+  s_run[tid] = 0;  // (kGateThreads == kMaxExperts)
+  griddep_wait();  // the previous kernel in the stream has completed
+  griddep_launch_dependents();
+
+  auto expert = [&](int i) { return VEC ? lane * NV + i : lane + 32 * i; };
+  auto load = [&](int t, float (&v)[NV]) {
+    const float *row = a.logits + static_cast<size_t>(t) * E;
+    if constexpr (VEC && NV == 8) {
+      if (t < last)
+        asm volatile("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                     : "l"(row + lane * 8));
+    } else if constexpr (VEC) {
+      if (t < last) {
+        const float4 q = __ldg(reinterpret_cast<const float4 *>(row + lane * 4));
+        v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[i] = t < last && expert(i) < E ? __ldg(row + expert(i)) : 0.f;
+    }
+  };
+  float ahead[NV] = {};
+  load(first + warp, ahead);
+
+  BiasInfo bi{kFixOne - 32.f, kFixOne + kFixLeast, static_cast<int>(kFixLeast), false};
+  __syncthreads();
+  if (KEY != kKeyLogit && a.bias) {
+    const float b = tid < E ? __ldg(a.bias + tid) : 0.f;
+    s_bias[tid] = b;
+    const bool odd = !(fabsf(b) <= FLT_MAX);
+    if (odd) s_bodd = 1;
+    float m = warp_max(odd ? 0.f : fabsf(b));
+    if (lane == 0) s_bmax[warp] = m;
+    __syncthreads();
+    m = s_bmax[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) m = fmaxf(m, s_bmax[w]);
+    bi.scale = (kFixOne - 32.f) / (1.f + 2.f * m);
+    const float O = ceilf(m * bi.scale);
+    bi.base = kFixOne + kFixLeast + O;
+    bi.off = static_cast<int>(kFixLeast + O);
+    bi.odd = s_bodd != 0;
+  }
+  float add[KEY == kKeyLogit ? 1 : NV];  // the bias' part of the number (of a bias of -inf, NaN, inf: itself)
+  if constexpr (KEY != kKeyLogit) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) add[i] = a.bias && expert(i) < E ? fmaf(s_bias[expert(i)], bi.scale, bi.base) : bi.base;
+  }
+  // groups: VEC: run of lanes per group, where that is a power of two (else, and without VEC, by way of shared memory)
+  const int gs = a.group_size, G = a.groups;
+  int gP = 1, gits = 0;
+  if constexpr (KEYS) {
+    while (2 * gP * G <= 32) gP *= 2;
+    gits = (gs + gP - 1) / gP;
+  }
+  const int my_g = VEC ? lane * NV / gs : lane % G, my_p = VEC ? 0 : lane / G;
+  const bool whole_sum = !a.sigmoid && !a.renormalise;  // the weights need the softmax' sum over all experts
+  bool bad = false;
+
+  for (int t0 = first; t0 < last; t0 += kGateTok) {
+    // ---- choice: this warp's tokens, kWarps apart
+#pragma unroll 1
+    for (int tl = warp; tl < kGateTok; tl += kWarps) {
+      const int t = t0 + tl;
+      if (t >= last) break;
+      float l[NV], fin = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        l[i] = ahead[i];
+        fin = fmaf(l[i], 0.f, fin);  // NaN where one is not finite
+      }
+      load(t + kWarps, ahead);  // (of the next round after the last)
+      const bool odd = __any_sync(0xffffffffu, fin != 0.f);
+      if (odd) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) l[i] = clean_logit(l[i], bad);
+      }
+      uint32_t key[NV];
+      float m = 0.f, z = 0.f;
+      if (KEY == kKeySoftmax || (KEY == kKeyLogit && whole_sum)) {
+        m = -FLT_MAX;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) m = VEC || expert(i) < E ? fmaxf(m, l[i]) : m;
+        m = warp_max(m);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const float e = VEC || expert(i) < E ? ex2((l[i] - m) * kLog2e) : 0.f;
+          if (KEY == kKeySoftmax) key[i] = __float_as_uint(e);
+          z += e;
+        }
+        z = warp_sum(z);
+        if (lane == 0) s_soft[tl] = make_float2(m, z);
+      }
+      if constexpr (KEY == kKeyLogit) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) key[i] = (order_of(l[i]) & 0xFFFFFF00u) | (255u - expert(i));
+        if (odd) {
+#pragma unroll
+          for (int i = 0; i < NV; ++i) key[i] = l[i] >= -FLT_MAX ? key[i] : 0u;
+        }
+      } else {
+        const float rz = KEY == kKeySoftmax ? rcp(z) : 0.f;
+        float x[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const float s = KEY == kKeySigmoid ? sigmoid_fast(l[i]) : __uint_as_float(key[i]) * rz;
+          x[i] = fmaf(s, bi.scale, add[i]);  // a whole number in [2^23, 2^24), or inf
+        }
+        if (odd || bi.odd) {  // what may not be chosen: the number 0
+#pragma unroll
+          for (int i = 0; i < NV; ++i) x[i] = l[i] >= -FLT_MAX ? fmaxf(x[i], kFixOne) : kFixOne;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i)  // the number's three bytes over the index
+          key[i] = __byte_perm(__float_as_uint(x[i]), 255u - expert(i), 0x2104);
+      }
+      if constexpr (!VEC) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) key[i] = expert(i) < E ? key[i] : 0u;
+      }
+      Undecided u{0xffffffffu, 0};
+      bool undecided = false;
+      if constexpr (GROUPS) {
+        uint32_t k1, k2;
+        if constexpr (VEC) {
+          sort_keys<NV>(key);
+          k1 = key[0];
+          k2 = NV > 1 ? key[1] : 0u;
+          for (int o = 1; o * NV < gs; o <<= 1) {
+            const uint32_t o1 = __shfl_xor_sync(0xffffffffu, k1, o), o2 = __shfl_xor_sync(0xffffffffu, k2, o);
+            k2 = max(max(k2, o2), min(k1, o1));
+            k1 = max(k1, o1);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < NV; ++i) sh.keys[warp][lane + 32 * i] = key[i];
+          __syncwarp();
+          k1 = k2 = 0;
+          if (my_p < gP) {
+            int it = my_g % gits;  // each group starts elsewhere: other banks
+            for (int n = 0; n < gits; ++n) {
+              const int j = my_p + gP * it;
+              const uint32_t v = j < gs ? sh.keys[warp][my_g * gs + j] : 0u;
+              k2 = max(k2, min(k1, v));
+              k1 = max(k1, v);
+              if (++it == gits) it = 0;
+            }
+          }
+          for (int o = gP / 2; o > 0; o >>= 1) {
+            const uint32_t o1 = __shfl_down_sync(0xffffffffu, k1, o * G), o2 = __shfl_down_sync(0xffffffffu, k2, o * G);
+            k2 = max(max(k2, o2), min(k1, o1));
+            k1 = max(k1, o1);
+          }
+          __syncwarp();
+        }
+        // a group's number (its second score, where it has none: that of c = 0) over its index
+        uint32_t gq = k1 >> 8;
+        if (KEY != kKeyLogit && a.group_best == 2 && gq) gq += (k2 >> 8) ? k2 >> 8 : static_cast<uint32_t>(bi.off);
+        uint32_t gkey = VEC || lane < G ? (gq << 5) | (31u - my_g) : 0u;
+        uint32_t r = 0;
+        bool kept = false;
+        for (int j = 0; j < a.top_groups; ++j) {
+          r = __reduce_max_sync(0xffffffffu, gkey);
+          if (gkey == r) {
+            kept = true;
+            gkey = 0;
+          }
+        }
+        const uint32_t next = __reduce_max_sync(0xffffffffu, gkey);
+        undecided = a.top_groups < G && (next >> 5) != 0 && (bi.odd || (r >> 5) - (next >> 5) <= 2 * kNear);
+        u.runs = undecided ? 0u : __ballot_sync(0xffffffffu, kept && (VEC || lane < G));
+        if constexpr (VEC) {
+          if (!kept) key[0] = 0;  // (and the lane hands out nothing)
+          if (!kept)
+#pragma unroll
+            for (int i = 1; i < NV; ++i) key[i] = 0;
+        } else {
+#pragma unroll
+          for (int i = 0; i < NV; ++i) key[i] = (u.runs >> (expert(i) / gs & 31)) & 1u ? key[i] : 0u;
+        }
+      }
+      if (!undecided) {
+        if constexpr (!(GROUPS && VEC)) sort_keys<NV>(key);
+        uint32_t prev = 0xffffffffu, gap = 0xffffffffu, end = 0;
+#pragma unroll
+        for (int j = 0; j <= KMAX; ++j) {
+          if (j > k) break;
+          const uint32_t r = __reduce_max_sync(0xffffffffu, key[0]);
+          gap = min(gap, prev - r);
+          prev = r;
+          if (j < k) end = r;
+          if (key[0] == r) {
+            if (j < k) s_slot[tl * k + j] = static_cast<uint16_t>(255u - (r & 255u));
+#pragma unroll
+            for (int i = 0; i + 1 < NV; ++i)
+              if (i < KMAX - j) key[i] = key[i + 1];  // (further back none is needed any more)
+            if (NV <= KMAX - j) key[NV - 1] = 0;
+            if (NV == 1) key[0] = 0;
+          }
+        }
+        // two neighbours too near to tell, or fewer than k that may be chosen
+        undecided = gap < (kNear + 1) * 256u || (end >> 8) == 0;
+        u.least = static_cast<int>(end >> 8) > 2 * kNear + 1 ? static_cast<int>(end >> 8) - 2 * kNear : 0;
+      }
+      if (undecided && lane == 0) {
+        s_und[tl] = u;
+        s_list[atomicAdd(&s_count, 1)] = static_cast<uint8_t>(tl);
+      }
+    }
+    __syncthreads();
+
+    // ---- what is left to decide
+    const int count = s_count;
+    for (int i = warp; i < count; i += kWarps) {
+      const int tl = s_list[i];
+      resolve_token<KEY>(a, a.logits + static_cast<size_t>(t0 + tl) * E, s_bias, bi, s_und[tl], GROUPS ? (VEC ? NV : gs) : E,
+                         sh.val[warp], s_cand[warp], s_slot + tl * k);
+    }
+    __syncthreads();
+    const int ntok = min(kGateTok, last - t0), words = (ntok + 31) / 32;
+    if (tid == 0) s_count = 0;
+    for (int w = 0; w < words; ++w) sh.rank.emask[w][tid] = 0u;
+    __syncthreads();
+
+    // ---- weights: a thread per slot, the slots of a token side by side in a power of two of lanes
+    int width = 1;
+    while (width < k) width *= 2;
+    for (int p = tid; p < words * 32 * width; p += kGateThreads) {
+      const int tl = p / width, j = p % width;
+      const bool in = tl < ntok && j < k;
+      const int v = in ? s_slot[tl * k + j] : 0x8000, e = v & 0x7FFF;
+      bool unused = false;
+      const float l = v & 0x8000 ? -INFINITY : clean_logit(__ldg(a.logits + static_cast<size_t>(t0 + tl) * E + e), unused);
+      float top = l;
+      for (int o = width / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      // Renormalised, scores enter by their ratios: relative to e^top, which keeps scores that
+      // underflow (sigmoid: relative to e^min(top, 0), since s <= 1).
+      const bool none = top == -INFINITY;
+      float w;
+      if (a.sigmoid) {
+        const float ref = a.renormalise && !none ? fminf(top, 0.f) : 0.f;
+        const float x = expf(-fabsf(l));  // e^(l - ref) / (1 + e^l), by the exponential that does not overflow
+        w = l > 0.f ? 1.f / (1.f + x) : expf(l - ref) / (1.f + x);
+      } else {
+        w = none ? 0.f : expf(l - (whole_sum && in ? s_soft[tl].x : top));
+      }
+      float sum = w;
+      for (int o = width / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (whole_sum && in) sum = s_soft[tl].y;
+      if (in) {
+        const size_t at = static_cast<size_t>(t0 + tl) * k + j;
+        a.topk_idx[at] = e;
+        a.topk_w[at] = none ? 0.f : w * (a.scale / (a.sigmoid && !a.renormalise ? 1.f : sum));
+        atomicOr(&sh.rank.emask[tl >> 5][e], 1u << (tl & 31));
+      }
+    }
+    __syncthreads();
+
+    // ---- ranks: a slot's place among the chunk's slots of its expert
+    int run = s_run[tid];
+    for (int w = 0; w < words; ++w) {
+      sh.rank.before[w][tid] = static_cast<uint16_t>(run - s_run[tid]);
+      run += __popc(sh.rank.emask[w][tid]);
+    }
+    __syncthreads();
+    for (int sl = tid; sl < ntok * k; sl += kGateThreads) {
+      const int tl = sl / k, e = s_slot[sl] & 0x7FFF, w = tl >> 5;
+      a.row_of_slot[static_cast<size_t>(t0) * k + sl] =
+          s_run[e] + sh.rank.before[w][e] + __popc(sh.rank.emask[w][e] & ((1u << (tl & 31)) - 1u));
+    }
+    __syncthreads();
+    s_run[tid] = run;
+  }
+  if (bad) s_flag = 1;
+  __syncthreads();
+
+  // ---- the cluster's chunks in front of this one
+  if (a.cluster > 1) cluster_sync();
+  const int rank = blockIdx.x % a.cluster, cluster = blockIdx.x / a.cluster;
+  int before = 0, all = 0, n;
+  if (tid < E)
+    for (int c = 0; c < a.cluster; ++c) {
+      const int v = a.cluster > 1 ? ld_peer(&s_run[tid], c) : s_run[tid];
+      before += c < rank ? v : 0;
+      all += v;
+    }
+  int flag = 0;
+  if (tid == 0 && rank == 0)
+    for (int c = 0; c < a.cluster; ++c) flag |= (a.cluster > 1 ? ld_peer(&s_flag, c) : s_flag) ? kDevNonfiniteLogit : 0;
+  if (static_cast<int>(gridDim.x) > a.cluster) {  // the second kernel goes on
+    if (tid < E) {
+      a.before[static_cast<size_t>(blockIdx.x) * E + tid] = before;
+      if (rank == 0) a.total[static_cast<size_t>(cluster) * E + tid] = all;
+    }
+    if (tid == 0 && rank == 0) a.flags[cluster] = flag;
+  } else {
+    const int off = expert_prefix(all, s_w, &n);
+    s_base[tid] = off + before;
+    if (rank == 0) {
+      if (tid < E) {
+        a.counts[tid] = all;
+        a.offsets[tid] = off;
+      }
+      if (tid == 0) {
+        a.offsets[E] = n;
+        *a.status = flag;
+      }
+    }
+    __syncthreads();
+    for (int64_t s = static_cast<int64_t>(first) * k + tid; s < static_cast<int64_t>(last) * k; s += kGateThreads) {
+      const int row = s_base[a.topk_idx[s]] + a.row_of_slot[s];  // (this block's own writes)
+      a.row_of_slot[s] = row;
+      a.slot_of_row[row] = static_cast<int32_t>(s);
+      a.w_row[row] = a.topk_w[s];
+    }
+  }
+  if (a.cluster > 1) cluster_sync();  // before a block leaves that others read
+}
+
+template <int NV, bool VEC, int KEY, int KMAX>
+cudaError_t launch_variant(const GateArgs &a, cudaStream_t s) {
+  const int blocks = (a.chunks + a.cluster - 1) / a.cluster * a.cluster;
+  if (a.groups > 1)
+    return launch_pdl(gate_select_kernel<NV, VEC, KEY, true, KMAX>, dim3(blocks), dim3(kGateThreads), 0, s, a.cluster, a);
+  return launch_pdl(gate_select_kernel<NV, VEC, KEY, false, KMAX>, dim3(blocks), dim3(kGateThreads), 0, s, a.cluster, a);
+}
+template <int KEY, int KMAX>
+cudaError_t launch_by_width(const GateArgs &a, cudaStream_t s) {
+  if (a.E <= 32) return launch_variant<1, false, KEY, KMAX>(a, s);
+  if (a.E <= 64) return launch_variant<2, false, KEY, KMAX>(a, s);
+  if (a.E <= 128) return launch_variant<4, false, KEY, KMAX>(a, s);
+  return launch_variant<8, false, KEY, KMAX>(a, s);
+}
+
+}  // namespace
+
+template <int KEY>
+cudaError_t launch_gate_select(const GateArgs &a, cudaStream_t s) {
+  // VEC: whole vectors, on their own alignment; groups of a lane's vectors, a power of two of them
+  const int nv = a.E / 32, lanes = a.group_size / (nv > 0 ? nv : 1);
+  const bool runs = a.groups == 1 || (a.group_size % (nv > 0 ? nv : 1) == 0 && (lanes & (lanes - 1)) == 0);
+  if (a.k <= 8) {
+    if (a.E == 128 && runs) return launch_variant<4, true, KEY, 8>(a, s);
+    if (a.E == 256 && runs && (reinterpret_cast<uintptr_t>(a.logits) & 31) == 0) return launch_variant<8, true, KEY, 8>(a, s);
+    return launch_by_width<KEY, 8>(a, s);
+  }
+  return launch_by_width<KEY, kMaxTopK>(a, s);
+}
+
+}  // namespace moe
+#endif  // MOE_GATE_SELECT
