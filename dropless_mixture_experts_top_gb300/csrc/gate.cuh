@@ -15,12 +15,16 @@
 // decided by more than that is chosen again from scores in 64 bits.  Without a bias the
 // logits themselves are compared.
 //
-// One warp per token, a few experts per lane.  A score becomes a 23-bit fixed-point
-// number above the expert's index in one 32-bit key, so that keys are unique and one
-// warp-wide maximum (redux) gives both the next score and whose it is.  Each lane sorts
-// its keys once and hands out its largest.  Without a bias the key is the upper 24 bits
-// of the logit.  Where 32 lanes hold all experts in whole vectors, a lane's experts are
-// neighbours (VEC): one load per token, and groups are runs of lanes.
+// LPT lanes have a token (8, 16 or 32: four, two or one token per warp), with NV of its
+// experts each.  A score becomes a 23-bit fixed-point number above the expert's index in
+// one 32-bit key, so that keys are unique and one maximum over the token's lanes gives
+// both the next score and whose it is.  Each lane sorts its keys once and hands out its
+// largest.  Without a bias the key is the upper 24 bits of the logit.  Where the lanes hold
+// all experts in whole vectors, a lane's experts are neighbours (VEC): whole sectors per
+// load, and groups are runs of lanes.
+//
+// Bound by instructions: fewer lanes per token share the steps that pick the next score
+// among more tokens, at the price of longer lists to sort.
 #pragma once
 
 #include <float.h>
@@ -145,9 +149,9 @@ __device__ __forceinline__ uint32_t order_of(float l) {
   return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
 
-// Sorts NV keys, largest first.
+// Sorts NV keys, largest first; of 16, the first 8.
 template <int NV>
-__device__ __forceinline__ void sort_keys(uint32_t (&v)[NV]) {
+__device__ __forceinline__ void sort_keys(uint32_t *v) {
   auto cas = [&](int a, int b) {
     const uint32_t hi = max(v[a], v[b]), lo = min(v[a], v[b]);
     v[a] = hi;
@@ -165,6 +169,16 @@ __device__ __forceinline__ void sort_keys(uint32_t (&v)[NV]) {
     cas(1, 4), cas(3, 6);
     cas(2, 4), cas(3, 5);
     cas(3, 4);
+  } else if constexpr (NV == 16) {
+    sort_keys<8>(v);
+    sort_keys<8>(v + 8);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = max(v[i], v[15 - i]);  // the 8 largest, falling and rising
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if ((i & d) == 0) cas(i, i + d);
   }
 }
 
@@ -298,11 +312,15 @@ __device__ __noinline__ void resolve_token(const GateArgs &a, const float *row, 
   __syncwarp();
 }
 
-// NV experts per lane: e = lane + 32 i, or NV lane + i (VEC; E = 32 NV).  KMAX: k at most.
-template <int NV, bool VEC, int KEY, bool GROUPS, int KMAX>
-__global__ void __launch_bounds__(kGateThreads, NV == 8 ? 3 : 4) gate_select_kernel(const GateArgs a) {
+// LPT lanes per token, NV experts per lane: with l the lane's place among the token's, e = l + LPT i, or NV l + i
+// (VEC; E = LPT NV).  KMAX: k at most.
+template <int LPT, int NV, bool VEC, int KEY, bool GROUPS, int KMAX>
+__global__ void __launch_bounds__(kGateThreads, NV == 16 ? 3 : 4) gate_select_kernel(const GateArgs a) {
   constexpr int kNear = KEY == kKeyLogit ? 0 : (KEY == kKeySigmoid ? kNearSigmoid : kNearSoftmax);
-  constexpr bool KEYS = GROUPS && !VEC;
+  constexpr bool KEYS = GROUPS && !VEC;                  // groups by way of shared memory
+  static_assert(!KEYS || LPT == 32, "a lane per group");
+  constexpr int TPW = 32 / LPT, kStep = kWarps * TPW;    // tokens of a warp, of the block, at once
+  constexpr int ND = NV < 8 ? NV : 8;                    // a lane's sorted keys
   constexpr int kWords = kGateTok / 32;
   __shared__ union {                                     // one after the other:
     uint32_t keys[KEYS ? kWarps : 1][KEYS ? kMaxExperts : 1];  // the choice's
@@ -313,6 +331,7 @@ __global__ void __launch_bounds__(kGateThreads, NV == 8 ? 3 : 4) gate_select_ker
     } rank;
   } sh;
   __shared__ float s_bias[kMaxExperts];
+  __shared__ __align__(16) float s_add[kMaxExperts];     // the bias' part of the number (of -inf, NaN, inf: itself)
   __shared__ int32_t s_run[kMaxExperts];                 // the chunk's slots of expert e in earlier rounds
   __shared__ uint16_t s_slot[kGateTok * KMAX];           // expert of each slot; bit 15: without a score
   __shared__ float2 s_soft[kGateTok];                    // softmax weights: a token's largest logit, and its sum
@@ -324,7 +343,7 @@ __global__ void __launch_bounds__(kGateThreads, NV == 8 ? 3 : 4) gate_select_ker
   __shared__ int32_t s_base[kMaxExperts];
   __shared__ int s_w[kMaxExperts / 32];
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, l = lane % LPT;
   const int E = a.E, k = a.k;
   const int first = gate_first(a, blockIdx.x), last = min(a.T, gate_first(a, blockIdx.x + 1));
   if (tid == 0) s_count = 0, s_flag = 0, s_bodd = 0;
@@ -332,18 +351,17 @@ __global__ void __launch_bounds__(kGateThreads, NV == 8 ? 3 : 4) gate_select_ker
   griddep_wait();  // the previous kernel in the stream has completed
   griddep_launch_dependents();
 
-  auto expert = [&](int i) { return VEC ? lane * NV + i : lane + 32 * i; };
+  auto expert = [&](int i) { return VEC ? l * NV + i : l + LPT * i; };
   auto load = [&](int t, float (&v)[NV]) {
     const float *row = a.logits + static_cast<size_t>(t) * E;
-    if constexpr (VEC && NV == 8) {
-      if (t < last)
-        asm volatile("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
-                     : "l"(row + lane * 8));
-    } else if constexpr (VEC) {
+    if constexpr (VEC) {
       if (t < last) {
-        const float4 q = __ldg(reinterpret_cast<const float4 *>(row + lane * 4));
-        v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+#pragma unroll
+        for (int i = 0; i < NV; i += 8)
+          asm volatile("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                       : "=f"(v[i]), "=f"(v[i + 1]), "=f"(v[i + 2]), "=f"(v[i + 3]), "=f"(v[i + 4]), "=f"(v[i + 5]),
+                         "=f"(v[i + 6]), "=f"(v[i + 7])
+                       : "l"(row + l * NV + i));
       }
     } else {
 #pragma unroll
@@ -351,112 +369,142 @@ __global__ void __launch_bounds__(kGateThreads, NV == 8 ? 3 : 4) gate_select_ker
     }
   };
   float ahead[NV] = {};
-  load(first + warp, ahead);
+  load(first + warp * TPW + lane / LPT, ahead);
 
   BiasInfo bi{kFixOne - 32.f, kFixOne + kFixLeast, static_cast<int>(kFixLeast), false};
   __syncthreads();
-  if (KEY != kKeyLogit && a.bias) {
-    const float b = tid < E ? __ldg(a.bias + tid) : 0.f;
+  if (KEY != kKeyLogit) {
+    const float b = a.bias && tid < E ? __ldg(a.bias + tid) : 0.f;
     s_bias[tid] = b;
-    const bool odd = !(fabsf(b) <= FLT_MAX);
-    if (odd) s_bodd = 1;
-    float m = warp_max(odd ? 0.f : fabsf(b));
-    if (lane == 0) s_bmax[warp] = m;
+    if (a.bias) {
+      const bool odd = !(fabsf(b) <= FLT_MAX);
+      if (odd) s_bodd = 1;
+      float m = warp_max(odd ? 0.f : fabsf(b));
+      if (lane == 0) s_bmax[warp] = m;
+      __syncthreads();
+      m = s_bmax[0];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) m = fmaxf(m, s_bmax[w]);
+      bi.scale = (kFixOne - 32.f) / (1.f + 2.f * m);
+      const float O = ceilf(m * bi.scale);
+      bi.base = kFixOne + kFixLeast + O;
+      bi.off = static_cast<int>(kFixLeast + O);
+      bi.odd = s_bodd != 0;
+    }
+    // (VEC: in the order in which the lanes read vectors of four)
+    const int at = VEC ? (tid % NV / 4) * (LPT * 4) + tid / NV * 4 + tid % 4 : tid;
+    if (!VEC || tid < LPT * NV) s_add[at] = fmaf(b, bi.scale, bi.base);
     __syncthreads();
-    m = s_bmax[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) m = fmaxf(m, s_bmax[w]);
-    bi.scale = (kFixOne - 32.f) / (1.f + 2.f * m);
-    const float O = ceilf(m * bi.scale);
-    bi.base = kFixOne + kFixLeast + O;
-    bi.off = static_cast<int>(kFixLeast + O);
-    bi.odd = s_bodd != 0;
   }
-  float add[KEY == kKeyLogit ? 1 : NV];  // the bias' part of the number (of a bias of -inf, NaN, inf: itself)
-  if constexpr (KEY != kKeyLogit) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) add[i] = a.bias && expert(i) < E ? fmaf(s_bias[expert(i)], bi.scale, bi.base) : bi.base;
-  }
-  // groups: VEC: run of lanes per group, where that is a power of two (else, and without VEC, by way of shared memory)
+  // groups: VEC: runs of lanes; else by way of shared memory, with gP lanes for each
   const int gs = a.group_size, G = a.groups;
   int gP = 1, gits = 0;
   if constexpr (KEYS) {
     while (2 * gP * G <= 32) gP *= 2;
     gits = (gs + gP - 1) / gP;
   }
-  const int my_g = VEC ? lane * NV / gs : lane % G, my_p = VEC ? 0 : lane / G;
+  const int my_g = VEC ? l * NV / gs : lane % G, my_p = VEC ? 0 : lane / G;
   const bool whole_sum = !a.sigmoid && !a.renormalise;  // the weights need the softmax' sum over all experts
   bool bad = false;
 
+  auto top_of = [](uint32_t v) {  // over the token's lanes
+    if constexpr (LPT == 32) {
+      return __reduce_max_sync(0xffffffffu, v);
+    } else {
+#pragma unroll
+      for (int o = LPT / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+      return v;
+    }
+  };
+
   for (int t0 = first; t0 < last; t0 += kGateTok) {
-    // ---- choice: this warp's tokens, kWarps apart
+    // ---- choice: a warp's tokens, kStep apart
 #pragma unroll 1
-    for (int tl = warp; tl < kGateTok; tl += kWarps) {
-      const int t = t0 + tl;
-      if (t >= last) break;
-      float l[NV], fin = 0.f;
+    for (int tw = warp * TPW; tw < kGateTok && t0 + tw < last; tw += kStep) {
+      const int tl = tw + lane / LPT, t = t0 + tl;
+      const bool valid = t < last;
+      float x[NV], fin = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        l[i] = ahead[i];
-        fin = fmaf(l[i], 0.f, fin);  // NaN where one is not finite
+        x[i] = ahead[i];
+        fin = fmaf(x[i], 0.f, fin);  // NaN where one is not finite
       }
-      load(t + kWarps, ahead);  // (of the next round after the last)
+      load(t + kStep, ahead);  // (of the next round after the last)
       const bool odd = __any_sync(0xffffffffu, fin != 0.f);
+      uint32_t off = 0;  // experts that may not be chosen
       if (odd) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) l[i] = clean_logit(l[i], bad);
+        for (int i = 0; i < NV; ++i) {
+          x[i] = clean_logit(x[i], bad);
+          off |= static_cast<uint32_t>(!(x[i] >= -FLT_MAX)) << i;
+        }
       }
       uint32_t key[NV];
-      float m = 0.f, z = 0.f;
       if (KEY == kKeySoftmax || (KEY == kKeyLogit && whole_sum)) {
-        m = -FLT_MAX;
+        float m = -FLT_MAX, z = 0.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) m = VEC || expert(i) < E ? fmaxf(m, l[i]) : m;
-        m = warp_max(m);
+        for (int i = 0; i < NV; ++i) m = VEC || expert(i) < E ? fmaxf(m, x[i]) : m;
+#pragma unroll
+        for (int o = LPT / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          const float e = VEC || expert(i) < E ? ex2((l[i] - m) * kLog2e) : 0.f;
-          if (KEY == kKeySoftmax) key[i] = __float_as_uint(e);
+          const float e = VEC || expert(i) < E ? ex2((x[i] - m) * kLog2e) : 0.f;
+          if (KEY == kKeySoftmax) x[i] = e;
           z += e;
         }
-        z = warp_sum(z);
-        if (lane == 0) s_soft[tl] = make_float2(m, z);
+#pragma unroll
+        for (int o = LPT / 2; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        if (l == 0 && valid) s_soft[tl] = make_float2(m, z);
+        if (KEY == kKeySoftmax) {
+          const float rz = rcp(z);
+#pragma unroll
+          for (int i = 0; i < NV; ++i) x[i] *= rz;
+        }
       }
       if constexpr (KEY == kKeyLogit) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) key[i] = (order_of(l[i]) & 0xFFFFFF00u) | (255u - expert(i));
-        if (odd) {
-#pragma unroll
-          for (int i = 0; i < NV; ++i) key[i] = l[i] >= -FLT_MAX ? key[i] : 0u;
-        }
+        for (int i = 0; i < NV; ++i) key[i] = (order_of(x[i]) & 0xFFFFFF00u) | (255u - expert(i));
       } else {
-        const float rz = KEY == kKeySoftmax ? rcp(z) : 0.f;
-        float x[NV];
+        float add[NV];
+        if constexpr (VEC) {
+#pragma unroll
+          for (int i = 0; i < NV; i += 4) {
+            const float4 q = *reinterpret_cast<const float4 *>(s_add + i / 4 * (LPT * 4) + l * 4);
+            add[i] = q.x, add[i + 1] = q.y, add[i + 2] = q.z, add[i + 3] = q.w;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < NV; ++i) add[i] = s_add[expert(i) & (kMaxExperts - 1)];
+        }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          const float s = KEY == kKeySigmoid ? sigmoid_fast(l[i]) : __uint_as_float(key[i]) * rz;
+          const float s = KEY == kKeySigmoid ? sigmoid_fast(x[i]) : x[i];
           x[i] = fmaf(s, bi.scale, add[i]);  // a whole number in [2^23, 2^24), or inf
         }
-        if (odd || bi.odd) {  // what may not be chosen: the number 0
+        if (bi.odd) {  // a bias of -inf or NaN: the number 0
 #pragma unroll
-          for (int i = 0; i < NV; ++i) x[i] = l[i] >= -FLT_MAX ? fmaxf(x[i], kFixOne) : kFixOne;
+          for (int i = 0; i < NV; ++i) x[i] = fmaxf(x[i], kFixOne);
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i)  // the number's three bytes over the index
           key[i] = __byte_perm(__float_as_uint(x[i]), 255u - expert(i), 0x2104);
+      }
+      if (odd) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) key[i] = (off >> i) & 1u ? 0u : key[i];
       }
       if constexpr (!VEC) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) key[i] = expert(i) < E ? key[i] : 0u;
       }
       Undecided u{0xffffffffu, 0};
-      bool undecided = false;
+      bool open_groups = false;
       if constexpr (GROUPS) {
         uint32_t k1, k2;
         if constexpr (VEC) {
           sort_keys<NV>(key);
           k1 = key[0];
-          k2 = NV > 1 ? key[1] : 0u;
+          k2 = key[1];
           for (int o = 1; o * NV < gs; o <<= 1) {
             const uint32_t o1 = __shfl_xor_sync(0xffffffffu, k1, o), o2 = __shfl_xor_sync(0xffffffffu, k2, o);
             k2 = max(max(k2, o2), min(k1, o1));
@@ -491,49 +539,50 @@ __global__ void __launch_bounds__(kGateThreads, NV == 8 ? 3 : 4) gate_select_ker
         uint32_t r = 0;
         bool kept = false;
         for (int j = 0; j < a.top_groups; ++j) {
-          r = __reduce_max_sync(0xffffffffu, gkey);
+          r = top_of(gkey);
           if (gkey == r) {
             kept = true;
             gkey = 0;
           }
         }
-        const uint32_t next = __reduce_max_sync(0xffffffffu, gkey);
-        undecided = a.top_groups < G && (next >> 5) != 0 && (bi.odd || (r >> 5) - (next >> 5) <= 2 * kNear);
-        u.runs = undecided ? 0u : __ballot_sync(0xffffffffu, kept && (VEC || lane < G));
+        const uint32_t next = top_of(gkey);
+        open_groups = a.top_groups < G && (next >> 5) != 0 && (bi.odd || (r >> 5) - (next >> 5) <= 2 * kNear);
+        const uint32_t runs = __ballot_sync(0xffffffffu, kept && (VEC || lane < G));
+        u.runs = open_groups ? 0u : (VEC && LPT < 32 ? runs >> (lane - l) & ((1u << (LPT & 31)) - 1u) : runs);
         if constexpr (VEC) {
-          if (!kept) key[0] = 0;  // (and the lane hands out nothing)
-          if (!kept)
 #pragma unroll
-            for (int i = 1; i < NV; ++i) key[i] = 0;
+          for (int i = 0; i < ND; ++i) key[i] = kept ? key[i] : 0u;
         } else {
 #pragma unroll
-          for (int i = 0; i < NV; ++i) key[i] = (u.runs >> (expert(i) / gs & 31)) & 1u ? key[i] : 0u;
+          for (int i = 0; i < NV; ++i) key[i] = (runs >> (expert(i) / gs & 31)) & 1u ? key[i] : 0u;
         }
       }
-      if (!undecided) {
-        if constexpr (!(GROUPS && VEC)) sort_keys<NV>(key);
-        uint32_t prev = 0xffffffffu, gap = 0xffffffffu, end = 0;
+      if constexpr (!(GROUPS && VEC)) sort_keys<NV>(key);
+      uint32_t prev = 0xffffffffu, gap = 0xffffffffu, end = 0;
+      int taken = 0;
 #pragma unroll
-        for (int j = 0; j <= KMAX; ++j) {
-          if (j > k) break;
-          const uint32_t r = __reduce_max_sync(0xffffffffu, key[0]);
-          gap = min(gap, prev - r);
-          prev = r;
-          if (j < k) end = r;
-          if (key[0] == r) {
-            if (j < k) s_slot[tl * k + j] = static_cast<uint16_t>(255u - (r & 255u));
+      for (int j = 0; j <= KMAX; ++j) {
+        if (j > k) break;
+        const uint32_t r = top_of(key[0]);
+        gap = min(gap, prev - r);
+        prev = r;
+        if (j < k) end = r;
+        if (key[0] == r) {
+          if (j < k && valid) s_slot[tl * k + j] = static_cast<uint16_t>(255u - (r & 255u));
+          if (NV > ND) ++taken;
 #pragma unroll
-            for (int i = 0; i + 1 < NV; ++i)
-              if (i < KMAX - j) key[i] = key[i + 1];  // (further back none is needed any more)
-            if (NV <= KMAX - j) key[NV - 1] = 0;
-            if (NV == 1) key[0] = 0;
-          }
+          for (int i = 0; i + 1 < ND; ++i)
+            if (i < KMAX - j) key[i] = key[i + 1];  // (further back none is needed any more)
+          if (ND <= KMAX - j || ND == 1) key[ND - 1] = 0;
         }
-        // two neighbours too near to tell, or fewer than k that may be chosen
-        undecided = gap < (kNear + 1) * 256u || (end >> 8) == 0;
-        u.least = static_cast<int>(end >> 8) > 2 * kNear + 1 ? static_cast<int>(end >> 8) - 2 * kNear : 0;
       }
-      if (undecided && lane == 0) {
+      // two neighbours too near to tell, fewer than k that may be chosen, groups too near, or a lane
+      // whose sorted keys were used up
+      bool undecided = open_groups || gap < (kNear + 1) * 256u || (end >> 8) == 0;
+      if (NV > ND) undecided |= __any_sync(0xffffffffu, taken >= ND);
+      if (undecided && l == 0 && valid) {
+        const int q = static_cast<int>(end >> 8);
+        u.least = q > 2 * kNear + 1 ? q - 2 * kNear : 0;
         s_und[tl] = u;
         s_list[atomicAdd(&s_count, 1)] = static_cast<uint8_t>(tl);
       }
@@ -648,34 +697,45 @@ __global__ void __launch_bounds__(kGateThreads, NV == 8 ? 3 : 4) gate_select_ker
   if (a.cluster > 1) cluster_sync();  // before a block leaves that others read
 }
 
-template <int NV, bool VEC, int KEY, int KMAX>
+template <int LPT, int NV, bool VEC, int KEY, bool GROUPS, int KMAX>
 cudaError_t launch_variant(const GateArgs &a, cudaStream_t s) {
   const int blocks = (a.chunks + a.cluster - 1) / a.cluster * a.cluster;
-  if (a.groups > 1)
-    return launch_pdl(gate_select_kernel<NV, VEC, KEY, true, KMAX>, dim3(blocks), dim3(kGateThreads), 0, s, a.cluster, a);
-  return launch_pdl(gate_select_kernel<NV, VEC, KEY, false, KMAX>, dim3(blocks), dim3(kGateThreads), 0, s, a.cluster, a);
+  return launch_pdl(gate_select_kernel<LPT, NV, VEC, KEY, GROUPS, KMAX>, dim3(blocks), dim3(kGateThreads), 0, s, a.cluster, a);
 }
-template <int KEY, int KMAX>
-cudaError_t launch_by_width(const GateArgs &a, cudaStream_t s) {
-  if (a.E <= 32) return launch_variant<1, false, KEY, KMAX>(a, s);
-  if (a.E <= 64) return launch_variant<2, false, KEY, KMAX>(a, s);
-  if (a.E <= 128) return launch_variant<4, false, KEY, KMAX>(a, s);
-  return launch_variant<8, false, KEY, KMAX>(a, s);
+template <int KEY, bool GROUPS>
+cudaError_t launch_wide(const GateArgs &a, cudaStream_t s) {  // a warp per token
+  if (a.E <= 32) return launch_variant<32, 1, false, KEY, GROUPS, kMaxTopK>(a, s);
+  if (a.E <= 64) return launch_variant<32, 2, false, KEY, GROUPS, kMaxTopK>(a, s);
+  if (a.E <= 128) return launch_variant<32, 4, false, KEY, GROUPS, kMaxTopK>(a, s);
+  return launch_variant<32, 8, false, KEY, GROUPS, kMaxTopK>(a, s);
 }
 
 }  // namespace
 
+// Several tokens per warp up to k = 8, whole vectors where a token's row and a group are made of a lane's.
 template <int KEY>
 cudaError_t launch_gate_select(const GateArgs &a, cudaStream_t s) {
-  // VEC: whole vectors, on their own alignment; groups of a lane's vectors, a power of two of them
-  const int nv = a.E / 32, lanes = a.group_size / (nv > 0 ? nv : 1);
-  const bool runs = a.groups == 1 || (a.group_size % (nv > 0 ? nv : 1) == 0 && (lanes & (lanes - 1)) == 0);
-  if (a.k <= 8) {
-    if (a.E == 128 && runs) return launch_variant<4, true, KEY, 8>(a, s);
-    if (a.E == 256 && runs && (reinterpret_cast<uintptr_t>(a.logits) & 31) == 0) return launch_variant<8, true, KEY, 8>(a, s);
-    return launch_by_width<KEY, 8>(a, s);
+  const bool sectors = (reinterpret_cast<uintptr_t>(a.logits) & 31) == 0;
+  auto runs = [&](int nv) {  // groups of a power of two of lanes
+    const int lanes = a.group_size / nv;
+    return a.group_size % nv == 0 && (lanes & (lanes - 1)) == 0;
+  };
+  if (a.k <= 8 && a.groups == 1) {
+    if (a.E <= 8) return launch_variant<8, 1, false, KEY, false, 8>(a, s);
+    if (a.E <= 32) return launch_variant<8, 4, false, KEY, false, 8>(a, s);
+    if (a.E == 64 && sectors) return launch_variant<8, 8, true, KEY, false, 8>(a, s);
+    if (a.E <= 64) return launch_variant<8, 8, false, KEY, false, 8>(a, s);
+    if (a.E == 128 && sectors) return launch_variant<8, 16, true, KEY, false, 8>(a, s);
+    if (a.E <= 128) return launch_variant<8, 16, false, KEY, false, 8>(a, s);
+    if (a.E == 256 && sectors) return launch_variant<16, 16, true, KEY, false, 8>(a, s);
+    return launch_variant<16, 16, false, KEY, false, 8>(a, s);
   }
-  return launch_by_width<KEY, kMaxTopK>(a, s);
+  if (a.k <= 8 && sectors) {
+    if (a.E == 64 && runs(8)) return launch_variant<8, 8, true, KEY, true, 8>(a, s);
+    if (a.E == 128 && runs(16)) return launch_variant<8, 16, true, KEY, true, 8>(a, s);
+    if (a.E == 256 && runs(16)) return launch_variant<16, 16, true, KEY, true, 8>(a, s);
+  }
+  return a.groups > 1 ? launch_wide<KEY, true>(a, s) : launch_wide<KEY, false>(a, s);
 }
 
 }  // namespace moe
