@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(kGateThreads) gate_index_kernel(const GateArgs
   int before = 0, all = 0, n;
   const int here = tid < E && clusters ? __ldcg(a.before + static_cast<size_t>(blockIdx.x) * E + tid) : 0;
   if (tid < E) {
-    constexpr int kBatch = 10;  // 76 clusters over 8 blocks
+    constexpr int kBatch = 8;  // 57 clusters over 8 blocks
     for (int c = rank; c < clusters; c += a.cluster * kBatch) {
       int h[kBatch];
 #pragma unroll
@@ -271,9 +271,9 @@ bool gate_ok(const moe_gate_config *c) {
   return c->scale > 0.f && c->scale <= FLT_MAX;  // (not where it is NaN)
 }
 
-// Chunks: 32 tokens each while that makes at most four blocks for each of 152 SMs, then more each; up to
+// Chunks: 32 tokens each while that makes at most three blocks for each of 152 SMs, then more each; up to
 // 64 tokens for each of one cluster's blocks are one launch.
-constexpr int kLeastTok = 32, kMostChunks = 608;
+constexpr int kLeastTok = 32, kMostChunks = 456;
 struct GateLayout {
   int chunks, cluster;
   size_t flags, before, total, bytes;

@@ -56,7 +56,7 @@ struct GateArgs {
 };
 
 constexpr int kGateThreads = 256;
-constexpr int kGateTok = 256;      // tokens of one round of a block at most
+constexpr int kGateTok = 320;      // tokens of one round of a block at most
 constexpr int kGateCluster = 8;    // blocks of a cluster at most
 
 enum GateKey : int { kKeyLogit = 0, kKeySigmoid = 1, kKeySoftmax = 2 };
@@ -198,8 +198,237 @@ struct Undecided {
   int least;
 };
 
-// Its choice from 64-bit scores, by one warp.  val: E doubles of this warp, list: E bytes; slot: its k
-// slots, bit 15 set where an expert had no score.
+// ---- Scores as pairs of floats (hi + lo, about 48 bits), from error-free sums and products: the part's 64-bit
+// unit is a hundredth as fast as this.  (Dekker, Knuth: two_sum, two_prod by a fused multiply-add.)
+struct Pair {
+  float h, l;
+};
+__device__ __forceinline__ Pair quick_two_sum(float a, float b) {  // |a| >= |b|
+  const float s = __fadd_rn(a, b);
+  return {s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
+  const Pair s = two_sum(a.h, b.h);
+  return quick_two_sum(s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l)));
+}
+__device__ __forceinline__ Pair pair_mul(Pair a, Pair b) {
+  const float p = __fmul_rn(a.h, b.h);
+  return quick_two_sum(p, __fmaf_rn(a.h, b.h, -p) + __fmaf_rn(a.h, b.l, a.l * b.h));
+}
+__device__ __forceinline__ Pair pair_div(Pair a, Pair b) {
+  const float q = __fdiv_rn(a.h, b.h);
+  const float r = __fmaf_rn(-q, b.h, a.h) + __fmaf_rn(-q, b.l, a.l);
+  return quick_two_sum(q, __fdiv_rn(r, b.h));
+}
+// e^-(a + b) for a >= 0, b at most half an ulp of a; 0 from a = 40 on (4e-18).
+// n ln 2 comes off in three parts (15, 17 and 24 bits: the first two products are exact), then the series:
+// to r^6 / 6! in pairs, the rest, below 2e-7 of the sum, in single floats: off by 2^-45 at most.
+__device__ __forceinline__ Pair pair_exp_neg(float a, float b) {
+  if (!(a < 40.f)) return {0.f, 0.f};
+  const float n = rintf(a * 1.4426950408889634f);
+  const Pair t = two_sum(__fmaf_rn(n, 0.693145751953125f, -a), __fmul_rn(n, 1.428605173714459e-06f));  // n ln 2 - a
+  const Pair r = quick_two_sum(t.h, t.l + __fmaf_rn(n, 1.6465949582897e-12f, -b));
+  float q = 1.f / 6227020800.f;  // 1 / 13!
+  q = fmaf(q, r.h, 1.f / 479001600.f);
+  q = fmaf(q, r.h, 1.f / 39916800.f);
+  q = fmaf(q, r.h, 1.f / 3628800.f);
+  q = fmaf(q, r.h, 1.f / 362880.f);
+  q = fmaf(q, r.h, 1.f / 40320.f);
+  q = fmaf(q, r.h, 1.f / 5040.f);
+  Pair s = pair_add(pair_mul({q, 0.f}, r), {1.3888889225e-03f, -3.3631094437e-11f});  // 1 / 6!
+  s = pair_add(pair_mul(s, r), {8.3333337680e-03f, -4.3461720333e-10f});  // 1 / 5!
+  s = pair_add(pair_mul(s, r), {4.1666667908e-02f, -1.2417634698e-09f});  // 1 / 4!
+  s = pair_add(pair_mul(s, r), {1.6666667163e-01f, -4.9670538794e-09f});  // 1 / 3!
+  s = pair_add(pair_mul(s, r), {0.5f, 0.f});
+  s = pair_add(pair_mul(s, r), {1.f, 0.f});
+  s = pair_add(pair_mul(s, r), {1.f, 0.f});
+  const float f = __int_as_float((127 - static_cast<int>(n)) << 23);  // 2^-n
+  return {s.h * f, s.l * f};
+}
+__device__ __forceinline__ Pair pair_sigmoid(float l) {
+  const Pair e = pair_exp_neg(fabsf(l), 0.f), d = pair_add({1.f, 0.f}, e);
+  return pair_div(l < 0.f ? e : Pair{1.f, 0.f}, d);
+}
+// In units of 2^-42, from pairs: off by under 8 (2^-39; the exponential's 2^-45, those of Z and the quotient, the
+// conversions').  Scores that differ by more than twice that are in the order of the exact ones.
+constexpr long long kNearFixed = 16;
+constexpr float kFixedOne = 4398046511104.f;  // 2^42
+constexpr float kFixedMost = 1024.f;          // of a bias
+__device__ __forceinline__ long long to_fixed(Pair s, float b) {
+  return __float2ll_rn(s.h * kFixedOne) + __float2ll_rn(s.l * kFixedOne) + __float2ll_rn(b * kFixedOne);
+}
+
+// An undecided token's choice by one warp: from fixed-point scores, or, without a bias, from the logits'
+// order.  Whether these decide it (logits do); if not, nothing is written.  val: E numbers of this warp, list: E bytes;
+// slot: the token's k slots, bit 15 set where an expert had no score.
+template <int KEY>
+__device__ __noinline__ bool resolve_fixed(const GateArgs &a, const float *row, const float *s_bias, BiasInfo bi, Undecided u,
+                                           int run, long long *val, uint8_t *list, uint16_t *slot) {
+  constexpr int NR = kMaxExperts / 32;
+  const int lane = threadIdx.x & 31, E = a.E;
+  const bool biased = a.bias != nullptr;
+  const long long least = LLONG_MIN;
+  bool bad = false, in_range = true;
+  float l[NR], b[NR];
+  uint32_t scored = 0;
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    const int e = lane + 32 * i;
+    l[i] = e < E ? clean_logit(__ldg(row + e), bad) : -INFINITY;
+    b[i] = KEY != kKeyLogit && biased && e < E ? s_bias[e] : 0.f;
+  }
+  float top = -FLT_MAX, low = FLT_MAX;
+  bool whole = true;  // biases that are whole numbers of units
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    top = fmaxf(top, l[i]);
+    if (l[i] >= -FLT_MAX && b[i] > -INFINITY) {
+      scored |= 1u << i;
+      low = fminf(low, l[i]);
+      in_range = in_range && fabsf(b[i]) <= kFixedMost;
+      whole = whole && rintf(b[i] * kFixedOne) == b[i] * kFixedOne;
+    }
+  }
+  if (!__all_sync(0xffffffffu, in_range)) return false;
+  // Equal logits (rows of zeros: padding): the scores are one number, which says the same of all, and the biases are exact.
+  const bool even = __all_sync(0xffffffffu, whole) && warp_max(-low) == -warp_max(top);
+  const long long near = KEY == kKeyLogit || even ? 0 : kNearFixed;
+  Pair z = {0.f, 0.f};
+  if (KEY == kKeySoftmax) {
+    top = warp_max(top);
+#pragma unroll 1
+    for (int i = 0; i < NR; ++i) {
+      const float x = i == 0 ? l[0] : i == 1 ? l[1] : i == 2 ? l[2] : i == 3 ? l[3] : i == 4 ? l[4] : i == 5 ? l[5] : i == 6 ? l[6] : l[7];
+      const Pair d = two_sum(top, -x);
+      if (x >= -FLT_MAX) z = pair_add(z, pair_exp_neg(d.h, d.l));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      z = pair_add(z, {__shfl_xor_sync(0xffffffffu, z.h, o), __shfl_xor_sync(0xffffffffu, z.l, o)});
+  }
+  // the number of a logit and a bias in the order of the experts (order) or of the groups
+  auto number = [&](float x, float c, bool order) -> long long {
+    if (KEY == kKeyLogit || (order && !biased)) return static_cast<long long>(order_of(x));
+    if (KEY == kKeySigmoid) return to_fixed(pair_sigmoid(x), c);
+    const Pair d = two_sum(top, -x);
+    return to_fixed(pair_div(pair_exp_neg(d.h, d.l), z), c);
+  };
+  if (u.runs == 0) {  // the groups as well
+    float last = NAN;
+    long long v = 0;
+#pragma unroll 1
+    for (int e = lane, i = 0; e < E; e += 32, ++i) {
+      const float x = clean_logit(__ldg(row + e), bad), c = biased ? s_bias[e] : 0.f;
+      if (x != last) v = number(x, 0.f, false);  // (rows of equal logits take one)
+      last = x;
+      val[e] = (scored >> i) & 1u ? v + (KEY == kKeyLogit ? 0 : __float2ll_rn(c * kFixedOne)) : least;
+    }
+    __syncwarp();
+    long long g1 = least, g2 = least;
+    if (lane < a.groups)
+      for (int m = 0; m < a.group_size; ++m) {
+        const long long v = val[lane * a.group_size + m];
+        g2 = max(g2, min(g1, v));
+        g1 = max(g1, v);
+      }
+    const long long gv = a.group_best == 2 && g2 > least ? g1 + g2 : g1;
+    int before = 0;
+    long long next = least;  // the best of those behind
+    for (int h = 0; h < a.groups; ++h) {
+      const long long o = __shfl_sync(0xffffffffu, gv, h);
+      const bool first = o > gv || (o == gv && h < lane);
+      before += first ? 1 : 0;
+      if (!first && h != lane) next = max(next, o);
+    }
+    const bool open = lane < a.groups && before == a.top_groups - 1 && next > least && gv - next <= 2 * near && near > 0;
+    if (__any_sync(0xffffffffu, open)) return false;
+    u.runs = __ballot_sync(0xffffffffu, lane < a.groups && before < a.top_groups);
+    u.least = 0;
+    run = a.group_size;
+    __syncwarp();
+  }
+  // the experts in question, by index
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    const int e = lane + 32 * i;
+    bool use = (scored >> i & 1u) && ((u.runs >> (e / run & 31)) & 1u);
+    if (KEY != kKeyLogit && use && u.least > 0) {
+      // the fp32 number once more, with the distance that decides off for safety
+      const float s = KEY == kKeySigmoid ? sigmoid_fast(l[i]) : ex2((l[i] - top) * kLog2e) * rcp(z.h);
+      use = fmaf(s + b[i], bi.scale, static_cast<float>(bi.off)) >= static_cast<float>(u.least) - kNearSoftmax;
+    }
+    const uint32_t set = __ballot_sync(0xffffffffu, use);
+    if (use) list[n + __popc(set & ((1u << lane) - 1u))] = static_cast<uint8_t>(e);
+    n += __popc(set);
+  }
+  __syncwarp();
+  {
+    float last = NAN;
+    long long v = 0;
+#pragma unroll 1
+    for (int i = lane; i < n; i += 32) {
+      const int e = list[i];
+      const float x = clean_logit(__ldg(row + e), bad);
+      if (x != last) v = number(x, 0.f, true);
+      last = x;
+      val[i] = v + (KEY == kKeyLogit || !biased ? 0 : __float2ll_rn(s_bias[e] * kFixedOne));
+    }
+  }
+  __syncwarp();
+  // k times the best of what is left; lane j keeps the j-th
+  const int found = min(n, a.k);
+  const long long tie = biased && KEY != kKeyLogit ? near : 0;  // (logits alone decide exactly)
+  long long mine = 0, end = 0;
+  int at_mine = 0;
+  for (int j = 0; j < found; ++j) {
+    long long best = least;
+    int at = INT_MAX;
+    for (int i = lane; i < n; i += 32) {
+      const long long v = val[i];
+      if (v > best) best = v, at = i;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const long long ov = __shfl_xor_sync(0xffffffffu, best, o);
+      const int oa = __shfl_xor_sync(0xffffffffu, at, o);
+      if (ov > best || (ov == best && oa < at)) best = ov, at = oa;
+    }
+    if (lane == j) mine = best, at_mine = at;
+    end = best;
+    if ((at & 31) == lane) val[at] = least;
+    __syncwarp();
+  }
+  bool open = false;
+  if (tie > 0) {
+    auto same = [&](int e0, int e1) { return __ldg(row + e0) == __ldg(row + e1) && s_bias[e0] == s_bias[e1]; };
+    const long long next = __shfl_down_sync(0xffffffffu, mine, 1);
+    const int at_next = __shfl_down_sync(0xffffffffu, at_mine, 1);
+    if (lane + 1 < found && mine - next <= tie) open = !same(list[at_mine], list[at_next]);
+    const int at_end = __shfl_sync(0xffffffffu, at_mine, max(0, found - 1));
+    for (int i = lane; i < n; i += 32)  // those behind the last one
+      if (val[i] > least && end - val[i] <= tie) open |= !same(list[at_end], list[i]);
+  }
+  if (__any_sync(0xffffffffu, open)) return false;
+  if (lane < found) slot[lane] = list[at_mine];
+  if (lane == 0) {  // fewer than k: the others by index
+    int i = 0, e = 0;
+    for (int j = found; j < a.k; ++e) {
+      if (i < n && list[i] == e)
+        ++i;
+      else
+        slot[j++] = static_cast<uint16_t>(e | 0x8000);
+    }
+  }
+  __syncwarp();
+  return true;
+}
+
+// The same in 64 bits: scores that are equal to 2^-38, biases past 1024.
 template <int KEY>
 __device__ __noinline__ void resolve_token(const GateArgs &a, const float *row, const float *s_bias, BiasInfo bi, Undecided u,
                                            int run, double *val, uint8_t *list, uint16_t *slot) {
@@ -336,7 +565,7 @@ __global__ void __launch_bounds__(kGateThreads, NV == 16 ? 3 : 4) gate_select_ke
   __shared__ uint16_t s_slot[kGateTok * KMAX];           // expert of each slot; bit 15: without a score
   __shared__ float2 s_soft[kGateTok];                    // softmax weights: a token's largest logit, and its sum
   __shared__ Undecided s_und[kGateTok];
-  __shared__ uint8_t s_list[kGateTok];                   // undecided tokens
+  __shared__ uint16_t s_list[kGateTok];                  // undecided tokens
   __shared__ uint8_t s_cand[kWarps][kMaxExperts];
   __shared__ int32_t s_count, s_flag, s_bodd;
   __shared__ float s_bmax[kWarps];
@@ -536,19 +765,34 @@ __global__ void __launch_bounds__(kGateThreads, NV == 16 ? 3 : 4) gate_select_ke
         uint32_t gq = k1 >> 8;
         if (KEY != kKeyLogit && a.group_best == 2 && gq) gq += (k2 >> 8) ? k2 >> 8 : static_cast<uint32_t>(bi.off);
         uint32_t gkey = VEC || lane < G ? (gq << 5) | (31u - my_g) : 0u;
-        uint32_t r = 0;
         bool kept = false;
-        for (int j = 0; j < a.top_groups; ++j) {
-          r = top_of(gkey);
-          if (gkey == r) {
-            kept = true;
-            gkey = 0;
+        if constexpr (VEC) {  // a lane counts the groups in front of its own
+          const int lanes = gs / NV;
+          uint32_t below = 0;
+          int before = 0;
+          for (int o = lanes; o < LPT; o += lanes) {
+            const uint32_t other = __shfl_sync(0xffffffffu, gkey, (lane - l) + ((l + o) & (LPT - 1)));
+            before += other > gkey ? 1 : 0;
+            below = max(below, other < gkey ? other : 0u);
           }
+          kept = before < a.top_groups;
+          const bool near = before == a.top_groups - 1 && (below >> 5) != 0 &&
+                            (bi.odd || (gkey >> 5) - (below >> 5) <= 2 * kNear);
+          open_groups = (__ballot_sync(0xffffffffu, near) >> (lane - l) & ((1u << LPT) - 1u)) != 0;
+        } else {
+          uint32_t r = 0;
+          for (int j = 0; j < a.top_groups; ++j) {
+            r = top_of(gkey);
+            if (gkey == r) {
+              kept = true;
+              gkey = 0;
+            }
+          }
+          const uint32_t next = top_of(gkey);
+          open_groups = a.top_groups < G && (next >> 5) != 0 && (bi.odd || (r >> 5) - (next >> 5) <= 2 * kNear);
         }
-        const uint32_t next = top_of(gkey);
-        open_groups = a.top_groups < G && (next >> 5) != 0 && (bi.odd || (r >> 5) - (next >> 5) <= 2 * kNear);
         const uint32_t runs = __ballot_sync(0xffffffffu, kept && (VEC || lane < G));
-        u.runs = open_groups ? 0u : (VEC && LPT < 32 ? runs >> (lane - l) & ((1u << (LPT & 31)) - 1u) : runs);
+        u.runs = open_groups ? 0u : (VEC ? runs >> (lane - l) & ((1u << (LPT & 31)) - 1u) : runs);
         if constexpr (VEC) {
 #pragma unroll
           for (int i = 0; i < ND; ++i) key[i] = kept ? key[i] : 0u;
@@ -558,33 +802,75 @@ __global__ void __launch_bounds__(kGateThreads, NV == 16 ? 3 : 4) gate_select_ke
         }
       }
       if constexpr (!(GROUPS && VEC)) sort_keys<NV>(key);
-      uint32_t prev = 0xffffffffu, gap = 0xffffffffu, end = 0;
-      int taken = 0;
+      uint32_t gap = 0xffffffffu, end = 0;  // the least distance of neighbours; the k-th
+      bool undecided = open_groups;
+      if constexpr (LPT < 32) {
+        // the lanes' sorted lists merged in pairs, 8 kept: of two falling lists, the larger of v[i] and w[7 - i] are the
+        // 8 largest, and fall and rise
+        static_assert(KMAX == 8, "lists of 8");
+        uint32_t v[8];
 #pragma unroll
-      for (int j = 0; j <= KMAX; ++j) {
-        if (j > k) break;
-        const uint32_t r = top_of(key[0]);
-        gap = min(gap, prev - r);
-        prev = r;
-        if (j < k) end = r;
-        if (key[0] == r) {
-          if (j < k && valid) s_slot[tl * k + j] = static_cast<uint16_t>(255u - (r & 255u));
-          if (NV > ND) ++taken;
+        for (int i = 0; i < 8; ++i) v[i] = i < ND ? key[i] : 0u;
 #pragma unroll
-          for (int i = 0; i + 1 < ND; ++i)
-            if (i < KMAX - j) key[i] = key[i + 1];  // (further back none is needed any more)
-          if (ND <= KMAX - j || ND == 1) key[ND - 1] = 0;
+        for (int o = 1; o < LPT; o <<= 1) {
+          uint32_t w[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = __shfl_xor_sync(0xffffffffu, v[i], o);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = max(v[i], w[7 - i]);
+#pragma unroll
+          for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if ((i & d) == 0) {
+                const uint32_t hi = max(v[i], v[i + d]), lo = min(v[i], v[i + d]);
+                v[i] = hi;
+                v[i + d] = lo;
+              }
+        }
+        uint32_t ninth = 0;
+        if (k == 8) {
+#pragma unroll
+          for (int i = 0; i < ND; ++i) ninth = max(ninth, key[i] < v[7] ? key[i] : 0u);
+          ninth = top_of(ninth);
+          // (a lane whose whole list is among the 8 may have one behind it that was not sorted)
+          if (NV > ND) undecided |= (__ballot_sync(0xffffffffu, key[ND - 1] == v[7]) >> (lane - l) & ((1u << LPT) - 1u)) != 0;
+        }
+        uint32_t got = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (j < k) {
+            gap = min(gap, v[j] - (j < 7 ? v[j + 1] : ninth));
+            end = v[j];
+          }
+          got = l == j ? v[j] : got;
+        }
+        if (l < k && valid) s_slot[tl * k + l] = static_cast<uint16_t>(255u - (got & 255u));
+      } else {
+        uint32_t prev = 0xffffffffu;
+#pragma unroll
+        for (int j = 0; j <= KMAX; ++j) {
+          if (j > k) break;
+          const uint32_t r = top_of(key[0]);
+          gap = min(gap, prev - r);
+          prev = r;
+          if (j < k) end = r;
+          if (key[0] == r) {
+            if (j < k && valid) s_slot[tl * k + j] = static_cast<uint16_t>(255u - (r & 255u));
+#pragma unroll
+            for (int i = 0; i + 1 < ND; ++i)
+              if (i < KMAX - j) key[i] = key[i + 1];  // (further back none is needed any more)
+            if (ND <= KMAX - j || ND == 1) key[ND - 1] = 0;
+          }
         }
       }
-      // two neighbours too near to tell, fewer than k that may be chosen, groups too near, or a lane
-      // whose sorted keys were used up
-      bool undecided = open_groups || gap < (kNear + 1) * 256u || (end >> 8) == 0;
-      if (NV > ND) undecided |= __any_sync(0xffffffffu, taken >= ND);
+      // two neighbours too near to tell, or fewer than k that may be chosen
+      undecided |= gap < (kNear + 1) * 256u || (end >> 8) == 0;
       if (undecided && l == 0 && valid) {
         const int q = static_cast<int>(end >> 8);
         u.least = q > 2 * kNear + 1 ? q - 2 * kNear : 0;
         s_und[tl] = u;
-        s_list[atomicAdd(&s_count, 1)] = static_cast<uint8_t>(tl);
+        s_list[atomicAdd(&s_count, 1)] = static_cast<uint16_t>(tl);
       }
     }
     __syncthreads();
@@ -592,9 +878,12 @@ __global__ void __launch_bounds__(kGateThreads, NV == 16 ? 3 : 4) gate_select_ke
     // ---- what is left to decide
     const int count = s_count;
     for (int i = warp; i < count; i += kWarps) {
-      const int tl = s_list[i];
-      resolve_token<KEY>(a, a.logits + static_cast<size_t>(t0 + tl) * E, s_bias, bi, s_und[tl], GROUPS ? (VEC ? NV : gs) : E,
-                         sh.val[warp], s_cand[warp], s_slot + tl * k);
+      const int tl = s_list[i], run = GROUPS ? (VEC ? NV : gs) : E;
+      const float *row = a.logits + static_cast<size_t>(t0 + tl) * E;
+      const bool done = resolve_fixed<KEY>(a, row, s_bias, bi, s_und[tl], run, reinterpret_cast<long long *>(sh.val[warp]),
+                                           s_cand[warp], s_slot + tl * k);
+      if (KEY != kKeyLogit && !done)
+        resolve_token<KEY>(a, row, s_bias, bi, s_und[tl], run, sh.val[warp], s_cand[warp], s_slot + tl * k);
     }
     __syncthreads();
     const int ntok = min(kGateTok, last - t0), words = (ntok + 31) / 32;
