@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(kGateThreads) gate_index_kernel(const GateArgs
   int before = 0, all = 0, n;
   const int here = tid < E && clusters ? __ldcg(a.before + static_cast<size_t>(blockIdx.x) * E + tid) : 0;
   if (tid < E) {
-    constexpr int kBatch = 8;  // 57 clusters over 8 blocks
+    constexpr int kBatch = 15;  // 114 clusters over 8 blocks
     for (int c = rank; c < clusters; c += a.cluster * kBatch) {
       int h[kBatch];
 #pragma unroll
@@ -110,11 +110,12 @@ __global__ void __launch_bounds__(kGateThreads) gate_index_kernel(const GateArgs
 //   sigmoid                 dl_j = w_j (1 - s_j) g_j
 // and zero for the others; softmax that is not renormalised gives every expert a gradient:
 //   dl_e = w_e g_e - p_e sum_i w_i g_i       (w_e = 0 for the others)
-// A slot of weight zero has none.  Bound by the gradient's bytes (and the dense kind's
-// logits): a block builds whole rows in shared memory and one bulk copy takes them out.
+// A slot of weight zero has none.  Bound by the gradient's bytes (and the dense kind's logits).  A warp has a
+// token: it writes the row without the chosen experts, then their elements over it, in lanes that hold a slot each;
+// the next token's inputs are on their way meanwhile.
 
 constexpr int kGradThreads = 256;
-constexpr int kGradBytes = 16 * 1024;  // rows of one buffer at most
+constexpr int kGradBlocksPerSm = 6;
 
 struct GradArgs {
   const float *logits;
@@ -122,140 +123,142 @@ struct GradArgs {
   const float *topk_w, *d_topk_w;
   float *d_logits;
   int T, E, k;
-  int rows;  // tokens per round, a multiple of 4
   bool sigmoid, renormalise;
   float scale;
 };
 
-__device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes)
-               : "memory");
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-
-template <bool DENSE>
-__global__ void __launch_bounds__(kGradThreads) gate_grad_kernel(const GradArgs a) {
-  extern __shared__ __align__(128) float s_rows[];  // [2][rows * E]
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int E = a.E, k = a.k, span = a.rows * E;
+// VEC: rows of whole 16-byte vectors.
+template <bool DENSE, bool VEC>
+__global__ void __launch_bounds__(kGradThreads, DENSE ? 4 : kGradBlocksPerSm) gate_grad_kernel(const GradArgs a) {
+  constexpr int NV = kMaxExperts / 32;
+  const int lane = threadIdx.x & 31, E = a.E, k = a.k;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kGradThreads / 32);
   griddep_wait();  // the previous kernel in the stream has completed
   griddep_launch_dependents();
-  int buf = 0;
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.rows; t0 < a.T; t0 += static_cast<int64_t>(gridDim.x) * a.rows) {
-    const int n = static_cast<int>(min(static_cast<int64_t>(a.rows), a.T - t0));
-    float *rows = s_rows + buf * span;
-    // the copy before the last has read this buffer
-    if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-    __syncthreads();
-    if constexpr (!DENSE) {
-      for (int i = tid * 4; i < span; i += kGradThreads * 4) *reinterpret_cast<float4 *>(rows + i) = make_float4(0, 0, 0, 0);
-      __syncthreads();
+  // a slot's expert (-1: none), weight and gradient, its logit, and the dense kind's row
+  struct Slot {
+    int e;
+    float w, g;
+  };
+  auto slot_of = [&](int64_t t) {
+    Slot s{-1, 0.f, 0.f};
+    if (t < a.T && lane < k) {
+      s.e = __ldg(a.topk_idx + t * k + lane);
+      s.w = __ldg(a.topk_w + t * k + lane);
+      s.g = __ldg(a.d_topk_w + t * k + lane);
+      if (s.e < 0 || s.e >= E || s.w == 0.f) s.e = -1;
     }
-    if constexpr (DENSE) {
-      for (int r = warp; r < n; r += kGradThreads / 32) {  // a warp per token
-        const int64_t t = t0 + r;
-        const float *lr = a.logits + t * E;
-        float wg = 0.f;
-        int e = -1;
-        if (lane < k) {
-          e = __ldg(a.topk_idx + t * k + lane);
-          if (e < 0 || e >= E) e = -1;
-          if (e >= 0) wg = __ldg(a.topk_w + t * k + lane) * __ldg(a.d_topk_w + t * k + lane);
-        }
-        float v[kMaxExperts / 32];
-        float top = -INFINITY, z = 0.f;
-        bool bad = false;
+    return s;
+  };
+  auto row_of = [&](int64_t t, float (&v)[NV]) {
+    const float *lr = a.logits + t * E;
+    if constexpr (VEC) {
 #pragma unroll
-        for (int i = 0; i < kMaxExperts / 32; ++i) {
-          const int c = lane + 32 * i;
-          v[i] = c < E ? clean_logit(__ldg(lr + c), bad) : -INFINITY;
-          top = fmaxf(top, v[i]);
-        }
-        top = warp_max(top);
-        const bool none = top == -INFINITY;
-#pragma unroll
-        for (int i = 0; i < kMaxExperts / 32; ++i) {
-          v[i] = none ? 0.f : expf(v[i] - top);
-          z += v[i];
-        }
-        const float dot = warp_sum(wg);
-        z = warp_sum(z);
-        const float f = none ? 0.f : -dot / z;
-#pragma unroll
-        for (int i = 0; i < kMaxExperts / 32; ++i)
-          if (lane + 32 * i < E) rows[r * E + lane + 32 * i] = v[i] * f;
-        __syncwarp();
-        if (e >= 0) rows[r * E + e] += wg;
+      for (int i = 0; i < NV; i += 4) {
+        const int c = 4 * lane + 32 * i;
+        const float4 q = t < a.T && c < E ? __ldg(reinterpret_cast<const float4 *>(lr + c))
+                                          : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
       }
     } else {
-      for (int r = tid; r < n; r += kGradThreads) {  // a thread per token
-        const int64_t at = (t0 + r) * k;
-        const float *lr = a.logits + (t0 + r) * E;
-        float w[kMaxTopK], g[kMaxTopK];
-        int e[kMaxTopK];
-        float dot = 0.f;
 #pragma unroll
-        for (int j = 0; j < kMaxTopK; ++j) {
-          if (j < k) {
-            e[j] = __ldg(a.topk_idx + at + j);
-            w[j] = __ldg(a.topk_w + at + j);
-            g[j] = __ldg(a.d_topk_w + at + j);
-            if (e[j] < 0 || e[j] >= E || w[j] == 0.f) e[j] = -1;
-            if (e[j] >= 0) dot = fmaf(w[j] / a.scale, g[j], dot);
-          }
-        }
+      for (int i = 0; i < NV; ++i) v[i] = t < a.T && lane + 32 * i < E ? __ldg(lr + lane + 32 * i) : -INFINITY;
+    }
+  };
+  int64_t t = static_cast<int64_t>(blockIdx.x) * (kGradThreads / 32) + (threadIdx.x >> 5);
+  Slot next = slot_of(t);
+  float ahead[DENSE ? NV : 1];
+  if constexpr (DENSE) row_of(t, ahead);
+  for (; t < a.T; t += step) {
+    const Slot s = next;
+    float *out = a.d_logits + t * E;
+    bool bad = false;
+    float l = s.e >= 0 ? clean_logit(__ldg(a.logits + t * E + s.e), bad) : 0.f;
+    float d;
+    if constexpr (DENSE) {
+      float v[NV];
 #pragma unroll
-        for (int j = 0; j < kMaxTopK; ++j) {
-          if (j < k && e[j] >= 0) {
-            float d = w[j] * (a.renormalise ? g[j] - dot : g[j]);
-            if (a.sigmoid) {  // 1 - s = 1 / (1 + e^l)
-              const float l = __ldg(lr + e[j]);
-              d *= 1.f / (1.f + expf(l));
-            }
-            rows[r * E + e[j]] = d;
-          }
-        }
+      for (int i = 0; i < NV; ++i) v[i] = clean_logit(ahead[i], bad);
+      next = slot_of(t + step);
+      row_of(t + step, ahead);
+      float top = -FLT_MAX, z = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) top = fmaxf(top, v[i]);
+      top = warp_max(top);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        v[i] = __expf(v[i] - top);
+        z += v[i];
       }
+      z = warp_sum(z);
+      const float own = s.e >= 0 ? s.w * s.g : 0.f;
+      const float f = z > 0.f ? -warp_sum(own) / z : 0.f;  // (z is the same in all lanes)
+      if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < NV; i += 4)
+          if (4 * lane + 32 * i < E)
+            *reinterpret_cast<float4 *>(out + 4 * lane + 32 * i) = make_float4(v[i] * f, v[i + 1] * f, v[i + 2] * f, v[i + 3] * f);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (lane + 32 * i < E) out[lane + 32 * i] = v[i] * f;
+      }
+      d = fmaf(__expf(l - top), f, own);
+    } else {
+      if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < NV; i += 4)
+          if (4 * lane + 32 * i < E) *reinterpret_cast<float4 *>(out + 4 * lane + 32 * i) = make_float4(0.f, 0.f, 0.f, 0.f);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (lane + 32 * i < E) out[lane + 32 * i] = 0.f;
+      }
+      next = slot_of(t + step);
+      float dot = 0.f;
+      if (a.renormalise) {
+        dot = s.e >= 0 ? s.w / a.scale * s.g : 0.f;
+#pragma unroll
+        for (int o = kMaxTopK / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      }
+      d = s.w * (s.g - dot);
+      if (a.sigmoid) d *= 1.f / (1.f + expf(l));  // 1 - s
     }
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncthreads();
-    // whole 16-byte vectors go out in one copy (t0 * E is a multiple of four); what is left of
-    // the tensor's end as single elements
-    const int len = n * E, whole = len & ~3;
-    float *dst = a.d_logits + t0 * E;
-    if (tid == 0) {
-      if (whole)
-        bulk_store(dst, rows, static_cast<uint32_t>(whole) * 4);
-      else
-        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-    }
-    if (tid < len - whole) dst[whole + tid] = rows[whole + tid];
-    buf ^= 1;
+    __syncwarp();  // the row's other writes come first
+    if (s.e >= 0) out[s.e] = d;
   }
-  if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // bias_e += rate * sign(mean load - load of e), the counts of all rows added up; compared as
 // whole numbers: sum_e' c_e' against E c_e.
+// Threads: the experts, times the parts of the rows.
 __global__ void __launch_bounds__(kBiasThreads) gate_bias_kernel(const int32_t *counts, int rows, int E, float rate,
-                                                                  float *bias) {
-  __shared__ unsigned long long s_load[kMaxExperts], s_all;
-  const int e = threadIdx.x % kMaxExperts, part = threadIdx.x / kMaxExperts;
-  if (threadIdx.x < kMaxExperts) s_load[threadIdx.x] = 0;
-  if (threadIdx.x == 0) s_all = 0;
-  __syncthreads();
+                                                                 float *bias) {
+  __shared__ long long s_load[kBiasThreads], s_all[kMaxExperts / 32];
+  const int e = threadIdx.x % kMaxExperts, part = threadIdx.x / kMaxExperts, parts = blockDim.x / kMaxExperts;
   griddep_wait();  // the previous kernel in the stream has completed
   griddep_launch_dependents();
   long long c = 0;
   if (e < E)
-    for (int r = part; r < rows; r += (kBiasThreads / kMaxExperts)) c += __ldg(counts + static_cast<size_t>(r) * E + e);
-  atomicAdd(&s_load[e], static_cast<unsigned long long>(c));
-  atomicAdd(&s_all, static_cast<unsigned long long>(c));
+    for (int r = part; r < rows; r += parts) c += __ldg(counts + static_cast<size_t>(r) * E + e);
+  const float was = e < E ? bias[e] : 0.f;
+  s_load[threadIdx.x] = c;
   __syncthreads();
-  if (threadIdx.x >= E) return;
-  const long long d = static_cast<long long>(s_all) - static_cast<long long>(s_load[e]) * E;
-  if (d != 0) bias[e] += d > 0 ? rate : -rate;
+  if (part > 0) return;
+  for (int p = 1; p < parts; ++p) c += s_load[p * kMaxExperts + e];
+  long long all = c;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+  if ((e & 31) == 0) s_all[e >> 5] = all;
+  asm volatile("bar.sync 1, 256;" ::: "memory");  // (the first kMaxExperts threads)
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < kMaxExperts / 32; ++w) all += s_all[w];
+  if (e >= E) return;
+  const long long d = all - c * E;
+  if (d != 0) bias[e] = was + (d > 0 ? rate : -rate);
 }
+static_assert(kMaxExperts == 256, "the barrier's threads");
 
 // ---------------------------------------------------------------- host side
 
@@ -271,9 +274,11 @@ bool gate_ok(const moe_gate_config *c) {
   return c->scale > 0.f && c->scale <= FLT_MAX;  // (not where it is NaN)
 }
 
-// Chunks: 32 tokens each while that makes at most three blocks for each of 152 SMs, then more each; up to
-// 64 tokens for each of one cluster's blocks are one launch.
-constexpr int kLeastTok = 32, kMostChunks = 456;
+// Chunks: 32 tokens each while that makes at most six blocks for each of 152 SMs, then more each (four of them fit
+// at once: the others follow as those end, which evens out the blocks with undecided tokens.  131072 x 256 in
+// 456, 608, 912, 1216 and 1824 chunks: 107, 98, 98, 95 and 110 us); up to 64 tokens for each of one cluster's
+// blocks are one launch.
+constexpr int kLeastTok = 32, kMostChunks = 912;
 struct GateLayout {
   int chunks, cluster;
   size_t flags, before, total, bytes;
@@ -386,16 +391,13 @@ moe_status moe_gate_backward(const moe_gate_config *cfg, const float *logits, co
   a.sigmoid = cfg->score == MOE_SCORE_SIGMOID;
   a.renormalise = cfg->renormalise != 0;
   a.scale = cfg->scale;
-  const int most = kGradBytes / (4 * a.E) / 4 * 4;  // at least 16
-  const int even = static_cast<int>((static_cast<int64_t>(a.T) + 4 * di.sms - 1) / (4 * di.sms) + 3) / 4 * 4;
-  a.rows = even < most ? even : most;
-  const int64_t rounds = (static_cast<int64_t>(a.T) + a.rows - 1) / a.rows;
-  const int blocks = static_cast<int>(rounds < 6 * di.sms ? rounds : 6 * di.sms);
-  const size_t smem = 2 * static_cast<size_t>(a.rows) * a.E * 4;
-  const bool dense = !a.sigmoid && !a.renormalise;
+  const bool dense = !a.sigmoid && !a.renormalise, vec = a.E % 4 == 0;
+  const int64_t wanted = (static_cast<int64_t>(a.T) + kGradThreads / 32 - 1) / (kGradThreads / 32);
+  const int most = kGradBlocksPerSm * di.sms, blocks = static_cast<int>(wanted < most ? wanted : most);
   return timed("gate_backward", s, [&] {
-    return dense ? launch_pdl(gate_grad_kernel<true>, dim3(blocks), dim3(kGradThreads), smem, s, 1, a)
-                 : launch_pdl(gate_grad_kernel<false>, dim3(blocks), dim3(kGradThreads), smem, s, 1, a);
+    auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(blocks), dim3(kGradThreads), 0, s, 1, a); };
+    if (dense) return vec ? go(gate_grad_kernel<true, true>) : go(gate_grad_kernel<true, false>);
+    return vec ? go(gate_grad_kernel<false, true>) : go(gate_grad_kernel<false, false>);
   });
 }
 
@@ -409,7 +411,7 @@ moe_status moe_gate_update_bias(const moe_gate_config *cfg, float *bias, const i
   if (rows == 0) return MOE_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return timed("gate_bias", s, [&] {
-    return launch_pdl(gate_bias_kernel, dim3(1), dim3(kBiasThreads), 0, s, 1, counts, static_cast<int>(rows),
+    return launch_pdl(gate_bias_kernel, dim3(1), dim3(rows < 4 ? kMaxExperts : kBiasThreads), 0, s, 1, counts, static_cast<int>(rows),
                       static_cast<int>(cfg->E), rate, bias);
   });
 }

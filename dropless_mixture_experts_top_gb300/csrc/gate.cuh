@@ -380,28 +380,48 @@ __device__ __noinline__ bool resolve_fixed(const GateArgs &a, const float *row, 
     }
   }
   __syncwarp();
-  // k times the best of what is left; lane j keeps the j-th
+  // lane j keeps the j-th of the order
   const int found = min(n, a.k);
   const long long tie = biased && KEY != kKeyLogit ? near : 0;  // (logits alone decide exactly)
-  long long mine = 0, end = 0;
+  long long mine = least, end = least;
   int at_mine = 0;
-  for (int j = 0; j < found; ++j) {
-    long long best = least;
-    int at = INT_MAX;
-    for (int i = lane; i < n; i += 32) {
-      const long long v = val[i];
-      if (v > best) best = v, at = i;
+  if (n <= 32) {  // every lane counts those in front of its own
+    const long long v = lane < n ? val[lane] : least;
+    int before = 0;
+    for (int o = 0; o < n; ++o) {
+      const long long other = __shfl_sync(0xffffffffu, v, o);
+      before += other > v || (other == v && o < lane) ? 1 : 0;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const long long ov = __shfl_xor_sync(0xffffffffu, best, o);
-      const int oa = __shfl_xor_sync(0xffffffffu, at, o);
-      if (ov > best || (ov == best && oa < at)) best = ov, at = oa;
-    }
-    if (lane == j) mine = best, at_mine = at;
-    end = best;
-    if ((at & 31) == lane) val[at] = least;
     __syncwarp();
+    if (lane < n) val[before] = (v << 8) | lane;  // (numbers below 2^54)
+    __syncwarp();
+    if (lane < n) {
+      mine = val[lane] >> 8;
+      at_mine = static_cast<int>(val[lane] & 0xff);
+    }
+    end = __shfl_sync(0xffffffffu, mine, max(0, found - 1));
+    __syncwarp();
+    if (lane < n) val[at_mine] = lane < found ? least : mine;
+    __syncwarp();
+  } else {  // k times the best of what is left
+    for (int j = 0; j < found; ++j) {
+      long long best = least;
+      int at = INT_MAX;
+      for (int i = lane; i < n; i += 32) {
+        const long long v = val[i];
+        if (v > best) best = v, at = i;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const long long ov = __shfl_xor_sync(0xffffffffu, best, o);
+        const int oa = __shfl_xor_sync(0xffffffffu, at, o);
+        if (ov > best || (ov == best && oa < at)) best = ov, at = oa;
+      }
+      if (lane == j) mine = best, at_mine = at;
+      end = best;
+      if ((at & 31) == lane) val[at] = least;
+      __syncwarp();
+    }
   }
   bool open = false;
   if (tie > 0) {
@@ -544,7 +564,7 @@ __device__ __noinline__ void resolve_token(const GateArgs &a, const float *row, 
 // LPT lanes per token, NV experts per lane: with l the lane's place among the token's, e = l + LPT i, or NV l + i
 // (VEC; E = LPT NV).  KMAX: k at most.
 template <int LPT, int NV, bool VEC, int KEY, bool GROUPS, int KMAX>
-__global__ void __launch_bounds__(kGateThreads, NV == 16 ? 3 : 4) gate_select_kernel(const GateArgs a) {
+__global__ void __launch_bounds__(kGateThreads, 4) gate_select_kernel(const GateArgs a) {
   constexpr int kNear = KEY == kKeyLogit ? 0 : (KEY == kKeySigmoid ? kNearSigmoid : kNearSoftmax);
   constexpr bool KEYS = GROUPS && !VEC;                  // groups by way of shared memory
   static_assert(!KEYS || LPT == 32, "a lane per group");
