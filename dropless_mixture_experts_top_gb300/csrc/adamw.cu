@@ -12,10 +12,11 @@
 // positive root is never rounded to zero, since a zero under a nonzero m would make
 // an update as large as m / eps.
 //
-// Bound by memory: fp32 states with bf16 gradients and copies move 28 bytes per element, 8-bit
-// ones 16.  A warp takes 256 elements (a block of the states) in 16-byte accesses of
-// whole lines and reduces the block's largest by redux; with 32 warps an SM holds 115
-// (64) KB of loads in flight, enough for HBM without staging.  The tensors' addresses
+// Bound by memory: fp32 states with bf16 gradients and copies move 28 bytes per element (302 million elements: 1277 us, 99%
+// of what a copy moves in that time), 8-bit ones 16 (788 us, 92%).  A warp takes 256 elements (a block of the states)
+// in accesses of whole lines and reduces the block's largest by redux; with 8-bit states it has the next 256 under way
+// meanwhile (without that, and with checks and choices for every element, it was bound by its instructions: 1260 us).
+// The tensors' addresses
 // travel in the launch's parameters: no table on the device, nothing to copy.
 //
 // The number of steps is device memory, so that a captured step counts on: every
@@ -23,6 +24,8 @@
 #include <cuda_fp16.h>
 #include <float.h>
 #include <math.h>
+
+#include <type_traits>
 
 #include "abi.h"
 #include "common.cuh"
@@ -32,7 +35,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBlocksPerSm = 4;
+// Blocks per SM, by the states' bits.  Measured, 302 million elements: 32 bits 2, 3 and 4 blocks 1277, 1297 and 1347 us (4
+// spill); 8 bits 2, 3 and 4 blocks 840, 788 and 945 us.
+constexpr int kBlocks32 = 2, kBlocks8 = 3;
 constexpr int kBlock = 256;       // elements of a warp's unit, which share a scale
 constexpr int kPerLaunch = 64;    // tensors of one launch (its parameters stay below 4 KB)
 constexpr float kTiny = 1e-30f;   // the least largest value of a block that a scale is made for
@@ -61,105 +66,181 @@ struct StepArgs {
 };
 static_assert(sizeof(StepArgs) <= 4096, "the launch's parameters");
 
-// Eight elements of a lane: four from `at`, four from at + 128, of which `left` are in the tensor.
+// A lane's eight elements of a unit: four from 4 lane on, four from 4 lane + 128; `left`: how many of each four the
+// tensor has.  As they come from memory (El: float, uint16_t bf16 bits, uint8_t e4m3 codes):
 template <class El>
-__device__ __forceinline__ void load4(const El *src, int left, float *f) {
-  if (left >= 4) {
+struct Eight {
+  static constexpr int W = static_cast<int>(sizeof(El));  // words of four elements
+  uint32_t r[2 * W];
+  __device__ __forceinline__ void load(const El *src, const int (&left)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const El *s = src + 128 * h;
+      if (left[h] == 4) {
+        if constexpr (W == 4) {
+          const uint4 q = __ldcs(reinterpret_cast<const uint4 *>(s));
+          r[4 * h] = q.x, r[4 * h + 1] = q.y, r[4 * h + 2] = q.z, r[4 * h + 3] = q.w;
+        } else if constexpr (W == 2) {
+          const uint2 q = __ldcs(reinterpret_cast<const uint2 *>(s));
+          r[2 * h] = q.x, r[2 * h + 1] = q.y;
+        } else {
+          r[h] = __ldcs(reinterpret_cast<const uint32_t *>(s));
+        }
+      } else {
+#pragma unroll
+        for (int w = 0; w < W; ++w) r[W * h + w] = 0;
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          if (i < left[h]) {
+            if constexpr (W == 4)
+              r[4 * h + i] = __float_as_uint(s[i]);
+            else
+              r[W * h + i * W / 4] |= static_cast<uint32_t>(s[i]) << (8 * W * i % 32);
+          }
+      }
+    }
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if constexpr (W == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[4 * h + i] = __uint_as_float(r[4 * h + i]);
+      } else if constexpr (W == 2) {
+        f[4 * h] = bf16_lo(r[2 * h]), f[4 * h + 1] = bf16_hi(r[2 * h]);
+        f[4 * h + 2] = bf16_lo(r[2 * h + 1]), f[4 * h + 3] = bf16_hi(r[2 * h + 1]);
+      } else {
+        uint32_t lo, hi;
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+            : "=r"(lo), "=r"(hi)
+            : "r"(r[h]));
+        const float2 a = __half22float2(*reinterpret_cast<__half2 *>(&lo)), b = __half22float2(*reinterpret_cast<__half2 *>(&hi));
+        f[4 * h] = a.x, f[4 * h + 1] = a.y, f[4 * h + 2] = b.x, f[4 * h + 3] = b.y;
+      }
+    }
+  }
+};
+template <class El>
+__device__ __forceinline__ void store_eight(El *dst, const int (&left)[2], const float (&f)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    El *d = dst + 128 * h;
+    const float *v = f + 4 * h;
     if constexpr (sizeof(El) == 4) {
-      const float4 q = __ldcs(reinterpret_cast<const float4 *>(src));
-      f[0] = q.x, f[1] = q.y, f[2] = q.z, f[3] = q.w;
+      if (left[h] == 4) {
+        __stcs(reinterpret_cast<float4 *>(d), make_float4(v[0], v[1], v[2], v[3]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          if (i < left[h]) d[i] = v[i];
+      }
+    } else if constexpr (sizeof(El) == 2) {
+      const uint32_t lo = pack_bf16x2(v[0], v[1]), hi = pack_bf16x2(v[2], v[3]);
+      if (left[h] == 4) {
+        __stcs(reinterpret_cast<uint2 *>(d), make_uint2(lo, hi));
+      } else {
+        if (left[h] > 0) d[0] = static_cast<uint16_t>(lo);
+        if (left[h] > 1) d[1] = static_cast<uint16_t>(lo >> 16);
+        if (left[h] > 2) d[2] = static_cast<uint16_t>(hi);
+      }
     } else {
-      const uint2 q = __ldcs(reinterpret_cast<const uint2 *>(src));
-      f[0] = bf16_lo(q.x), f[1] = bf16_hi(q.x), f[2] = bf16_lo(q.y), f[3] = bf16_hi(q.y);
-    }
-  } else {
+      uint32_t c;
+      asm("{\n\t.reg .b16 a, b;\n\t"
+          "cvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
+          "mov.b32 %0, {a, b};\n\t}"
+          : "=r"(c)
+          : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]));
+      if (left[h] == 4) {
+        __stcs(reinterpret_cast<uint32_t *>(d), c);
+      } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[i] = 0.f;
-      if (i < left) {
-        if constexpr (sizeof(El) == 4)
-          f[i] = src[i];
-        else
-          f[i] = __uint_as_float(static_cast<uint32_t>(src[i]) << 16);
+        for (int i = 0; i < 3; ++i)
+          if (i < left[h]) d[i] = static_cast<uint8_t>(c >> (8 * i));
       }
     }
   }
 }
-template <class El>
-__device__ __forceinline__ void store4(El *dst, int left, const float *f) {
-  if (left >= 4) {
-    if constexpr (sizeof(El) == 4)
-      __stcs(reinterpret_cast<float4 *>(dst), make_float4(f[0], f[1], f[2], f[3]));
-    else
-      __stcs(reinterpret_cast<uint2 *>(dst), make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < left) {
-        if constexpr (sizeof(El) == 4)
-          dst[i] = f[i];
-        else
-          dst[i] = __bfloat16_as_ushort(__float2bfloat16_rn(f[i]));
-      }
-  }
+
+__device__ __forceinline__ float sqrt_fast(float x) {
+  float y;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// Four e4m3 codes in a word.
-__device__ __forceinline__ void decode4(uint32_t c, float *f) {
-  uint32_t lo, hi;
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(c));
-  const float2 a = __half22float2(*reinterpret_cast<__half2 *>(&lo)), b = __half22float2(*reinterpret_cast<__half2 *>(&hi));
-  f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
-}
-__device__ __forceinline__ uint32_t encode4(const float *f) {
-  uint32_t c;
-  asm("{\n\t.reg .b16 a, b;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
-      "mov.b32 %0, {a, b};\n\t}"
-      : "=r"(c)
-      : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]));
-  return c;
-}
-__device__ __forceinline__ void load_codes(const uint8_t *src, int left, float *f) {
-  uint32_t c = 0;
-  if (left >= 4) {
-    c = __ldcs(reinterpret_cast<const uint32_t *>(src));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-      if (i < left) c |= static_cast<uint32_t>(src[i]) << (8 * i);
-  }
-  decode4(c, f);
-}
-__device__ __forceinline__ void store_codes(uint8_t *dst, int left, const float *f) {
-  const uint32_t c = encode4(f);
-  if (left >= 4) {
-    __stcs(reinterpret_cast<uint32_t *>(dst), c);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-      if (i < left) dst[i] = static_cast<uint8_t>(c >> (8 * i));
-  }
-}
-
-// The largest finite |x| of the warp's 256, at least kTiny.
-__device__ __forceinline__ float block_most(const float (&x)[8]) {
+// The largest |x| of the warp's 256, at least kTiny (what is not finite left out, where `odd` says that there is some).
+__device__ __forceinline__ float block_most(const float (&x)[8], bool odd) {
   float m = kTiny;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = fabsf(x[i]) <= FLT_MAX ? fmaxf(m, fabsf(x[i])) : m;
+  for (int i = 0; i < 8; ++i) m = odd && !(fabsf(x[i]) <= FLT_MAX) ? m : fmaxf(m, fabsf(x[i]));
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
 }
 
-// Products and sums are rounded one by one (no fused multiply-add) where they enter the 8-bit
-// codes, so that a code is the same wherever the formula is written out in fp32.
+// Where the u-th unit of a launch lies.
+struct Place {
+  int64_t x0, s0;  // the lane's first element in the tensor, in the states
+  int have;        // elements of the unit in the tensor
+  __device__ __forceinline__ Place(const Entry &e, int64_t u, int lane) {
+    x0 = (u - e.first) * kBlock;
+    const int64_t n = e.n - x0;
+    have = n >= kBlock ? kBlock : static_cast<int>(n);
+    s0 = e.unit * kBlock + x0 + lane * 4;
+    x0 += lane * 4;
+  }
+};
+// f(left) with what the lane has of a unit: constants for a whole one.
+template <class F>
+__device__ __forceinline__ void with_left(int have, int lane, F &&f) {
+  if (have == kBlock) {
+    const int left[2] = {4, 4};
+    f(left);
+  } else {
+    const int left[2] = {max(0, min(4, have - 4 * lane)), max(0, min(4, have - 128 - 4 * lane))};
+    f(left);
+  }
+}
+
+// A unit as it comes from memory.
 template <class P, class G, bool EIGHT>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) adamw_kernel(const __grid_constant__ StepArgs a) {
+struct Unit {
+  using S = typename std::conditional<EIGHT, uint8_t, float>::type;
+  Eight<P> p;
+  Eight<G> g;
+  Eight<S> m, v;
+  float sm, sv;
+  int at;  // its tensor
+  __device__ __forceinline__ void load(const StepArgs &a, int64_t u, int lane) {
+    if (u >= a.units) return;
+    while (at + 1 < a.tensors && u >= a.e[at + 1].first) ++at;
+    const Entry &e = a.e[at];
+    const Place l(e, u, lane);
+    with_left(l.have, lane, [&](const int(&left)[2]) {
+      p.load(static_cast<const P *>(e.p) + l.x0, left);
+      g.load(static_cast<const G *>(e.g) + l.x0, left);
+      m.load(static_cast<const S *>(a.m) + l.s0, left);
+      v.load(static_cast<const S *>(a.v) + l.s0, left);
+    });
+    if constexpr (EIGHT) {
+      sm = __ldg(a.m_scale + l.s0 / kBlock);
+      sv = __ldg(a.v_scale + l.s0 / kBlock);
+    }
+  }
+};
+
+// Products and sums are rounded one by one (no fused multiply-add), and the root is the exact one, where they enter the
+// 8-bit codes: a code is then the same wherever the formula is written out in fp32, as in a run that goes on from a
+// checkpoint elsewhere.
+template <class P, class G, bool EIGHT>
+__global__ void __launch_bounds__(kThreads, EIGHT ? kBlocks8 : kBlocks32) adamw_kernel(const __grid_constant__ StepArgs a) {
+  using U = Unit<P, G, EIGHT>;
   griddep_wait();  // the previous kernel in the stream has completed
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
+  int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  U next;
+  next.at = 0;
+  if (EIGHT) next.load(a, u, lane);
   const int steps = __ldcg(a.step + 1) + 1;
   const float lr = a.lr_dev ? __ldg(a.lr_dev) : a.lr;
   const float gs = a.scale ? __ldg(a.scale) : 1.f;
@@ -168,85 +249,74 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) adamw_kernel(const __g
   const float corr1 = -expm1f(static_cast<float>(steps) * a.log_b1), corr2 = -expm1f(static_cast<float>(steps) * a.log_b2);
   const float rate = lr / corr1, root = rsqrtf(corr2);
   bool bad = skip;
-  int at = 0;
-  if (!skip) {
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp; u < a.units; u += static_cast<int64_t>(gridDim.x) * kWarps) {
-      while (at + 1 < a.tensors && u >= a.e[at + 1].first) ++at;
-      const Entry &e = a.e[at];
-      const int64_t x0 = (u - e.first) * kBlock + lane * 4;  // the lane's first element in the tensor
-      const int64_t s0 = (e.unit + (u - e.first)) * kBlock + lane * 4;
-      P *p = static_cast<P *>(e.p) + x0;
-      const G *g = static_cast<const G *>(e.g) + x0;
-      float pv[8], gv[8], mv[8], vv[8];
-      int left[2];
+  auto advance = [&](const U &x, int64_t u) {
+    using S = typename U::S;
+    const Entry &e = a.e[x.at];
+    float pv[8], gv[8], mv[8], vv[8], r[8];
+    x.p.get(pv);
+    x.g.get(gv);
+    x.m.get(mv);
+    x.v.get(vv);
+    const float keep = 1.f - lr * e.decay;
+    float fin = 0.f;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t n = e.n - x0 - 128 * h;
-        left[h] = n >= 4 ? 4 : (n > 0 ? static_cast<int>(n) : 0);
-      }
-      float sm = 0.f, sv = 0.f;
+    for (int i = 0; i < 8; ++i) {
       if constexpr (EIGHT) {
-        sm = __ldg(a.m_scale + s0 / kBlock);
-        sv = __ldg(a.v_scale + s0 / kBlock);
+        mv[i] = __fmul_rn(mv[i], x.sm);
+        vv[i] = __fmul_rn(vv[i], x.sv);
+        vv[i] = __fmul_rn(vv[i], vv[i]);
       }
+      const float gr = __fmul_rn(gv[i], gs);
+      mv[i] = __fadd_rn(__fmul_rn(a.b1, mv[i]), __fmul_rn(a.c1, gr));
+      vv[i] = __fadd_rn(__fmul_rn(a.b2, vv[i]), __fmul_rn(a.c2, __fmul_rn(gr, gr)));
+      const float root_v = EIGHT ? __fsqrt_rn(vv[i]) : sqrt_fast(vv[i]);
+      if (EIGHT) r[i] = root_v;
+      pv[i] = fmaf(pv[i], keep, -__fdividef(rate * mv[i], fmaf(root_v, root, a.eps)));
+      fin = fmaf(vv[i], 0.f, fmaf(pv[i], 0.f, fin));  // NaN where one is not finite
+    }
+    const Place l(e, u, lane);
+    bool odd = fin != 0.f;
+    if (odd) {  // (elements past a tensor's end are zeros, of which eps = 0 makes NaN)
+      odd = false;
+      with_left(l.have, lane, [&](const int(&left)[2]) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        load4(p + 128 * h, left[h], pv + 4 * h);
-        load4(g + 128 * h, left[h], gv + 4 * h);
-        if constexpr (EIGHT) {
-          load_codes(static_cast<const uint8_t *>(a.m) + s0 + 128 * h, left[h], mv + 4 * h);
-          load_codes(static_cast<const uint8_t *>(a.v) + s0 + 128 * h, left[h], vv + 4 * h);
-        } else {
-          load4(static_cast<const float *>(a.m) + s0 + 128 * h, left[h], mv + 4 * h);
-          load4(static_cast<const float *>(a.v) + s0 + 128 * h, left[h], vv + 4 * h);
-        }
+        for (int i = 0; i < 8; ++i) odd |= (i & 3) < left[i >> 2] && !(fabsf(pv[i]) <= FLT_MAX && vv[i] <= FLT_MAX);
+      });
+      bad |= odd;
+    }
+    if constexpr (EIGHT) {
+      odd = __any_sync(0xffffffffu, odd);
+      const float most_m = block_most(mv, odd), most_r = block_most(r, odd);
+      const float im = __fmul_rn(__frcp_rn(most_m), kCodeMax), ir = __fmul_rn(__frcp_rn(most_r), kCodeMax);
+      if (lane == 0) {
+        a.m_scale[l.s0 / kBlock] = __fmul_rn(most_m, 1.f / kCodeMax);
+        a.v_scale[l.s0 / kBlock] = __fmul_rn(most_r, 1.f / kCodeMax);
       }
-      const float keep = 1.f - lr * e.decay;
-      float r[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if constexpr (EIGHT) {
-          mv[i] = __fmul_rn(mv[i], sm);
-          vv[i] = __fmul_rn(vv[i], sv);
-          vv[i] = __fmul_rn(vv[i], vv[i]);
-        }
-        const float gr = __fmul_rn(gv[i], gs);
-        mv[i] = __fadd_rn(__fmul_rn(a.b1, mv[i]), __fmul_rn(a.c1, gr));
-        vv[i] = __fadd_rn(__fmul_rn(a.b2, vv[i]), __fmul_rn(a.c2, __fmul_rn(gr, gr)));
-        r[i] = __fsqrt_rn(vv[i]);
-        pv[i] = fmaf(pv[i], keep, -__fdividef(rate * mv[i], fmaf(r[i], root, a.eps)));
-        bad |= (i & 3) < left[i >> 2] && !(fabsf(pv[i]) <= FLT_MAX && vv[i] <= FLT_MAX);
+        const bool fine = !odd || (fabsf(pv[i]) <= FLT_MAX && vv[i] <= FLT_MAX);  // else e4m3's NaN
+        mv[i] = fine ? mv[i] * im : NAN;
+        vv[i] = r[i] > 0.f ? fmaxf(r[i] * ir, kCodeLeast) : 0.f;
+        vv[i] = fine ? vv[i] : NAN;
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        store4(p + 128 * h, left[h], pv + 4 * h);
-        if constexpr (sizeof(P) == 4)
-          if (e.copy) store4(e.copy + x0 + 128 * h, left[h], pv + 4 * h);
-      }
-      if constexpr (EIGHT) {
-        const float most_m = block_most(mv), most_r = block_most(r);
-        const float im = __fdiv_rn(kCodeMax, most_m), ir = __fdiv_rn(kCodeMax, most_r);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {  // (what is not finite becomes e4m3's NaN)
-          mv[i] = fabsf(mv[i]) <= FLT_MAX ? __fmul_rn(mv[i], im) : NAN;
-          const float q = r[i] <= FLT_MAX ? __fmul_rn(r[i], ir) : NAN;
-          r[i] = r[i] > 0.f && q < kCodeLeast ? kCodeLeast : q;
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          store_codes(static_cast<uint8_t *>(a.m) + s0 + 128 * h, left[h], mv + 4 * h);
-          store_codes(static_cast<uint8_t *>(a.v) + s0 + 128 * h, left[h], r + 4 * h);
-        }
-        if (lane == 0) {
-          a.m_scale[s0 / kBlock] = __fmul_rn(most_m, 1.f / kCodeMax);
-          a.v_scale[s0 / kBlock] = __fmul_rn(most_r, 1.f / kCodeMax);
-        }
+    }
+    with_left(l.have, lane, [&](const int(&left)[2]) {
+      store_eight(static_cast<P *>(e.p) + l.x0, left, pv);
+      if constexpr (sizeof(P) == 4)
+        if (e.copy) store_eight(e.copy + l.x0, left, pv);
+      store_eight(static_cast<S *>(a.m) + l.s0, left, mv);
+      store_eight(static_cast<S *>(a.v) + l.s0, left, vv);
+    });
+  };
+  if (!skip) {
+    for (; u < a.units; u += step) {
+      if constexpr (EIGHT) {  // the next unit's loads are under way meanwhile
+        const U x = next;
+        next.load(a, u + step, lane);
+        advance(x, u);
       } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          store4(static_cast<float *>(a.m) + s0 + 128 * h, left[h], mv + 4 * h);
-          store4(static_cast<float *>(a.v) + s0 + 128 * h, left[h], vv + 4 * h);
-        }
+        next.load(a, u, lane);
+        advance(next, u);
       }
     }
   }
@@ -364,7 +434,7 @@ moe_status moe_adamw_step(const moe_adamw_config *cfg, const int64_t *n, const d
       unit += u;
     }
     a.last = i == cfg->tensors;
-    const int64_t wanted = (a.units + kWarps - 1) / kWarps, most = static_cast<int64_t>(di.sms) * kBlocksPerSm;
+    const int64_t wanted = (a.units + kWarps - 1) / kWarps, most = static_cast<int64_t>(di.sms) * (eight ? kBlocks8 : kBlocks32);
     const int blocks = static_cast<int>(wanted < 1 ? 1 : (wanted < most ? wanted : most));
     const bool p32 = cfg->param_dtype == MOE_DTYPE_FP32, g32 = cfg->grad_dtype == MOE_DTYPE_FP32;
     MOE_TRY(timed("adamw_step", s, [&] {

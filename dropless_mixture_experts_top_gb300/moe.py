@@ -643,9 +643,9 @@ class AdamW:
                         _addr(state["v_scale"], "v_scale", self._blocks, _F32, d) if eight else None,
                         _addr(state["step"], "step", _STEP, _I32, d))
         rc = self._step(
-            self._cfg, self._n, self._decay, self._array(*[_addr(p, "params", s, pt, d) for p, s in zip(params, shapes)]),
-            self._array(*[_addr(g, "grads", s, gt, d) for g, s in zip(grads, shapes)]),
-            None if copies is None else self._array(*[_addr(c, "copies", s, _BF16, d) for c, s in zip(copies, shapes)]),
+            self._cfg, self._n, self._decay, self._array(*_addrs(params, "params", shapes, pt, d)),
+            self._array(*_addrs(grads, "grads", shapes, gt, d)),
+            None if copies is None else self._array(*_addrs(copies, "copies", shapes, _BF16, d)),
             ctypes.byref(st), 0.0 if on_device else lr, _one(lr, "lr", d) if on_device else None,
             _one(grad_scale, "grad_scale", d), _raw_stream(stream, d))
         if rc:
@@ -657,6 +657,12 @@ class AdamW:
 
 
 _E4M3, _STEP = (torch.float8_e4m3fn,), torch.Size((4,))
+
+
+def _addrs(ts, name, shapes, dtypes, dev):
+    """_addr of each (in one loop: a step over many tensors is made of these checks)."""
+    return [t.data_ptr() if t is not None and t.dtype in dtypes and t.shape == s and t.is_contiguous()
+            and t.get_device() == dev else _addr(t, name, s, dtypes, dev) for t, s in zip(ts, shapes)]
 
 
 def _one(t, name, dev):

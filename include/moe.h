@@ -439,8 +439,8 @@ moe_status moe_gate_update_bias(const moe_gate_config *cfg, float *bias, const i
  * (moe_adamw_state_elements gives the elements of an array; the padding is not touched):
  *   state_bits 32: m, v fp32;
  *   state_bits 8: m and the root of v as e4m3 codes, m_scale and v_scale fp32, one per 256 elements: a value
- *   is its code's times the scale, which is the block's largest (1e-30 at least) / 448; rounded to
- *   nearest even, a root above zero to 2^-9 of the scale at least.  This step uses m and v from before the rounding.
+ *   is its code's times the scale, which is the block's largest (1e-30 at least) times 1/448; the code is the
+ *   value times 448 times the reciprocal of that largest, rounded to nearest even, a root above zero to 2^-9 of the scale at least.  This step uses m and v from before the rounding.
  *   step: int32 [4]: the status word, the number of steps so far, and two words that are zero between
  *   calls.  A call adds one to the steps.
  * All of it starts as zeros.  A step after which a parameter or v is not finite sets MOE_DEV_NONFINITE_UPDATE
