@@ -46,7 +46,7 @@ constexpr int kGemmThreads = 64 + 32 * kEpiWarps;
 constexpr int kGemmSmem = kStages * kStageBytes + 256 + 1024 /*align*/;
 static_assert(kGemmSmem <= 227 * 1024, "shared memory budget");
 constexpr int kRuleSms = 152;         // the workspace's size is known without a GPU
-constexpr int kMaxSplit = 8;
+constexpr int kMaxSplit = 16;
 constexpr int kLeastStages = 4;       // of a part of a split reduction
 
 enum Product : int { kFwd = 0, kDx = 1, kDw = 2 };
@@ -63,7 +63,7 @@ struct ProductArgs {
   int full;       // tiles that are computed whole; the others in `split` parts
   int split;
   int units;      // tiles and parts in all
-  float *part;    // [parts][tile][tile]
+  float *part;    // the parts' sums (part_at)
   Ends e;
   int32_t *status;
   bool first;     // of the call's kernels: clears the status word
@@ -92,6 +92,14 @@ __device__ __forceinline__ Unit unit_of(int u, const ProductArgs &p, int nstage)
   t.m0 = mt * TS;
   t.n0 = (tile - mt * p.nn) * TS;
   return t;
+}
+
+// Where a lane's sums of 32 rows x 32 columns of a part lie (row: the lane): eight times four columns, 128 floats apart, so
+// that the lanes' 16 bytes are side by side.
+template <int CG>
+__device__ __forceinline__ int64_t part_at(int part, int row0, int col0) {
+  constexpr int TS = tile_size(CG);
+  return (static_cast<int64_t>(part) * (TS / 32) + row0 / 32) * TS * 32 + col0 * 32 + (threadIdx.x & 31) * 4;
 }
 
 // A lane's 32 columns of a row (64 bytes, eight columns a piece), of which ncols (a multiple of
@@ -243,7 +251,8 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t s, int j, bool mn) {
 
 template <int KIND, int CG>
 __global__ void __launch_bounds__(kGemmThreads, 1)
-    linear_product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const ProductArgs p) {
+    linear_product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
+                          const __grid_constant__ CUtensorMap tmB, const ProductArgs p) {
   constexpr int TS = tile_size(CG);
   constexpr uint32_t kTmemCols = 2 * TS;
   constexpr bool AMN = KIND == kDw, BMN = KIND != kDx;
@@ -277,6 +286,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmA);
+    if (!AMN) tma_prefetch_desc(&tmA32);
     tma_prefetch_desc(&tmB);
   }
   if (warp == 1) {
@@ -303,18 +313,29 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       bool ok = true;
       for (int u = group; u < p.units && ok; u += ngroups) {
         const Unit t = unit_of<CG>(u, p, nstage);
+        // Rows of A contiguous along K: where they end inside a CTA's 128, only the boxes of 32 that hold some (the MMA
+        // reads what was there before in the others, whose sums are never stored).  With whole boxes a single row took
+        // 17.4 us for 4096 x 4096.
+        auto boxes = [&](int r) { return AMN ? 4 : max(0, min(4, (p.M - (t.m0 + BM * r) + 31) / 32)); };
+        const int mine = boxes(rank);
+        const uint32_t bytes = CG * kStageBytes - (CG * 4 - boxes(0) - (CG == 2 ? boxes(1) : 0)) * (2 * 32 * BK * 2);
         for (int ks = t.ks0; ks < t.ks1; ++ks) {
           if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) {
             ok = false;
             break;
           }
           uint8_t *sa = smem + stage * kStageBytes;
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], CG * kStageBytes);  // the group's bytes
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], bytes);  // the group's
           // a K block past the end is zero fill, and no MMA reads it
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int k0 = (ks * 2 + h) * BK;
-            load_operand<AMN, CG>(sa + h * kHalf, &tmA, &full[stage], full0 + 8u * stage, k0, t.m0 + BM * rank);
+            if (mine == 4)
+              load_operand<AMN, CG>(sa + h * kHalf, &tmA, &full[stage], full0 + 8u * stage, k0, t.m0 + BM * rank);
+            else
+              for (int b = 0; b < mine; ++b)
+                load_operand<false, CG>(sa + h * kHalf + b * (32 * BK * 2), &tmA32, &full[stage], full0 + 8u * stage, k0,
+                                        t.m0 + BM * rank + 32 * b);
             load_operand<BMN, CG>(sa + (2 + h) * kHalf, &tmB, &full[stage], full0 + 8u * stage, k0, t.n0 + BM * rank);
           }
           armed |= 1u << stage;
@@ -420,11 +441,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         uint32_t acc[32];
         tmem_ld32(tb + 32 * j, acc);
         tmem_ld_wait();
-        if (t.part >= 0) {  // sums of a part: the whole tile, rows and columns past the ends among it
-          float *to = p.part + (static_cast<int64_t>(t.part) * TS + BM * rank + q * 32 + lane) * TS + half * (TS / 2) + 32 * j;
+        if (t.part >= 0) {  // sums of a part, rows and columns past the ends among them
+          float *to = p.part + part_at<CG>(t.part, BM * rank + q * 32, half * (TS / 2) + 32 * j);
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<uint4 *>(to + i) = make_uint4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4 *>(to + i * 128) = make_uint4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
         } else if (row < p.M) {
           float v[32];
 #pragma unroll
@@ -456,58 +477,41 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
 }
 
-// The tiles in parts: their sums in the order of the parts, then the epilogue.  A thread has eight
-// columns of a row.
-constexpr int kFinishThreads = 256;
+// The tiles in parts: their sums in the order of the parts, then the epilogue.  A warp has 32 rows x 32 columns.
+constexpr int kFinishThreads = 128;
 template <int KIND, int CG>
 __global__ void __launch_bounds__(kFinishThreads) linear_finish_kernel(const ProductArgs p) {
-  constexpr int TS = tile_size(CG), kPer = TS / 8;
+  constexpr int TS = tile_size(CG), kSide = TS / 32;
   griddep_wait();  // the previous kernel in the stream has completed
   griddep_launch_dependents();
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kFinishThreads + threadIdx.x;
-  const int r = static_cast<int>(i / (TS * kPer)), in = static_cast<int>(i % (TS * kPer));
-  const int tile = p.full + r;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * (kFinishThreads / 32) + (threadIdx.x >> 5);
+  const int r = static_cast<int>(w / (kSide * kSide)), in = static_cast<int>(w % (kSide * kSide)), tile = p.full + r;
   if (tile >= p.nm * p.nn) return;
-  const int mt = tile / p.nn, row = mt * TS + in / kPer, c0 = (tile - mt * p.nn) * TS + in % kPer * 8;
-  if (row >= p.M || c0 >= p.N) return;
-  const float *from = p.part + (static_cast<int64_t>(r) * p.split * TS + in / kPer) * TS + in % kPer * 8;
-  float v[8] = {};
-  float4 a[kMaxSplit][2];
+  const int mt = tile / p.nn, r0 = in / kSide * 32, c0 = in % kSide * 32;
+  const int row0 = mt * TS + r0, row = row0 + (threadIdx.x & 31), col = (tile - mt * p.nn) * TS + c0;
+  if (row0 >= p.M || col >= p.N) return;
+  const int64_t at = static_cast<int64_t>(row) * p.N + col;
+  uint4 res[4];
+  if (KIND == kFwd && p.e.res && row < p.M) ld_row(p.e.res + at, p.N - col, p.e.sectors, res);
+  float v[32] = {};
+  constexpr int kBatch = 4;  // parts under way at once
+  for (int s0 = 0; s0 < p.split; s0 += kBatch) {
+    float4 a[kBatch][8];
 #pragma unroll
-  for (int s = 0; s < kMaxSplit; ++s) {
-    if (s < p.split) {
-      const float4 *f = reinterpret_cast<const float4 *>(from + static_cast<int64_t>(s) * TS * TS);
-      a[s][0] = __ldcg(f);
-      a[s][1] = __ldcg(f + 1);
-    }
+    for (int b = 0; b < kBatch; ++b)
+      if (s0 + b < p.split) {
+        const float *from = p.part + part_at<CG>(r * p.split + s0 + b, r0, c0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[b][i] = __ldcg(reinterpret_cast<const float4 *>(from + i * 128));
+      }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+      if (s0 + b < p.split)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          v[4 * i] += a[b][i].x, v[4 * i + 1] += a[b][i].y, v[4 * i + 2] += a[b][i].z, v[4 * i + 3] += a[b][i].w;
   }
-#pragma unroll
-  for (int s = 0; s < kMaxSplit; ++s) {
-    if (s < p.split) {
-      v[0] += a[s][0].x, v[1] += a[s][0].y, v[2] += a[s][0].z, v[3] += a[s][0].w;
-      v[4] += a[s][1].x, v[5] += a[s][1].y, v[6] += a[s][1].z, v[7] += a[s][1].w;
-    }
-  }
-  const int64_t at = static_cast<int64_t>(row) * p.N + c0;
-  auto pack = [&] {
-    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-  };
-  auto add = [&](const uint4 &w) {
-    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      v[2 * h] += bf16_lo(x[h]);
-      v[2 * h + 1] += bf16_hi(x[h]);
-    }
-  };
-  if constexpr (KIND == kFwd) {
-    if (p.e.bias) add(__ldg(reinterpret_cast<const uint4 *>(p.e.bias + c0)));
-    if (p.e.z) *reinterpret_cast<uint4 *>(p.e.z + at) = pack();
-#pragma unroll
-    for (int h = 0; h < 8; ++h) v[h] = activate(v[h], p.e.act);
-    if (p.e.res) add(*reinterpret_cast<const uint4 *>(p.e.res + at));
-  }
-  *reinterpret_cast<uint4 *>(p.e.y + at) = pack();
+  if (row < p.M) finish_row<KIND>(v, p.e, res, at, col, min(32, p.N - col));
 }
 
 // ---------------------------------------------------------------- dz and dbias
@@ -526,6 +530,7 @@ struct DzArgs {
   int T, N, act, split;
   int32_t *status;
 };
+template <bool ACT>
 __global__ void __launch_bounds__(kDzThreads) linear_dz_kernel(const DzArgs a) {
   __shared__ float s_sum[kDzRows / 4][kDzCols];
   griddep_wait();  // the previous kernel in the stream has completed
@@ -535,7 +540,7 @@ __global__ void __launch_bounds__(kDzThreads) linear_dz_kernel(const DzArgs a) {
   const int step = kDzRows * a.split;
   float sum[8] = {};
   if (c < a.N) {
-    constexpr int kAhead = 4;
+    constexpr int kAhead = ACT ? 4 : 8;
     for (int64_t t0 = blockIdx.y * kDzRows + (threadIdx.x >> 3); t0 < a.T; t0 += static_cast<int64_t>(step) * kAhead) {
       uint4 dy[kAhead], z[kAhead];
 #pragma unroll
@@ -543,7 +548,7 @@ __global__ void __launch_bounds__(kDzThreads) linear_dz_kernel(const DzArgs a) {
         const int64_t t = t0 + static_cast<int64_t>(i) * step;
         if (t < a.T) {
           dy[i] = __ldg(reinterpret_cast<const uint4 *>(a.dy + t * a.N + c));
-          if (a.dz) z[i] = __ldg(reinterpret_cast<const uint4 *>(a.z + t * a.N + c));
+          if (ACT) z[i] = __ldg(reinterpret_cast<const uint4 *>(a.z + t * a.N + c));
         }
       }
 #pragma unroll
@@ -557,7 +562,7 @@ __global__ void __launch_bounds__(kDzThreads) linear_dz_kernel(const DzArgs a) {
           v[2 * h] = bf16_lo(y[h]);
           v[2 * h + 1] = bf16_hi(y[h]);
         }
-        if (a.dz) {
+        if constexpr (ACT) {
           const uint32_t x[4] = {z[i].x, z[i].y, z[i].z, z[i].w};
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
@@ -622,12 +627,16 @@ bool map2(CUtensorMap *m, const void *ptr, int inner, int rows, int box_rows) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How a product is cut: the whole tiles, and the parts of those that are left.
+// How a product is cut: the whole tiles, and the parts of those that are left.  By the time in us that each way takes
+// apart from what they share: a round of tiles 0.58 us a stage of 128 and 1.4 for its ends with pairs, 0.46 and 0.8 with
+// single CTAs; parts cost another 5, for their sums and the second kernel.  Measured, single whole, single in parts, pairs
+// whole, pairs in parts: 1024 x 1024 x 1024 7.6, 10.3, 10.1, 11.6; 512 x 2048 x 768 11.1, 9.6, 14.2, 11.7; 4096 x 1536 x 1536 22.7,
+// 22.5, 20.4, 21.2; 16 x 4096 x 4096 18.4, 11.9, 22.0, 14.9; 2048 x 4096 x 4096 67.4, 64.0, 42.4, 42.2.
 struct Cut {
   int cg, nm, nn, full, split, units;
   double cost;
 };
-Cut cut_with(int64_t M, int64_t N, int64_t K, int cg, int sms) {
+Cut cut_with(int64_t M, int64_t N, int64_t K, int cg, bool parts, int sms) {
   const int ts = tile_size(cg), groups = sms / cg;
   Cut c;
   c.cg = cg;
@@ -637,23 +646,27 @@ Cut cut_with(int64_t M, int64_t N, int64_t K, int cg, int sms) {
   const int nstage = static_cast<int>((K + 2 * BK - 1) / (2 * BK));
   const int left = static_cast<int>(tiles % groups);
   c.split = 1;
-  if (left) c.split = std::max(1, std::min({groups / left, kMaxSplit, nstage / kLeastStages}));
+  if (left && parts) c.split = std::max(1, std::min({groups / left, kMaxSplit, nstage / kLeastStages}));
   c.full = static_cast<int>(c.split > 1 ? tiles - left : tiles);
   c.units = static_cast<int>(c.split > 1 ? c.full + left * c.split : tiles);
   const int64_t rounds = c.split > 1 ? c.full / groups : (tiles + groups - 1) / groups;
-  const double stage = cg == 2 ? 1.0 : 0.8, extra = cg == 2 ? 4 : 2;
-  c.cost = rounds * (nstage * stage + extra);
-  if (c.split > 1) c.cost += (nstage + c.split - 1) / c.split * stage + extra + 5;
+  const double stage = cg == 2 ? 0.58 : 0.46, ends = cg == 2 ? 1.4 : 0.8;
+  c.cost = rounds * (nstage * stage + ends);
+  if (c.split > 1) c.cost += (nstage + c.split - 1) / c.split * stage + ends + 5;
   return c;
 }
 Cut cut_of(int64_t M, int64_t N, int64_t K, int sms) {
-  const Cut one = cut_with(M, N, K, 1, sms), two = cut_with(M, N, K, 2, sms);
-  return two.cost <= one.cost ? two : one;
+  Cut best = cut_with(M, N, K, 2, false, sms);
+  for (int way = 1; way < 4; ++way) {
+    const Cut c = cut_with(M, N, K, way & 1 ? 1 : 2, way > 1, sms);
+    if (c.cost < best.cost) best = c;
+  }
+  return best;
 }
 constexpr size_t kPartBytes = static_cast<size_t>(kRuleSms) * BM * BM * 4 * 2;  // parts of a round of pairs (or singles)
 
 template <int KIND, int CG>
-cudaError_t launch_cut(const CUtensorMap &a, const CUtensorMap &b, ProductArgs p, const Cut &c, int sms, cudaStream_t s) {
+cudaError_t launch_cut(const CUtensorMap &a, const CUtensorMap &a32, const CUtensorMap &b, ProductArgs p, const Cut &c, int sms, cudaStream_t s) {
   static DeviceOnce once;  // the shared-memory opt-in, and how many groups of CTAs fit at once
   auto kernel = linear_product_kernel<KIND, CG>;
   int groups = 0;
@@ -681,10 +694,10 @@ cudaError_t launch_cut(const CUtensorMap &a, const CUtensorMap &b, ProductArgs p
       &groups);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kernel, dim3(static_cast<unsigned>(CG * std::min(c.units, groups))), dim3(kGemmThreads), kGemmSmem, s, CG, a,
-                 b, p);
+                 a32, b, p);
   if (e != cudaSuccess || c.split == 1) return e;
   constexpr int TS = tile_size(CG);
-  const int64_t threads = static_cast<int64_t>(c.nm * c.nn - c.full) * TS * (TS / 8);
+  const int64_t threads = static_cast<int64_t>(c.nm * c.nn - c.full) * (TS / 32) * (TS / 32) * 32;
   return launch_pdl(linear_finish_kernel<KIND, CG>, dim3(static_cast<unsigned>((threads + kFinishThreads - 1) / kFinishThreads)),
                     dim3(kFinishThreads), 0, s, 1, p);
 }
@@ -694,8 +707,9 @@ template <int KIND>
 moe_status product(const char *label, const void *a, const void *b, int M, int N, int K, const Ends &ends, float *part,
                    int32_t *status, bool first, int sms, cudaStream_t s) {
   const Cut c = cut_of(M, N, K, std::min(sms, kRuleSms));
-  CUtensorMap ma, mb;
+  CUtensorMap ma, ma32, mb;
   const bool ok = (KIND == kDw ? map2(&ma, a, M, K, 64) : map2(&ma, a, K, M, 128)) &&
+                  (KIND == kDw ? map2(&ma32, a, M, K, 64) : map2(&ma32, a, K, M, 32)) &&
                   (KIND == kDx ? map2(&mb, b, K, N, 128) : map2(&mb, b, N, K, 64));
   if (!ok) return MOE_ERR_CUDA;
   ProductArgs p{};
@@ -714,7 +728,7 @@ moe_status product(const char *label, const void *a, const void *b, int M, int N
   p.status = status;
   p.first = first;
   return timed(label, s, [&] {
-    return c.cg == 2 ? launch_cut<KIND, 2>(ma, mb, p, c, sms, s) : launch_cut<KIND, 1>(ma, mb, p, c, sms, s);
+    return c.cg == 2 ? launch_cut<KIND, 2>(ma, ma32, mb, p, c, sms, s) : launch_cut<KIND, 1>(ma, ma32, mb, p, c, sms, s);
   });
 }
 
@@ -814,7 +828,10 @@ moe_status moe_linear_backward(const moe_linear_config *cfg, const void *dy, con
     // enough blocks for four on each SM, of at least four rows a thread
     const int cols = (N + kDzCols - 1) / kDzCols, rounds = (T + kDzRows * 4 - 1) / (kDzRows * 4);
     a.split = std::max(1, std::min({(4 * di.sms + cols - 1) / cols, rounds, kDzSplit}));
-    MOE_TRY(timed("linear_dz", s, [&] { return launch_pdl(linear_dz_kernel, dim3(cols, a.split), dim3(kDzThreads), 0, s, 1, a); }));
+    MOE_TRY(timed("linear_dz", s, [&] { 
+      return act ? launch_pdl(linear_dz_kernel<true>, dim3(cols, a.split), dim3(kDzThreads), 0, s, 1, a)
+                 : launch_pdl(linear_dz_kernel<false>, dim3(cols, a.split), dim3(kDzThreads), 0, s, 1, a);
+    }));
     if (dbias && a.split > 1)
       MOE_TRY(timed("linear_dbias", s, [&] {
         return launch_pdl(linear_dbias_kernel, dim3((N + 127) / 128), dim3(128), 0, s, 1, static_cast<const float *>(a.part),
