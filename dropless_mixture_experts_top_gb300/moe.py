@@ -753,7 +753,9 @@ class Gate(_Plan):
 
     The routing is what MoELayer.route leaves: forward(..., out=layer.routing) routes
     a layer.  After the layer's backward, backward(..., grads["d_topk_w"],
-    d_logits=grads["d_logits"]) replaces the gradient of the layer's own routing."""
+    d_logits=grads["d_logits"]) replaces the gradient of the layer's own routing.
+    The gate's status then stands in for the "route" of the layer's, which only its
+    own route sets."""
 
     def __init__(self, T, E, k, score="softmax", groups=1, top_groups=1, group_best=1, renormalise=True, scale=1.0,
                  device="cuda"):
