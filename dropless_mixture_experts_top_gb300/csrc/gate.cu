@@ -24,10 +24,28 @@ __global__ void __launch_bounds__(kGateThreads) gate_index_kernel(const GateArgs
   const int rank = blockIdx.x % a.cluster, mine = blockIdx.x / a.cluster;
   griddep_wait();  // the previous kernel in the stream has completed
   griddep_launch_dependents();
+  // the block's first slots, on their way during what follows
+  constexpr int kSlots = 4;
+  const int64_t first = clusters ? static_cast<int64_t>(gate_first(a, blockIdx.x)) * a.k : 0,
+                last = clusters ? static_cast<int64_t>(gate_first(a, blockIdx.x + 1)) * a.k : 0;
+  int slot_e[kSlots], slot_r[kSlots];
+  float slot_w[kSlots];
+  auto load = [&](int64_t s0) {
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+      const int64_t s = s0 + i * kGateThreads;
+      if (s < last) {
+        slot_e[i] = __ldcg(a.topk_idx + s);
+        slot_r[i] = __ldcg(a.row_of_slot + s);
+        slot_w[i] = __ldcg(a.topk_w + s);
+      }
+    }
+  };
+  load(first + tid);
   int before = 0, all = 0, n;
   const int here = tid < E && clusters ? __ldcg(a.before + static_cast<size_t>(blockIdx.x) * E + tid) : 0;
   if (tid < E) {
-    constexpr int kBatch = 15;  // 114 clusters over 8 blocks
+    constexpr int kBatch = 10;  // 76 clusters over 8 blocks
     for (int c = rank; c < clusters; c += a.cluster * kBatch) {
       int h[kBatch];
 #pragma unroll
@@ -72,30 +90,16 @@ __global__ void __launch_bounds__(kGateThreads) gate_index_kernel(const GateArgs
     }
   }
   __syncthreads();
-  if (clusters) {
-    const int64_t s1 = static_cast<int64_t>(gate_first(a, blockIdx.x + 1)) * a.k;
-    constexpr int kBatch = 4;
-    for (int64_t s0 = static_cast<int64_t>(gate_first(a, blockIdx.x)) * a.k + tid; s0 < s1; s0 += kGateThreads * kBatch) {
-      int e[kBatch], r[kBatch];
-      float w[kBatch];
+  for (int64_t s0 = first + tid; s0 < last; s0 += kGateThreads * kSlots) {
+    if (s0 > first + tid) load(s0);
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int64_t s = s0 + i * kGateThreads;
-        if (s < s1) {
-          e[i] = __ldcg(a.topk_idx + s);
-          r[i] = __ldcg(a.row_of_slot + s);
-          w[i] = __ldcg(a.topk_w + s);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int64_t s = s0 + i * kGateThreads;
-        if (s < s1) {
-          const int row = s_base[e[i]] + r[i];
-          a.row_of_slot[s] = row;
-          a.slot_of_row[row] = static_cast<int32_t>(s);
-          a.w_row[row] = w[i];
-        }
+    for (int i = 0; i < kSlots; ++i) {
+      const int64_t s = s0 + i * kGateThreads;
+      if (s < last) {
+        const int row = s_base[slot_e[i]] + slot_r[i];
+        a.row_of_slot[s] = row;
+        a.slot_of_row[row] = static_cast<int32_t>(s);
+        a.w_row[row] = slot_w[i];
       }
     }
   }
@@ -275,10 +279,9 @@ bool gate_ok(const moe_gate_config *c) {
 }
 
 // Chunks: 32 tokens each while that makes at most six blocks for each of 152 SMs, then more each (four of them fit
-// at once: the others follow as those end, which evens out the blocks with undecided tokens.  131072 x 256 in
-// 456, 608, 912, 1216 and 1824 chunks: 107, 98, 98, 95 and 110 us); up to 64 tokens for each of one cluster's
+// at once: the others follow as those end, which evens out the blocks with undecided tokens); up to 64 tokens for each of one cluster's
 // blocks are one launch.
-constexpr int kLeastTok = 32, kMostChunks = 912;
+constexpr int kLeastTok = 32, kMostChunks = 608;
 struct GateLayout {
   int chunks, cluster;
   size_t flags, before, total, bytes;

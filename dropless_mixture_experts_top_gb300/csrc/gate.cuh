@@ -121,12 +121,12 @@ constexpr int kWarps = kGateThreads / 32;
 //   sigmoid: 1 / (1 + e), e = 2^(-l log2 e) by the part's ex2: off by 2^-22 of itself, and by |l| 2^-23 for the
 //   rounded argument, of which s (1 - s) reaches s (at most 1/4, with the |l| 0.23); the sum by half an ulp, the
 //   reciprocal by one: 2^-24 + 0.23 2^-23 + s (2^-24 + 2^-23), 2.2 units; bias * scale + base rounded,
-//   half a unit, the product rounded, half: 3.2.  Two numbers that differ by more than 7 are in the order
-//   of the exact ones; 10 leaves room.
+//   half a unit, the product rounded, half: 3.2.  Two numbers that differ by more than 6.4 are in the order
+//   of the exact ones.
 //   softmax: e = 2^((l - m) log2 e) off by 2^-22 of itself and by |l - m| 2^-22 for the rounded difference and
 //   argument, which with the e^-|l - m| of its size is at most 0.37 2^-22; the sum Z by 13 roundings and its
-//   terms, 1.3e-6; the quotient by 2 ulp: 1.9e-6 in all, 16 units, with the roundings 17: 35, and 40 with room.
-constexpr int kNearSigmoid = 10, kNearSoftmax = 40;
+//   terms, 1.3e-6; the quotient by 2 ulp: 1.9e-6 in all, 16 units, with the roundings 17: 35.
+constexpr int kNearSigmoid = 7, kNearSoftmax = 35;
 constexpr float kFixOne = 8388608.f;       // 2^23
 constexpr float kFixLeast = 8.f;           // the least number of an expert that may be chosen; 0: it may not
 constexpr float kLog2e = 1.4426950408889634f;
@@ -149,7 +149,7 @@ __device__ __forceinline__ uint32_t order_of(float l) {
   return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
 
-// Sorts NV keys, largest first; of 16, the first 8.
+// Sorts NV keys, largest first; of 16 and 32, the first 8.
 template <int NV>
 __device__ __forceinline__ void sort_keys(uint32_t *v) {
   auto cas = [&](int a, int b) {
@@ -169,11 +169,12 @@ __device__ __forceinline__ void sort_keys(uint32_t *v) {
     cas(1, 4), cas(3, 6);
     cas(2, 4), cas(3, 5);
     cas(3, 4);
-  } else if constexpr (NV == 16) {
-    sort_keys<8>(v);
-    sort_keys<8>(v + 8);
+  } else if constexpr (NV >= 16) {
+    constexpr int H = NV / 2;
+    sort_keys<H>(v);
+    sort_keys<H>(v + H);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = max(v[i], v[15 - i]);  // the 8 largest, falling and rising
+    for (int i = 0; i < 8; ++i) v[i] = max(v[i], v[H + 7 - i]);  // the 8 largest, falling and rising
 #pragma unroll
     for (int d = 4; d > 0; d >>= 1)
 #pragma unroll
@@ -188,18 +189,22 @@ struct BiasInfo {
   float base;   // 2^23 + 8 + O
   int off;      // 8 + O: the number of c = 0
   bool odd;     // some entry is not finite
+  float most;   // the largest |bias| (inf: some entry is not finite)
 };
 
 // A token whose order fp32 does not decide.  runs: which runs of `run` experts may be used
 // (bit e / run), or 0 to choose the groups as well; only experts whose fp32 number is at least
-// `least` can be among the chosen (0: every one).
+// `least` can be among the chosen (0: every one).  extra: where it is known that none but the chosen k and one more come into
+// question, that one (-1: not even one more, -2: unknown).
 struct Undecided {
   uint32_t runs;
-  int least;
+  int least, extra;
 };
 
 // ---- Scores as pairs of floats (hi + lo, about 48 bits), from error-free sums and products: the part's 64-bit
-// unit is a hundredth as fast as this.  (Dekker, Knuth: two_sum, two_prod by a fused multiply-add.)
+// unit is a hundredth as fast as this.  (Dekker, Knuth: two_sum, two_prod by a fused multiply-add.)  What follows is run by
+// few warps, once or twice per SM: its time is that of fetching its instructions (some 60 cycles each), so it
+// is written as loops, nothing unrolled, and its functions are not inlined twice.
 struct Pair {
   float h, l;
 };
@@ -219,15 +224,19 @@ __device__ __forceinline__ Pair pair_mul(Pair a, Pair b) {
   const float p = __fmul_rn(a.h, b.h);
   return quick_two_sum(p, __fmaf_rn(a.h, b.h, -p) + __fmaf_rn(a.h, b.l, a.l * b.h));
 }
-__device__ __forceinline__ Pair pair_div(Pair a, Pair b) {
+__device__ __noinline__ Pair pair_div(Pair a, Pair b) {
   const float q = __fdiv_rn(a.h, b.h);
   const float r = __fmaf_rn(-q, b.h, a.h) + __fmaf_rn(-q, b.l, a.l);
   return quick_two_sum(q, __fdiv_rn(r, b.h));
 }
+// 1 / 6!, 1 / 5!, ... 1 / 0!
+__constant__ Pair kFactorials[7] = {{1.3888889225e-03f, -3.3631094437e-11f}, {8.3333337680e-03f, -4.3461720333e-10f},
+                                    {4.1666667908e-02f, -1.2417634698e-09f}, {1.6666667163e-01f, -4.9670538794e-09f},
+                                    {0.5f, 0.f}, {1.f, 0.f}, {1.f, 0.f}};
 // e^-(a + b) for a >= 0, b at most half an ulp of a; 0 from a = 40 on (4e-18).
 // n ln 2 comes off in three parts (15, 17 and 24 bits: the first two products are exact), then the series:
 // to r^6 / 6! in pairs, the rest, below 2e-7 of the sum, in single floats: off by 2^-45 at most.
-__device__ __forceinline__ Pair pair_exp_neg(float a, float b) {
+__device__ __noinline__ Pair pair_exp_neg(float a, float b) {
   if (!(a < 40.f)) return {0.f, 0.f};
   const float n = rintf(a * 1.4426950408889634f);
   const Pair t = two_sum(__fmaf_rn(n, 0.693145751953125f, -a), __fmul_rn(n, 1.428605173714459e-06f));  // n ln 2 - a
@@ -239,13 +248,9 @@ __device__ __forceinline__ Pair pair_exp_neg(float a, float b) {
   q = fmaf(q, r.h, 1.f / 362880.f);
   q = fmaf(q, r.h, 1.f / 40320.f);
   q = fmaf(q, r.h, 1.f / 5040.f);
-  Pair s = pair_add(pair_mul({q, 0.f}, r), {1.3888889225e-03f, -3.3631094437e-11f});  // 1 / 6!
-  s = pair_add(pair_mul(s, r), {8.3333337680e-03f, -4.3461720333e-10f});  // 1 / 5!
-  s = pair_add(pair_mul(s, r), {4.1666667908e-02f, -1.2417634698e-09f});  // 1 / 4!
-  s = pair_add(pair_mul(s, r), {1.6666667163e-01f, -4.9670538794e-09f});  // 1 / 3!
-  s = pair_add(pair_mul(s, r), {0.5f, 0.f});
-  s = pair_add(pair_mul(s, r), {1.f, 0.f});
-  s = pair_add(pair_mul(s, r), {1.f, 0.f});
+  Pair s = {q, 0.f};
+#pragma unroll 1
+  for (int k = 0; k < 7; ++k) s = pair_add(pair_mul(s, r), kFactorials[k]);
   const float f = __int_as_float((127 - static_cast<int>(n)) << 23);  // 2^-n
   return {s.h * f, s.l * f};
 }
@@ -268,45 +273,39 @@ __device__ __forceinline__ long long to_fixed(Pair s, float b) {
 template <int KEY>
 __device__ __noinline__ bool resolve_fixed(const GateArgs &a, const float *row, const float *s_bias, BiasInfo bi, Undecided u,
                                            int run, long long *val, uint8_t *list, uint16_t *slot) {
-  constexpr int NR = kMaxExperts / 32;
   const int lane = threadIdx.x & 31, E = a.E;
-  const bool biased = a.bias != nullptr;
+  const bool biased = KEY != kKeyLogit && a.bias != nullptr;
   const long long least = LLONG_MIN;
-  bool bad = false, in_range = true;
-  float l[NR], b[NR];
-  uint32_t scored = 0;
-#pragma unroll
-  for (int i = 0; i < NR; ++i) {
-    const int e = lane + 32 * i;
-    l[i] = e < E ? clean_logit(__ldg(row + e), bad) : -INFINITY;
-    b[i] = KEY != kKeyLogit && biased && e < E ? s_bias[e] : 0.f;
-  }
+  bool bad = false, in_range = true, whole = true;  // whole: biases that are whole numbers of units
+  uint32_t scored = 0;                              // by a lane's experts lane + 32 i
   float top = -FLT_MAX, low = FLT_MAX;
-  bool whole = true;  // biases that are whole numbers of units
-#pragma unroll
-  for (int i = 0; i < NR; ++i) {
-    top = fmaxf(top, l[i]);
-    if (l[i] >= -FLT_MAX && b[i] > -INFINITY) {
+  const bool few = KEY != kKeySoftmax && u.extra > -2 && bi.most <= kFixedMost;
+  if (!few && lane * 8 < E) asm volatile("prefetch.global.L1 [%0];" ::"l"(row + lane * 8));
+#pragma unroll 1
+  for (int e = lane, i = 0; e < E && !few; e += 32, ++i) {
+    const float l = clean_logit(__ldg(row + e), bad), b = biased ? s_bias[e] : 0.f;
+    top = fmaxf(top, l);
+    if (l >= -FLT_MAX && b > -INFINITY) {
       scored |= 1u << i;
-      low = fminf(low, l[i]);
-      in_range = in_range && fabsf(b[i]) <= kFixedMost;
-      whole = whole && rintf(b[i] * kFixedOne) == b[i] * kFixedOne;
+      low = fminf(low, l);
+      in_range = in_range && fabsf(b) <= kFixedMost;
+      whole = whole && rintf(b * kFixedOne) == b * kFixedOne;
     }
   }
   if (!__all_sync(0xffffffffu, in_range)) return false;
   // Equal logits (rows of zeros: padding): the scores are one number, which says the same of all, and the biases are exact.
-  const bool even = __all_sync(0xffffffffu, whole) && warp_max(-low) == -warp_max(top);
+  const bool even = !few && __all_sync(0xffffffffu, whole) && warp_max(-low) == -warp_max(top);
   const long long near = KEY == kKeyLogit || even ? 0 : kNearFixed;
   Pair z = {0.f, 0.f};
   if (KEY == kKeySoftmax) {
     top = warp_max(top);
 #pragma unroll 1
-    for (int i = 0; i < NR; ++i) {
-      const float x = i == 0 ? l[0] : i == 1 ? l[1] : i == 2 ? l[2] : i == 3 ? l[3] : i == 4 ? l[4] : i == 5 ? l[5] : i == 6 ? l[6] : l[7];
+    for (int e = lane; e < E; e += 32) {
+      const float x = clean_logit(__ldg(row + e), bad);
       const Pair d = two_sum(top, -x);
       if (x >= -FLT_MAX) z = pair_add(z, pair_exp_neg(d.h, d.l));
     }
-#pragma unroll
+#pragma unroll 1
     for (int o = 16; o > 0; o >>= 1)
       z = pair_add(z, {__shfl_xor_sync(0xffffffffu, z.h, o), __shfl_xor_sync(0xffffffffu, z.l, o)});
   }
@@ -351,16 +350,22 @@ __device__ __noinline__ bool resolve_fixed(const GateArgs &a, const float *row, 
     run = a.group_size;
     __syncwarp();
   }
-  // the experts in question, by index
+  // the experts in question
   int n = 0;
-#pragma unroll
-  for (int i = 0; i < NR; ++i) {
-    const int e = lane + 32 * i;
+  if (few) {
+    if (lane < a.k) list[lane] = static_cast<uint8_t>(slot[lane]);
+    if (lane == a.k) list[lane] = static_cast<uint8_t>(u.extra);
+    n = a.k + (u.extra >= 0 ? 1 : 0);
+  }
+#pragma unroll 1
+  for (int e0 = 0, i = 0; e0 < E && !few; e0 += 32, ++i) {
+    const int e = e0 + lane;
     bool use = (scored >> i & 1u) && ((u.runs >> (e / run & 31)) & 1u);
     if (KEY != kKeyLogit && use && u.least > 0) {
       // the fp32 number once more, with the distance that decides off for safety
-      const float s = KEY == kKeySigmoid ? sigmoid_fast(l[i]) : ex2((l[i] - top) * kLog2e) * rcp(z.h);
-      use = fmaf(s + b[i], bi.scale, static_cast<float>(bi.off)) >= static_cast<float>(u.least) - kNearSoftmax;
+      const float l = clean_logit(__ldg(row + e), bad), b = biased ? s_bias[e] : 0.f;
+      const float s = KEY == kKeySigmoid ? sigmoid_fast(l) : ex2((l - top) * kLog2e) * rcp(z.h);
+      use = fmaf(s + b, bi.scale, static_cast<float>(bi.off)) >= static_cast<float>(u.least) - kNearSoftmax;
     }
     const uint32_t set = __ballot_sync(0xffffffffu, use);
     if (use) list[n + __popc(set & ((1u << lane) - 1u))] = static_cast<uint8_t>(e);
@@ -387,10 +392,13 @@ __device__ __noinline__ bool resolve_fixed(const GateArgs &a, const float *row, 
   int at_mine = 0;
   if (n <= 32) {  // every lane counts those in front of its own
     const long long v = lane < n ? val[lane] : least;
+    const int e = lane < n ? list[lane] : 0;
     int before = 0;
+#pragma unroll 1
     for (int o = 0; o < n; ++o) {
       const long long other = __shfl_sync(0xffffffffu, v, o);
-      before += other > v || (other == v && o < lane) ? 1 : 0;
+      const int other_e = __shfl_sync(0xffffffffu, e, o);
+      before += other > v || (other == v && other_e < e) ? 1 : 0;
     }
     __syncwarp();
     if (lane < n) val[before] = (v << 8) | lane;  // (numbers below 2^54)
@@ -564,7 +572,7 @@ __device__ __noinline__ void resolve_token(const GateArgs &a, const float *row, 
 // LPT lanes per token, NV experts per lane: with l the lane's place among the token's, e = l + LPT i, or NV l + i
 // (VEC; E = LPT NV).  KMAX: k at most.
 template <int LPT, int NV, bool VEC, int KEY, bool GROUPS, int KMAX>
-__global__ void __launch_bounds__(kGateThreads, 4) gate_select_kernel(const GateArgs a) {
+__global__ void __launch_bounds__(kGateThreads, NV == 32 ? 2 : 4) gate_select_kernel(const GateArgs a) {
   constexpr int kNear = KEY == kKeyLogit ? 0 : (KEY == kKeySigmoid ? kNearSigmoid : kNearSoftmax);
   constexpr bool KEYS = GROUPS && !VEC;                  // groups by way of shared memory
   static_assert(!KEYS || LPT == 32, "a lane per group");
@@ -620,7 +628,7 @@ __global__ void __launch_bounds__(kGateThreads, 4) gate_select_kernel(const Gate
   float ahead[NV] = {};
   load(first + warp * TPW + lane / LPT, ahead);
 
-  BiasInfo bi{kFixOne - 32.f, kFixOne + kFixLeast, static_cast<int>(kFixLeast), false};
+  BiasInfo bi{kFixOne - 32.f, kFixOne + kFixLeast, static_cast<int>(kFixLeast), false, 0.f};
   __syncthreads();
   if (KEY != kKeyLogit) {
     const float b = a.bias && tid < E ? __ldg(a.bias + tid) : 0.f;
@@ -639,6 +647,7 @@ __global__ void __launch_bounds__(kGateThreads, 4) gate_select_kernel(const Gate
       bi.base = kFixOne + kFixLeast + O;
       bi.off = static_cast<int>(kFixLeast + O);
       bi.odd = s_bodd != 0;
+      bi.most = bi.odd ? INFINITY : m;
     }
     // (VEC: in the order in which the lanes read vectors of four)
     const int at = VEC ? (tid % NV / 4) * (LPT * 4) + tid / NV * 4 + tid % 4 : tid;
@@ -746,7 +755,7 @@ __global__ void __launch_bounds__(kGateThreads, 4) gate_select_kernel(const Gate
 #pragma unroll
         for (int i = 0; i < NV; ++i) key[i] = expert(i) < E ? key[i] : 0u;
       }
-      Undecided u{0xffffffffu, 0};
+      Undecided u{0xffffffffu, 0, -2};
       bool open_groups = false;
       if constexpr (GROUPS) {
         uint32_t k1, k2;
@@ -866,6 +875,17 @@ __global__ void __launch_bounds__(kGateThreads, 4) gate_select_kernel(const Gate
           got = l == j ? v[j] : got;
         }
         if (l < k && valid) s_slot[tl * k + l] = static_cast<uint16_t>(255u - (got & 255u));
+        if (__any_sync(0xffffffffu, gap < (kNear + 1) * 256u)) {  // who comes into question
+          uint32_t next = ninth;
+#pragma unroll
+          for (int j = 1; j < 8; ++j) next = j == k ? v[j] : next;
+          const uint32_t bound = end - min(end, (kNear + 1) * 256u);
+          bool more = ND < NV && key[ND - 1] >= bound;
+#pragma unroll
+          for (int i = 0; i < ND; ++i) more |= key[i] < next && key[i] >= bound;
+          if ((__ballot_sync(0xffffffffu, more) >> (lane - l) & ((1u << LPT) - 1u)) == 0)
+            u.extra = next >= bound && (next >> 8) ? static_cast<int>(255u - (next & 255u)) : -1;
+        }
       } else {
         uint32_t prev = 0xffffffffu;
 #pragma unroll
@@ -889,6 +909,7 @@ __global__ void __launch_bounds__(kGateThreads, 4) gate_select_kernel(const Gate
       if (undecided && l == 0 && valid) {
         const int q = static_cast<int>(end >> 8);
         u.least = q > 2 * kNear + 1 ? q - 2 * kNear : 0;
+        if (open_groups || q == 0) u.extra = -2;
         s_und[tl] = u;
         s_list[atomicAdd(&s_count, 1)] = static_cast<uint16_t>(tl);
       }
@@ -1036,12 +1057,13 @@ cudaError_t launch_gate_select(const GateArgs &a, cudaStream_t s) {
     if (a.E <= 64) return launch_variant<8, 8, false, KEY, false, 8>(a, s);
     if (a.E == 128 && sectors) return launch_variant<8, 16, true, KEY, false, 8>(a, s);
     if (a.E <= 128) return launch_variant<8, 16, false, KEY, false, 8>(a, s);
-    if (a.E == 256 && sectors) return launch_variant<16, 16, true, KEY, false, 8>(a, s);
-    return launch_variant<16, 16, false, KEY, false, 8>(a, s);
+    if (a.E == 256 && sectors) return launch_variant<8, 32, true, KEY, false, 8>(a, s);
+    return launch_variant<8, 32, false, KEY, false, 8>(a, s);
   }
   if (a.k <= 8 && sectors) {
     if (a.E == 64 && runs(8)) return launch_variant<8, 8, true, KEY, true, 8>(a, s);
     if (a.E == 128 && runs(16)) return launch_variant<8, 16, true, KEY, true, 8>(a, s);
+    if (a.E == 256 && runs(32)) return launch_variant<8, 32, true, KEY, true, 8>(a, s);
     if (a.E == 256 && runs(16)) return launch_variant<16, 16, true, KEY, true, 8>(a, s);
   }
   return a.groups > 1 ? launch_wide<KEY, true>(a, s) : launch_wide<KEY, false>(a, s);
