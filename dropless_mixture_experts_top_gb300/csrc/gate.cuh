@@ -50,6 +50,7 @@ struct GateArgs {
   int chunks;           // chunk c: the tokens [c T / chunks, (c + 1) T / chunks)
   int cluster;          // chunks per cluster
   int32_t *before;      // [chunks][E]: the slots of expert e in the cluster's earlier chunks
+  int32_t *count;       // [chunks][E]: its own
   int32_t *total;       // [clusters][E]
   int32_t *flags;       // [clusters]
   int32_t *status;
@@ -1000,6 +1001,7 @@ __global__ void __launch_bounds__(kGateThreads, NV == 32 ? 2 : 4) gate_select_ke
   if (static_cast<int>(gridDim.x) > a.cluster) {  // the second kernel goes on
     if (tid < E) {
       a.before[static_cast<size_t>(blockIdx.x) * E + tid] = before;
+      a.count[static_cast<size_t>(blockIdx.x) * E + tid] = s_run[tid];
       if (rank == 0) a.total[static_cast<size_t>(cluster) * E + tid] = all;
     }
     if (tid == 0 && rank == 0) a.flags[cluster] = flag;

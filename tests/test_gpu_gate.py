@@ -78,6 +78,27 @@ def test_a_large_batch():
     check(logits, torch.round(20 * rand(256, seed=2)) * 1e-3, 8, scale=2.5, groups=8, top_groups=4, group_best=2)
 
 
+@pytest.mark.parametrize("E,k,biased", [(40, 8, True), (8, 2, False), (256, 1, True)])
+def test_several_rounds_per_block(E, k, biased):
+    """More tokens than the blocks take in one round, and more slots than the second kernel sorts at once."""
+    check(rand(500003, E), 0.1 * rand(E) if biased else None, k)
+
+
+@pytest.mark.parametrize("T", [255, 256, 257, 511, 512, 513, 4095, 19456, 19457, 194560, 194561])
+def test_edges_of_chunks_and_clusters(T):
+    check(rand(T, 16, seed=T), None, 3)
+
+
+def test_rows_off_the_vectors_alignment():
+    """Logits that start 16 and not 32 bytes off, for the widths that are otherwise read in whole sectors."""
+    for E in (64, 128, 256):
+        buf = rand(200 * E + 4)
+        z = buf[4:].view(200, E)
+        assert z.data_ptr() % 32 == 16
+        check(z, 0.1 * rand(E, seed=1), 8)
+        check(z, 0.1 * rand(E, seed=1), 8, groups=8, top_groups=3, group_best=2)
+
+
 @pytest.mark.parametrize("E,k,groups", [(8, 3, {}), (64, 6, {}), (256, 8, dict(groups=8, top_groups=3, group_best=2)),
                                         (96, 5, dict(groups=6, top_groups=2, group_best=1))])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
