@@ -36,7 +36,7 @@ def randn(*s, seed=0, scale=1.0):
 # one row; ragged rows and columns; less than a tile; several; long reductions of few tiles (in parts); more tiles than a round
 SIZES = [(1, 8, 8), (1, 64, 64), (2, 8, 4096), (3, 72, 40), (127, 128, 136), (129, 200, 264), (512, 128, 64), (777, 1000, 520),
          (300, 4096, 8), (1, 4096, 4096), (257, 5000, 2056), (2048, 64, 4096), (5000, 264, 1032), (30000, 128, 64),
-         (4104, 1032, 4104), (16000, 520, 520)]
+         (4104, 1032, 4104), (16000, 520, 520), (2049, 1024, 4096), (2400, 264, 6144), (2300, 520, 4104)]
 
 
 @pytest.mark.parametrize("T,K,N", SIZES)
