@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kGateThreads) gate_index_kernel(const GateArgs
 // the next token's inputs are on their way meanwhile.
 
 constexpr int kGradThreads = 256;
-constexpr int kGradBlocksPerSm = 6;
+constexpr int kGradBlocks = 6, kDenseBlocks = 4;  // per SM
 
 struct GradArgs {
   const float *logits;
@@ -155,9 +155,31 @@ struct GradArgs {
   float scale;
 };
 
-// VEC: rows of whole 16-byte vectors.
-template <bool DENSE, bool VEC>
-__global__ void __launch_bounds__(kGradThreads, DENSE ? 4 : kGradBlocksPerSm) gate_grad_kernel(const GradArgs a) {
+// VW: elements per access, by the rows' alignment.
+template <int VW>
+__device__ __forceinline__ void load_vec(const float *p, float *v) {
+  if constexpr (VW == 4) {
+    const float4 q = __ldg(reinterpret_cast<const float4 *>(p));
+    v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+  } else if constexpr (VW == 2) {
+    const float2 q = __ldg(reinterpret_cast<const float2 *>(p));
+    v[0] = q.x, v[1] = q.y;
+  } else {
+    v[0] = __ldg(p);
+  }
+}
+template <int VW>
+__device__ __forceinline__ void store_vec(float *p, const float *v, float f) {
+  if constexpr (VW == 4)
+    *reinterpret_cast<float4 *>(p) = make_float4(v[0] * f, v[1] * f, v[2] * f, v[3] * f);
+  else if constexpr (VW == 2)
+    *reinterpret_cast<float2 *>(p) = make_float2(v[0] * f, v[1] * f);
+  else
+    *p = v[0] * f;
+}
+
+template <bool DENSE, int VW>
+__global__ void __launch_bounds__(kGradThreads, DENSE ? kDenseBlocks : kGradBlocks) gate_grad_kernel(const GradArgs a) {
   constexpr int NV = kMaxExperts / 32;
   const int lane = threadIdx.x & 31, E = a.E, k = a.k;
   const int64_t step = static_cast<int64_t>(gridDim.x) * (kGradThreads / 32);
@@ -180,17 +202,12 @@ __global__ void __launch_bounds__(kGradThreads, DENSE ? 4 : kGradBlocksPerSm) ga
   };
   auto row_of = [&](int64_t t, float (&v)[NV]) {
     const float *lr = a.logits + t * E;
-    if constexpr (VEC) {
 #pragma unroll
-      for (int i = 0; i < NV; i += 4) {
-        const int c = 4 * lane + 32 * i;
-        const float4 q = t < a.T && c < E ? __ldg(reinterpret_cast<const float4 *>(lr + c))
-                                          : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
-      }
-    } else {
+    for (int i = 0; i < NV; i += VW) {
+      const int c = VW * lane + 32 * i;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] = t < a.T && lane + 32 * i < E ? __ldg(lr + lane + 32 * i) : -INFINITY;
+      for (int q = 0; q < VW; ++q) v[i + q] = -INFINITY;
+      if (t < a.T && c < E) load_vec<VW>(lr + c, v + i);
     }
   };
   int64_t t = static_cast<int64_t>(blockIdx.x) * (kGradThreads / 32) + (threadIdx.x >> 5);
@@ -221,27 +238,15 @@ __global__ void __launch_bounds__(kGradThreads, DENSE ? 4 : kGradBlocksPerSm) ga
       z = warp_sum(z);
       const float own = s.e >= 0 ? s.w * s.g : 0.f;
       const float f = z > 0.f ? -warp_sum(own) / z : 0.f;  // (z is the same in all lanes)
-      if constexpr (VEC) {
 #pragma unroll
-        for (int i = 0; i < NV; i += 4)
-          if (4 * lane + 32 * i < E)
-            *reinterpret_cast<float4 *>(out + 4 * lane + 32 * i) = make_float4(v[i] * f, v[i + 1] * f, v[i + 2] * f, v[i + 3] * f);
-      } else {
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-          if (lane + 32 * i < E) out[lane + 32 * i] = v[i] * f;
-      }
+      for (int i = 0; i < NV; i += VW)
+        if (VW * lane + 32 * i < E) store_vec<VW>(out + VW * lane + 32 * i, v + i, f);
       d = fmaf(__expf(l - top), f, own);
     } else {
-      if constexpr (VEC) {
+      const float zero[VW] = {};
 #pragma unroll
-        for (int i = 0; i < NV; i += 4)
-          if (4 * lane + 32 * i < E) *reinterpret_cast<float4 *>(out + 4 * lane + 32 * i) = make_float4(0.f, 0.f, 0.f, 0.f);
-      } else {
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-          if (lane + 32 * i < E) out[lane + 32 * i] = 0.f;
-      }
+      for (int i = 0; i < NV; i += VW)
+        if (VW * lane + 32 * i < E) store_vec<VW>(out + VW * lane + 32 * i, zero, 0.f);
       next = slot_of(t + step);
       float dot = 0.f;
       if (a.renormalise) {
@@ -420,13 +425,13 @@ moe_status moe_gate_backward(const moe_gate_config *cfg, const float *logits, co
   a.sigmoid = cfg->score == MOE_SCORE_SIGMOID;
   a.renormalise = cfg->renormalise != 0;
   a.scale = cfg->scale;
-  const bool dense = !a.sigmoid && !a.renormalise, vec = a.E % 4 == 0;
+  const bool dense = !a.sigmoid && !a.renormalise, two = a.E % 2 == 0, four = a.E % 4 == 0;
   const int64_t wanted = (static_cast<int64_t>(a.T) + kGradThreads / 32 - 1) / (kGradThreads / 32);
-  const int most = kGradBlocksPerSm * di.sms, blocks = static_cast<int>(wanted < most ? wanted : most);
+  const int most = (dense ? kDenseBlocks : kGradBlocks) * di.sms, blocks = static_cast<int>(wanted < most ? wanted : most);
   return timed("gate_backward", s, [&] {
     auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(blocks), dim3(kGradThreads), 0, s, 1, a); };
-    if (dense) return vec ? go(gate_grad_kernel<true, true>) : go(gate_grad_kernel<true, false>);
-    return vec ? go(gate_grad_kernel<false, true>) : go(gate_grad_kernel<false, false>);
+    if (dense) return four ? go(gate_grad_kernel<true, 4>) : two ? go(gate_grad_kernel<true, 2>) : go(gate_grad_kernel<true, 1>);
+    return four ? go(gate_grad_kernel<false, 4>) : two ? go(gate_grad_kernel<false, 2>) : go(gate_grad_kernel<false, 1>);
   });
 }
 
