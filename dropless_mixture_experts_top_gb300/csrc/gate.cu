@@ -307,18 +307,23 @@ bool gate_ok(const moe_gate_config *c) {
   return c->scale > 0.f && c->scale <= FLT_MAX;  // (not where it is NaN)
 }
 
-// Chunks: 32 tokens each while that makes at most six blocks for each of 152 SMs, then more each (four of them fit
-// at once: the others follow as those end, which evens out the blocks with undecided tokens); up to 64 tokens for each of one cluster's
-// blocks are one launch.
-constexpr int kLeastTok = 32, kMostChunks = 608;
+// Chunks: one cluster of blocks up to 512 tokens, which needs no second kernel; then 16 tokens each up to two blocks for each
+// of 152 SMs (4096 x 128, the choice alone, in 128, 256 and 512 chunks: 9.2, 7.3 and 9.7 us), 32 each up to four
+// (16384 x 128 in 304, 512 and 608: 18, 14 and 17 us), then more each (131072 x 256 in 608, 912 and 1216: 89, 98 and 105).
+constexpr int kOneCluster = 512, kTwoBlocks = 304, kFourBlocks = 608;
 struct GateLayout {
   int chunks, cluster;
   size_t flags, before, count, total, bytes;
 };
 GateLayout gate_layout(const moe_gate_config *c) {
   GateLayout L;
-  const int parts = (c->T + kLeastTok - 1) / kLeastTok, most = parts <= 2 * kGateCluster ? kGateCluster : kMostChunks;
-  L.chunks = parts < most ? parts : most;
+  auto parts = [&](int tokens) { return (c->T + tokens - 1) / tokens; };
+  if (c->T <= kOneCluster)
+    L.chunks = parts(32) < kGateCluster ? parts(32) : kGateCluster;
+  else if (parts(32) >= kTwoBlocks)
+    L.chunks = parts(32) < kFourBlocks ? parts(32) : kFourBlocks;
+  else
+    L.chunks = parts(16) < kTwoBlocks ? parts(16) : kTwoBlocks;
   L.cluster = L.chunks < kGateCluster ? (L.chunks < 1 ? 1 : L.chunks) : kGateCluster;
   const size_t clusters = static_cast<size_t>(L.chunks + L.cluster - 1) / L.cluster;
   L.flags = kHeader;
