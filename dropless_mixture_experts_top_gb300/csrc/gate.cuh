@@ -23,8 +23,9 @@
 // all experts in whole vectors, a lane's experts are neighbours (VEC): whole sectors per
 // load, and groups are runs of lanes.
 //
-// Bound by instructions: fewer lanes per token share the steps that pick the next score
-// among more tokens, at the price of longer lists to sort.
+// Bound by instructions (131072 x 256: 317 a token) and by the few warps that its registers leave: fewer lanes per
+// token share the steps between lanes among more tokens, at the price of longer lists to sort, and four
+// blocks an SM without loads ahead hide more than two with (131072 x 256 in 8 groups 72 and 94 us; 16 lanes a token 104).
 #pragma once
 
 #include <float.h>
@@ -573,7 +574,7 @@ __device__ __noinline__ void resolve_token(const GateArgs &a, const float *row, 
 // LPT lanes per token, NV experts per lane: with l the lane's place among the token's, e = l + LPT i, or NV l + i
 // (VEC; E = LPT NV).  KMAX: k at most.
 template <int LPT, int NV, bool VEC, int KEY, bool GROUPS, int KMAX>
-__global__ void __launch_bounds__(kGateThreads, NV == 32 ? 2 : 4) gate_select_kernel(const GateArgs a) {
+__global__ void __launch_bounds__(kGateThreads, 4) gate_select_kernel(const GateArgs a) {
   constexpr int kNear = KEY == kKeyLogit ? 0 : (KEY == kKeySigmoid ? kNearSigmoid : kNearSoftmax);
   constexpr bool KEYS = GROUPS && !VEC;                  // groups by way of shared memory
   static_assert(!KEYS || LPT == 32, "a lane per group");
@@ -626,8 +627,6 @@ __global__ void __launch_bounds__(kGateThreads, NV == 32 ? 2 : 4) gate_select_ke
       for (int i = 0; i < NV; ++i) v[i] = t < last && expert(i) < E ? __ldg(row + expert(i)) : 0.f;
     }
   };
-  float ahead[NV] = {};
-  load(first + warp * TPW + lane / LPT, ahead);
 
   BiasInfo bi{kFixOne - 32.f, kFixOne + kFixLeast, static_cast<int>(kFixLeast), false, 0.f};
   __syncthreads();
@@ -682,13 +681,12 @@ __global__ void __launch_bounds__(kGateThreads, NV == 32 ? 2 : 4) gate_select_ke
     for (int tw = warp * TPW; tw < kGateTok && t0 + tw < last; tw += kStep) {
       const int tl = tw + lane / LPT, t = t0 + tl;
       const bool valid = t < last;
-      float x[NV], fin = 0.f;
+      float x[NV] = {}, fin = 0.f;
+      load(t, x);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        x[i] = ahead[i];
         fin = fmaf(x[i], 0.f, fin);  // NaN where one is not finite
       }
-      load(t + kStep, ahead);  // (of the next round after the last)
       const bool odd = __any_sync(0xffffffffu, fin != 0.f);
       uint32_t off = 0;  // experts that may not be chosen
       if (odd) {
