@@ -21,6 +21,12 @@
 // Tiles that do not fill a last round are split along the reduction, so that the round
 // is full: their parts leave fp32 sums in the workspace, which a second kernel adds in
 // a fixed order before the same epilogue.
+//
+// What bounds it, measured (graphs of ten calls): 16384 x 4096 x 4096 280 us, 1970 TFLOP/s (a library's
+// product 269); 16384 x 1536 x 4096 114 us, 101 without the epilogue's stores, 126 with a residual, 135 with bias and
+// gelu (which stores z, too): the tensor pipe is busy 72% of the time with residual.  Back to back the part's
+// power cap holds both to 1.4e15 per second.  The backward of 16384 x 4096 x 1536 with silu takes 275: 118 for each
+// product, 45 for dz and dbias.  Few tiles: 4 us and 0.46 us for each 128 of the reduction, 5 more in parts.
 // Every wait is bounded; on a timeout the kernel flags the status word, drains its
 // copies and MMAs, frees TMEM and returns.
 #include <cuda.h>
