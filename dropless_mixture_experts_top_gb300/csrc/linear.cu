@@ -20,7 +20,8 @@
 //   warps 2-9  epilogue: tcgen05.ld, bias, activation, residual, bf16 rows
 // Tiles that do not fill a last round are split along the reduction, so that the round
 // is full: their parts leave fp32 sums in the workspace, which a second kernel adds in
-// a fixed order before the same epilogue.
+// a fixed order before the same epilogue.  Where the tiles of dx and dW are one round
+// together, one launch takes both.
 //
 // What bounds it, measured (graphs of ten calls): 16384 x 4096 x 4096 280 us, 1970 TFLOP/s (a library's
 // product 269); 16384 x 1536 x 4096 114 us, 101 without the epilogue's stores, 126 with a residual, 135 with bias and
@@ -55,7 +56,7 @@ constexpr int kRuleSms = 152;         // the workspace's size is known without a
 constexpr int kMaxSplit = 16;
 constexpr int kLeastStages = 4;       // of a part of a split reduction
 
-enum Product : int { kFwd = 0, kDx = 1, kDw = 2 };
+enum Product : int { kFwd = 0, kDx = 1, kDw = 2, kBoth = 3 };  // kBoth: dx and dW in one launch
 
 struct Ends {  // what an epilogue adds and writes
   const uint16_t *bias, *res;
@@ -234,8 +235,8 @@ __device__ __forceinline__ void finish_row(float (&v)[32], const Ends &e, const 
 
 // ---------------------------------------------------------------- the product
 
-template <bool MN, int CG>
-__device__ __forceinline__ void load_operand(uint8_t *dst, const CUtensorMap *map, uint64_t *bar, uint32_t bar0, int k0,
+template <int CG>
+__device__ __forceinline__ void load_operand(bool mn, uint8_t *dst, const CUtensorMap *map, uint64_t *bar, uint32_t bar0, int k0,
                                              int r0) {
   auto load = [&](uint8_t *to, int x, int y) {
     if constexpr (CG == 2)
@@ -243,7 +244,7 @@ __device__ __forceinline__ void load_operand(uint8_t *dst, const CUtensorMap *ma
     else
       tma_load_2d(to, map, bar, x, y);
   };
-  if constexpr (MN) {
+  if (mn) {
     load(dst, r0, k0);
     load(dst + kBox, r0 + 64, k0);
   } else {
@@ -258,10 +259,15 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t s, int j, bool mn) {
 template <int KIND, int CG>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     linear_product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
-                          const __grid_constant__ CUtensorMap tmB, const ProductArgs p) {
+                          const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmA2,
+                          const __grid_constant__ CUtensorMap tmB2, const ProductArgs p1, const ProductArgs p2) {
   constexpr int TS = tile_size(CG);
   constexpr uint32_t kTmemCols = 2 * TS;
-  constexpr bool AMN = KIND == kDw, BMN = KIND != kDx;
+  // kBoth: a tile per block, those of dx first
+  const bool second = KIND == kBoth && static_cast<int>(blockIdx.x) >= p1.units;
+  const ProductArgs &p = second ? p2 : p1;
+  const bool amn = KIND == kBoth ? second : KIND == kDw, bmn = KIND == kBoth ? second : KIND != kDx;
+  const CUtensorMap *const mA = second ? &tmA2 : &tmA, *const mB = second ? &tmB2 : &tmB;
   constexpr int kChunks = TS / 64;  // 32-column chunks of a warp's half of the columns
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem =
@@ -276,7 +282,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CG == 2 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int group = blockIdx.x / CG, ngroups = gridDim.x / CG;
+  const int group = blockIdx.x / CG - (second ? p1.units : 0), ngroups = gridDim.x / CG;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -291,9 +297,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tmA);
-    if (!AMN) tma_prefetch_desc(&tmA32);
-    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(mA);
+    if (!amn) tma_prefetch_desc(&tmA32);
+    tma_prefetch_desc(mB);
   }
   if (warp == 1) {
     if constexpr (CG == 2)
@@ -303,7 +309,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
   griddep_wait();  // the set-up above overlaps the previous kernel's end; its outputs are read below
   // (a wait that runs out takes two seconds: no block flags one before this)
-  if (p.first && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
+  if (p1.first && blockIdx.x == 0 && threadIdx.x == 0) *p1.status = 0;
   tc_fence_before();
   __syncthreads();
   if constexpr (CG == 2) cluster_sync();  // both CTAs' barriers initialised before any remote arrival
@@ -322,7 +328,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         // Rows of A contiguous along K: where they end inside a CTA's 128, only the boxes of 32 that hold some (the MMA
         // reads what was there before in the others, whose sums are never stored).  With whole boxes a single row took
         // 17.4 us for 4096 x 4096.
-        auto boxes = [&](int r) { return AMN ? 4 : max(0, min(4, (p.M - (t.m0 + BM * r) + 31) / 32)); };
+        auto boxes = [&](int r) { return amn ? 4 : max(0, min(4, (p.M - (t.m0 + BM * r) + 31) / 32)); };
         const int mine = boxes(rank);
         const uint32_t bytes = CG * kStageBytes - (CG * 4 - boxes(0) - (CG == 2 ? boxes(1) : 0)) * (2 * 32 * BK * 2);
         for (int ks = t.ks0; ks < t.ks1; ++ks) {
@@ -337,12 +343,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           for (int h = 0; h < 2; ++h) {
             const int k0 = (ks * 2 + h) * BK;
             if (mine == 4)
-              load_operand<AMN, CG>(sa + h * kHalf, &tmA, &full[stage], full0 + 8u * stage, k0, t.m0 + BM * rank);
+              load_operand<CG>(amn, sa + h * kHalf, mA, &full[stage], full0 + 8u * stage, k0, t.m0 + BM * rank);
             else
               for (int b = 0; b < mine; ++b)
-                load_operand<false, CG>(sa + h * kHalf + b * (32 * BK * 2), &tmA32, &full[stage], full0 + 8u * stage, k0,
-                                        t.m0 + BM * rank + 32 * b);
-            load_operand<BMN, CG>(sa + (2 + h) * kHalf, &tmB, &full[stage], full0 + 8u * stage, k0, t.n0 + BM * rank);
+                load_operand<CG>(false, sa + h * kHalf + b * (32 * BK * 2), &tmA32, &full[stage], full0 + 8u * stage, k0,
+                                 t.m0 + BM * rank + 32 * b);
+            load_operand<CG>(bmn, sa + (2 + h) * kHalf, mB, &full[stage], full0 + 8u * stage, k0, t.n0 + BM * rank);
           }
           armed |= 1u << stage;
           arm_par = (arm_par & ~(1u << stage)) | (phase << stage);
@@ -376,7 +382,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         else
           tc_commit(bar);
       };
-      constexpr uint32_t idesc = idesc_bf16(TS, TS, AMN, BMN);
+      const uint32_t idesc = idesc_bf16(TS, TS, amn, bmn);
       int stage = 0, it = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -399,7 +405,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             if (h < nblk) {
 #pragma unroll
               for (int j = 0; j < BK / 16; ++j)
-                mma(d, operand_desc(ab + h * kHalf, j, AMN), operand_desc(bb + h * kHalf, j, BMN), idesc,
+                mma(d, operand_desc(ab + h * kHalf, j, amn), operand_desc(bb + h * kHalf, j, bmn), idesc,
                     (ks != t.ks0 || (h | j) != 0) ? 1u : 0u);
             }
           }
@@ -671,12 +677,12 @@ Cut cut_of(int64_t M, int64_t N, int64_t K, int sms) {
 }
 constexpr size_t kPartBytes = static_cast<size_t>(kRuleSms) * BM * BM * 4 * 2;  // parts of a round of pairs (or singles)
 
+// The kernel's shared-memory opt-in, and how many groups of CTAs fit at once; once per device.
 template <int KIND, int CG>
-cudaError_t launch_cut(const CUtensorMap &a, const CUtensorMap &a32, const CUtensorMap &b, ProductArgs p, const Cut &c, int sms, cudaStream_t s) {
-  static DeviceOnce once;  // the shared-memory opt-in, and how many groups of CTAs fit at once
+cudaError_t groups_of(int sms, int *groups) {
+  static DeviceOnce once;
   auto kernel = linear_product_kernel<KIND, CG>;
-  int groups = 0;
-  cudaError_t e = once.get(
+  return once.get(
       [&](int *out) {
         cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
         if (r != cudaSuccess) return r;
@@ -697,27 +703,20 @@ cudaError_t launch_cut(const CUtensorMap &a, const CUtensorMap &a32, const CUten
         *out = n < sms / CG ? n : sms / CG;
         return cudaSuccess;
       },
-      &groups);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(kernel, dim3(static_cast<unsigned>(CG * std::min(c.units, groups))), dim3(kGemmThreads), kGemmSmem, s, CG, a,
-                 a32, b, p);
-  if (e != cudaSuccess || c.split == 1) return e;
-  constexpr int TS = tile_size(CG);
-  const int64_t threads = static_cast<int64_t>(c.nm * c.nn - c.full) * (TS / 32) * (TS / 32) * 32;
-  return launch_pdl(linear_finish_kernel<KIND, CG>, dim3(static_cast<unsigned>((threads + kFinishThreads - 1) / kFinishThreads)),
-                    dim3(kFinishThreads), 0, s, 1, p);
+      groups);
 }
 
-// One product [M,N] over K of a (its rows contiguous along K, or along M where KIND is kDw) and b.
-template <int KIND>
-moe_status product(const char *label, const void *a, const void *b, int M, int N, int K, const Ends &ends, float *part,
-                   int32_t *status, bool first, int sms, cudaStream_t s) {
-  const Cut c = cut_of(M, N, K, std::min(sms, kRuleSms));
-  CUtensorMap ma, ma32, mb;
-  const bool ok = (KIND == kDw ? map2(&ma, a, M, K, 64) : map2(&ma, a, K, M, 128)) &&
-                  (KIND == kDw ? map2(&ma32, a, M, K, 64) : map2(&ma32, a, K, M, 32)) &&
-                  (KIND == kDx ? map2(&mb, b, K, N, 128) : map2(&mb, b, N, K, 64));
-  if (!ok) return MOE_ERR_CUDA;
+// One product [M,N] over K of a (its rows contiguous along K, or along M for dW) and b: its maps and arguments.
+struct Operands {
+  CUtensorMap a, a32, b;
+  ProductArgs p;
+};
+bool operands(Operands *o, int kind, const void *a, const void *b, int M, int N, int K, const Cut &c, const Ends &ends,
+              float *part, int32_t *status, bool first) {
+  if (!(kind == kDw ? map2(&o->a, a, M, K, 64) : map2(&o->a, a, K, M, 128)) ||
+      !(kind == kDw ? map2(&o->a32, a, M, K, 64) : map2(&o->a32, a, K, M, 32)) ||
+      !(kind == kDx ? map2(&o->b, b, K, N, 128) : map2(&o->b, b, N, K, 64)))
+    return false;
   ProductArgs p{};
   p.M = M;
   p.N = N;
@@ -733,8 +732,56 @@ moe_status product(const char *label, const void *a, const void *b, int M, int N
   p.e.sectors = N % 16 == 0 && al32(ends.res) && al32(ends.y) && al32(ends.z);
   p.status = status;
   p.first = first;
-  return timed(label, s, [&] {
-    return c.cg == 2 ? launch_cut<KIND, 2>(ma, ma32, mb, p, c, sms, s) : launch_cut<KIND, 1>(ma, ma32, mb, p, c, sms, s);
+  o->p = p;
+  return true;
+}
+
+template <int KIND, int CG>
+cudaError_t launch_cut(const Operands &o, const Cut &c, int sms, cudaStream_t s) {
+  int groups = 0;
+  cudaError_t e = groups_of<KIND, CG>(sms, &groups);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(linear_product_kernel<KIND, CG>, dim3(static_cast<unsigned>(CG * std::min(c.units, groups))),
+                 dim3(kGemmThreads), kGemmSmem, s, CG, o.a, o.a32, o.b, o.a, o.b, o.p, o.p);
+  if (e != cudaSuccess || c.split == 1) return e;
+  constexpr int TS = tile_size(CG);
+  const int64_t threads = static_cast<int64_t>(c.nm * c.nn - c.full) * (TS / 32) * (TS / 32) * 32;
+  return launch_pdl(linear_finish_kernel<KIND, CG>, dim3(static_cast<unsigned>((threads + kFinishThreads - 1) / kFinishThreads)),
+                    dim3(kFinishThreads), 0, s, 1, o.p);
+}
+
+template <int KIND>
+moe_status product(const char *label, const void *a, const void *b, int M, int N, int K, const Ends &ends, float *part,
+                   int32_t *status, bool first, int sms, cudaStream_t s) {
+  const Cut c = cut_of(M, N, K, std::min(sms, kRuleSms));
+  Operands o;
+  if (!operands(&o, KIND, a, b, M, N, K, c, ends, part, status, first)) return MOE_ERR_CUDA;
+  return timed(label, s, [&] { return c.cg == 2 ? launch_cut<KIND, 2>(o, c, sms, s) : launch_cut<KIND, 1>(o, c, sms, s); });
+}
+
+// dx and dW in one launch (*done), where their tiles of single CTAs are one round together and that is not longer than the
+// two one after the other: tokens, in, out in one and in two launches: 16 x 1024 x 1024 8.4 us and 12.4; 777 x 1000 x 520
+// 13.3 and 19.8; 2048 x 512 x 512 15.7 and 16.5; by the rule in two: 3000 x 384 x 384 20.9 and 18.0, 8192 x 128 x 128 42.2
+// and 18.0 (their dW is cut along the tokens).
+moe_status both_products(const void *dz, const void *W, const void *x, int T, int K, int N, const Ends &dx, const Ends &dw,
+                         int32_t *status, bool first, int sms, cudaStream_t s, bool *done) {
+  const int most = std::min(sms, kRuleSms);
+  const Cut cx = cut_with(T, K, N, 1, false, most), cw = cut_with(K, N, T, 1, false, most);
+  *done = false;
+  if (static_cast<int64_t>(cx.units) + cw.units > most ||
+      std::max(cx.cost, cw.cost) > cut_of(T, K, N, most).cost + cut_of(K, N, T, most).cost)
+    return MOE_OK;
+  int groups = 0;
+  if (groups_of<kBoth, 1>(sms, &groups) != cudaSuccess) return MOE_ERR_CUDA;
+  if (cx.units + cw.units > groups) return MOE_OK;
+  Operands ox, ow;
+  if (!operands(&ox, kDx, dz, W, T, K, N, cx, dx, nullptr, status, first) ||
+      !operands(&ow, kDw, x, dz, K, N, T, cw, dw, nullptr, status, first))
+    return MOE_ERR_CUDA;
+  *done = true;
+  return timed("linear_dx_dW", s, [&] {
+    return launch_pdl(linear_product_kernel<kBoth, 1>, dim3(static_cast<unsigned>(cx.units + cw.units)), dim3(kGemmThreads),
+                      kGemmSmem, s, 1, ox.a, ox.a32, ox.b, ow.a, ow.b, ox.p, ow.p);
   });
 }
 
@@ -846,17 +893,16 @@ moe_status moe_linear_backward(const moe_linear_config *cfg, const void *dy, con
     if (act) dz = a.dz;
     first = false;
   }
-  if (dx) {
-    Ends e{};
-    e.y = static_cast<uint16_t *>(dx);
-    MOE_TRY(product<kDx>("linear_dx", dz, W, T, K, N, e, part, status, first, di.sms, s));
+  Ends ex{}, ew{};
+  ex.y = static_cast<uint16_t *>(dx);
+  ew.y = static_cast<uint16_t *>(dW);
+  bool done = false;
+  if (dx && dW) MOE_TRY(both_products(dz, W, x, T, K, N, ex, ew, status, first, di.sms, s, &done));
+  if (dx && !done) {
+    MOE_TRY(product<kDx>("linear_dx", dz, W, T, K, N, ex, part, status, first, di.sms, s));
     first = false;
   }
-  if (dW) {
-    Ends e{};
-    e.y = static_cast<uint16_t *>(dW);
-    MOE_TRY(product<kDw>("linear_dW", x, dz, K, N, T, e, part, status, first, di.sms, s));
-  }
+  if (dW && !done) MOE_TRY(product<kDw>("linear_dW", x, dz, K, N, T, ew, part, status, first, di.sms, s));
   return MOE_OK;
 }
 

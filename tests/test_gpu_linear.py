@@ -170,6 +170,21 @@ def test_single_gradients_and_reused_buffers():
         assert torch.equal(none.backward(dy, x, W, grads=g)[n], full[n])
 
 
+# the two products in one launch or in two, of one round or more, whole or in parts
+@pytest.mark.parametrize("T,K,N", [(1, 1024, 1024), (16, 1024, 1024), (100, 1536, 1408), (100, 1544, 1408), (2048, 512, 512),
+                                   (3000, 384, 384), (8192, 128, 128), (9729, 128, 8), (64, 4096, 256), (1000, 264, 1000)])
+def test_both_products_and_each_alone(T, K, N):
+    x, W, dy = whole(T, K, seed=1), whole(K, N, seed=2), whole(T, N, seed=3)
+    lin = moe.Linear(T, K, N, bias=False)
+    full = lin.backward(dy, x, W)
+    assert torch.equal(full["dx"], (dy.double() @ W.double().T).to(BF))
+    assert torch.equal(full["dW"], (x.double().T @ dy.double()).to(BF))
+    for n in ("dx", "dW"):
+        g = {"dx": None, "dW": None, "dbias": None, n: torch.full_like(full[n], 3)}
+        assert torch.equal(lin.backward(dy, x, W, grads=g)[n], full[n])
+    assert lin.status() == {"last": 0}
+
+
 def test_the_residual_in_place_and_int16_views():
     T, K, N = 700, 264, 392
     x, W, b, r = whole(T, K, seed=1), whole(K, N, seed=2), whole(N, seed=3), whole(T, N, seed=4)
