@@ -26,8 +26,8 @@
 // What bounds it, measured (graphs of ten calls): 16384 x 4096 x 4096 280 us, 1970 TFLOP/s (a library's
 // product 269); 16384 x 1536 x 4096 114 us, 101 without the epilogue's stores, 126 with a residual, 135 with bias and
 // gelu (which stores z, too): the tensor pipe is busy 72% of the time with residual.  Back to back the part's
-// power cap holds both to 1.4e15 per second.  The backward of 16384 x 4096 x 1536 with silu takes 275: 118 for each
-// product, 45 for dz and dbias.  Few tiles: 4 us and 0.46 us for each 128 of the reduction, 5 more in parts.
+// power cap holds both to 1.4e15 per second.  The backward of 16384 x 4096 x 1536 with silu takes 260: 117 for each
+// product, 27 for dz and dbias.  Few tiles: 4 us and 0.46 us for each 128 of the reduction, 5 more in parts.
 // Every wait is bounded; on a timeout the kernel flags the status word, drains its
 // copies and MMAs, frees TMEM and returns.
 #include <cuda.h>
@@ -531,19 +531,27 @@ __global__ void __launch_bounds__(kFinishThreads) linear_finish_kernel(const Pro
 // dz = dy act'(z) in bf16 (where there is an activation), and the column sums of it unrounded.  A block
 // takes 64 columns and every `split`-th run of rows: 8 threads a row, 32 rows at once; its sums over
 // those go to a partial row, which the second kernel adds in order.
+// Bound by HBM, with its loads in flight: 16384 x 1536 and 16384 x 4096 with silu 26.7 and 64.4 us with the second kernel, 84%
+// and 93% of the copy rate.  Three rows ahead at four blocks an SM, which are one wave; with one thread a column in the second
+// kernel 28.8 and 65.9, four rows ahead at three blocks an SM 28.7 and 66.4, two at four 29.6 and 69.8; more blocks than fit
+// at once 45.0 and 106.5.
 
-constexpr int kDzThreads = 256, kDzCols = 64, kDzRows = kDzThreads / 8;
-constexpr int kDzSplit = 64;  // partial rows at most
+constexpr int kDzThreads = 256, kDzCols = 64, kDzRows = kDzThreads / 8, kDzAhead = 3, kDzPerSm = 4;
+// how many blocks share a run of 64 columns: one wave, of at least kDzAhead rows a thread
+int dz_split(int T, int N) {
+  const int cols = (N + kDzCols - 1) / kDzCols, rounds = (T + kDzRows * kDzAhead - 1) / (kDzRows * kDzAhead);
+  return std::max(1, std::min(kDzPerSm * kRuleSms / cols, rounds));
+}
 struct DzArgs {
   const uint16_t *dy, *z;
   uint16_t *dz;    // null: no activation, dy itself
   float *part;     // [split][N], or null: no bias
   float *dbias;
-  int T, N, act, split;
+  int T, N, split;
   int32_t *status;
 };
-template <bool ACT>
-__global__ void __launch_bounds__(kDzThreads) linear_dz_kernel(const DzArgs a) {
+template <int ACT>
+__global__ void __launch_bounds__(kDzThreads, kDzPerSm) linear_dz_kernel(const DzArgs a) {
   __shared__ float s_sum[kDzRows / 4][kDzCols];
   griddep_wait();  // the previous kernel in the stream has completed
   griddep_launch_dependents();
@@ -552,7 +560,7 @@ __global__ void __launch_bounds__(kDzThreads) linear_dz_kernel(const DzArgs a) {
   const int step = kDzRows * a.split;
   float sum[8] = {};
   if (c < a.N) {
-    constexpr int kAhead = ACT ? 4 : 8;
+    constexpr int kAhead = ACT != MOE_ACT_NONE ? kDzAhead : 2 * kDzAhead;
     for (int64_t t0 = blockIdx.y * kDzRows + (threadIdx.x >> 3); t0 < a.T; t0 += static_cast<int64_t>(step) * kAhead) {
       uint4 dy[kAhead], z[kAhead];
 #pragma unroll
@@ -560,7 +568,7 @@ __global__ void __launch_bounds__(kDzThreads) linear_dz_kernel(const DzArgs a) {
         const int64_t t = t0 + static_cast<int64_t>(i) * step;
         if (t < a.T) {
           dy[i] = __ldg(reinterpret_cast<const uint4 *>(a.dy + t * a.N + c));
-          if (ACT) z[i] = __ldg(reinterpret_cast<const uint4 *>(a.z + t * a.N + c));
+          if (ACT != MOE_ACT_NONE) z[i] = __ldg(reinterpret_cast<const uint4 *>(a.z + t * a.N + c));
         }
       }
 #pragma unroll
@@ -574,12 +582,12 @@ __global__ void __launch_bounds__(kDzThreads) linear_dz_kernel(const DzArgs a) {
           v[2 * h] = bf16_lo(y[h]);
           v[2 * h + 1] = bf16_hi(y[h]);
         }
-        if constexpr (ACT) {
+        if constexpr (ACT != MOE_ACT_NONE) {
           const uint32_t x[4] = {z[i].x, z[i].y, z[i].z, z[i].w};
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
-            v[2 * h] *= slope(bf16_lo(x[h]), a.act);
-            v[2 * h + 1] *= slope(bf16_hi(x[h]), a.act);
+            v[2 * h] *= slope(bf16_lo(x[h]), ACT);
+            v[2 * h + 1] *= slope(bf16_hi(x[h]), ACT);
           }
           *reinterpret_cast<uint4 *>(a.dz + t * a.N + c) =
               make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
@@ -609,14 +617,22 @@ __global__ void __launch_bounds__(kDzThreads) linear_dz_kernel(const DzArgs a) {
     (a.split == 1 ? a.dbias : a.part + static_cast<int64_t>(blockIdx.y) * a.N)[col] = s;
   }
 }
-__global__ void __launch_bounds__(128) linear_dbias_kernel(const float *part, int split, int N, float *dbias) {
+// 32 columns a block, a warp each for every eighth partial row
+__global__ void __launch_bounds__(kDzThreads) linear_dbias_kernel(const float *part, int split, int N, float *dbias) {
+  __shared__ float s_sum[kDzThreads / 32][32];
   griddep_wait();  // the previous kernel in the stream has completed
   griddep_launch_dependents();
-  const int c = blockIdx.x * 128 + threadIdx.x;
-  if (c >= N) return;
+  const int c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
   float s = 0.f;
-#pragma unroll 16
-  for (int i = 0; i < split; ++i) s += __ldcg(part + static_cast<int64_t>(i) * N + c);
+  if (c < N) {
+#pragma unroll 8
+    for (int i = w; i < split; i += kDzThreads / 32) s += __ldcg(part + static_cast<int64_t>(i) * N + c);
+  }
+  s_sum[w][threadIdx.x & 31] = s;
+  __syncthreads();
+  if (w || c >= N) return;
+#pragma unroll
+  for (int i = 1; i < kDzThreads / 32; ++i) s += s_sum[i][threadIdx.x];
   dbias[c] = s;
 }
 
@@ -801,7 +817,7 @@ LinearLayout linear_layout(const moe_linear_config *c) {
   L.fwd = L.part + kPartBytes;
   L.dz = L.fwd;
   L.sums = L.dz + (c->act == MOE_ACT_NONE ? 0 : align256(static_cast<size_t>(c->T) * c->N * 2));
-  L.bwd = L.sums + align256(static_cast<size_t>(kDzSplit) * c->N * 4);
+  L.bwd = L.sums + align256(static_cast<size_t>(dz_split(c->T, c->N)) * c->N * 4);
   return L;
 }
 
@@ -876,19 +892,19 @@ moe_status moe_linear_backward(const moe_linear_config *cfg, const void *dy, con
     a.part = dbias ? reinterpret_cast<float *>(sc + L.sums) : nullptr;
     a.T = T;
     a.N = N;
-    a.act = cfg->act;
     a.status = status;
-    // enough blocks for four on each SM, of at least four rows a thread
-    const int cols = (N + kDzCols - 1) / kDzCols, rounds = (T + kDzRows * 4 - 1) / (kDzRows * 4);
-    a.split = std::max(1, std::min({(4 * di.sms + cols - 1) / cols, rounds, kDzSplit}));
-    MOE_TRY(timed("linear_dz", s, [&] { 
-      return act ? launch_pdl(linear_dz_kernel<true>, dim3(cols, a.split), dim3(kDzThreads), 0, s, 1, a)
-                 : launch_pdl(linear_dz_kernel<false>, dim3(cols, a.split), dim3(kDzThreads), 0, s, 1, a);
+    a.split = dz_split(T, N);
+    const auto kernel = cfg->act == MOE_ACT_RELU   ? linear_dz_kernel<MOE_ACT_RELU>
+                        : cfg->act == MOE_ACT_SILU ? linear_dz_kernel<MOE_ACT_SILU>
+                        : cfg->act == MOE_ACT_GELU ? linear_dz_kernel<MOE_ACT_GELU>
+                                                   : linear_dz_kernel<MOE_ACT_NONE>;
+    MOE_TRY(timed("linear_dz", s, [&] {
+      return launch_pdl(kernel, dim3((N + kDzCols - 1) / kDzCols, a.split), dim3(kDzThreads), 0, s, 1, a);
     }));
     if (dbias && a.split > 1)
       MOE_TRY(timed("linear_dbias", s, [&] {
-        return launch_pdl(linear_dbias_kernel, dim3((N + 127) / 128), dim3(128), 0, s, 1, static_cast<const float *>(a.part),
-                          a.split, N, dbias);
+        return launch_pdl(linear_dbias_kernel, dim3((N + 31) / 32), dim3(kDzThreads), 0, s, 1,
+                          static_cast<const float *>(a.part), a.split, N, dbias);
       }));
     if (act) dz = a.dz;
     first = false;
