@@ -21,7 +21,8 @@
 // Tiles that do not fill a last round are split along the reduction, so that the round
 // is full: their parts leave fp32 sums in the workspace, which a second kernel adds in
 // a fixed order before the same epilogue.  Where the tiles of dx and dW are one round
-// together, one launch takes both.
+// together, one launch takes both.  The forward of a few tokens is a pass over W on the
+// CUDA cores (linear_rows_kernel).
 //
 // What bounds it, measured (graphs of ten calls): 16384 x 4096 x 4096 280 us, 1970 TFLOP/s (a library's
 // product 269); 16384 x 1536 x 4096 114 us, 101 without the epilogue's stores, 126 with a residual, 135 with bias and
@@ -526,6 +527,126 @@ __global__ void __launch_bounds__(kFinishThreads) linear_finish_kernel(const Pro
   if (row < p.M) finish_row<KIND>(v, p.e, res, at, col, min(32, p.N - col));
 }
 
+// a b + c of two floats, one instruction for both.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n.reg .b64 a, b, c;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmov.b64 c, {%6, %7};\n"
+      "fma.rn.f32x2 c, a, b, c;\nmov.b64 {%0, %1}, c;\n}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+// A float of a block of the cluster.
+__device__ __forceinline__ float ld_peer(const float *p, uint32_t rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer_smem_addr(p, rank)) : "memory");
+  return v;
+}
+
+// ---------------------------------------------------------------- a few tokens
+//
+// y of at most TM tokens, on the CUDA cores: a pass over W, which is all that it has to read.  A thread takes 8 columns of 8
+// rows of W at a time, CT threads side by side a block's columns; a cluster's blocks share the rows, as many as are one wave.
+// Sums over the lanes, the warps and the cluster's blocks, in that order, in fp32.
+// Bound by W's bytes, and for small W by the launch: one token and W from HBM, 4096 x 4096 8.4 us, 60% of the copy rate, 7168 x
+// 18432 43.4, 91%, 1024 x 1024 2.8; a library's product 8.6, 40.6, 2.8, the tensor cores' tiles 12.5, 46.5, 6.9.
+
+constexpr int kRowThreads = 256;
+// For up to two tokens, and up to eight while the products take no longer than the tiles' part sums.  Here and in tiles: 8 x
+// 1024 x 1024 4.4 us and 6.9, 8 x 4096 x 1536 8.9 and 9.5, 8 x 4096 x 4096 13.1 and 12.4, 4 x 4096 x 4096 10.5 and 12.5,
+// 4 x 7168 x 18432 48.9 and 46.2, 2 x 7168 x 18432 46.4 and 46.0.
+bool few_rows(int64_t T, int64_t K, int64_t N) { return T <= 2 || (T <= 8 && T * K * N < 1 << 27); }
+// 16 columns a block up to here, else 64: one token, 16384 x 64 4.4 and 5.7 us, 1024 x 1024 2.8 and 3.0, 4096 x 1536 6.8 and 5.7.
+constexpr int kNarrow = 1024;
+constexpr int rows_per_sm(int tm) { return tm == 1 ? 4 : tm == 2 ? 3 : 2; }  // blocks an SM holds
+struct RowArgs {
+  const uint16_t *x, *W;
+  Ends e;
+  int T, K, N;
+  int parts, per;  // blocks that share a run of columns, and their 8 rows each
+  int32_t *status;
+};
+template <int TM, int CT>
+__global__ void __launch_bounds__(kRowThreads, rows_per_sm(TM)) linear_rows_kernel(const RowArgs a) {
+  constexpr int kCols = 8 * CT, kGroups = kRowThreads / CT, kWarps = kRowThreads / 32;
+  __shared__ float s_sum[kWarps][TM][kCols];
+  __shared__ float s_out[TM * kCols];
+  griddep_wait();  // the previous kernel in the stream has completed
+  griddep_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
+  const int part = blockIdx.x % a.parts, c0 = blockIdx.x / a.parts * kCols, c = c0 + threadIdx.x % CT * 8;
+  float2 sum[TM][4] = {};
+  if (c < a.N) {
+    const int end = min(a.K / 8, (part + 1) * a.per);
+    for (int u = part * a.per + threadIdx.x / CT; u < end; u += kGroups) {
+      uint4 w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = __ldg(reinterpret_cast<const uint4 *>(a.W + (8 * static_cast<int64_t>(u) + i) * a.N + c));
+      constexpr int kAt = TM < 4 ? TM : 4;  // tokens whose x is held at once
+#pragma unroll
+      for (int t0 = 0; t0 < TM; t0 += kAt) {
+        uint4 xv[kAt];
+#pragma unroll
+        for (int t = 0; t < kAt; ++t)
+          xv[t] = t0 + t < a.T ? __ldg(reinterpret_cast<const uint4 *>(a.x + static_cast<int64_t>(t0 + t) * a.K + 8 * u)) : uint4{};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t wi[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+          float2 wf[4];
+#pragma unroll
+          for (int h = 0; h < 4; ++h) wf[h] = make_float2(bf16_lo(wi[h]), bf16_hi(wi[h]));
+#pragma unroll
+          for (int t = 0; t < kAt; ++t) {
+            const uint32_t two = i < 2 ? xv[t].x : i < 4 ? xv[t].y : i < 6 ? xv[t].z : xv[t].w;
+            const float xi = i & 1 ? bf16_hi(two) : bf16_lo(two);
+#pragma unroll
+            for (int h = 0; h < 4; ++h) sum[t0 + t][h] = fma2(make_float2(xi, xi), wf[h], sum[t0 + t][h]);
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < TM; ++t) {
+#pragma unroll
+    for (int h = 0; h < 8; ++h) {
+      float v = h & 1 ? sum[t][h / 2].y : sum[t][h / 2].x;
+#pragma unroll
+      for (int d = CT; d < 32; d *= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
+      if ((threadIdx.x & 31) < CT) s_sum[threadIdx.x >> 5][t][(threadIdx.x & 31) * 8 + h] = v;
+    }
+  }
+  __syncthreads();
+  const int n = a.T * kCols;
+  for (int i = threadIdx.x; i < n; i += kRowThreads) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v += s_sum[w][i / kCols][i % kCols];
+    s_out[i] = v;
+  }
+  if (a.parts > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  const int mine = (n + a.parts - 1) / a.parts;
+  for (int i = part * mine + threadIdx.x; i < min(n, (part + 1) * mine); i += kRowThreads) {
+    const int col = c0 + i % kCols;
+    if (col >= a.N) continue;
+    const int64_t at = static_cast<int64_t>(i / kCols) * a.N + col;
+    float v = 0.f;
+    if (a.parts > 1)
+      for (int r = 0; r < a.parts; ++r) v += ld_peer(&s_out[i], r);
+    else
+      v = s_out[i];
+    if (a.e.bias) v += bf16_lo(a.e.bias[col]);
+    if (a.e.z) a.e.z[at] = static_cast<uint16_t>(pack_bf16x2(v, 0.f));
+    v = activate(v, a.e.act);
+    if (a.e.res) v += bf16_lo(a.e.res[at]);
+    a.e.y[at] = static_cast<uint16_t>(pack_bf16x2(v, 0.f));
+  }
+  if (a.parts > 1) cluster_sync();  // before a block leaves that others read
+}
+
 // ---------------------------------------------------------------- dz and dbias
 //
 // dz = dy act'(z) in bf16 (where there is an activation), and the column sums of it unrounded.  A block
@@ -801,6 +922,19 @@ moe_status both_products(const void *dz, const void *W, const void *x, int T, in
   });
 }
 
+template <int TM, int CT>
+cudaError_t launch_rows(RowArgs a, cudaStream_t s) {
+  const int tiles = (a.N + 8 * CT - 1) / (8 * CT), units = a.K / 8;
+  a.parts = 1;
+  while (a.parts < 8 && 2 * a.parts * tiles <= rows_per_sm(TM) * kRuleSms && units >= 2 * a.parts * (kRowThreads / CT)) a.parts *= 2;
+  a.per = (units + a.parts - 1) / a.parts;
+  return launch_pdl(linear_rows_kernel<TM, CT>, dim3(static_cast<unsigned>(tiles * a.parts)), dim3(kRowThreads), 0, s, a.parts, a);
+}
+template <int TM>
+cudaError_t rows_of(const RowArgs &a, cudaStream_t s) {
+  return a.N > kNarrow ? launch_rows<TM, 8>(a, s) : launch_rows<TM, 2>(a, s);
+}
+
 bool linear_ok(const moe_linear_config *c) {
   if (!c || c->T < 0 || c->T > (1 << 30)) return false;
   if (c->K < 8 || c->K > kMaxDim || c->K % 8 || c->N < 8 || c->N > kMaxDim || c->N % 8) return false;
@@ -854,6 +988,19 @@ moe_status moe_linear_forward(const moe_linear_config *cfg, const void *x, const
   e.y = static_cast<uint16_t *>(y);
   e.z = static_cast<uint16_t *>(z);
   e.act = cfg->act;
+  if (few_rows(cfg->T, cfg->K, cfg->N)) {
+    RowArgs a{};
+    a.x = static_cast<const uint16_t *>(x);
+    a.W = static_cast<const uint16_t *>(W);
+    a.e = e;
+    a.T = cfg->T;
+    a.K = cfg->K;
+    a.N = cfg->N;
+    a.status = reinterpret_cast<int32_t *>(sc);
+    return timed("linear_forward", s, [&] {
+      return a.T == 1 ? rows_of<1>(a, s) : a.T == 2 ? rows_of<2>(a, s) : a.T <= 4 ? rows_of<4>(a, s) : rows_of<8>(a, s);
+    });
+  }
   return product<kFwd>("linear_forward", x, W, cfg->T, cfg->N, cfg->K, e, reinterpret_cast<float *>(sc + L.part),
                        reinterpret_cast<int32_t *>(sc), true, di.sms, s);
 }

@@ -170,6 +170,44 @@ def test_single_gradients_and_reused_buffers():
         assert torch.equal(none.backward(dy, x, W, grads=g)[n], full[n])
 
 
+# few tokens: one to eight and more, few and many columns, one row of eight to the longest reduction, runs that end inside
+@pytest.mark.parametrize("K,N", [(8, 8), (8, 16), (16, 1032), (136, 1024), (1000, 72), (4096, 520), (1032, 4104), (65536, 8),
+                                 (65528, 24), (8, 65536), (4096, 4096)])
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 7, 8, 9])
+def test_few_tokens(T, K, N):
+    x, W, b, r = whole(T, K, seed=1), whole(K, N, seed=2), whole(N, seed=3, most=9), whole(T, N, seed=4, most=9)
+    z = x.double() @ W.double() + b.double()
+    plain = moe.Linear(T, K, N, bias=False)
+    assert torch.equal(plain.forward(x, W)["y"], (z - b.double()).to(BF))
+    lin = moe.Linear(T, K, N, activation="relu")
+    first = lin.forward(x, W, b, residual=r)
+    assert lin.status() == {"last": 0}
+    assert torch.equal(first["z"], z.to(BF)) and torch.equal(first["y"], (z.clamp_min(0) + r.double()).to(BF))
+    ends = torch.full((T + 2, N), 7, device="cuda", dtype=BF)  # the rows around it stay as they were; over the residual
+    ends[1:-1] = r
+    lin.forward(x, W, b, residual=ends[1:-1], save=False, out={"y": ends[1:-1], "z": None})
+    assert torch.equal(ends[1:-1], first["y"]) and bool((ends[0] == 7).all()) and bool((ends[-1] == 7).all())
+
+
+@pytest.mark.parametrize("T", [1, 3, 8])
+@pytest.mark.parametrize("act", ["none", "silu", "gelu"])
+def test_few_tokens_of_real_numbers(T, act):
+    K, N = 1536, 1096
+    x, W, b = randn(T, K, seed=1), randn(K, N, seed=2, scale=K ** -0.5), randn(N, seed=3)
+    x[-1, 5] = float("nan")
+    W[7, 9] = float("inf")
+    out = moe.Linear(T, K, N, activation=act).forward(x, W, b)
+    assert bool(out["y"][-1].isnan().all())
+    if act == "none":
+        assert not bool(out["y"][:, 9].isfinite().any())
+    ok = [c for c in range(N) if c != 9]
+    x, W = x[:-1], W[:, ok]
+    z = x.double() @ W.double() + b[ok].double()
+    terms = x.double().abs() @ W.double().abs() + b[ok].double().abs()
+    if T > 1:
+        close(out["y"][:-1, ok], ACTS[act](z), RMS * 1.01, terms, K)
+
+
 # the two products in one launch or in two, of one round or more, whole or in parts
 @pytest.mark.parametrize("T,K,N", [(1, 1024, 1024), (16, 1024, 1024), (100, 1536, 1408), (100, 1544, 1408), (2048, 512, 512),
                                    (3000, 384, 384), (8192, 128, 128), (9729, 128, 8), (64, 4096, 256), (1000, 264, 1000)])
