@@ -20,15 +20,17 @@
 //   warps 2-9  epilogue: tcgen05.ld, bias, activation, residual, bf16 rows
 // Tiles that do not fill a last round are split along the reduction, so that the round
 // is full: their parts leave fp32 sums in the workspace, which a second kernel adds in
-// a fixed order before the same epilogue.  Where the tiles of dx and dW are one round
+// a fixed order before the same epilogue; or, of a single round, split over the blocks of
+// a cluster, which add their sums over shared memory.  Where the tiles of dx and dW are one round
 // together, one launch takes both.  The forward of a few tokens is a pass over W on the
 // CUDA cores (linear_rows_kernel).
 //
 // What bounds it, measured (graphs of ten calls): 16384 x 4096 x 4096 280 us, 1970 TFLOP/s (a library's
 // product 269); 16384 x 1536 x 4096 114 us, 101 without the epilogue's stores, 126 with a residual, 135 with bias and
 // gelu (which stores z, too): the tensor pipe is busy 72% of the time with residual.  Back to back the part's
-// power cap holds both to 1.4e15 per second.  The backward of 16384 x 4096 x 1536 with silu takes 260: 117 for each
-// product, 27 for dz and dbias.  Few tiles: 4 us and 0.46 us for each 128 of the reduction, 5 more in parts.
+// power cap holds both to 1.4e15 per second.  The backward of 16384 x 4096 x 1536 with silu takes 258: 117 for each
+// product, 27 for dz and dbias.  Few tiles: 4 us and 0.46 us for each 128 of the reduction, 1.5 more in
+// clusters, 5 in parts.
 // Every wait is bounded; on a timeout the kernel flags the status word, drains its
 // copies and MMAs, frees TMEM and returns.
 #include <cuda.h>
@@ -71,6 +73,7 @@ struct ProductArgs {
   int full;       // tiles that are computed whole; the others in `split` parts
   int split;
   int units;      // tiles and parts in all
+  int cluster;    // blocks that share a tile's reduction, or 1
   float *part;    // the parts' sums (part_at)
   Ends e;
   int32_t *status;
@@ -234,6 +237,21 @@ __device__ __forceinline__ void finish_row(float (&v)[32], const Ends &e, const 
   st_row(e.y + at, ncols, e.sectors, v);
 }
 
+// A float, or four, of a block of the cluster.
+__device__ __forceinline__ float ld_peer(const float *p, uint32_t rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer_smem_addr(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_peer4(const float *p, uint32_t rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(peer_smem_addr(p, rank))
+               : "memory");
+  return v;
+}
+
 // ---------------------------------------------------------------- the product
 
 template <int CG>
@@ -283,7 +301,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CG == 2 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int group = blockIdx.x / CG - (second ? p1.units : 0), ngroups = gridDim.x / CG;
+  const int parts = CG == 1 ? p.cluster : 1, part = blockIdx.x % parts;
+  const int group = blockIdx.x / CG / parts - (second ? p1.units : 0), ngroups = gridDim.x / CG / parts;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -308,6 +327,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     else
       tmem_alloc(tmem_slot, kTmemCols);
   }
+  const int nkb = (p.K + BK - 1) / BK, nstage = (nkb + 1) / 2;
+  auto unit = [&](int u) {
+    Unit t = unit_of<CG>(u, p, nstage);
+    if (CG == 1 && parts > 1) {
+      t.ks0 = nstage * part / parts;
+      t.ks1 = nstage * (part + 1) / parts;
+    }
+    return t;
+  };
+  const Unit first = unit(group);
+  asm volatile("" ::"r"(first.m0), "r"(first.n0), "r"(first.ks0), "r"(first.ks1), "r"(first.part), "r"(nkb));  // here, not later
   griddep_wait();  // the set-up above overlaps the previous kernel's end; its outputs are read below
   // (a wait that runs out takes two seconds: no block flags one before this)
   if (p1.first && blockIdx.x == 0 && threadIdx.x == 0) *p1.status = 0;
@@ -316,8 +346,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   if constexpr (CG == 2) cluster_sync();  // both CTAs' barriers initialised before any remote arrival
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int nkb = (p.K + BK - 1) / BK, nstage = (nkb + 1) / 2;
-
   if (warp == 0) {
     if (lane == 0) {
       const uint32_t full0 = CG == 2 ? peer_smem_addr(&full[0], 0) : 0;
@@ -325,7 +353,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       uint32_t phase = 0, armed = 0, arm_par = 0;
       bool ok = true;
       for (int u = group; u < p.units && ok; u += ngroups) {
-        const Unit t = unit_of<CG>(u, p, nstage);
+        const Unit t = u == group ? first : unit(u);
         // Rows of A contiguous along K: where they end inside a CTA's 128, only the boxes of 32 that hold some (the MMA
         // reads what was there before in the others, whose sums are never stored).  With whole boxes a single row took
         // 17.4 us for 4096 x 4096.
@@ -333,7 +361,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int mine = boxes(rank);
         const uint32_t bytes = CG * kStageBytes - (CG * 4 - boxes(0) - (CG == 2 ? boxes(1) : 0)) * (2 * 32 * BK * 2);
         for (int ks = t.ks0; ks < t.ks1; ++ks) {
-          if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) {
+          if (!(armed >> stage & 1)) {  // its first use
+          } else if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) {
             ok = false;
             break;
           }
@@ -388,7 +417,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       uint32_t phase = 0;
       bool ok = true;
       for (int u = group; u < p.units && ok; u += ngroups, ++it) {
-        const Unit t = unit_of<CG>(u, p, nstage);
+        const Unit t = u == group ? first : unit(u);
         const int buf = it & 1;
         if (!mbar_wait(&tempty[buf], ((it >> 1) & 1) ^ 1, abort_flag)) break;
         tc_fence_after();
@@ -432,12 +461,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const uint32_t tempty0 = CG == 2 ? peer_smem_addr(&tempty[0], 0) : 0;
     int it = 0;
     for (int u = group; u < p.units; u += ngroups, ++it) {
-      const Unit t = unit_of<CG>(u, p, nstage);
+      const Unit t = u == group ? first : unit(u);
       const int buf = it & 1, row = t.m0 + BM * rank + q * 32 + lane, cols0 = t.n0 + half * (TS / 2);
       const int64_t row_at = static_cast<int64_t>(row) * p.N;
       uint4 res[KIND == kFwd ? kChunks : 1][4];
-      if constexpr (KIND == kFwd) {  // while the product runs
-        if (p.e.res && t.part < 0 && row < p.M) {
+      uint32_t warm = 0;
+      if constexpr (KIND == kFwd) {  // while the product runs: the residual, and the bias into the L1
+        if (p.e.bias && lane < TS / 16 && cols0 + 8 * lane < p.N)
+          warm = __ldg(reinterpret_cast<const uint32_t *>(p.e.bias + cols0 + 8 * lane));
+        if (p.e.res && t.part < 0 && parts == 1 && row < p.M) {
 #pragma unroll
           for (int j = 0; j < kChunks; ++j)
             if (cols0 + 32 * j < p.N) ld_row(p.e.res + row_at + cols0 + 32 * j, p.N - (cols0 + 32 * j), p.e.sectors, res[j]);
@@ -445,6 +477,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       }
       if (!wait_lane0(&tfull[buf], (it >> 1) & 1, abort_flag)) break;
       __syncwarp();
+      asm volatile("" ::"r"(warm));
       tc_fence_after();
       const uint32_t tb = tmem_base + buf * TS + (static_cast<uint32_t>(q * 32) << 16) + half * (TS / 2);
 #pragma unroll(KIND == kFwd ? kChunks : 1)
@@ -454,8 +487,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         uint32_t acc[32];
         tmem_ld32(tb + 32 * j, acc);
         tmem_ld_wait();
-        if (t.part >= 0) {  // sums of a part, rows and columns past the ends among them
-          float *to = p.part + part_at<CG>(t.part, BM * rank + q * 32, half * (TS / 2) + 32 * j);
+        if (t.part >= 0 || parts > 1) {  // sums of a part, rows and columns past the ends among them
+          // (a cluster's stay in shared memory: all that was loaded there has been read)
+          float *to = (parts > 1 ? reinterpret_cast<float *>(smem) : p.part) +
+                      part_at<CG>(parts > 1 ? 0 : t.part, BM * rank + q * 32, half * (TS / 2) + 32 * j);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             *reinterpret_cast<uint4 *>(to + i * 128) = make_uint4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
@@ -477,10 +512,38 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
   }
 
+  if (CG == 1 && parts > 1) {  // a tile's 16 squares of 32 x 32 among the cluster's blocks, a warp each
+    const int square = 16 / parts * part + warp - 2, at0 = square / 4 * 32, at1 = square % 4 * 32;
+    const int row = first.m0 + at0 + lane, col = first.n0 + at1;
+    const bool mine = warp >= 2 && warp - 2 < 16 / parts && row < p.M && col < p.N;
+    const int64_t at = static_cast<int64_t>(row) * p.N + col;
+    uint4 res[4];
+    if (KIND == kFwd && mine && p.e.res) ld_row(p.e.res + at, p.N - col, p.e.sectors, res);
+    __syncwarp();
+    cluster_sync();
+    if (mine) {
+      const float *from = reinterpret_cast<float *>(smem) + part_at<CG>(0, at0, at1);
+      float v[32] = {};
+      for (int r = 0; r < parts; r += 2) {
+        float4 a[2][8];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) a[i / 8][i % 8] = ld_peer4(from + i % 8 * 128, r + i / 8);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float4 x = a[i / 8][i % 8];
+          float *const to = v + i % 8 * 4;
+          to[0] += x.x, to[1] += x.y, to[2] += x.z, to[3] += x.w;
+        }
+      }
+      finish_row<KIND>(v, p.e, res, at, col, min(32, p.N - col));
+    }
+    __syncwarp();
+  }
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0 && *abort_flag) flag_status(p.status, kDevWaitTimeout);
-  if constexpr (CG == 2) cluster_sync();  // the pair is done with each other's barriers and TMEM
+  // a pair is done with each other's barriers and TMEM, a cluster with each other's sums
+  if (CG == 2 || parts > 1) cluster_sync();
   if (warp == 1) {
     tc_fence_after();
     if constexpr (CG == 2)
@@ -536,13 +599,6 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return r;
 }
-// A float of a block of the cluster.
-__device__ __forceinline__ float ld_peer(const float *p, uint32_t rank) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer_smem_addr(p, rank)) : "memory");
-  return v;
-}
-
 // ---------------------------------------------------------------- a few tokens
 //
 // y of at most TM tokens, on the CUDA cores: a pass over W, which is all that it has to read.  A thread takes 8 columns of 8
@@ -781,8 +837,12 @@ bool map2(CUtensorMap *m, const void *ptr, int inner, int rows, int box_rows) {
 // single CTAs; parts cost another 5, for their sums and the second kernel.  Measured, single whole, single in parts, pairs
 // whole, pairs in parts: 1024 x 1024 x 1024 7.6, 10.3, 10.1, 11.6; 512 x 2048 x 768 11.1, 9.6, 14.2, 11.7; 4096 x 1536 x 1536 22.7,
 // 22.5, 20.4, 21.2; 16 x 4096 x 4096 18.4, 11.9, 22.0, 14.9; 2048 x 4096 x 4096 67.4, 64.0, 42.4, 42.2.
+// Or a cluster of 2, 4 or 8 single CTAs shares each tile's reduction and adds its sums over shared memory, for another 1.5 us,
+// where all of them run at once (as the part's SMs lie, 76, 36 and 15 such clusters do): 16 x 4096 x 4096 9.4 us and 11.3
+// without, 777 x 1000 x 520 8.9 and 10.7, 1100 x 2048 x 1024 11.4 and 14.9, 16 x 4096 x 1536 7.8 and 9.1; 16 clusters of 8,
+// which are two rounds, 16.5 and 8.5 (256 x 1024 x 1024).
 struct Cut {
-  int cg, nm, nn, full, split, units;
+  int cg, nm, nn, full, split, units, cluster;
   double cost;
 };
 Cut cut_with(int64_t M, int64_t N, int64_t K, int cg, bool parts, int sms) {
@@ -800,6 +860,7 @@ Cut cut_with(int64_t M, int64_t N, int64_t K, int cg, bool parts, int sms) {
   c.units = static_cast<int>(c.split > 1 ? c.full + left * c.split : tiles);
   const int64_t rounds = c.split > 1 ? c.full / groups : (tiles + groups - 1) / groups;
   const double stage = cg == 2 ? 0.58 : 0.46, ends = cg == 2 ? 1.4 : 0.8;
+  c.cluster = 1;
   c.cost = rounds * (nstage * stage + ends);
   if (c.split > 1) c.cost += (nstage + c.split - 1) / c.split * stage + ends + 5;
   return c;
@@ -808,6 +869,14 @@ Cut cut_of(int64_t M, int64_t N, int64_t K, int sms) {
   Cut best = cut_with(M, N, K, 2, false, sms);
   for (int way = 1; way < 4; ++way) {
     const Cut c = cut_with(M, N, K, way & 1 ? 1 : 2, way > 1, sms);
+    if (c.cost < best.cost) best = c;
+  }
+  for (int blocks = 2; blocks <= 8; blocks *= 2) {
+    Cut c = cut_with(M, N, K, 1, false, sms);
+    const int nstage = static_cast<int>((K + 2 * BK - 1) / (2 * BK));
+    if (c.units > sms / 2 * (blocks == 2 ? 76 : blocks == 4 ? 36 : 15) / 76 || nstage < blocks) break;
+    c.cluster = blocks;
+    c.cost = (nstage + blocks - 1) / blocks * 0.46 + 0.8 + 1.5;
     if (c.cost < best.cost) best = c;
   }
   return best;
@@ -863,6 +932,7 @@ bool operands(Operands *o, int kind, const void *a, const void *b, int M, int N,
   p.full = c.full;
   p.split = c.split;
   p.units = c.units;
+  p.cluster = c.cluster;
   p.part = part;
   p.e = ends;
   auto al32 = [](const void *q) { return (reinterpret_cast<uintptr_t>(q) & 31) == 0; };
@@ -878,6 +948,9 @@ cudaError_t launch_cut(const Operands &o, const Cut &c, int sms, cudaStream_t s)
   int groups = 0;
   cudaError_t e = groups_of<KIND, CG>(sms, &groups);
   if (e != cudaSuccess) return e;
+  if (c.cluster > 1)
+    return launch_pdl(linear_product_kernel<KIND, CG>, dim3(static_cast<unsigned>(c.units * c.cluster)), dim3(kGemmThreads),
+                      kGemmSmem, s, c.cluster, o.a, o.a32, o.b, o.a, o.b, o.p, o.p);
   e = launch_pdl(linear_product_kernel<KIND, CG>, dim3(static_cast<unsigned>(CG * std::min(c.units, groups))),
                  dim3(kGemmThreads), kGemmSmem, s, CG, o.a, o.a32, o.b, o.a, o.b, o.p, o.p);
   if (e != cudaSuccess || c.split == 1) return e;

@@ -170,6 +170,31 @@ def test_single_gradients_and_reused_buffers():
         assert torch.equal(none.backward(dy, x, W, grads=g)[n], full[n])
 
 
+# few tiles: a reduction of two stages to many, whole, over clusters of 2, 4 and 8 (as many as run at once and more), in parts
+@pytest.mark.parametrize("T,K,N", [(16, 136, 64), (16, 264, 1032), (130, 520, 264), (9, 1024, 1920), (9, 1024, 2056),
+                                   (512, 1000, 1152), (513, 1000, 1152), (1216, 264, 1024), (1216, 264, 1032), (16, 16384, 64),
+                                   (100, 8200, 392), (256, 5000, 1024)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_few_tiles(T, K, N, residual):
+    x, W, b = whole(T, K, seed=1), whole(K, N, seed=2), whole(N, seed=3, most=9)
+    r = whole(T, N, seed=4, most=9) if residual else None
+    lin = moe.Linear(T, K, N, activation="relu")
+    out = lin.forward(x, W, b, residual=r)
+    z = x.double() @ W.double() + b.double()
+    assert torch.equal(out["z"], z.to(BF))
+    assert torch.equal(out["y"], (z.clamp_min(0) + (r.double() if residual else 0)).to(BF))
+    got = lin.backward(out["y"], x, W, out["z"])
+    dz = out["y"].double() * (out["z"] > 0)
+    assert lin.status() == {"last": 0}
+    for n, ref, terms, depth in (("dx", dz @ W.double().T, dz.abs() @ W.double().abs().T, N),
+                                 ("dW", x.double().T @ dz, x.double().abs().T @ dz.abs(), T)):
+        # a rounding, and those of fp32 sums of `depth` terms, each exact
+        assert torch.all((got[n].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + depth * 2.0 ** -24 * terms * 1.01)
+    again = lin.forward(x, W, b, residual=r)
+    assert torch.equal(again["y"], out["y"])
+    assert all(torch.equal(v, got[k]) for k, v in lin.backward(out["y"], x, W, out["z"]).items() if v is not None)
+
+
 # few tokens: one to eight and more, few and many columns, one row of eight to the longest reduction, runs that end inside
 @pytest.mark.parametrize("K,N", [(8, 8), (8, 16), (16, 1032), (136, 1024), (1000, 72), (4096, 520), (1032, 4104), (65536, 8),
                                  (65528, 24), (8, 65536), (4096, 4096)])
