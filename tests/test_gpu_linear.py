@@ -330,3 +330,53 @@ def test_two_plans_and_graphs():
         assert all(torch.equal(out[n], ref[n]) for n in ref)
         ref = other.backward(dy, x, W, ref["z"])
         assert all(torch.equal(grads[n], ref[n]) for n in ref)
+
+
+def test_layers_of_every_kind_in_one_graph():
+    """One token, few tokens, clusters, parts and whole tiles one after another, each on what the last one wrote."""
+    sizes = [(1, 512, 1024), (6, 264, 1032), (16, 2048, 512), (300, 4096, 136), (2048, 1024, 1280), (16, 16384, 64)]
+    plans, calls = [], []
+    for i, (T, K, N) in enumerate(sizes):
+        a, b = moe.Linear(T, K, N, activation="relu", bias=False), moe.Linear(T, N, K, bias=False)
+        x, W, V = whole(T, K, seed=i), whole(K, N, seed=20 + i, most=1), whole(N, K, seed=40 + i, most=1)
+        first = a.forward(x, W)
+        second = b.forward(first["y"], V, residual=x)
+        g2 = b.backward(second["y"], first["y"], V)
+        g1 = a.backward(g2["dx"], x, W, first["z"])
+        plans.append((a, b))
+        calls.append((x, W, V, first, second, g2, g1))
+
+    def step():
+        for (a, b), (x, W, V, first, second, g2, g1) in zip(plans, calls):
+            a.forward(x, W, out=first)
+            b.forward(first["y"], V, residual=x, out=second)
+            b.backward(second["y"], first["y"], V, grads=g2)
+            a.backward(g2["dx"], x, W, first["z"], grads=g1)
+
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    for turn in range(3):
+        for i, c in enumerate(calls):
+            c[0].copy_(whole(*c[0].shape, seed=100 * turn + i))
+        step()
+        torch.cuda.synchronize()
+        eager = [{k: v.clone() for d in c[3:] for k, v in d.items() if v is not None} for c in calls]
+        for c in calls:
+            for d in c[3:]:
+                for v in d.values():
+                    if v is not None:
+                        v.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        for c, e in zip(calls, eager):
+            last = {k: v for d in c[3:] for k, v in d.items() if v is not None}
+            assert all(torch.equal(v, e[k]) for k, v in last.items())
+            x, W, V, first, second, g2, g1 = c
+            z = x.double() @ W.double()
+            assert torch.equal(first["z"], z.to(BF)) and torch.equal(first["y"], z.to(BF).clamp_min(0))
+            terms = first["y"].double() @ V.double().abs()
+            ref = first["y"].double() @ V.double() + x.double()
+            assert torch.all((second["y"].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + V.shape[0] * 2.0 ** -24 * terms * 1.01)
+    assert all(p.status() == {"last": 0} for ab in plans for p in ab)
