@@ -29,12 +29,13 @@ __global__ void __launch_bounds__(kGateThreads) gate_index_kernel(const GateArgs
   __shared__ uint8_t q_e[kSorted];
   const int tid = threadIdx.x, E = a.E;
   const int rank = blockIdx.x % a.cluster, mine = blockIdx.x / a.cluster;
-  griddep_wait();  // the previous kernel in the stream has completed
-  griddep_launch_dependents();
-  // the block's first slots, on their way during what follows
   constexpr int kSlots = 4;
   const int64_t first = clusters ? static_cast<int64_t>(gate_first(a, blockIdx.x)) * a.k : 0,
                 last = clusters ? static_cast<int64_t>(gate_first(a, blockIdx.x + 1)) * a.k : 0;
+  asm volatile("" ::"l"(first), "l"(last), "r"(rank), "r"(mine));  // before the wait
+  griddep_wait();  // the previous kernel in the stream has completed
+  griddep_launch_dependents();
+  // the block's first slots, on their way during what follows
   int slot_e[kSlots], slot_r[kSlots];
   float slot_w[kSlots];
   auto load = [&](int64_t s0) {
@@ -388,6 +389,7 @@ moe_status moe_gate_forward(const moe_gate_config *cfg, const float *logits, con
   a.slot_of_row = routing->slot_of_row;
   a.w_row = routing->w_row;
   a.chunks = L.chunks;
+  if (L.chunks) a.chunk_tokens = cfg->T / L.chunks, a.longer = cfg->T % L.chunks;
   a.cluster = L.cluster;
   a.before = reinterpret_cast<int32_t *>(sc + L.before);
   a.count = reinterpret_cast<int32_t *>(sc + L.count);

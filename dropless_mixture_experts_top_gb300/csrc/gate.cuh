@@ -48,7 +48,8 @@ struct GateArgs {
   float *topk_w;
   int32_t *counts, *offsets, *row_of_slot, *slot_of_row;
   float *w_row;
-  int chunks;           // chunk c: the tokens [c T / chunks, (c + 1) T / chunks)
+  int chunks;           // runs of tokens, a block each
+  int chunk_tokens, longer;  // of a chunk; of the first `longer`, one more
   int cluster;          // chunks per cluster
   int32_t *before;      // [chunks][E]: the slots of expert e in the cluster's earlier chunks
   int32_t *count;       // [chunks][E]: its own
@@ -67,7 +68,8 @@ template <int KEY>
 cudaError_t launch_gate_select(const GateArgs &a, cudaStream_t s);
 
 __device__ __forceinline__ int gate_first(const GateArgs &a, int chunk) {
-  return static_cast<int>(static_cast<int64_t>(a.T) * min(chunk, a.chunks) / a.chunks);
+  const int c = min(chunk, a.chunks);
+  return c * a.chunk_tokens + min(c, a.longer);
 }
 
 __device__ __forceinline__ int32_t ld_peer(const int32_t *p, int rank) {
@@ -607,6 +609,7 @@ __global__ void __launch_bounds__(kGateThreads, 4) gate_select_kernel(const Gate
   const int first = gate_first(a, blockIdx.x), last = min(a.T, gate_first(a, blockIdx.x + 1));
   if (tid == 0) s_count = 0, s_flag = 0, s_bodd = 0;
   s_run[tid] = 0;  // (kGateThreads == kMaxExperts)
+  asm volatile("" ::"r"(first), "r"(last));  // before the wait
   griddep_wait();  // the previous kernel in the stream has completed
   griddep_launch_dependents();
 
@@ -662,6 +665,7 @@ __global__ void __launch_bounds__(kGateThreads, 4) gate_select_kernel(const Gate
     gits = (gs + gP - 1) / gP;
   }
   const int my_g = VEC ? l * NV / gs : lane % G, my_p = VEC ? 0 : lane / G;
+  const int shift = 32 - __clz(k - 1), width = 1 << shift;  // a token's slots in a power of two of threads
   const bool whole_sum = !a.sigmoid && !a.renormalise;  // the weights need the softmax' sum over all experts
   bool bad = false;
 
@@ -932,10 +936,8 @@ __global__ void __launch_bounds__(kGateThreads, 4) gate_select_kernel(const Gate
     __syncthreads();
 
     // ---- weights: a thread per slot, the slots of a token side by side in a power of two of lanes
-    int width = 1;
-    while (width < k) width *= 2;
     for (int p = tid; p < words * 32 * width; p += kGateThreads) {
-      const int tl = p / width, j = p % width;
+      const int tl = p >> shift, j = p & (width - 1);
       const bool in = tl < ntok && j < k;
       const int v = in ? s_slot[tl * k + j] : 0x8000, e = v & 0x7FFF;
       bool unused = false;
@@ -972,8 +974,10 @@ __global__ void __launch_bounds__(kGateThreads, 4) gate_select_kernel(const Gate
       run += __popc(sh.rank.emask[w][tid]);
     }
     __syncthreads();
-    for (int sl = tid; sl < ntok * k; sl += kGateThreads) {
-      const int tl = sl / k, e = s_slot[sl] & 0x7FFF, w = tl >> 5;
+    for (int p = tid; p < ntok * width; p += kGateThreads) {
+      const int tl = p >> shift, j = p & (width - 1), sl = tl * k + j;
+      if (j >= k) continue;
+      const int e = s_slot[sl] & 0x7FFF, w = tl >> 5;
       a.row_of_slot[static_cast<size_t>(t0) * k + sl] =
           s_run[e] + sh.rank.before[w][e] + __popc(sh.rank.emask[w][e] & ((1u << (tl & 31)) - 1u));
     }
