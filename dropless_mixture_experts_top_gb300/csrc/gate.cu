@@ -6,8 +6,8 @@
 // front of the chunk in its cluster of blocks, and the cluster's totals; the second
 // kernel adds up the totals in front of the cluster.  No block waits for one outside its cluster
 // and nothing has to be zero before a call.  Few tokens are one cluster, which needs no
-// second kernel.  Measured in graphs: 131072 x 256 in 8 groups 99 us (the choice 72 of them), 16384 x 128 with a
-// bias 19.6, 512 x 8 5.7; backward 100000 x 250 dense 39.6, 16384 x 128 with the bias' step 4.9.
+// second kernel.  Measured in graphs: 131072 x 256 in 8 groups 96 us (the choice 72 of them), 16384 x 128 with a
+// bias 18.6, 512 x 8 5.7; backward 100000 x 250 dense 39.6, 16384 x 128 with the bias' step 4.9.
 #include "gate.cuh"
 
 namespace moe {
