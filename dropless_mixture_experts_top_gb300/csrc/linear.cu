@@ -22,7 +22,7 @@
 // is full: their parts leave fp32 sums in the workspace, which a second kernel adds in
 // a fixed order before the same epilogue; or, of a single round, split over the blocks of
 // a cluster, which add their sums over shared memory.  Where the tiles of dx and dW are one round
-// together, one launch takes both.  The forward of a few tokens is a pass over W on the
+// together, one launch takes both, and the second step of dbias.  The forward of a few tokens is a pass over W on the
 // CUDA cores (linear_rows_kernel).
 //
 // What bounds it, measured (graphs of ten calls): 16384 x 4096 x 4096 280 us, 1970 TFLOP/s (a library's
@@ -78,6 +78,9 @@ struct ProductArgs {
   Ends e;
   int32_t *status;
   bool first;     // of the call's kernels: clears the status word
+  const float *sums;  // kBoth: dbias' partial rows, which blocks behind the tiles add up
+  int sum_rows;
+  float *dbias;
 };
 
 // The k-th unit of work: its tile, and its stages of the reduction.
@@ -275,6 +278,23 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t s, int j, bool mn) {
   return mn ? smem_desc_sw128(s + j * 2048, kBox, 1024) : smem_desc_sw128(s + j * 32, 16, 1024);
 }
 
+// dbias of 32 columns: a warp each for every WARPS-th partial row.  s_sum: [WARPS][32]
+template <int WARPS>
+__device__ __forceinline__ void add_sums(const float *sums, int rows, int N, float *dbias, int columns, float *s_sum) {
+  const int lane = threadIdx.x & 31, c = columns * 32 + lane, w = threadIdx.x >> 5;
+  float s = 0.f;
+  if (c < N) {
+#pragma unroll 8
+    for (int i = w; i < rows; i += WARPS) s += __ldcg(sums + static_cast<int64_t>(i) * N + c);
+  }
+  s_sum[w * 32 + lane] = s;
+  __syncthreads();
+  if (w || c >= N) return;
+#pragma unroll
+  for (int i = 1; i < WARPS; ++i) s += s_sum[i * 32 + lane];
+  dbias[c] = s;
+}
+
 template <int KIND, int CG>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     linear_product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
@@ -282,7 +302,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                           const __grid_constant__ CUtensorMap tmB2, const ProductArgs p1, const ProductArgs p2) {
   constexpr int TS = tile_size(CG);
   constexpr uint32_t kTmemCols = 2 * TS;
-  // kBoth: a tile per block, those of dx first
+  // kBoth: a tile per block, those of dx first; behind them 32 columns of dbias each
+  if constexpr (KIND == kBoth) {
+    const int columns = static_cast<int>(blockIdx.x) - p1.units - p2.units;
+    if (columns >= 0) {
+      extern __shared__ float s_sum[];
+      griddep_wait();
+      griddep_launch_dependents();
+      add_sums<kGemmThreads / 32>(p1.sums, p1.sum_rows, p2.N, p1.dbias, columns, s_sum);
+      return;
+    }
+  }
   const bool second = KIND == kBoth && static_cast<int>(blockIdx.x) >= p1.units;
   const ProductArgs &p = second ? p2 : p1;
   const bool amn = KIND == kBoth ? second : KIND == kDw, bmn = KIND == kBoth ? second : KIND != kDx;
@@ -794,23 +824,11 @@ __global__ void __launch_bounds__(kDzThreads, kDzPerSm) linear_dz_kernel(const D
     (a.split == 1 ? a.dbias : a.part + static_cast<int64_t>(blockIdx.y) * a.N)[col] = s;
   }
 }
-// 32 columns a block, a warp each for every eighth partial row
 __global__ void __launch_bounds__(kDzThreads) linear_dbias_kernel(const float *part, int split, int N, float *dbias) {
-  __shared__ float s_sum[kDzThreads / 32][32];
+  __shared__ float s_sum[kDzThreads];
   griddep_wait();  // the previous kernel in the stream has completed
   griddep_launch_dependents();
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
-  float s = 0.f;
-  if (c < N) {
-#pragma unroll 8
-    for (int i = w; i < split; i += kDzThreads / 32) s += __ldcg(part + static_cast<int64_t>(i) * N + c);
-  }
-  s_sum[w][threadIdx.x & 31] = s;
-  __syncthreads();
-  if (w || c >= N) return;
-#pragma unroll
-  for (int i = 1; i < kDzThreads / 32; ++i) s += s_sum[i][threadIdx.x];
-  dbias[c] = s;
+  add_sums<kDzThreads / 32>(part, split, N, dbias, blockIdx.x, s_sum);
 }
 
 // ---------------------------------------------------------------- host side
@@ -973,8 +991,11 @@ moe_status product(const char *label, const void *a, const void *b, int M, int N
 // two one after the other: tokens, in, out in one and in two launches: 16 x 1024 x 1024 8.4 us and 12.4; 777 x 1000 x 520
 // 13.3 and 19.8; 2048 x 512 x 512 15.7 and 16.5; by the rule in two: 3000 x 384 x 384 20.9 and 18.0, 8192 x 128 x 128 42.2
 // and 18.0 (their dW is cut along the tokens).
+// *sums_left: dbias' partial rows (sums, rows) are still to be added up; where blocks are left for that, this launch does
+// (777 x 1000 x 520 with gelu and bias 11.4 us, with a launch for it in front 12.2).
 moe_status both_products(const void *dz, const void *W, const void *x, int T, int K, int N, const Ends &dx, const Ends &dw,
-                         int32_t *status, bool first, int sms, cudaStream_t s, bool *done) {
+                         const float *sums, int rows, float *dbias, int32_t *status, bool first, int sms, cudaStream_t s,
+                         bool *sums_left, bool *done) {
   const int most = std::min(sms, kRuleSms);
   const Cut cx = cut_with(T, K, N, 1, false, most), cw = cut_with(K, N, T, 1, false, most);
   *done = false;
@@ -988,9 +1009,16 @@ moe_status both_products(const void *dz, const void *W, const void *x, int T, in
   if (!operands(&ox, kDx, dz, W, T, K, N, cx, dx, nullptr, status, first) ||
       !operands(&ow, kDw, x, dz, K, N, T, cw, dw, nullptr, status, first))
     return MOE_ERR_CUDA;
+  const int columns = (N + 31) / 32, extra = *sums_left && cx.units + cw.units + columns <= groups ? columns : 0;
+  if (extra) {
+    ox.p.sums = sums;
+    ox.p.sum_rows = rows;
+    ox.p.dbias = dbias;
+    *sums_left = false;
+  }
   *done = true;
   return timed("linear_dx_dW", s, [&] {
-    return launch_pdl(linear_product_kernel<kBoth, 1>, dim3(static_cast<unsigned>(cx.units + cw.units)), dim3(kGemmThreads),
+    return launch_pdl(linear_product_kernel<kBoth, 1>, dim3(static_cast<unsigned>(cx.units + cw.units + extra)), dim3(kGemmThreads),
                       kGemmSmem, s, 1, ox.a, ox.a32, ox.b, ow.a, ow.b, ox.p, ow.p);
   });
 }
@@ -1102,7 +1130,9 @@ moe_status moe_linear_backward(const moe_linear_config *cfg, const void *dy, con
   }
   float *part = reinterpret_cast<float *>(sc + L.part);
   const void *dz = dy;
-  bool first = true;
+  bool first = true, sums_left = false;
+  const float *sums = nullptr;  // dbias' partial rows
+  int rows = 0;
   if (act || dbias) {
     DzArgs a{};
     a.dy = static_cast<const uint16_t *>(dy);
@@ -1121,11 +1151,9 @@ moe_status moe_linear_backward(const moe_linear_config *cfg, const void *dy, con
     MOE_TRY(timed("linear_dz", s, [&] {
       return launch_pdl(kernel, dim3((N + kDzCols - 1) / kDzCols, a.split), dim3(kDzThreads), 0, s, 1, a);
     }));
-    if (dbias && a.split > 1)
-      MOE_TRY(timed("linear_dbias", s, [&] {
-        return launch_pdl(linear_dbias_kernel, dim3((N + 31) / 32), dim3(kDzThreads), 0, s, 1,
-                          static_cast<const float *>(a.part), a.split, N, dbias);
-      }));
+    sums = a.part;
+    rows = a.split;
+    sums_left = dbias && rows > 1;
     if (act) dz = a.dz;
     first = false;
   }
@@ -1133,7 +1161,12 @@ moe_status moe_linear_backward(const moe_linear_config *cfg, const void *dy, con
   ex.y = static_cast<uint16_t *>(dx);
   ew.y = static_cast<uint16_t *>(dW);
   bool done = false;
-  if (dx && dW) MOE_TRY(both_products(dz, W, x, T, K, N, ex, ew, status, first, di.sms, s, &done));
+  if (dx && dW)
+    MOE_TRY(both_products(dz, W, x, T, K, N, ex, ew, sums, rows, dbias, status, first, di.sms, s, &sums_left, &done));
+  if (sums_left)
+    MOE_TRY(timed("linear_dbias", s, [&] {
+      return launch_pdl(linear_dbias_kernel, dim3((N + 31) / 32), dim3(kDzThreads), 0, s, 1, sums, rows, N, dbias);
+    }));
   if (dx && !done) {
     MOE_TRY(product<kDx>("linear_dx", dz, W, T, K, N, ex, part, status, first, di.sms, s));
     first = false;

@@ -388,6 +388,7 @@ moe_status moe_ortho_update(const moe_ortho_config *cfg, const float *coefs, con
  * fields of *routing are written as moe_route writes them, so that moe_forward and moe_backward take it.
  * The choice is that of exact scores: tokens whose scores lie closer together than fp32 resolves are
  * chosen again from scores in 64 bits, so that a recomputed forward, or another program, chooses the same.
+ * (Sums of two softmax scores that are equal but for the last of those bits may go by their roundings.)
  * (A bias that is far larger than the scores, 1e3 and more, makes that every token, at some hundred times
  * the cost.)
  * A logit of -inf, or a bias of -inf or NaN, is an expert that may not be chosen; a group's score goes over
