@@ -168,11 +168,11 @@ __device__ __forceinline__ float sqrt_fast(float x) {
   return y;
 }
 
-// The largest |x| of the warp's 256, at least kTiny (what is not finite left out, where `odd` says that there is some).
-__device__ __forceinline__ float block_most(const float (&x)[8], bool odd) {
+// The largest |x| of the warp's 256, at least kTiny (NaN left out).
+__device__ __forceinline__ float block_most(const float (&x)[8]) {
   float m = kTiny;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = odd && !(fabsf(x[i]) <= FLT_MAX) ? m : fmaxf(m, fabsf(x[i]));
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
 }
 
@@ -285,8 +285,15 @@ __global__ void __launch_bounds__(kThreads, EIGHT ? kBlocks8 : kBlocks32) adamw_
       bad |= odd;
     }
     if constexpr (EIGHT) {
-      odd = __any_sync(0xffffffffu, odd);
-      const float most_m = block_most(mv, odd), most_r = block_most(r, odd);
+      // An element whose parameter or v is not finite becomes e4m3's NaN and has no part in the block's scales, though its
+      // m, or its root, be finite: a gradient of 1e20 makes v infinite and m so large that the other 255 would all be
+      // rounded to zero.
+      if (odd) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (!(fabsf(pv[i]) <= FLT_MAX && vv[i] <= FLT_MAX)) mv[i] = r[i] = NAN;
+      }
+      const float most_m = block_most(mv), most_r = block_most(r);
       const float im = __fmul_rn(__frcp_rn(most_m), kCodeMax), ir = __fmul_rn(__frcp_rn(most_r), kCodeMax);
       if (lane == 0) {
         a.m_scale[l.s0 / kBlock] = __fmul_rn(most_m, 1.f / kCodeMax);
@@ -294,10 +301,8 @@ __global__ void __launch_bounds__(kThreads, EIGHT ? kBlocks8 : kBlocks32) adamw_
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const bool fine = !odd || (fabsf(pv[i]) <= FLT_MAX && vv[i] <= FLT_MAX);  // else e4m3's NaN
-        mv[i] = fine ? mv[i] * im : NAN;
-        vv[i] = r[i] > 0.f ? fmaxf(r[i] * ir, kCodeLeast) : 0.f;
-        vv[i] = fine ? vv[i] : NAN;
+        mv[i] *= im;
+        vv[i] = r[i] > 0.f ? fmaxf(r[i] * ir, kCodeLeast) : r[i];
       }
     }
     with_left(l.have, lane, [&](const int(&left)[2]) {

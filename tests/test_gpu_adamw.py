@@ -243,3 +243,36 @@ def test_against_a_long_plain_run():
         moved += upd.abs()
     # m and v are off by at most 30 steps' roundings of their largest terms, relative to the root of v, which is of |g|'s size
     assert torch.all((p.double() - p64).abs() <= 30 * (2 * U * (p64.abs() + moved)) + 30 * 24 * U * (moved + 1e-2))
+
+
+
+@pytest.mark.parametrize("bits", ["fp32", "8bit"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), 1e20, 3e30, "parameter"])
+def test_an_element_that_is_not_finite_leaves_its_block_alone(bits, bad):
+    """The other elements' parameters, states and scales are those of a run in which the element has no gradient, in that
+    step and in the next one; a gradient of 1e20 makes v infinite and m no more than large."""
+    opt = moe.AdamW([(600,)], grad="fp32", state=bits, beta2=0.95)
+    rest = torch.arange(600, device="cuda") != 301
+    g = rand(600, seed=4)
+    runs = []
+    for odd in (False, True):
+        p, state, h = rand(600), opt.new_state(), g.clone()
+        h[301] = 0.0
+        if odd and bad == "parameter":
+            p[301], h[301] = float("inf"), 50.0  # m and v are finite, and the block's largest
+        elif odd:
+            h[301] = bad
+        held_after = []
+        for _ in range(2):
+            opt.step([p], [h], state, 1e-2)
+            assert opt.status(state) == {"step": moe.DEV_NONFINITE_UPDATE if odd else 0}
+            held_after.append([p[rest]] + [state[n].view(torch.uint8 if bits == "8bit" else torch.int32)[:600][rest]
+                                           for n in ("m", "v")] +
+                              [state[n].clone() for n in ("m_scale", "v_scale") if n in state])
+            h = rand(600, seed=5)
+            h[301] = 0.0
+        if odd and bits == "8bit":
+            assert torch.isnan(state["m"].float()[301]) and torch.isnan(state["v"].float()[301])
+        runs.append(held_after)
+    for a, b in zip(*runs):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
