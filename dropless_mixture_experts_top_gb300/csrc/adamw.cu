@@ -227,6 +227,10 @@ struct Unit {
   }
 };
 
+// A parameter is finite if what is stored of it is: bf16 rounds what is at least 2^128 - 2^119 to infinity.
+template <class P>
+constexpr float kMostParam = sizeof(P) == 2 ? 0x1.fefffep127f : FLT_MAX;
+
 // Products and sums are rounded one by one (no fused multiply-add), and the root is the exact one, where they enter the
 // 8-bit codes: a code is then the same wherever the formula is written out in fp32, as in a run that goes on from a
 // checkpoint elsewhere.
@@ -272,7 +276,8 @@ __global__ void __launch_bounds__(kThreads, EIGHT ? kBlocks8 : kBlocks32) adamw_
       const float root_v = EIGHT ? __fsqrt_rn(vv[i]) : sqrt_fast(vv[i]);
       if (EIGHT) r[i] = root_v;
       pv[i] = fmaf(pv[i], keep, -__fdividef(rate * mv[i], fmaf(root_v, root, a.eps)));
-      fin = fmaf(vv[i], 0.f, fmaf(pv[i], 0.f, fin));  // NaN where one is not finite
+      // NaN where one is not finite (of bf16, from 1.98 2^127 on)
+      fin = fmaf(vv[i], 0.f, fmaf(sizeof(P) == 2 ? pv[i] * 1.01f : pv[i], 0.f, fin));
     }
     const Place l(e, u, lane);
     bool odd = fin != 0.f;
@@ -280,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, EIGHT ? kBlocks8 : kBlocks32) adamw_
       odd = false;
       with_left(l.have, lane, [&](const int(&left)[2]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) odd |= (i & 3) < left[i >> 2] && !(fabsf(pv[i]) <= FLT_MAX && vv[i] <= FLT_MAX);
+        for (int i = 0; i < 8; ++i) odd |= (i & 3) < left[i >> 2] && !(fabsf(pv[i]) <= kMostParam<P> && vv[i] <= FLT_MAX);
       });
       bad |= odd;
     }
@@ -291,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, EIGHT ? kBlocks8 : kBlocks32) adamw_
       if (odd) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (!(fabsf(pv[i]) <= FLT_MAX && vv[i] <= FLT_MAX)) mv[i] = r[i] = NAN;
+          if (!(fabsf(pv[i]) <= kMostParam<P> && vv[i] <= FLT_MAX)) mv[i] = r[i] = NAN;
       }
       const float most_m = block_most(mv), most_r = block_most(r);
       const float im = __fmul_rn(__frcp_rn(most_m), kCodeMax), ir = __fmul_rn(__frcp_rn(most_r), kCodeMax);

@@ -276,3 +276,19 @@ def test_an_element_that_is_not_finite_leaves_its_block_alone(bits, bad):
         runs.append(held_after)
     for a, b in zip(*runs):
         assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+
+@pytest.mark.parametrize("bits", ["fp32", "8bit"])
+@pytest.mark.parametrize("param", ["fp32", "bf16"])
+@pytest.mark.parametrize("step,infinite", [(3e35, False), (1e36, True)])
+def test_a_parameter_that_rounds_to_infinity(bits, param, step, infinite):
+    """bf16's largest, (2 - 2^-7) 2^127, moved by less and by more than half a step of it, 2^119 = 6.6e35; fp32 holds both."""
+    opt = moe.AdamW([(300,)], param=param, grad="fp32", state=bits, weight_decay=0.0)
+    p, g = torch.ones(300, device="cuda", dtype=DT[param]), torch.zeros(300, device="cuda")
+    p[77], g[77] = torch.finfo(torch.bfloat16).max, -1.0  # m / root of v is 1 in the first step
+    state = opt.new_state()
+    opt.step([p], [g], state, step)
+    flagged = infinite and param == "bf16"
+    assert opt.status(state) == {"step": moe.DEV_NONFINITE_UPDATE if flagged else 0}
+    assert bool(torch.isinf(p[77])) == flagged
