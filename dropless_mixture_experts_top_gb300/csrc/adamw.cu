@@ -280,24 +280,20 @@ __global__ void __launch_bounds__(kThreads, EIGHT ? kBlocks8 : kBlocks32) adamw_
       fin = fmaf(vv[i], 0.f, fmaf(sizeof(P) == 2 ? pv[i] * 1.01f : pv[i], 0.f, fin));
     }
     const Place l(e, u, lane);
-    bool odd = fin != 0.f;
-    if (odd) {  // (elements past a tensor's end are zeros, of which eps = 0 makes NaN)
-      odd = false;
+    // An element whose parameter or v is not finite.  In 8 bits it becomes e4m3's NaN and has no part in its block's
+    // scales, though its m, or its root, be finite: a gradient of 1e20 makes v infinite and m so large that the other 255
+    // would all be rounded to zero.
+    if (fin != 0.f) {  // (elements past a tensor's end are zeros, of which eps = 0 makes NaN)
       with_left(l.have, lane, [&](const int(&left)[2]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) odd |= (i & 3) < left[i >> 2] && !(fabsf(pv[i]) <= kMostParam<P> && vv[i] <= FLT_MAX);
+        for (int i = 0; i < 8; ++i) {
+          const bool odd = !(fabsf(pv[i]) <= kMostParam<P> && vv[i] <= FLT_MAX);
+          bad |= odd && (i & 3) < left[i >> 2];
+          if (EIGHT && odd) mv[i] = r[i] = NAN;
+        }
       });
-      bad |= odd;
     }
     if constexpr (EIGHT) {
-      // An element whose parameter or v is not finite becomes e4m3's NaN and has no part in the block's scales, though its
-      // m, or its root, be finite: a gradient of 1e20 makes v infinite and m so large that the other 255 would all be
-      // rounded to zero.
-      if (odd) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (!(fabsf(pv[i]) <= kMostParam<P> && vv[i] <= FLT_MAX)) mv[i] = r[i] = NAN;
-      }
       const float most_m = block_most(mv), most_r = block_most(r);
       const float im = __fmul_rn(__frcp_rn(most_m), kCodeMax), ir = __fmul_rn(__frcp_rn(most_r), kCodeMax);
       if (lane == 0) {
