@@ -425,8 +425,9 @@ moe_status moe_adamw_step(const moe_adamw_config *cfg, const int64_t *n, const d
   do {
     a.tensors = 0;
     a.units = 0;
-    for (; i < cfg->tensors && a.tensors < kPerLaunch; ++i) {
+    for (; i < cfg->tensors; ++i) {
       if (n[i] == 0) continue;
+      if (a.tensors == kPerLaunch) break;
       Entry &e = a.e[a.tensors++];
       e.p = params[i];
       e.g = grads[i];

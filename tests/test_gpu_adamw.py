@@ -292,3 +292,24 @@ def test_a_parameter_that_rounds_to_infinity(bits, param, step, infinite):
     flagged = infinite and param == "bf16"
     assert opt.status(state) == {"step": moe.DEV_NONFINITE_UPDATE if flagged else 0}
     assert bool(torch.isinf(p[77])) == flagged
+
+
+
+@pytest.mark.parametrize("tensors,empty,launches", [(64, 0, 1), (64, 5, 1), (65, 0, 2), (128, 3, 2), (0, 3, 1)])
+def test_launches_of_a_call(tensors, empty, launches):
+    """64 tensors with elements are one launch, whatever empty ones stand around them."""
+    shapes = [(0,)] * empty + [(3,)] * tensors + [(0, 2)] * empty
+    opt = moe.AdamW(shapes)
+    params = [torch.ones(s, device="cuda") for s in shapes]
+    grads = [torch.ones(s, device="cuda", dtype=torch.bfloat16) for s in shapes]
+    state = opt.new_state()
+    opt.step(params, grads, state, 1e-2)
+    events = [torch.cuda.Event(enable_timing=True) for _ in range(16)]
+    moe.timing_attach(events)
+    try:
+        opt.step(params, grads, state, 1e-2)
+        torch.cuda.synchronize()
+        assert moe.timing_count() == launches
+    finally:
+        moe.timing_attach(None)
+    assert state["step"].tolist() == [0, 2, 0, 0]
