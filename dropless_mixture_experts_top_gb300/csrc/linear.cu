@@ -177,9 +177,15 @@ __device__ __forceinline__ float gelu_arg(float z) {
   const float c = fminf(fmaxf(z, -20.f), 20.f);
   return c * fmaf(kGelu3 * c, c, kGelu1);
 }
+// Maximum that is NaN where one of the two is: a NaN in front of an activation is one behind it.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
 __device__ __forceinline__ float activate(float z, int act) {
   switch (act) {
-    case MOE_ACT_RELU: return fmaxf(z, 0.f);
+    case MOE_ACT_RELU: return max_nan(z, 0.f);
     case MOE_ACT_SILU: return z * sigmoid_(z);
     case MOE_ACT_GELU: return z * sigmoid_(gelu_arg(z));
     default: return z;

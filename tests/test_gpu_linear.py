@@ -380,3 +380,26 @@ def test_layers_of_every_kind_in_one_graph():
             ref = first["y"].double() @ V.double() + x.double()
             assert torch.all((second["y"].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + V.shape[0] * 2.0 ** -24 * terms * 1.01)
     assert all(p.status() == {"last": 0} for ab in plans for p in ab)
+
+
+
+# few tokens, whole tiles of single CTAs and of pairs, clusters, parts of both
+PATHS = [(1, 1536, 1096), (8, 512, 520), (300, 136, 264), (2049, 1024, 4096), (16, 4096, 1536), (128, 30000, 64), (4104, 4104, 1032)]
+
+
+@pytest.mark.parametrize("T,K,N", PATHS)
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu"])
+def test_nan_passes_the_activation(T, K, N, act):
+    x, W, b, r = whole(T, K, seed=1), whole(K, N, seed=2), whole(N, seed=3, most=9), whole(T, N, seed=4, most=9)
+    lin = moe.Linear(T, K, N, activation=act)
+    want = lin.forward(x, W, b, residual=r)
+    bt = b.clone()
+    bt[5] = torch.nan
+    x[-1, K // 2] = torch.nan
+    out = lin.forward(x, W, bt, residual=r)
+    hit = torch.zeros(T, N, dtype=torch.bool, device="cuda")
+    hit[-1], hit[:, 5] = True, True
+    for n in ("y", "z"):
+        assert torch.equal(out[n].isnan(), hit)
+        assert torch.equal(out[n][~hit], want[n][~hit])
+    assert torch.equal(lin.forward(x, W, bt, residual=r, save=False)["y"].isnan(), hit)
