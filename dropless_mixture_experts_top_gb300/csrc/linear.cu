@@ -172,16 +172,22 @@ __device__ __forceinline__ void unpack_row(const uint4 (&w)[4], float (&v)[32]) 
 __device__ __forceinline__ float sigmoid_(float a) { return __fdividef(1.f, 1.f + __expf(-a)); }
 constexpr float kGelu1 = 1.5957691216057308f;   // 2 sqrt(2 / pi)
 constexpr float kGelu3 = 0.071354816272600252f; // times 0.044715
-// Past 20 gelu's sigmoid is 0 or 1 to the last bit, and its slope's polynomial would overflow first.
-__device__ __forceinline__ float gelu_arg(float z) {
-  const float c = fminf(fmaxf(z, -20.f), 20.f);
-  return c * fmaf(kGelu3 * c, c, kGelu1);
-}
-// Maximum that is NaN where one of the two is: a NaN in front of an activation is one behind it.
+// Maximum and minimum that are NaN where one of the two is: a NaN of z is one of y and of dz.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float y;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
   return y;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+// Past 20 gelu's sigmoid is 0 or 1 to the last bit, and its slope's polynomial would overflow first.
+__device__ __forceinline__ float gelu_clamp(float z) { return min_nan(max_nan(z, -20.f), 20.f); }
+__device__ __forceinline__ float gelu_arg(float z) {
+  const float c = gelu_clamp(z);
+  return c * fmaf(kGelu3 * c, c, kGelu1);
 }
 __device__ __forceinline__ float activate(float z, int act) {
   switch (act) {
@@ -193,13 +199,13 @@ __device__ __forceinline__ float activate(float z, int act) {
 }
 __device__ __forceinline__ float slope(float z, int act) {
   switch (act) {
-    case MOE_ACT_RELU: return z > 0.f ? 1.f : 0.f;
+    case MOE_ACT_RELU: return z > 0.f ? 1.f : max_nan(z, 0.f);  // 0, or NaN
     case MOE_ACT_SILU: {
       const float s = sigmoid_(z);
       return fmaf(z * s, 1.f - s, s);
     }
     case MOE_ACT_GELU: {
-      const float c = fminf(fmaxf(z, -20.f), 20.f), s = sigmoid_(gelu_arg(z));
+      const float c = gelu_clamp(z), s = sigmoid_(gelu_arg(z));
       return fmaf(c * s * (1.f - s), fmaf(3.f * kGelu3 * c, c, kGelu1), s);
     }
     default: return 1.f;

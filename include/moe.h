@@ -478,9 +478,9 @@ moe_status moe_adamw_step(const moe_adamw_config *cfg, const int64_t *n, const d
  *   not computed (W is only read for dx, x for dW).  z as the forward left it; NULL without an
  *   activation.  dz enters the products rounded to bf16, dbias as it is.  The residual's gradient is dy itself.
  *   Outputs overlap no input.
- * Activations: relu, silu z / (1 + e^-z), gelu in its tanh form (not the one by erf).  A NaN of z is one of y.
- * Sums run in a fixed order: the same call leaves the same bits (the order goes by the sizes and by which of dx and
- * dW are asked for).  0 <= T <= 2^30; K and N multiples of 8, 8 to 65536; T times either below 2^40.  With T == 0 the
+ * Activations: relu, silu z / (1 + e^-z), gelu in its tanh form (not the one by erf).  A NaN of z is a NaN of
+ * y and of dz.  Sums run in a fixed order: the same call leaves the same bits (the order goes by the sizes and by
+ * which of dx and dW are asked for).  0 <= T <= 2^30; K and N multiples of 8, 8 to 65536; T times either below 2^40.  With T == 0 the
  * weight gradients are zeroed.
  * Status word at the start of each scratch. */
 typedef enum {

@@ -403,3 +403,20 @@ def test_nan_passes_the_activation(T, K, N, act):
         assert torch.equal(out[n].isnan(), hit)
         assert torch.equal(out[n][~hit], want[n][~hit])
     assert torch.equal(lin.forward(x, W, bt, residual=r, save=False)["y"].isnan(), hit)
+
+
+
+@pytest.mark.parametrize("T,K,N", [(1, 64, 72), (777, 1000, 520), (2049, 1024, 4096)])
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu"])
+def test_nan_passes_the_slope(T, K, N, act):
+    """A NaN of z is one of dz: its row of dx, its column of dW and its element of dbias, and nothing else."""
+    x, W, dy, z = whole(T, K, seed=1), whole(K, N, seed=2), whole(T, N, seed=5), whole(T, N, seed=6)
+    lin = moe.Linear(T, K, N, activation=act)
+    z[-1, 9] = 0
+    want = {n: t.clone() for n, t in lin.backward(dy, x, W, z).items()}
+    z[-1, 9] = torch.nan
+    got = lin.backward(dy, x, W, z)
+    assert bool(got["dx"][-1].isnan().all()) and bool(got["dW"][:, 9].isnan().all()) and bool(got["dbias"][9].isnan())
+    cols = torch.arange(N, device="cuda") != 9
+    assert torch.equal(got["dx"][:-1], want["dx"][:-1])
+    assert torch.equal(got["dW"][:, cols], want["dW"][:, cols]) and torch.equal(got["dbias"][cols], want["dbias"][cols])
