@@ -55,7 +55,9 @@ constexpr int kEpiWarps = 8;
 constexpr int kGemmThreads = 64 + 32 * kEpiWarps;
 constexpr int kGemmSmem = kStages * kStageBytes + 256 + 1024 /*align*/;
 static_assert(kGemmSmem <= 227 * 1024, "shared memory budget");
-constexpr int kRuleSms = 152;         // the workspace's size is known without a GPU
+// Products are cut for 152 SMs wherever they run: the workspace's size is known without a GPU, the order of sums goes by the
+// sizes alone.
+constexpr int kRuleSms = 152;
 constexpr int kMaxSplit = 16;
 constexpr int kLeastStages = 4;       // of a part of a split reduction
 
@@ -875,8 +877,8 @@ struct Cut {
   int cg, nm, nn, full, split, units, cluster;
   double cost;
 };
-Cut cut_with(int64_t M, int64_t N, int64_t K, int cg, bool parts, int sms) {
-  const int ts = tile_size(cg), groups = sms / cg;
+Cut cut_with(int64_t M, int64_t N, int64_t K, int cg, bool parts) {
+  const int ts = tile_size(cg), groups = kRuleSms / cg;
   Cut c;
   c.cg = cg;
   c.nm = static_cast<int>((M + ts - 1) / ts);
@@ -895,23 +897,27 @@ Cut cut_with(int64_t M, int64_t N, int64_t K, int cg, bool parts, int sms) {
   if (c.split > 1) c.cost += (nstage + c.split - 1) / c.split * stage + ends + 5;
   return c;
 }
-Cut cut_of(int64_t M, int64_t N, int64_t K, int sms) {
-  Cut best = cut_with(M, N, K, 2, false, sms);
+Cut cut_of(int64_t M, int64_t N, int64_t K) {
+  Cut best = cut_with(M, N, K, 2, false);
   for (int way = 1; way < 4; ++way) {
-    const Cut c = cut_with(M, N, K, way & 1 ? 1 : 2, way > 1, sms);
+    const Cut c = cut_with(M, N, K, way & 1 ? 1 : 2, way > 1);
     if (c.cost < best.cost) best = c;
   }
   for (int blocks = 2; blocks <= 8; blocks *= 2) {
-    Cut c = cut_with(M, N, K, 1, false, sms);
+    Cut c = cut_with(M, N, K, 1, false);
     const int nstage = static_cast<int>((K + 2 * BK - 1) / (2 * BK));
-    if (c.units > sms / 2 * (blocks == 2 ? 76 : blocks == 4 ? 36 : 15) / 76 || nstage < blocks) break;
+    if (c.units > (blocks == 2 ? 76 : blocks == 4 ? 36 : 15) || nstage < blocks) break;
     c.cluster = blocks;
     c.cost = (nstage + blocks - 1) / blocks * 0.46 + 0.8 + 1.5;
     if (c.cost < best.cost) best = c;
   }
   return best;
 }
-constexpr size_t kPartBytes = static_cast<size_t>(kRuleSms) * BM * BM * 4 * 2;  // parts of a round of pairs (or singles)
+// The sums that the parts of a cut leave: part_at's, 16 bytes of each lane.  At most a round of pairs, 20 MB; most shapes
+// are not cut into parts.
+size_t part_bytes(const Cut &c) {
+  return static_cast<size_t>(c.units - c.full) * tile_size(c.cg) * tile_size(c.cg) * 4;
+}
 
 // The kernel's shared-memory opt-in, and how many groups of CTAs fit at once; once per device.
 template <int KIND, int CG>
@@ -991,9 +997,8 @@ cudaError_t launch_cut(const Operands &o, const Cut &c, int sms, cudaStream_t s)
 }
 
 template <int KIND>
-moe_status product(const char *label, const void *a, const void *b, int M, int N, int K, const Ends &ends, float *part,
-                   int32_t *status, bool first, int sms, cudaStream_t s) {
-  const Cut c = cut_of(M, N, K, std::min(sms, kRuleSms));
+moe_status product(const char *label, const Cut &c, const void *a, const void *b, int M, int N, int K, const Ends &ends,
+                   float *part, int32_t *status, bool first, int sms, cudaStream_t s) {
   Operands o;
   if (!operands(&o, KIND, a, b, M, N, K, c, ends, part, status, first)) return MOE_ERR_CUDA;
   return timed(label, s, [&] { return c.cg == 2 ? launch_cut<KIND, 2>(o, c, sms, s) : launch_cut<KIND, 1>(o, c, sms, s); });
@@ -1003,17 +1008,15 @@ moe_status product(const char *label, const void *a, const void *b, int M, int N
 // two one after the other: tokens, in, out in one and in two launches: 16 x 1024 x 1024 8.4 us and 12.4; 777 x 1000 x 520
 // 13.3 and 19.8; 2048 x 512 x 512 15.7 and 16.5; by the rule in two: 3000 x 384 x 384 20.9 and 18.0, 8192 x 128 x 128 42.2
 // and 18.0 (their dW is cut along the tokens).
-// *sums_left: dbias' partial rows (sums, rows) are still to be added up; where blocks are left for that, this launch does
-// (777 x 1000 x 520 with gelu and bias 11.4 us, with a launch for it in front 12.2).
-moe_status both_products(const void *dz, const void *W, const void *x, int T, int K, int N, const Ends &dx, const Ends &dw,
-                         const float *sums, int rows, float *dbias, int32_t *status, bool first, int sms, cudaStream_t s,
-                         bool *sums_left, bool *done) {
-  const int most = std::min(sms, kRuleSms);
-  const Cut cx = cut_with(T, K, N, 1, false, most), cw = cut_with(K, N, T, 1, false, most);
+// apart: what the two take one after the other.  *sums_left: dbias' partial rows (sums, rows) are still to be added up;
+// where blocks are left for that, this launch does (777 x 1000 x 520 with gelu and bias 11.4 us, with a launch for it in
+// front 12.2).
+moe_status both_products(double apart, const void *dz, const void *W, const void *x, int T, int K, int N, const Ends &dx,
+                         const Ends &dw, const float *sums, int rows, float *dbias, int32_t *status, bool first, int sms,
+                         cudaStream_t s, bool *sums_left, bool *done) {
+  const Cut cx = cut_with(T, K, N, 1, false), cw = cut_with(K, N, T, 1, false);
   *done = false;
-  if (static_cast<int64_t>(cx.units) + cw.units > most ||
-      std::max(cx.cost, cw.cost) > cut_of(T, K, N, most).cost + cut_of(K, N, T, most).cost)
-    return MOE_OK;
+  if (static_cast<int64_t>(cx.units) + cw.units > kRuleSms || std::max(cx.cost, cw.cost) > apart) return MOE_OK;
   int groups = 0;
   if (groups_of<kBoth, 1>(sms, &groups) != cudaSuccess) return MOE_ERR_CUDA;
   if (cx.units + cw.units > groups) return MOE_OK;
@@ -1055,14 +1058,23 @@ bool linear_ok(const moe_linear_config *c) {
   return c->act >= MOE_ACT_NONE && c->act <= MOE_ACT_GELU;
 }
 
+// The scratch: the status word and the parts' sums; the backward's holds those of any of the three products, so that it
+// serves the forward, too, then dz and dbias' partial rows.
+size_t fwd_bytes(const moe_linear_config *c, Cut *cut) {  // few rows: *cut is left as it is
+  if (few_rows(c->T, c->K, c->N)) return kHeader;
+  *cut = cut_of(c->T, c->N, c->K);
+  return kHeader + part_bytes(*cut);
+}
 struct LinearLayout {
-  size_t part, fwd, dz, sums, bwd;
+  Cut dx, dw;
+  size_t dz, sums, bwd;
 };
 LinearLayout linear_layout(const moe_linear_config *c) {
   LinearLayout L;
-  L.part = kHeader;
-  L.fwd = L.part + kPartBytes;
-  L.dz = L.fwd;
+  L.dx = cut_of(c->T, c->K, c->N);
+  L.dw = cut_of(c->K, c->N, c->T);
+  Cut fwd;
+  L.dz = align256(std::max(fwd_bytes(c, &fwd), kHeader + std::max(part_bytes(L.dx), part_bytes(L.dw))));
   L.sums = L.dz + (c->act == MOE_ACT_NONE ? 0 : align256(static_cast<size_t>(c->T) * c->N * 2));
   L.bwd = L.sums + align256(static_cast<size_t>(dz_split(c->T, c->N)) * c->N * 4);
   return L;
@@ -1077,9 +1089,9 @@ extern "C" {
 
 moe_status moe_linear_workspace(const moe_linear_config *cfg, size_t *fwd_scratch, size_t *bwd_scratch) {
   if (!linear_ok(cfg)) return MOE_ERR_INVALID_ARG;
-  const LinearLayout L = linear_layout(cfg);
-  if (fwd_scratch) *fwd_scratch = L.fwd;
-  if (bwd_scratch) *bwd_scratch = L.bwd;
+  Cut cut;
+  if (fwd_scratch) *fwd_scratch = fwd_bytes(cfg, &cut);
+  if (bwd_scratch) *bwd_scratch = linear_layout(cfg).bwd;
   return MOE_OK;
 }
 
@@ -1088,8 +1100,8 @@ moe_status moe_linear_forward(const moe_linear_config *cfg, const void *x, const
   if (!linear_ok(cfg)) return MOE_ERR_INVALID_ARG;
   if (!W || !scratch || (cfg->T > 0 && (!x || !y)) || (z && cfg->act == MOE_ACT_NONE)) return MOE_ERR_INVALID_ARG;
   if (!al16(x) || !al16(W) || !al16(bias) || !al16(residual) || !al16(y) || !al16(z) || !al16(scratch)) return MOE_ERR_ALIGNMENT;
-  const LinearLayout L = linear_layout(cfg);
-  if (scratch_bytes < L.fwd) return MOE_ERR_WORKSPACE;
+  Cut cut;
+  if (scratch_bytes < fwd_bytes(cfg, &cut)) return MOE_ERR_WORKSPACE;
   DevInfo di;
   MOE_TRY(device_info(&di));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1114,7 +1126,7 @@ moe_status moe_linear_forward(const moe_linear_config *cfg, const void *x, const
       return a.T == 1 ? rows_of<1>(a, s) : a.T == 2 ? rows_of<2>(a, s) : a.T <= 4 ? rows_of<4>(a, s) : rows_of<8>(a, s);
     });
   }
-  return product<kFwd>("linear_forward", x, W, cfg->T, cfg->N, cfg->K, e, reinterpret_cast<float *>(sc + L.part),
+  return product<kFwd>("linear_forward", cut, x, W, cfg->T, cfg->N, cfg->K, e, reinterpret_cast<float *>(sc + kHeader),
                        reinterpret_cast<int32_t *>(sc), true, di.sms, s);
 }
 
@@ -1140,7 +1152,7 @@ moe_status moe_linear_backward(const moe_linear_config *cfg, const void *dy, con
     if (dbias && cudaMemsetAsync(dbias, 0, static_cast<size_t>(N) * 4, s) != cudaSuccess) return MOE_ERR_CUDA;
     return MOE_OK;
   }
-  float *part = reinterpret_cast<float *>(sc + L.part);
+  float *part = reinterpret_cast<float *>(sc + kHeader);
   const void *dz = dy;
   bool first = true, sums_left = false;
   const float *sums = nullptr;  // dbias' partial rows
@@ -1174,16 +1186,17 @@ moe_status moe_linear_backward(const moe_linear_config *cfg, const void *dy, con
   ew.y = static_cast<uint16_t *>(dW);
   bool done = false;
   if (dx && dW)
-    MOE_TRY(both_products(dz, W, x, T, K, N, ex, ew, sums, rows, dbias, status, first, di.sms, s, &sums_left, &done));
+    MOE_TRY(both_products(L.dx.cost + L.dw.cost, dz, W, x, T, K, N, ex, ew, sums, rows, dbias, status, first, di.sms, s,
+                          &sums_left, &done));
   if (sums_left)
     MOE_TRY(timed("linear_dbias", s, [&] {
       return launch_pdl(linear_dbias_kernel, dim3((N + 31) / 32), dim3(kDzThreads), 0, s, 1, sums, rows, N, dbias);
     }));
   if (dx && !done) {
-    MOE_TRY(product<kDx>("linear_dx", dz, W, T, K, N, ex, part, status, first, di.sms, s));
+    MOE_TRY(product<kDx>("linear_dx", L.dx, dz, W, T, K, N, ex, part, status, first, di.sms, s));
     first = false;
   }
-  if (dW && !done) MOE_TRY(product<kDw>("linear_dW", x, dz, K, N, T, ew, part, status, first, di.sms, s));
+  if (dW && !done) MOE_TRY(product<kDw>("linear_dW", L.dw, x, dz, K, N, T, ew, part, status, first, di.sms, s));
   return MOE_OK;
 }
 

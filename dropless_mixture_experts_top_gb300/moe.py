@@ -693,8 +693,7 @@ class Linear(_Plan):
         self._dev, self._fwd, self._bwd = self.device.index, lib().moe_linear_forward, lib().moe_linear_backward
         self._tk, self._tn, self._kn, self._cols = (torch.Size(s) for s in ((T, K), (T, N), (K, N), (N,)))
         self._fwd_bytes = f.value
-        # one buffer for both: the backward starts with what the forward uses
-        self.scratch = self._take_scratch(b.value)
+        self.scratch = self._take_scratch(b.value)  # one buffer for both: the backward's serves the forward, too
         self._scratch = self.scratch.data_ptr()
 
     def forward(self, x, W, bias=None, residual=None, out=None, save=True, stream=None) -> dict:

@@ -480,8 +480,8 @@ moe_status moe_adamw_step(const moe_adamw_config *cfg, const int64_t *n, const d
  *   Outputs overlap no input.
  * Activations: relu, silu z / (1 + e^-z), gelu in its tanh form (not the one by erf).  A NaN of z is a NaN of
  * y and of dz.  Sums run in a fixed order: the same call leaves the same bits (the order goes by the sizes and by
- * which of dx and dW are asked for).  0 <= T <= 2^30; K and N multiples of 8, 8 to 65536; T times either below 2^40.  With T == 0 the
- * weight gradients are zeroed.
+ * which of dx and dW are asked for).  0 <= T <= 2^30; K and N multiples of 8, 8 to 65536; T times either below
+ * 2^40.  With T == 0 the weight gradients are zeroed.
  * Status word at the start of each scratch. */
 typedef enum {
   MOE_ACT_NONE = 0,

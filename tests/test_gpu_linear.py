@@ -420,3 +420,21 @@ def test_nan_passes_the_slope(T, K, N, act):
     cols = torch.arange(N, device="cuda") != 9
     assert torch.equal(got["dx"][:-1], want["dx"][:-1])
     assert torch.equal(got["dW"][:, cols], want["dW"][:, cols]) and torch.equal(got["dbias"][cols], want["dbias"][cols])
+
+
+
+@pytest.mark.parametrize("T,K,N", PATHS + [(1, 64, 72), (777, 1000, 520), (30000, 128, 64), (16000, 520, 520), (4104, 1032, 4104)])
+def test_the_workspace_is_all_that_is_written(T, K, N):
+    """Calls in a buffer that has 32 MB behind the workspace, as much as any product leaves in parts."""
+    x, W, b, dy, z = whole(T, K, seed=1), whole(K, N, seed=2), whole(N, seed=3), whole(T, N, seed=5), whole(T, N, seed=6)
+    lin = moe.Linear(T, K, N, activation="relu")
+    want = lin.forward(x, W, b), lin.backward(dy, x, W, z)
+    bwd = lin.scratch.numel()
+    big = torch.full((bwd + (32 << 20),), 77, dtype=torch.uint8, device="cuda")
+    lin.scratch, lin._scratch = big[:bwd], big.data_ptr()
+    for size, call, ref in ((lin._fwd_bytes, lambda: lin.forward(x, W, b), want[0]),
+                            (bwd, lambda: lin.backward(dy, x, W, z), want[1])):
+        big.fill_(77)
+        got = call()
+        assert all(torch.equal(got[n], ref[n]) for n in ref)
+        assert lin.status() == {"last": 0} and bool((big[size:] == 77).all())

@@ -100,3 +100,21 @@ def test_the_binding_s_refusals(monkeypatch):
     lin._dev = -1
     with pytest.raises(ValueError, match="bias: given"):
         lin.forward(bf(4, 8), bf(8, 16), bf(16))
+
+
+
+@pytest.mark.parametrize("T,K,N,fwd", [(1, 7168, 18432, 256), (2, 65536, 65536, 256), (512, 128, 64, 256), (777, 1000, 520, 256),
+                                       (2048, 4096, 4096, 256), (16384, 1536, 4096, 256), (0, 64, 64, 256),
+                                       (128, 30000, 64, 256 + 16 * 128 * 128 * 4), (16384, 4096, 4096, 256 + 72 * 256 * 256 * 4)])
+def test_workspaces_hold_what_the_products_leave(L, T, K, N, fwd):
+    """The status word; sums of the tiles that are cut into parts: none for most shapes.  The backward's: dz, and dbias' partial
+    rows (four blocks on each of 152 SMs at most), and the parts of the product that has the most, a round of pairs at most."""
+    for act in (0, 3):
+        f, b = ctypes.c_size_t(), ctypes.c_size_t()
+        assert L.moe_linear_workspace(ctypes.byref(moe.LinearConfig(T, K, N, act)), ctypes.byref(f), ctypes.byref(b)) == 0
+        assert f.value == fwd
+        dz = T * N * 2 if act else 0
+        assert fwd + dz + N * 4 <= b.value <= 256 + 76 * 256 * 256 * 4 + dz + 608 * 64 * 4 + N * 4 + 1024
+    f2, b2 = ctypes.c_size_t(), ctypes.c_size_t()
+    assert L.moe_linear_workspace(ctypes.byref(moe.LinearConfig(512, 128, 64, 0)), ctypes.byref(f2), ctypes.byref(b2)) == 0
+    assert b2.value <= 256 + 8 * 64 * 4  # a small layer: no parts anywhere
