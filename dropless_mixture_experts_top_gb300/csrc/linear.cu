@@ -765,7 +765,7 @@ int dz_split(int T, int N) {
 }
 struct DzArgs {
   const uint16_t *dy, *z;
-  uint16_t *dz;    // null: no activation, dy itself
+  uint16_t *dz;    // null: no activation, dy itself; or no product that reads it
   float *part;     // [split][N], or null: no bias
   float *dbias;
   int T, N, split;
@@ -810,8 +810,9 @@ __global__ void __launch_bounds__(kDzThreads, kDzPerSm) linear_dz_kernel(const D
             v[2 * h] *= slope(bf16_lo(x[h]), ACT);
             v[2 * h + 1] *= slope(bf16_hi(x[h]), ACT);
           }
-          *reinterpret_cast<uint4 *>(a.dz + t * a.N + c) =
-              make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+          if (a.dz)
+            *reinterpret_cast<uint4 *>(a.dz + t * a.N + c) =
+                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
         }
 #pragma unroll
         for (int h = 0; h < 8; ++h) sum[h] += v[h];
@@ -1161,7 +1162,7 @@ moe_status moe_linear_backward(const moe_linear_config *cfg, const void *dy, con
     DzArgs a{};
     a.dy = static_cast<const uint16_t *>(dy);
     a.z = static_cast<const uint16_t *>(z);
-    a.dz = act ? reinterpret_cast<uint16_t *>(sc + L.dz) : nullptr;
+    a.dz = act && (dx || dW) ? reinterpret_cast<uint16_t *>(sc + L.dz) : nullptr;
     a.dbias = dbias;
     a.part = dbias ? reinterpret_cast<float *>(sc + L.sums) : nullptr;
     a.T = T;

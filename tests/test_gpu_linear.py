@@ -438,3 +438,16 @@ def test_the_workspace_is_all_that_is_written(T, K, N):
         got = call()
         assert all(torch.equal(got[n], ref[n]) for n in ref)
         assert lin.status() == {"last": 0} and bool((big[size:] == 77).all())
+
+
+
+def test_the_bias_alone_writes_no_dz():
+    T, K, N = 3000, 64, 264
+    x, W, dy, z = whole(T, K, seed=1), whole(K, N, seed=2), whole(T, N, seed=5), whole(T, N, seed=6)
+    lin = moe.Linear(T, K, N, activation="relu")
+    want = lin.backward(dy, x, W, z)["dbias"].clone()
+    lin.scratch.fill_(77)
+    got = lin.backward(dy, x, W, z, grads={"dx": None, "dW": None, "dbias": torch.empty(N, device="cuda")})
+    assert torch.equal(got["dbias"], want) and lin.status() == {"last": 0}
+    # the status word, and a partial row of dbias for every 96 rows
+    assert int((lin.scratch != 77).sum()) <= 256 + -(-T // 96) * N * 4
