@@ -23,7 +23,7 @@
 // all experts in whole vectors, a lane's experts are neighbours (VEC): whole sectors per
 // load, and groups are runs of lanes.
 //
-// Bound by instructions (131072 x 256: 317 a token) and by the few warps that its registers leave: fewer lanes per
+// Bound by instructions (131072 x 256 in 8 groups: 314 a token) and by the few warps that its registers leave: fewer lanes per
 // token share the steps between lanes among more tokens, at the price of longer lists to sort, and four
 // blocks an SM without loads ahead hide more than two with (131072 x 256 in 8 groups 72 and 94 us; 16 lanes a token 104).
 #pragma once
@@ -127,10 +127,21 @@ constexpr int kWarps = kGateThreads / 32;
 //   reciprocal by one: 2^-24 + 0.23 2^-23 + s (2^-24 + 2^-23), 2.2 units; bias * scale + base rounded,
 //   half a unit, the product rounded, half: 3.2.  Two numbers that differ by more than 6.4 are in the order
 //   of the exact ones.
-//   softmax: e = 2^((l - m) log2 e) off by 2^-22 of itself and by |l - m| 2^-22 for the rounded difference and
-//   argument, which with the e^-|l - m| of its size is at most 0.37 2^-22; the sum Z by 13 roundings and its
-//   terms, 1.3e-6; the quotient by 2 ulp: 1.9e-6 in all, 16 units, with the roundings 17: 35.
+//   softmax: s = e / Z, e = 2^((l - m) log2 e). Two numbers of one token are compared. They share the error of 1 / Z, which
+//   enters their difference by |s_i - s_j| <= 1; their own errors go with s_i + s_j <= 1. In units:
+//     shared: half for each rounding of Z, NV - 1 in a lane and log2 LPT across the lanes (34 of 32 experts on 8 lanes:
+//     17); its terms, off by 2^-22 of themselves for the exponential (2) and by |l - m| 2.25 2^-24 for the argument
+//     (difference, constant and product), whose mean over the scores is at most 3.34 2.25 2^-24 with 256 experts (F of
+//     F e^F = 255 / e: one at the top, the others 1 + F below; 3.8); the reciprocal's ulp (1);
+//     own: the exponential (2), the argument (|l - m| e^-|l - m| <= 0.37 for each of the two: 0.9), the product (0.5);
+//     both numbers' roundings as above (2).
+//   12.2 and half for each rounding of Z: 29.2. Sums of two scores have 2 more for their numbers, and twice the distance.
 constexpr int kNearSigmoid = 7, kNearSoftmax = 35;
+constexpr bool softmax_bound_holds(int lanes, int experts) {
+  int roundings = experts - 1;
+  for (; lanes > 1; lanes /= 2) ++roundings;
+  return 2 * kNearSoftmax >= roundings + 25;
+}
 constexpr float kFixOne = 8388608.f;       // 2^23
 constexpr float kFixLeast = 8.f;           // the least number of an expert that may be chosen; 0: it may not
 constexpr float kLog2e = 1.4426950408889634f;
@@ -580,6 +591,7 @@ __global__ void __launch_bounds__(kGateThreads, 4) gate_select_kernel(const Gate
   constexpr int kNear = KEY == kKeyLogit ? 0 : (KEY == kKeySigmoid ? kNearSigmoid : kNearSoftmax);
   constexpr bool KEYS = GROUPS && !VEC;                  // groups by way of shared memory
   static_assert(!KEYS || LPT == 32, "a lane per group");
+  static_assert(KEY != kKeySoftmax || softmax_bound_holds(LPT, NV), "the sum over the experts has too many roundings");
   constexpr int TPW = 32 / LPT, kStep = kWarps * TPW;    // tokens of a warp, of the block, at once
   constexpr int ND = NV < 8 ? NV : 8;                    // a lane's sorted keys
   constexpr int kWords = kGateTok / 32;
