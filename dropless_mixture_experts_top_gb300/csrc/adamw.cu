@@ -12,8 +12,8 @@
 // positive root is never rounded to zero, since a zero under a nonzero m would make
 // an update as large as m / eps.
 //
-// Bound by memory: fp32 states with bf16 gradients and copies move 28 bytes per element (302 million elements: 1277 us, 99%
-// of what a copy moves in that time), 8-bit ones 16 (788 us, 92%).  A warp takes 256 elements (a block of the states)
+// Bound by memory: fp32 states with bf16 gradients and copies move 28 bytes per element (302 million elements: 1270 to 1290
+// us, 98 to 99% of what a copy moves in that time), 8-bit ones 16 (780 to 794 us, 91 to 93%).  A warp takes 256 elements (a block of the states)
 // in accesses of whole lines and reduces the block's largest by redux; with 8-bit states it has the next 256 under way
 // meanwhile (without that, and with checks and choices for every element, it was bound by its instructions: 1260 us).
 // The tensors' addresses
@@ -36,7 +36,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 // Blocks per SM, by the states' bits.  Measured, 302 million elements: 32 bits 2, 3 and 4 blocks 1277, 1297 and 1347 us (4
-// spill); 8 bits 2, 3 and 4 blocks 840, 788 and 945 us.
+// spill); 8 bits 2, 3 and 4 blocks 803, 794 and 900 us.
 constexpr int kBlocks32 = 2, kBlocks8 = 3;
 constexpr int kBlock = 256;       // elements of a warp's unit, which share a scale
 constexpr int kPerLaunch = 64;    // tensors of one launch (its parameters stay below 4 KB)

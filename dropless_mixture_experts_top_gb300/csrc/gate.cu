@@ -18,7 +18,7 @@ constexpr int kMaxGroups = 32;
 
 // A block per chunk, in the clusters of the first kernel: they share the adding of the totals.  The chunk's slots are put
 // in the order of their rows in shared memory first, where they fit: an expert's are neighbours in the rows' arrays, and
-// written one by one each would be a sector of its own (131072 x 8 slots, both kernels: 116 us).
+// written one by one each would be a sector of its own (131072 x 8 slots: 116 us for the gate instead of 96).
 constexpr int kSorted = 4096;
 __global__ void __launch_bounds__(kGateThreads) gate_index_kernel(const GateArgs a, int clusters) {
   __shared__ int32_t s_sum[2][kMaxExperts];  // this block's part of the totals: the clusters in front, and all

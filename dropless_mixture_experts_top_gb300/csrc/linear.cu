@@ -3,8 +3,10 @@
 //
 //   forward   z = x W + bias,   y = act(z) + residual        x [T,K], W [K,N]
 //   backward  dz = dy act'(z),  dx = dz W^T,  dW = x^T dz,  dbias = sum_t dz
-// x, W, bias, residual, z, y, dy, dx and dW are bf16, sums fp32; dz is rounded to
-// bf16 as an operand of the two products (dbias adds it up unrounded).
+// x, W, bias, residual, z, y, dy, dx and dW are bf16, sums fp32.  dz is rounded to bf16 as
+// an operand of the two products (dbias adds it up unrounded): dx and dW are then 2.3e-3 of
+// themselves off in the mean square where their own rounding alone makes 1.7e-3; the tensor core
+// multiplies bf16 by bf16, so that dz as the sum of two would be each product twice.
 //
 // Activations, in fp32:  relu;  silu z s(z);  gelu z s(2 sqrt(2/pi) (z + 0.044715 z^3)), the
 // tanh form written with the sigmoid s, which takes one exponential and one reciprocal.
@@ -25,10 +27,10 @@
 // together, one launch takes both, and the second step of dbias.  The forward of a few tokens is a pass over W on the
 // CUDA cores (linear_rows_kernel).
 //
-// What bounds it, measured (graphs of ten calls): 16384 x 4096 x 4096 280 us, 1970 TFLOP/s (a library's
-// product 269); 16384 x 1536 x 4096 114 us, 101 without the epilogue's stores, 126 with a residual, 135 with bias and
-// gelu (which stores z, too): the tensor pipe is busy 72% of the time with residual.  Back to back the part's
-// power cap holds both to 1.4e15 per second.  The backward of 16384 x 4096 x 1536 with silu takes 258: 117 for each
+// What bounds it, measured (graphs of ten calls): 16384 x 4096 x 4096 277 to 280 us, 1980 TFLOP/s (a library's
+// product 266 to 269); 16384 x 1536 x 4096 114 us, 101 without the epilogue's stores, 124 to 127 with a residual, 135 with
+// bias and gelu (which stores z, too): the tensor pipe is busy 72% of the time with residual.  Back to back the part's
+// power cap holds both to 1.4e15 per second.  The backward of 16384 x 4096 x 1536 with silu takes 258 to 262: 117 for each
 // product, 27 for dz and dbias.  Few tiles: 4 us and 0.46 us for each 128 of the reduction, 1.5 more in
 // clusters, 5 in parts.
 // Every wait is bounded; on a timeout the kernel flags the status word, drains its

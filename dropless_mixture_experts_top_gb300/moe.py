@@ -679,7 +679,8 @@ ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 
 class Linear(_Plan):
     """A dense layer over [T, K]: y = act(x W + bias) + residual, W [K, N], and its
-    backward, all in bf16 with fp32 sums (the bias' gradient is fp32).
+    backward, all in bf16 with fp32 sums (the bias' gradient is fp32).  activation:
+    "none", "relu", "silu", "gelu" (the form by tanh, not the one by erf).
 
     Dictionaries that a call returned may be handed to the next one, which then
     writes into the same tensors."""
