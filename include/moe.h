@@ -449,9 +449,10 @@ moe_status moe_gate_update_bias(const moe_gate_config *cfg, float *bias, const i
  *   value times 448 times the reciprocal of that largest, rounded to nearest even, a root above zero to 2^-9 of the scale at least.  This step uses m and v from before the rounding.
  *   step: int32 [4]: the status word, the number of steps so far, and two words that are zero between
  *   calls.  A call adds one to the steps.
- * All of it starts as zeros.  A step after which a parameter or v is not finite sets MOE_DEV_NONFINITE_UPDATE
- * in the status word (of the last call; moe_get_device_status reads it from step); such an element is stored as
- * e4m3's NaN and leaves the scale of its block alone.  Where *grad_scale is not finite the step
+ * All of it starts as zeros.  A step after which a parameter (as it is stored: bf16 rounds what is too large to
+ * infinity) or v is not finite sets MOE_DEV_NONFINITE_UPDATE in the status word (of the last call;
+ * moe_get_device_status reads it from step); with 8 bits such an element's m and v are stored as e4m3's NaN and
+ * leave the scales of their block alone.  Where *grad_scale is not finite the step
  * is left out: nothing changes but the status word, which gets that flag.
  * Tensors overlap neither each other nor the states.  Calls of up to 64 tensors with elements are one launch. */
 typedef struct {
